@@ -327,6 +327,104 @@ int32_t oft_linear_bwd_noalloc(const oft_linear_desc* d, const uint16_t* dy, con
 int32_t oft_logprob_diff(int32_t T, int32_t V, const float* logits_actor, const float* logits_ref,
                          const int32_t* labels, float* out, void* stream);
 
+/* ---- losses on vocabulary logits -------------------------------------------
+ * What a training step of the adapter and a rollout server compute from rows
+ * of logits (the pages' RL objective compares policies by the
+ * log-probabilities of sampled tokens; the chooseai.io page's "Five design
+ * features of the adapter-first architecture").  Row t holds
+ * x_i = logits[t ld + i], i < V, tau the temperature:
+ *   m = max_i x_i, z_i = (x_i - m) / tau, l = log sum_i exp z_i,
+ *   log p_i = z_i - l,
+ * and the forward calls leave stats [T, 2] = (m, l) for the backward ones.
+ * All arithmetic is fp32; a gradient is rounded once, to d_logits' type.
+ *
+ * Rows in which this has no plain meaning:
+ *   - a logit of -inf (a masked token) has p = 0 and gets no gradient from p;
+ *   - a row of nothing but -inf has stats (-inf, -inf) and log p = -inf; its
+ *     entropy is 0 and its whole gradient 0;
+ *   - a NaN or +inf logit makes l, the row's log-probabilities, entropy and
+ *     loss, and (unless its upstream gradients are 0) its gradient NaN. */
+#define OFT_MAX_TOP 128     /* top alternatives of oft_token_logprobs     */
+#define OFT_MAX_TEACHER 256 /* listed teacher entries of oft_distill_topk */
+#define OFT_NO_LABEL (-1)   /* a row (teacher entry) without a token      */
+
+/* Constraints: T >= 0 (T == 0 is a no-op), V >= 1, ld >= V, ld_grad >= V,
+ * temperature finite and > 0 with 1 / temperature finite, accumulate in
+ * {0, 1} (else OFT_EINVAL); dtype OFT_DT_BF16 or OFT_DT_F32 (else
+ * OFT_EDTYPE).  oft_token_logprobs: 0 <= k <= OFT_MAX_TOP (else
+ * OFT_EUNSUPPORTED) and k <= V (else OFT_ESHAPE); oft_distill_topk and its
+ * backward: 1 <= k <= OFT_MAX_TEACHER (else OFT_EUNSUPPORTED);
+ * oft_token_logprobs_bwd ignores k.  Size range (else OFT_EUNSUPPORTED):
+ * T <= 2^22, V <= 2^24, T ld and T ld_grad < 2^40. */
+typedef struct {
+  int32_t T, V;       /* rows, vocabulary                                    */
+  int32_t dtype;      /* of logits and d_logits                              */
+  int32_t k;          /* top alternatives, or listed teacher entries         */
+  int64_t ld;         /* elements from one logits row to the next            */
+  int64_t ld_grad;    /* elements from one d_logits row to the next; the
+                         forward calls only check it                         */
+  float temperature;  /* tau                                                 */
+  int32_t accumulate; /* backward: 0 writes d_logits, 1 adds to it           */
+} oft_vocab_desc;
+
+/* Workspace of either forward call with this descriptor (the backward calls
+ * need none); writes *bytes. */
+int32_t oft_vocab_workspace_bytes(const oft_vocab_desc* d, size_t* bytes);
+
+/* Log-probabilities of given tokens, entropy and top alternatives.
+ *   logp[t]      log p_labels[t]; 0 where labels[t] == OFT_NO_LABEL, NaN for
+ *                any other label outside [0, V)
+ *   entropy[t]   -sum_i p_i log p_i
+ *   top_idx      int32 [T, k]: the columns of the k largest logits, best
+ *                first, equal ones by lower column (NaN ranks as -inf)
+ *   top_logp     [T, k]: their log p
+ *   stats        [T, 2]
+ * logits and d_logits need only their element type's alignment (2 or 4
+ * bytes); elements between the rows are neither read nor written.  labels
+ * and logp may be NULL together (no given tokens), entropy may be NULL;
+ * top_idx and top_logp are required when k > 0 and ignored when k == 0.
+ * Errors: OFT_EINVAL (null / misaligned pointer, ws included when the query
+ * gives more than 0 bytes), OFT_EWORKSPACE, and the descriptor's. */
+int32_t oft_token_logprobs(const oft_vocab_desc* d, const void* logits, const int32_t* labels_or_null,
+                           float* logp_or_null, float* entropy_or_null, int32_t* top_idx_or_null,
+                           float* top_logp_or_null, float* stats, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradient of sum_t g_logp[t] logp[t] + g_entropy[t] entropy[t]:
+ *   d_logits_i = (g_logp (1[i = label] - p_i) - g_entropy p_i (log p_i + H)) / tau
+ * labels, g_logp: both or neither NULL; entropy (as the forward wrote it)
+ * is required with g_entropy; one of the two gradients must be given.  A row
+ * with label OFT_NO_LABEL has g_logp 0 whatever the array holds; a row whose
+ * gradients are both 0 gets exactly 0 without being read, and a row with
+ * another label outside [0, V) gets NaN.  d_logits may be logits itself
+ * (same pointer, ld_grad == ld, accumulate == 0); any other overlap of the
+ * two is OFT_EINVAL. */
+int32_t oft_token_logprobs_bwd(const oft_vocab_desc* d, const void* logits, const int32_t* labels_or_null,
+                               const float* stats, const float* entropy_or_null, const float* g_logp_or_null,
+                               const float* g_entropy_or_null, void* d_logits, void* stream);
+
+/* Distillation from a teacher's top logits: teacher_idx int32 [T, k] names
+ * columns, teacher_logits [T, k] holds the teacher's logits or
+ * log-probabilities there (any shift per row; as oft_token_logprobs writes
+ * top_idx and top_logp).  With q = softmax(teacher_logits / tau) over the
+ * row's k entries,
+ *   loss[t] = sum_j q_j (log q_j - log p_{idx_j}).
+ * An entry with index OFT_NO_LABEL, or at -inf, has q = 0; a row without any
+ * other has loss 0 and gradient 0.  An index listed twice counts with both
+ * its q.  Any other index outside [0, V) makes the row's loss NaN, as does a
+ * NaN or +inf teacher value.  Errors as oft_token_logprobs. */
+int32_t oft_distill_topk(const oft_vocab_desc* d, const void* logits, const int32_t* teacher_idx,
+                         const float* teacher_logits, float* loss, float* stats, void* ws, size_t ws_bytes,
+                         void* stream);
+
+/* Gradient of sum_t g_loss[t] loss[t]:
+ *   d_logits_i = g_loss (p_i - sum_{j: idx_j = i} q_j) / tau.
+ * A row with g_loss 0 gets exactly 0 without being read; a row whose loss
+ * is NaN for its teacher entries gets NaN.  d_logits may be logits itself,
+ * as in oft_token_logprobs_bwd. */
+int32_t oft_distill_topk_bwd(const oft_vocab_desc* d, const void* logits, const int32_t* teacher_idx,
+                             const float* teacher_logits, const float* stats, const float* g_loss, void* d_logits,
+                             void* stream);
+
 /* ---- MoE layer ------------------------------------------------------------ */
 int32_t oft_moe_workspace_bytes(const oft_moe_desc* d, int32_t pass, size_t* bytes);
 
@@ -393,6 +491,37 @@ int32_t oft_moe_grouped_bwd(const oft_moe_desc* d, const uint16_t* dy, const oft
  * misaligned pointer when T > 0).  T == 0 is a no-op. */
 int32_t oft_moe_router_bwd(const oft_moe_desc* d, const float* logits, const int32_t* topk_idx,
                            const float* dw, float* d_logits, void* stream);
+
+/* Balance loss of the router over sequences of seq_len tokens, T = S seq_len
+ * (the pages' section "Dedicated optimisation for low-precision MoE models"
+ * runs the experts that the router selects: a batch is fast when they are
+ * evenly chosen).  mask uint8 [T], 0 for a padding token (NULL: no padding;
+ * a padded token's rows are not read).  Per sequence s, over its n unmasked
+ * tokens, with p the softmax over E of a token's logits:
+ *   counts[s, e] = pairs of topk_idx with value e (int32; an index outside
+ *                  [0, E) counts nowhere)
+ *   tokens[s]    = n
+ *   mean_prob[s, e] = (1 / n) sum_t p_te       (optional output)
+ *   loss[s]      = E sum_e counts[s, e] / (n k) mean_prob[s, e]
+ * (1 when evenly spread); n == 0 gives zeros.  As in the router calls a NaN
+ * logit ranks as -inf; a token of nothing but -inf has p = 0.  Uses T, E and
+ * k of the descriptor; the rest is only validated.  Deterministic.
+ * Errors: as oft_moe_route; OFT_EINVAL (seq_len < 1), OFT_ESHAPE
+ * (T % seq_len != 0). */
+int32_t oft_moe_balance_workspace_bytes(const oft_moe_desc* d, int32_t seq_len, size_t* bytes);
+int32_t oft_moe_balance(const oft_moe_desc* d, int32_t seq_len, const float* logits, const int32_t* topk_idx,
+                        const uint8_t* mask_or_null, int32_t* counts, int32_t* tokens, float* loss,
+                        float* mean_prob_or_null, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradient of sum_s g_loss[s] loss[s] with the counts held fixed (they are
+ * piecewise constant in the logits), f_e = counts[s, e] / (n k):
+ *   d_logits[t, e] = g_loss E / n p_te (f_e - sum_j f_j p_tj),
+ * 0 for padded tokens.  accumulate 1 adds it to d_logits (as
+ * oft_moe_router_bwd writes it), 0 writes it.  No workspace.  Errors: as
+ * oft_moe_balance; OFT_EINVAL (accumulate not 0 or 1). */
+int32_t oft_moe_balance_bwd(const oft_moe_desc* d, int32_t seq_len, const float* logits,
+                            const uint8_t* mask_or_null, const int32_t* counts, const int32_t* tokens,
+                            const float* g_loss, float* d_logits, int32_t accumulate, void* stream);
 
 #ifdef __cplusplus
 }

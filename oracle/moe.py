@@ -290,3 +290,52 @@ def bruteforce_forward(inp: dict, idx: np.ndarray, w: np.ndarray) -> np.ndarray:
         _, _, _, O = expert_forward(X, Wgu, Wd, R, I)
         y += gate[:, None] * O
     return y
+
+
+def balance(logits, topk_idx, seq_len, mask=None):
+    """Balance loss of the router per sequence of seq_len tokens: a dict of
+    counts [S, E], tokens [S], mean_prob [S, E] and loss [S], with
+    loss = E sum_e counts_e / (n k) mean_prob_e over the n unmasked tokens."""
+    L = np.asarray(logits, dtype=np.float64)
+    T, E = L.shape
+    idx = np.asarray(topk_idx, dtype=np.int64)
+    use = np.ones(T, bool) if mask is None else np.asarray(mask).astype(bool)
+    S = T // seq_len
+    p = _router_softmax(L)
+    counts, tokens = np.zeros((S, E), np.int64), np.zeros(S, np.int64)
+    P = np.zeros((S, E))
+    for s in range(S):
+        rows = [t for t in range(s * seq_len, (s + 1) * seq_len) if use[t]]
+        tokens[s] = len(rows)
+        for t in rows:
+            P[s] += p[t]
+            for e in idx[t]:
+                if 0 <= e < E:
+                    counts[s, e] += 1
+    n = np.maximum(tokens, 1)[:, None]
+    P /= n
+    loss = E * (counts / (n * idx.shape[1]) * P).sum(axis=1)
+    return {"counts": counts, "tokens": tokens, "mean_prob": P, "loss": loss}
+
+
+def _router_softmax(L):
+    """Row softmax; NaN ranks as -inf, a row of nothing but -inf gives 0."""
+    L = np.where(np.isnan(L), -np.inf, L)
+    mx = L.max(axis=1, keepdims=True)
+    e = np.exp(L - np.where(mx == -np.inf, 0.0, mx))
+    s = e.sum(axis=1, keepdims=True)
+    return np.where(s == 0, 0.0, e / np.where(s == 0, 1.0, s))
+
+
+def balance_grad(logits, counts, tokens, g_loss, k, seq_len, mask=None):
+    """d_logits of sum_s g_loss[s] loss[s], the counts held fixed."""
+    L = np.asarray(logits, dtype=np.float64)
+    T, E = L.shape
+    p = _router_softmax(L)
+    s = np.arange(T) // seq_len
+    n = np.maximum(np.asarray(tokens), 1)[s].astype(np.float64)
+    f = np.asarray(counts)[s] / (n * k)[:, None]
+    d = (np.asarray(g_loss, dtype=np.float64)[s] * E / n)[:, None] * p * (f - (f * p).sum(axis=1, keepdims=True))
+    if mask is not None:
+        d[~np.asarray(mask).astype(bool)] = 0.0
+    return d

@@ -10,18 +10,20 @@ import ctypes as C
 
 from . import _lib
 from ._lib import (OFT_DT_BF16, OFT_DT_F32, OFT_PASS_BWD, OFT_PASS_FWD, OFT_W_BF16,
-                   OFT_W_FP4_E2M1, OFT_W_FP8_E4M3, OFT_W_INT4, OFT_W_INT4_TILED, OftError, oft_linear_desc,
-                   oft_moe_desc, oft_moe_routing)
+                   OFT_W_FP4_E2M1, OFT_W_FP8_E4M3, OFT_W_INT4, OFT_W_INT4_TILED, OFT_MAX_TEACHER, OFT_MAX_TOP,
+                   OFT_NO_LABEL, OftError, oft_linear_desc, oft_moe_desc, oft_moe_routing, oft_vocab_desc)
 
 __all__ = [
     "OftError", "linear_desc", "moe_desc", "moe_routing", "cayley_build", "oft_dequant", "oft_pack_int4_tiled",
     "oft_linear_workspace_bytes", "oft_linear_fwd", "oft_linear_fwd_base", "oft_linear_bwd", "oft_linear_bwd_noalloc", "oft_logprob_diff",
     "oft_slots_switch", "oft_linear_fwd_slots",
     "oft_moe_workspace_bytes", "oft_moe_route", "oft_moe_router_bwd", "oft_moe_grouped_fwd", "oft_moe_grouped_fwd_base", "oft_moe_grouped_bwd", "abi_version",
+    "vocab_desc", "oft_vocab_workspace_bytes", "oft_token_logprobs", "oft_token_logprobs_bwd", "oft_distill_topk",
+    "oft_distill_topk_bwd", "oft_moe_balance_workspace_bytes", "oft_moe_balance", "oft_moe_balance_bwd",
     "prof_enable", "prof_records",
     "OFT_DT_BF16", "OFT_DT_F32", "OFT_W_INT4", "OFT_W_FP8_E4M3", "OFT_W_BF16", "OFT_W_FP4_E2M1", "OFT_W_INT4_TILED",
     "OFT_PASS_FWD",
-    "OFT_PASS_BWD",
+    "OFT_PASS_BWD", "OFT_MAX_TOP", "OFT_MAX_TEACHER", "OFT_NO_LABEL",
 ]
 
 
@@ -155,6 +157,201 @@ def oft_logprob_diff(logits_actor, logits_ref, labels, out, stream=None):
     T, V = logits_actor.shape
     _lib.check(_lib.load().oft_logprob_diff(int(T), int(V), _ptr(logits_actor), _ptr(logits_ref), _ptr(labels),
                                             _ptr(out), _stream(stream)), "oft_logprob_diff")
+
+
+# ---- losses on vocabulary logits and the router's balance loss -------------
+# These calls check their tensors against the descriptor (device, type, shape,
+# strides) and launch on the logits' device, on its current stream unless one
+# is given.
+def vocab_desc(T, V, dtype=OFT_DT_BF16, k=0, ld=None, ld_grad=None, temperature=1.0, accumulate=0) -> oft_vocab_desc:
+    """ld, ld_grad: elements from one row of logits / d_logits to the next
+    (ld defaults to V, ld_grad to ld)."""
+    d = oft_vocab_desc()
+    ld = V if ld is None else ld
+    d.T, d.V, d.dtype, d.k = int(T), int(V), int(dtype), int(k)
+    d.ld, d.ld_grad = int(ld), int(ld if ld_grad is None else ld_grad)
+    d.temperature, d.accumulate = float(temperature), int(accumulate)
+    return d
+
+
+def _names(*names):
+    import torch
+
+    return tuple(getattr(torch, n) for n in names)
+
+
+def _tensor(what, t, names, shape, dev, ld=None):
+    """t: a GPU tensor on `dev` of one of the named types and the given shape,
+    contiguous, or with rows `ld` apart."""
+    if t.device.type != "cuda" or t.device != dev:
+        raise ValueError(f"{what}: on {t.device}, want the GPU of the logits ({dev})")
+    if t.dtype not in _names(*names):
+        raise ValueError(f"{what}: {t.dtype}, want {' or '.join(names)}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, want {tuple(shape)}")
+    if ld is None:
+        if not t.is_contiguous():
+            raise ValueError(f"{what}: not contiguous")
+    elif (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) != ld):
+        raise ValueError(f"{what}: strides {t.stride()}, want ({ld}, 1)")
+
+
+def _rows(what, t, d, ld, dev):
+    _tensor(what, t, ("float32",) if d.dtype == OFT_DT_F32 else ("bfloat16", "int16", "uint16"), (d.T, d.V), dev, ld)
+
+
+def _optional(what, t, names, shape, dev):
+    if t is not None:
+        _tensor(what, t, names, shape, dev)
+
+
+def _workspace(ws, ws_bytes, dev):
+    if ws is None:
+        return
+    if ws.device != dev or not ws.is_contiguous() or ws.numel() * ws.element_size() < ws_bytes:
+        raise ValueError("ws: want a contiguous tensor of at least ws_bytes on the logits' device")
+
+
+class _on:
+    """Enter the logits' device; `stream(s)`: s, or that device's current stream."""
+
+    def __init__(self, t):
+        import torch
+
+        self.dev = t.device
+        self.guard = torch.cuda.device(t.device)
+
+    def __enter__(self):
+        self.guard.__enter__()
+        return _stream
+
+    def __exit__(self, *a):
+        return self.guard.__exit__(*a)
+
+
+def oft_vocab_workspace_bytes(desc) -> int:
+    n = C.c_size_t(0)
+    _lib.check(_lib.load().oft_vocab_workspace_bytes(C.byref(desc), C.byref(n)), "oft_vocab_workspace_bytes")
+    return n.value
+
+
+def oft_token_logprobs(desc, logits, labels, logp, stats, entropy=None, top_idx=None, top_logp=None, ws=None,
+                       ws_bytes=0, stream=None):
+    """Log-probabilities of the given tokens, entropy and top alternatives of
+    each row of logits; labels and logp may both be None."""
+    d, dev = desc, logits.device
+    _rows("logits", logits, d, d.ld, dev)
+    _optional("labels", labels, ("int32",), (d.T,), dev)
+    for what, t in (("logp", logp), ("entropy", entropy)):
+        _optional(what, t, ("float32",), (d.T,), dev)
+    _tensor("stats", stats, ("float32",), (d.T, 2), dev)
+    if d.k > 0:
+        _optional("top_idx", top_idx, ("int32",), (d.T, d.k), dev)
+        _optional("top_logp", top_logp, ("float32",), (d.T, d.k), dev)
+    _workspace(ws, ws_bytes, dev)
+    with _on(logits) as st:
+        _lib.check(_lib.load().oft_token_logprobs(C.byref(d), _ptr(logits), _ptr(labels), _ptr(logp), _ptr(entropy),
+                                                  _ptr(top_idx), _ptr(top_logp), _ptr(stats), _ptr(ws), ws_bytes,
+                                                  st(stream)), "oft_token_logprobs")
+
+
+def oft_token_logprobs_bwd(desc, logits, labels, stats, g_logp, d_logits, entropy=None, g_entropy=None, stream=None):
+    """d_logits of g_logp . logp + g_entropy . entropy; labels and g_logp may
+    both be None, and g_entropy may be None."""
+    d, dev = desc, logits.device
+    _rows("logits", logits, d, d.ld, dev)
+    _rows("d_logits", d_logits, d, d.ld_grad, dev)
+    _optional("labels", labels, ("int32",), (d.T,), dev)
+    _tensor("stats", stats, ("float32",), (d.T, 2), dev)
+    for what, t in (("g_logp", g_logp), ("entropy", entropy), ("g_entropy", g_entropy)):
+        _optional(what, t, ("float32",), (d.T,), dev)
+    with _on(logits) as st:
+        _lib.check(_lib.load().oft_token_logprobs_bwd(C.byref(d), _ptr(logits), _ptr(labels), _ptr(stats),
+                                                      _ptr(entropy), _ptr(g_logp), _ptr(g_entropy), _ptr(d_logits),
+                                                      st(stream)), "oft_token_logprobs_bwd")
+
+
+def _teacher(d, teacher_idx, teacher_logits, dev):
+    _tensor("teacher_idx", teacher_idx, ("int32",), (d.T, d.k), dev)
+    _tensor("teacher_logits", teacher_logits, ("float32",), (d.T, d.k), dev)
+
+
+def oft_distill_topk(desc, logits, teacher_idx, teacher_logits, loss, stats, ws=None, ws_bytes=0, stream=None):
+    """Per-row loss against the teacher's renormalised top list."""
+    d, dev = desc, logits.device
+    _rows("logits", logits, d, d.ld, dev)
+    _teacher(d, teacher_idx, teacher_logits, dev)
+    _tensor("loss", loss, ("float32",), (d.T,), dev)
+    _tensor("stats", stats, ("float32",), (d.T, 2), dev)
+    _workspace(ws, ws_bytes, dev)
+    with _on(logits) as st:
+        _lib.check(_lib.load().oft_distill_topk(C.byref(d), _ptr(logits), _ptr(teacher_idx), _ptr(teacher_logits),
+                                                _ptr(loss), _ptr(stats), _ptr(ws), ws_bytes, st(stream)),
+                   "oft_distill_topk")
+
+
+def oft_distill_topk_bwd(desc, logits, teacher_idx, teacher_logits, stats, g_loss, d_logits, stream=None):
+    """d_logits of g_loss . loss."""
+    d, dev = desc, logits.device
+    _rows("logits", logits, d, d.ld, dev)
+    _rows("d_logits", d_logits, d, d.ld_grad, dev)
+    _teacher(d, teacher_idx, teacher_logits, dev)
+    _tensor("stats", stats, ("float32",), (d.T, 2), dev)
+    _tensor("g_loss", g_loss, ("float32",), (d.T,), dev)
+    with _on(logits) as st:
+        _lib.check(_lib.load().oft_distill_topk_bwd(C.byref(d), _ptr(logits), _ptr(teacher_idx), _ptr(teacher_logits),
+                                                    _ptr(stats), _ptr(g_loss), _ptr(d_logits), st(stream)),
+                   "oft_distill_topk_bwd")
+
+
+def oft_moe_balance_workspace_bytes(desc, seq_len) -> int:
+    n = C.c_size_t(0)
+    _lib.check(_lib.load().oft_moe_balance_workspace_bytes(C.byref(desc), int(seq_len), C.byref(n)),
+               "oft_moe_balance_workspace_bytes")
+    return n.value
+
+
+def _sequences(desc, seq_len):
+    if seq_len < 1 or desc.T % seq_len:
+        raise ValueError(f"seq_len {seq_len}: want a divisor of the {desc.T} tokens")
+    return desc.T // seq_len
+
+
+def oft_moe_balance(desc, seq_len, logits, topk_idx, counts, tokens, loss, mean_prob=None, mask=None, ws=None,
+                    ws_bytes=0, stream=None):
+    """Balance loss, per-expert counts and mean probabilities of each
+    sequence of seq_len tokens; mask: uint8 or bool, false for padding."""
+    d, dev = desc, logits.device
+    S = _sequences(d, seq_len)
+    _tensor("logits", logits, ("float32",), (d.T, d.E), dev)
+    _tensor("topk_idx", topk_idx, ("int32",), (d.T, d.k), dev)
+    _optional("mask", mask, ("uint8", "bool"), (d.T,), dev)
+    _tensor("counts", counts, ("int32",), (S, d.E), dev)
+    _tensor("tokens", tokens, ("int32",), (S,), dev)
+    _tensor("loss", loss, ("float32",), (S,), dev)
+    _optional("mean_prob", mean_prob, ("float32",), (S, d.E), dev)
+    _workspace(ws, ws_bytes, dev)
+    with _on(logits) as st:
+        _lib.check(_lib.load().oft_moe_balance(C.byref(d), int(seq_len), _ptr(logits), _ptr(topk_idx), _ptr(mask),
+                                               _ptr(counts), _ptr(tokens), _ptr(loss), _ptr(mean_prob), _ptr(ws),
+                                               ws_bytes, st(stream)), "oft_moe_balance")
+
+
+def oft_moe_balance_bwd(desc, seq_len, logits, counts, tokens, g_loss, d_logits, mask=None, accumulate=0,
+                        stream=None):
+    """d_logits of g_loss . loss, written or (accumulate=1) added."""
+    d, dev = desc, logits.device
+    S = _sequences(d, seq_len)
+    _tensor("logits", logits, ("float32",), (d.T, d.E), dev)
+    _optional("mask", mask, ("uint8", "bool"), (d.T,), dev)
+    _tensor("counts", counts, ("int32",), (S, d.E), dev)
+    _tensor("tokens", tokens, ("int32",), (S,), dev)
+    _tensor("g_loss", g_loss, ("float32",), (S,), dev)
+    _tensor("d_logits", d_logits, ("float32",), (d.T, d.E), dev)
+    with _on(logits) as st:
+        _lib.check(_lib.load().oft_moe_balance_bwd(C.byref(d), int(seq_len), _ptr(logits), _ptr(mask), _ptr(counts),
+                                                   _ptr(tokens), _ptr(g_loss), _ptr(d_logits), int(accumulate),
+                                                   st(stream)), "oft_moe_balance_bwd")
 
 
 def oft_moe_workspace_bytes(desc, pass_) -> int:

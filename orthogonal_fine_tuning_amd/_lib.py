@@ -18,6 +18,7 @@ OFT_W_INT4, OFT_W_FP8_E4M3, OFT_W_BF16, OFT_W_FP4_E2M1, OFT_W_INT4_TILED = 0, 1,
 OFT_PASS_FWD, OFT_PASS_BWD = 0, 1
 OFT_MAX_SEGMENTS = 8
 OFT_NOALLOC_SCRATCH_BYTES = 128 << 20
+OFT_MAX_TOP, OFT_MAX_TEACHER, OFT_NO_LABEL = 128, 256, -1
 
 
 class oft_linear_desc(C.Structure):
@@ -37,6 +38,12 @@ class oft_moe_routing(C.Structure):
                 ("offsets", C.c_void_p), ("perm", C.c_void_p), ("inv_perm", C.c_void_p),
                 ("active", C.c_void_p), ("n_active", C.c_void_p),
                 ("chunk_of_expert", C.c_void_p)]
+
+
+class oft_vocab_desc(C.Structure):
+    _fields_ = [("T", C.c_int32), ("V", C.c_int32), ("dtype", C.c_int32), ("k", C.c_int32),
+                ("ld", C.c_int64), ("ld_grad", C.c_int64), ("temperature", C.c_float),
+                ("accumulate", C.c_int32)]
 
 
 _P = C.c_void_p
@@ -64,6 +71,14 @@ SIGNATURES = {
                             _P]),
     "oft_linear_bwd_noalloc": (_I, [C.POINTER(oft_linear_desc), _P, _P, _P, _P, _P, _P, _P, _P, _P]),
     "oft_logprob_diff": (_I, [_I, _I, _P, _P, _P, _P, _P]),
+    "oft_vocab_workspace_bytes": (_I, [C.POINTER(oft_vocab_desc), C.POINTER(_SZ)]),
+    "oft_token_logprobs": (_I, [C.POINTER(oft_vocab_desc), _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "oft_token_logprobs_bwd": (_I, [C.POINTER(oft_vocab_desc), _P, _P, _P, _P, _P, _P, _P, _P]),
+    "oft_distill_topk": (_I, [C.POINTER(oft_vocab_desc), _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "oft_distill_topk_bwd": (_I, [C.POINTER(oft_vocab_desc), _P, _P, _P, _P, _P, _P, _P]),
+    "oft_moe_balance_workspace_bytes": (_I, [C.POINTER(oft_moe_desc), _I, C.POINTER(_SZ)]),
+    "oft_moe_balance": (_I, [C.POINTER(oft_moe_desc), _I, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "oft_moe_balance_bwd": (_I, [C.POINTER(oft_moe_desc), _I, _P, _P, _P, _P, _P, _P, _I, _P]),
     "oft_moe_workspace_bytes": (_I, [C.POINTER(oft_moe_desc), _I, C.POINTER(_SZ)]),
     "oft_moe_route": (_I, [C.POINTER(oft_moe_desc), _P, C.POINTER(oft_moe_routing), _P, _SZ, _P]),
     "oft_moe_grouped_fwd": (_I, [C.POINTER(oft_moe_desc), _P, _P, _P, _P, _P, _P, _P,

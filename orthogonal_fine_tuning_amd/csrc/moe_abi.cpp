@@ -37,6 +37,13 @@ int32_t validate_moe(const oft_moe_desc* d) {
   return OFT_OK;
 }
 
+int32_t validate_balance(const oft_moe_desc* d, int32_t seq_len) {
+  const int32_t v = validate_moe(d);
+  if (v != OFT_OK) return v;
+  if (seq_len < 1) return OFT_EINVAL;
+  return d->T % seq_len != 0 ? OFT_ESHAPE : OFT_OK;
+}
+
 oft::MoeDims dims(const oft_moe_desc* d) {
   const int wf = d->w_fmt == OFT_W_INT4         ? oft::WF_INT4
                  : d->w_fmt == OFT_W_INT4_TILED ? oft::WF_INT4T
@@ -102,6 +109,43 @@ int32_t oft_moe_router_bwd(const oft_moe_desc* d, const float* logits, const int
   if (!ptr_ok(logits) || !ptr_ok(topk_idx) || !ptr_ok(dw) || !ptr_ok(d_logits)) return OFT_EINVAL;
   return hip_status(oft::launch_moe_router_bwd(dims(d), logits, topk_idx, dw, d_logits,
                                                static_cast<hipStream_t>(stream)));
+}
+
+int32_t oft_moe_balance_workspace_bytes(const oft_moe_desc* d, int32_t seq_len, size_t* bytes) {
+  if (bytes == nullptr) return OFT_EINVAL;
+  const int32_t v = validate_balance(d, seq_len);
+  if (v != OFT_OK) return v;
+  *bytes = oft::moe_balance_ws_bytes(dims(d), seq_len);
+  return OFT_OK;
+}
+
+int32_t oft_moe_balance(const oft_moe_desc* d, int32_t seq_len, const float* logits, const int32_t* topk_idx,
+                        const uint8_t* mask_or_null, int32_t* counts, int32_t* tokens, float* loss,
+                        float* mean_prob_or_null, void* ws, size_t ws_bytes, void* stream) {
+  const int32_t v = validate_balance(d, seq_len);
+  if (v != OFT_OK) return v;
+  if (d->T == 0) return OFT_OK;
+  if (!ptr_ok(logits) || !ptr_ok(topk_idx) || !opt_ok(mask_or_null) || !ptr_ok(counts) || !ptr_ok(tokens) ||
+      !ptr_ok(loss) || !opt_ok(mean_prob_or_null) || !ptr_ok(ws))
+    return OFT_EINVAL;
+  if (ws_bytes < oft::moe_balance_ws_bytes(dims(d), seq_len)) return OFT_EWORKSPACE;
+  const oft::MoeBalancePtrs q{logits, topk_idx, mask_or_null, counts, tokens, loss, mean_prob_or_null};
+  return hip_status(oft::launch_moe_balance(dims(d), seq_len, q, static_cast<char*>(ws),
+                                            static_cast<hipStream_t>(stream)));
+}
+
+int32_t oft_moe_balance_bwd(const oft_moe_desc* d, int32_t seq_len, const float* logits,
+                            const uint8_t* mask_or_null, const int32_t* counts, const int32_t* tokens,
+                            const float* g_loss, float* d_logits, int32_t accumulate, void* stream) {
+  const int32_t v = validate_balance(d, seq_len);
+  if (v != OFT_OK) return v;
+  if (accumulate != 0 && accumulate != 1) return OFT_EINVAL;
+  if (d->T == 0) return OFT_OK;
+  if (!ptr_ok(logits) || !opt_ok(mask_or_null) || !ptr_ok(counts) || !ptr_ok(tokens) || !ptr_ok(g_loss) ||
+      !ptr_ok(d_logits))
+    return OFT_EINVAL;
+  return hip_status(oft::launch_moe_balance_bwd(dims(d), seq_len, logits, mask_or_null, counts, tokens, g_loss,
+                                                d_logits, accumulate == 1, static_cast<hipStream_t>(stream)));
 }
 
 int32_t oft_moe_grouped_fwd(const oft_moe_desc* d, const uint16_t* x, const float* logits,

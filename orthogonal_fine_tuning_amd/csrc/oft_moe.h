@@ -73,4 +73,20 @@ hipError_t launch_moe_bwd(const MoeDims& d, const MoeBwdPtrs& q, const MoeRoutin
 hipError_t launch_moe_router_bwd(const MoeDims& d, const float* logits, const int* topk_idx, const float* dw,
                                  float* d_logits, hipStream_t st);
 
+// Router balance loss over sequences of seq_len tokens (T a multiple of it)
+struct MoeBalancePtrs {
+  const float* logits;
+  const int* topk_idx;
+  const uint8_t* mask;  // NULL: every token counts
+  int* counts;
+  int* tokens;
+  float* loss;
+  float* mean_prob;  // optional
+};
+size_t moe_balance_ws_bytes(const MoeDims& d, int seq_len);
+hipError_t launch_moe_balance(const MoeDims& d, int seq_len, const MoeBalancePtrs& q, char* ws, hipStream_t st);
+hipError_t launch_moe_balance_bwd(const MoeDims& d, int seq_len, const float* logits, const uint8_t* mask,
+                                  const int* counts, const int* tokens, const float* g_loss, float* d_logits,
+                                  bool accumulate, hipStream_t st);
+
 }  // namespace oft
