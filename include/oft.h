@@ -349,8 +349,7 @@ int32_t oft_logprob_diff(int32_t T, int32_t V, const float* logits_actor, const 
 #define OFT_NO_LABEL (-1)   /* a row (teacher entry) without a token      */
 
 /* Constraints: T >= 0 (T == 0 is a no-op), V >= 1, ld >= V, ld_grad >= V,
- * temperature finite and > 0 with 1 / temperature finite, accumulate in
- * {0, 1} (else OFT_EINVAL); dtype OFT_DT_BF16 or OFT_DT_F32 (else
+ * 2^-20 <= temperature <= 2^20, accumulate in {0, 1} (else OFT_EINVAL); dtype OFT_DT_BF16 or OFT_DT_F32 (else
  * OFT_EDTYPE).  oft_token_logprobs: 0 <= k <= OFT_MAX_TOP (else
  * OFT_EUNSUPPORTED) and k <= V (else OFT_ESHAPE); oft_distill_topk and its
  * backward: 1 <= k <= OFT_MAX_TEACHER (else OFT_EUNSUPPORTED);
@@ -376,7 +375,7 @@ int32_t oft_vocab_workspace_bytes(const oft_vocab_desc* d, size_t* bytes);
  *                any other label outside [0, V)
  *   entropy[t]   -sum_i p_i log p_i
  *   top_idx      int32 [T, k]: the columns of the k largest logits, best
- *                first, equal ones by lower column (NaN ranks as -inf)
+ *                first, equal ones by lower column (a quiet NaN ranks as -inf)
  *   top_logp     [T, k]: their log p
  *   stats        [T, 2]
  * logits and d_logits need only their element type's alignment (2 or 4

@@ -174,59 +174,64 @@ def vocab_desc(T, V, dtype=OFT_DT_BF16, k=0, ld=None, ld_grad=None, temperature=
     return d
 
 
-def _names(*names):
-    import torch
+_TYPES = {}
 
-    return tuple(getattr(torch, n) for n in names)
+
+def _types(names):
+    """The torch types of a kind of tensor ("int32", "bfloat16 int16 uint16"), looked up once."""
+    if names not in _TYPES:
+        import torch
+
+        _TYPES[names] = tuple(getattr(torch, n) for n in names.split())
+    return _TYPES[names]
 
 
 def _tensor(what, t, names, shape, dev, ld=None):
-    """t: a GPU tensor on `dev` of one of the named types and the given shape,
-    contiguous, or with rows `ld` apart."""
-    if t.device.type != "cuda" or t.device != dev:
-        raise ValueError(f"{what}: on {t.device}, want the GPU of the logits ({dev})")
-    if t.dtype not in _names(*names):
-        raise ValueError(f"{what}: {t.dtype}, want {' or '.join(names)}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{what}: shape {tuple(t.shape)}, want {tuple(shape)}")
+    """The address of t: a tensor on GPU `dev` of one of the named types and
+    the given shape, contiguous or with rows `ld` apart."""
+    if t.get_device() != dev or dev < 0:
+        raise ValueError(f"{what}: on {t.device}, want the logits' GPU")
+    if t.dtype not in _types(names):
+        raise ValueError(f"{what}: {t.dtype}, want one of {names}")
+    if t.shape != shape:
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, want {shape}")
     if ld is None:
         if not t.is_contiguous():
             raise ValueError(f"{what}: not contiguous")
-    elif (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) != ld):
+    elif (shape[1] > 1 and t.stride(1) != 1) or (shape[0] > 1 and t.stride(0) != ld):
         raise ValueError(f"{what}: strides {t.stride()}, want ({ld}, 1)")
+    return t.data_ptr()
+
+
+def _maybe(what, t, names, shape, dev):
+    return None if t is None else _tensor(what, t, names, shape, dev)
 
 
 def _rows(what, t, d, ld, dev):
-    _tensor(what, t, ("float32",) if d.dtype == OFT_DT_F32 else ("bfloat16", "int16", "uint16"), (d.T, d.V), dev, ld)
-
-
-def _optional(what, t, names, shape, dev):
-    if t is not None:
-        _tensor(what, t, names, shape, dev)
+    return _tensor(what, t, "float32" if d.dtype == OFT_DT_F32 else "bfloat16 int16 uint16", (d.T, d.V), dev, ld)
 
 
 def _workspace(ws, ws_bytes, dev):
     if ws is None:
-        return
-    if ws.device != dev or not ws.is_contiguous() or ws.numel() * ws.element_size() < ws_bytes:
-        raise ValueError("ws: want a contiguous tensor of at least ws_bytes on the logits' device")
+        return None
+    if ws.get_device() != dev or not ws.is_contiguous() or ws.numel() * ws.element_size() < ws_bytes:
+        raise ValueError("ws: want a contiguous tensor of at least ws_bytes on the logits' GPU")
+    return ws.data_ptr()
 
 
-class _on:
-    """Enter the logits' device; `stream(s)`: s, or that device's current stream."""
+def _launch(name, dev, stream, *args):
+    """Call `name` with the logits' GPU current, on its current stream unless one is given."""
+    import torch
 
-    def __init__(self, t):
-        import torch
-
-        self.dev = t.device
-        self.guard = torch.cuda.device(t.device)
-
-    def __enter__(self):
-        self.guard.__enter__()
-        return _stream
-
-    def __exit__(self, *a):
-        return self.guard.__exit__(*a)
+    f = getattr(_lib.load(), name)
+    if stream is None:
+        stream = torch.cuda.current_stream(dev).cuda_stream
+    if torch.cuda.current_device() == dev:
+        status = f(*args, int(stream))
+    else:
+        with torch.cuda.device(dev):
+            status = f(*args, int(stream))
+    _lib.check(status, name)
 
 
 def oft_vocab_workspace_bytes(desc) -> int:
@@ -239,69 +244,55 @@ def oft_token_logprobs(desc, logits, labels, logp, stats, entropy=None, top_idx=
                        ws_bytes=0, stream=None):
     """Log-probabilities of the given tokens, entropy and top alternatives of
     each row of logits; labels and logp may both be None."""
-    d, dev = desc, logits.device
-    _rows("logits", logits, d, d.ld, dev)
-    _optional("labels", labels, ("int32",), (d.T,), dev)
-    for what, t in (("logp", logp), ("entropy", entropy)):
-        _optional(what, t, ("float32",), (d.T,), dev)
-    _tensor("stats", stats, ("float32",), (d.T, 2), dev)
+    d, dev, row = desc, logits.get_device(), (desc.T,)
+    x = _rows("logits", logits, d, d.ld, dev)
+    lab = _maybe("labels", labels, "int32", row, dev)
+    lp = _maybe("logp", logp, "float32", row, dev)
+    ent = _maybe("entropy", entropy, "float32", row, dev)
+    st = _tensor("stats", stats, "float32", (d.T, 2), dev)
+    ti = tl = None
     if d.k > 0:
-        _optional("top_idx", top_idx, ("int32",), (d.T, d.k), dev)
-        _optional("top_logp", top_logp, ("float32",), (d.T, d.k), dev)
-    _workspace(ws, ws_bytes, dev)
-    with _on(logits) as st:
-        _lib.check(_lib.load().oft_token_logprobs(C.byref(d), _ptr(logits), _ptr(labels), _ptr(logp), _ptr(entropy),
-                                                  _ptr(top_idx), _ptr(top_logp), _ptr(stats), _ptr(ws), ws_bytes,
-                                                  st(stream)), "oft_token_logprobs")
+        ti = _maybe("top_idx", top_idx, "int32", (d.T, d.k), dev)
+        tl = _maybe("top_logp", top_logp, "float32", (d.T, d.k), dev)
+    _launch("oft_token_logprobs", dev, stream, C.byref(d), x, lab, lp, ent, ti, tl, st, _workspace(ws, ws_bytes, dev),
+            ws_bytes)
 
 
 def oft_token_logprobs_bwd(desc, logits, labels, stats, g_logp, d_logits, entropy=None, g_entropy=None, stream=None):
     """d_logits of g_logp . logp + g_entropy . entropy; labels and g_logp may
     both be None, and g_entropy may be None."""
-    d, dev = desc, logits.device
-    _rows("logits", logits, d, d.ld, dev)
-    _rows("d_logits", d_logits, d, d.ld_grad, dev)
-    _optional("labels", labels, ("int32",), (d.T,), dev)
-    _tensor("stats", stats, ("float32",), (d.T, 2), dev)
-    for what, t in (("g_logp", g_logp), ("entropy", entropy), ("g_entropy", g_entropy)):
-        _optional(what, t, ("float32",), (d.T,), dev)
-    with _on(logits) as st:
-        _lib.check(_lib.load().oft_token_logprobs_bwd(C.byref(d), _ptr(logits), _ptr(labels), _ptr(stats),
-                                                      _ptr(entropy), _ptr(g_logp), _ptr(g_entropy), _ptr(d_logits),
-                                                      st(stream)), "oft_token_logprobs_bwd")
-
-
-def _teacher(d, teacher_idx, teacher_logits, dev):
-    _tensor("teacher_idx", teacher_idx, ("int32",), (d.T, d.k), dev)
-    _tensor("teacher_logits", teacher_logits, ("float32",), (d.T, d.k), dev)
+    d, dev, row = desc, logits.get_device(), (desc.T,)
+    x = _rows("logits", logits, d, d.ld, dev)
+    dx = _rows("d_logits", d_logits, d, d.ld_grad, dev)
+    lab = _maybe("labels", labels, "int32", row, dev)
+    st = _tensor("stats", stats, "float32", (d.T, 2), dev)
+    gl = _maybe("g_logp", g_logp, "float32", row, dev)
+    ent = _maybe("entropy", entropy, "float32", row, dev)
+    ge = _maybe("g_entropy", g_entropy, "float32", row, dev)
+    _launch("oft_token_logprobs_bwd", dev, stream, C.byref(d), x, lab, st, ent, gl, ge, dx)
 
 
 def oft_distill_topk(desc, logits, teacher_idx, teacher_logits, loss, stats, ws=None, ws_bytes=0, stream=None):
     """Per-row loss against the teacher's renormalised top list."""
-    d, dev = desc, logits.device
-    _rows("logits", logits, d, d.ld, dev)
-    _teacher(d, teacher_idx, teacher_logits, dev)
-    _tensor("loss", loss, ("float32",), (d.T,), dev)
-    _tensor("stats", stats, ("float32",), (d.T, 2), dev)
-    _workspace(ws, ws_bytes, dev)
-    with _on(logits) as st:
-        _lib.check(_lib.load().oft_distill_topk(C.byref(d), _ptr(logits), _ptr(teacher_idx), _ptr(teacher_logits),
-                                                _ptr(loss), _ptr(stats), _ptr(ws), ws_bytes, st(stream)),
-                   "oft_distill_topk")
+    d, dev, listed = desc, logits.get_device(), (desc.T, desc.k)
+    x = _rows("logits", logits, d, d.ld, dev)
+    ti = _tensor("teacher_idx", teacher_idx, "int32", listed, dev)
+    tl = _tensor("teacher_logits", teacher_logits, "float32", listed, dev)
+    out = _tensor("loss", loss, "float32", (d.T,), dev)
+    st = _tensor("stats", stats, "float32", (d.T, 2), dev)
+    _launch("oft_distill_topk", dev, stream, C.byref(d), x, ti, tl, out, st, _workspace(ws, ws_bytes, dev), ws_bytes)
 
 
 def oft_distill_topk_bwd(desc, logits, teacher_idx, teacher_logits, stats, g_loss, d_logits, stream=None):
     """d_logits of g_loss . loss."""
-    d, dev = desc, logits.device
-    _rows("logits", logits, d, d.ld, dev)
-    _rows("d_logits", d_logits, d, d.ld_grad, dev)
-    _teacher(d, teacher_idx, teacher_logits, dev)
-    _tensor("stats", stats, ("float32",), (d.T, 2), dev)
-    _tensor("g_loss", g_loss, ("float32",), (d.T,), dev)
-    with _on(logits) as st:
-        _lib.check(_lib.load().oft_distill_topk_bwd(C.byref(d), _ptr(logits), _ptr(teacher_idx), _ptr(teacher_logits),
-                                                    _ptr(stats), _ptr(g_loss), _ptr(d_logits), st(stream)),
-                   "oft_distill_topk_bwd")
+    d, dev, listed = desc, logits.get_device(), (desc.T, desc.k)
+    x = _rows("logits", logits, d, d.ld, dev)
+    dx = _rows("d_logits", d_logits, d, d.ld_grad, dev)
+    ti = _tensor("teacher_idx", teacher_idx, "int32", listed, dev)
+    tl = _tensor("teacher_logits", teacher_logits, "float32", listed, dev)
+    st = _tensor("stats", stats, "float32", (d.T, 2), dev)
+    g = _tensor("g_loss", g_loss, "float32", (d.T,), dev)
+    _launch("oft_distill_topk_bwd", dev, stream, C.byref(d), x, ti, tl, st, g, dx)
 
 
 def oft_moe_balance_workspace_bytes(desc, seq_len) -> int:
@@ -321,37 +312,29 @@ def oft_moe_balance(desc, seq_len, logits, topk_idx, counts, tokens, loss, mean_
                     ws_bytes=0, stream=None):
     """Balance loss, per-expert counts and mean probabilities of each
     sequence of seq_len tokens; mask: uint8 or bool, false for padding."""
-    d, dev = desc, logits.device
-    S = _sequences(d, seq_len)
-    _tensor("logits", logits, ("float32",), (d.T, d.E), dev)
-    _tensor("topk_idx", topk_idx, ("int32",), (d.T, d.k), dev)
-    _optional("mask", mask, ("uint8", "bool"), (d.T,), dev)
-    _tensor("counts", counts, ("int32",), (S, d.E), dev)
-    _tensor("tokens", tokens, ("int32",), (S,), dev)
-    _tensor("loss", loss, ("float32",), (S,), dev)
-    _optional("mean_prob", mean_prob, ("float32",), (S, d.E), dev)
-    _workspace(ws, ws_bytes, dev)
-    with _on(logits) as st:
-        _lib.check(_lib.load().oft_moe_balance(C.byref(d), int(seq_len), _ptr(logits), _ptr(topk_idx), _ptr(mask),
-                                               _ptr(counts), _ptr(tokens), _ptr(loss), _ptr(mean_prob), _ptr(ws),
-                                               ws_bytes, st(stream)), "oft_moe_balance")
+    d, dev, S = desc, logits.get_device(), _sequences(desc, seq_len)
+    x = _tensor("logits", logits, "float32", (d.T, d.E), dev)
+    ti = _tensor("topk_idx", topk_idx, "int32", (d.T, d.k), dev)
+    mk = _maybe("mask", mask, "uint8 bool", (d.T,), dev)
+    cn = _tensor("counts", counts, "int32", (S, d.E), dev)
+    tk = _tensor("tokens", tokens, "int32", (S,), dev)
+    out = _tensor("loss", loss, "float32", (S,), dev)
+    mp = _maybe("mean_prob", mean_prob, "float32", (S, d.E), dev)
+    _launch("oft_moe_balance", dev, stream, C.byref(d), int(seq_len), x, ti, mk, cn, tk, out, mp,
+            _workspace(ws, ws_bytes, dev), ws_bytes)
 
 
 def oft_moe_balance_bwd(desc, seq_len, logits, counts, tokens, g_loss, d_logits, mask=None, accumulate=0,
                         stream=None):
     """d_logits of g_loss . loss, written or (accumulate=1) added."""
-    d, dev = desc, logits.device
-    S = _sequences(d, seq_len)
-    _tensor("logits", logits, ("float32",), (d.T, d.E), dev)
-    _optional("mask", mask, ("uint8", "bool"), (d.T,), dev)
-    _tensor("counts", counts, ("int32",), (S, d.E), dev)
-    _tensor("tokens", tokens, ("int32",), (S,), dev)
-    _tensor("g_loss", g_loss, ("float32",), (S,), dev)
-    _tensor("d_logits", d_logits, ("float32",), (d.T, d.E), dev)
-    with _on(logits) as st:
-        _lib.check(_lib.load().oft_moe_balance_bwd(C.byref(d), int(seq_len), _ptr(logits), _ptr(mask), _ptr(counts),
-                                                   _ptr(tokens), _ptr(g_loss), _ptr(d_logits), int(accumulate),
-                                                   st(stream)), "oft_moe_balance_bwd")
+    d, dev, S = desc, logits.get_device(), _sequences(desc, seq_len)
+    x = _tensor("logits", logits, "float32", (d.T, d.E), dev)
+    mk = _maybe("mask", mask, "uint8 bool", (d.T,), dev)
+    cn = _tensor("counts", counts, "int32", (S, d.E), dev)
+    tk = _tensor("tokens", tokens, "int32", (S,), dev)
+    g = _tensor("g_loss", g_loss, "float32", (S,), dev)
+    dx = _tensor("d_logits", d_logits, "float32", (d.T, d.E), dev)
+    _launch("oft_moe_balance_bwd", dev, stream, C.byref(d), int(seq_len), x, mk, cn, tk, g, dx, int(accumulate))
 
 
 def oft_moe_workspace_bytes(desc, pass_) -> int:

@@ -2,7 +2,6 @@
 // include/oft.h).  Arguments are validated on the host before anything is
 // enqueued.
 #include <hip/hip_runtime.h>
-#include <math.h>
 
 #include "oft.h"
 #include "oft_launch.h"
@@ -24,7 +23,7 @@ int32_t validate_vocab(const oft_vocab_desc* d) {
   if (d->T < 0 || d->V < 1 || d->ld < d->V || d->ld_grad < d->V) return OFT_EINVAL;
   if (d->accumulate != 0 && d->accumulate != 1) return OFT_EINVAL;
   // (a NaN temperature fails the comparison)
-  if (!(d->temperature > 0.0f) || !isfinite(d->temperature) || !isfinite(1.0f / d->temperature)) return OFT_EINVAL;
+  if (!(d->temperature >= 0x1p-20f && d->temperature <= 0x1p20f)) return OFT_EINVAL;
   if (d->dtype != OFT_DT_BF16 && d->dtype != OFT_DT_F32) return OFT_EDTYPE;
   if (d->T > (1 << 22) || d->V > (1 << 24)) return OFT_EUNSUPPORTED;
   // (the first two comparisons keep the products inside 64 bits)

@@ -39,7 +39,10 @@ def _query(d):
     (dict(temperature=-1.0), _lib.OFT_EINVAL),
     (dict(temperature=float("nan")), _lib.OFT_EINVAL),
     (dict(temperature=float("inf")), _lib.OFT_EINVAL),
-    (dict(temperature=1e-40), _lib.OFT_EINVAL),  # its reciprocal is not finite
+    (dict(temperature=2.0 ** -20), _lib.OFT_OK),
+    (dict(temperature=2.0 ** -21), _lib.OFT_EINVAL),
+    (dict(temperature=2.0 ** 20), _lib.OFT_OK),
+    (dict(temperature=2.0 ** 21), _lib.OFT_EINVAL),
     (dict(accumulate=2), _lib.OFT_EINVAL),
     (dict(k=-1), _lib.OFT_EUNSUPPORTED),
     (dict(k=257), _lib.OFT_EUNSUPPORTED),
