@@ -97,11 +97,29 @@ __device__ __forceinline__ void store16(E* p, const u32x4& v) {
   *reinterpret_cast<u32x4_row*>(p) = v;
 }
 
-// lane-wise maximum with another lane of the same 16 (DPP)
+// value of another lane of the same 16 (DPP)
 template <int CTRL>
-__device__ __forceinline__ float dpp_max(float v) {
-  const int o = __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, v), __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, false);
-  return fmaxf(v, __builtin_bit_cast(float, o));
+__device__ __forceinline__ float dpp(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
+}
+constexpr int PAIR = 0xB1, QUAD = 0x4E, EIGHT = 0x141, ROW = 0x140;  // lanes ^ 1, ^ 2, 7 - i of 8, 15 - i of 16
+__device__ __forceinline__ float lane_value(float v, int l) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), l));
+}
+// over the wave's 64 lanes (all active), the same bits in every lane
+__device__ __forceinline__ float wave_sum(float v) {
+  v += dpp<PAIR>(v);
+  v += dpp<QUAD>(v);
+  v += dpp<EIGHT>(v);
+  v += dpp<ROW>(v);
+  return (lane_value(v, 0) + lane_value(v, 16)) + (lane_value(v, 32) + lane_value(v, 48));
+}
+__device__ __forceinline__ float wave_max(float v) {
+  v = fmaxf(v, dpp<PAIR>(v));
+  v = fmaxf(v, dpp<QUAD>(v));
+  v = fmaxf(v, dpp<EIGHT>(v));
+  v = fmaxf(v, dpp<ROW>(v));
+  return fmaxf(fmaxf(lane_value(v, 0), lane_value(v, 16)), fmaxf(lane_value(v, 32), lane_value(v, 48)));
 }
 
 // ------------------------------------------------------------------ triples
@@ -109,24 +127,23 @@ struct Triple {
   float m, s, w;
 };
 
-// the triple of both sets; an empty set has s = 0
-__device__ __forceinline__ Triple join(const Triple& a, const Triple& b, float c) {
-  if (b.s == 0.0f) return a;
-  if (a.s == 0.0f) return b;
-  const float M = fmaxf(a.m, b.m), da = a.m - M, db = b.m - M;
-  const float fa = exp2_hw(c * da), fb = exp2_hw(c * db);
-  return Triple{M, fmaf(a.s, fa, b.s * fb),
-                fa * fmaf(a.s, fmaxf(da, FAR), a.w) + fb * fmaf(b.s, fmaxf(db, FAR), b.w)};
+// the triple moved to the maximum M >= m; an empty set has s = 0
+__device__ __forceinline__ Triple moved(const Triple& a, float M, float c) {
+  const float d = a.s == 0.0f ? 0.0f : a.m - M;
+  const float f = exp2_hw(c * d);
+  return Triple{M, a.s * f, f * fmaf(a.s, fmaxf(d, FAR), a.w)};
 }
 
-__device__ __forceinline__ Triple wave_join(Triple a, float c) {
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) {
-    const Triple b{__shfl_xor(a.m, off), __shfl_xor(a.s, off), __shfl_xor(a.w, off)};
-    // the lower lane's set comes first on both sides, so both get the same bits
-    a = (threadIdx.x & off) ? join(b, a, c) : join(a, b, c);
-  }
-  return a;
+__device__ __forceinline__ Triple join(const Triple& a, const Triple& b, float c) {
+  const float M = fmaxf(a.m, b.m);
+  const Triple x = moved(a, M, c), y = moved(b, M, c);
+  return Triple{M, x.s + y.s, x.w + y.w};
+}
+
+__device__ __forceinline__ Triple wave_join(const Triple& a, float c) {
+  const float M = wave_max(a.m);
+  const Triple x = moved(a, M, c);
+  return Triple{M, wave_sum(x.s), wave_sum(x.w)};
 }
 
 // ------------------------------------------------------------- forward pass
@@ -152,14 +169,8 @@ __device__ __forceinline__ void fwd_step(const float (&x)[FU * Ty::VE], int base
   float bm = vm[0];
 #pragma unroll
   for (int u = 1; u < FU; ++u) bm = fmaxf(bm, vm[u]);
-  // larger maximum: move the sums to it (from -inf: they are 0)
-  const float M = fmaxf(a.m, bm);
-  const float d0 = a.s == 0.0f ? 0.0f : a.m - M;
-  const float f = exp2_hw(c * d0);
-  a.w = f * fmaf(a.s, fmaxf(d0, FAR), a.w);
-  a.s *= f;
-  a.m = M;
-  const float ref = M == -INFINITY ? 0.0f : M;
+  a = moved(a, fmaxf(a.m, bm), c);
+  const float ref = a.m == -INFINITY ? 0.0f : a.m;
   float s[2] = {0.0f, 0.0f}, w[2] = {0.0f, 0.0f};
 #pragma unroll
   for (int i = 0; i < N; ++i) {
@@ -177,10 +188,10 @@ __device__ __forceinline__ void fwd_step(const float (&x)[FU * Ty::VE], int base
     float mine = -INFINITY;
 #pragma unroll
     for (int u = 0; u < FU; ++u) {
-      float v = dpp_max<0xB1>(vm[u]);   // lanes of a pair
-      v = dpp_max<0x4E>(v);             // of a quad
-      v = dpp_max<0x141>(v);            // of eight
-      if constexpr (G == 16) v = dpp_max<0x140>(v);
+      float v = fmaxf(vm[u], dpp<PAIR>(vm[u]));
+      v = fmaxf(v, dpp<QUAD>(v));
+      v = fmaxf(v, dpp<EIGHT>(v));
+      if constexpr (G == 16) v = fmaxf(v, dpp<ROW>(v));
       mine = (lane % G) == u ? v : mine;
     }
     // lane u of a group stores the block of vector u
@@ -241,22 +252,7 @@ __global__ __launch_bounds__(256) void vocab_stats_kernel(const typename Ty::E* 
   }
 }
 
-// a row's triple from its slices, in every lane of the wave
-__device__ __forceinline__ Triple row_triple(const float4* part, int S, float c) {
-  Triple a{-INFINITY, 0.0f, 0.0f};
-  for (int i = threadIdx.x & 63; i < S; i += 64) {
-    const float4 p = part[i];
-    a = join(a, Triple{p.x, p.y, p.z}, c);
-  }
-  return wave_join(a, c);
-}
-
 // ---------------------------------------------------------- top alternatives
-// A wave's selection of the k best of a stream of (value, id), ids ascending:
-// candidates wait in LDS in order of id; when the list is full it is cut to
-// its k best, whose last value is then what a later candidate must exceed.
-constexpr int QCAP = 512, MAXTOP = 128;
-
 __device__ __forceinline__ uint32_t ordered(float v) {  // unsigned order of values
   const uint32_t b = __builtin_bit_cast(uint32_t, v + 0.0f);  // -0 as +0
   return b ^ ((uint32_t)((int)b >> 31) | 0x80000000u);
@@ -269,20 +265,43 @@ __device__ __forceinline__ int below(unsigned long long mask) {  // set bits of 
   return __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
 }
 
-// k-th largest of the N lane values (in `ordered` form)
-template <int N>
+template <class Ty>
+__device__ __forceinline__ float rank_value(typename Ty::E v) {  // NaN ranks as -inf
+  const float f = Ty::get(v);
+  return f != f ? -INFINITY : f;
+}
+
+// k-th largest of the N lane values (in `ordered` form), two bits a step.
+// Values of 16 bits (LOW = 16) are told apart by their upper half.
+template <int N, int LOW>
 __device__ __forceinline__ uint32_t kth(const uint32_t (&o)[N], int k) {
   uint32_t r = 0;
-  for (int bit = 31; bit >= 0; --bit) {
-    const uint32_t tryv = r | (1u << bit);
-    int n = 0;
+  for (int bit = 30; bit >= LOW; bit -= 2) {
+    int n1 = 0, n2 = 0, n3 = 0;
+    const uint32_t t1 = r | (1u << bit), t2 = r | (2u << bit), t3 = r | (3u << bit);
 #pragma unroll
-    for (int j = 0; j < N; ++j) n += __popcll(__ballot(o[j] >= tryv));
-    if (n >= k) r = tryv;
+    for (int j = 0; j < N; ++j) {
+      n1 += __popcll(__ballot(o[j] >= t1));
+      n2 += __popcll(__ballot(o[j] >= t2));
+      n3 += __popcll(__ballot(o[j] >= t3));
+    }
+    r = n3 >= k ? t3 : n2 >= k ? t2 : n1 >= k ? t1 : r;
   }
   return r;
 }
 
+// LDS of one wave, written and read by its lanes
+__device__ __forceinline__ void wave_lds() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// A wave's selection of the k best of a stream of (value, id), ids ascending:
+// candidates wait in LDS in order of id; when the list is full it is cut to
+// its k best, whose last value is then what a later candidate must exceed.
+// Right for any input, whatever its ties.
+constexpr int QCAP = 512, MAXTOP = 128;
 struct Select {
   float* val;  // [QCAP] in LDS
   int* id;     // [QCAP]
@@ -290,7 +309,8 @@ struct Select {
   float floor;  // a candidate must reach it, or exceed it once `strict`
   bool strict;
 
-  __device__ __forceinline__ Select(float* v, int* i, int kk, float f) : val(v), id(i), k(kk), n(0), floor(f), strict(false) {}
+  __device__ __forceinline__ Select(float* v, int* i, int kk, float f)
+      : val(v), id(i), k(kk), n(0), floor(f), strict(false) {}
 
   __device__ __forceinline__ void feed(float v, int i, bool ok) {
     const bool take = ok && (strict ? v > floor : v >= floor);
@@ -307,7 +327,7 @@ struct Select {
 
   // keep the k best, in order of id
   __device__ void cut() {
-    __syncthreads();
+    wave_lds();
     if (n <= k) return;
     constexpr int N = QCAP / 64;
     const int lane = threadIdx.x & 63;
@@ -319,16 +339,17 @@ struct Select {
       o[j] = in ? ordered(val[j * 64 + lane]) : 0u;
       ids[j] = in ? id[j * 64 + lane] : 0;
     }
-    const uint32_t last = kth<N>(o, k);
+    const uint32_t last = kth<N, 0>(o, k);
     int above = 0;
 #pragma unroll
     for (int j = 0; j < N; ++j) above += __popcll(__ballot(o[j] > last));
     int ties = k - above, m = 0;
-    __syncthreads();
+    wave_lds();
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      const unsigned long long eq = __ballot(o[j] == last && j * 64 + lane < n);
-      const bool keep = o[j] > last || (o[j] == last && j * 64 + lane < n && below(eq) < ties);
+      const bool tie = o[j] == last && j * 64 + lane < n;
+      const unsigned long long eq = __ballot(tie);
+      const bool keep = o[j] > last || (tie && below(eq) < ties);
       const unsigned long long mask = __ballot(keep);
       if (keep) {
         val[m + below(mask)] = unordered(o[j]);
@@ -340,15 +361,9 @@ struct Select {
     n = m;
     floor = unordered(last);
     strict = true;
-    __syncthreads();
+    wave_lds();
   }
 };
-
-template <class Ty>
-__device__ __forceinline__ float rank_value(typename Ty::E v) {  // NaN ranks as -inf
-  const float f = Ty::get(v);
-  return f != f ? -INFINITY : f;
-}
 
 struct FinishArgs {
   int V, k, S, nb;
@@ -356,79 +371,180 @@ struct FinishArgs {
   float c, invtau;
 };
 
-// one wave per row
+// Top alternatives of a row by one wave: the k best blocks, then the k best of
+// their elements.  val, id: [2][QCAP]; the result is val[1], id[1] in order
+// of column, at least k of them.
+template <class Ty>
+__device__ void select_any(const FinishArgs& f, const typename Ty::E* row, const typename Ty::E* brow,
+                           float (*val)[QCAP], int (*id)[QCAP]) {
+  constexpr int U = 8;  // loads in flight
+  const int lane = threadIdx.x & 63;
+  // a value that at least k blocks reach: the k-th best of 128 interleaved
+  // groups of blocks
+  float best[2] = {-INFINITY, -INFINITY};
+  for (int b = lane; b < f.nb; b += 64 * U) {
+#pragma unroll
+    for (int j = 0; j < U; ++j)
+      if (b + 64 * j < f.nb) best[j & 1] = fmaxf(best[j & 1], Ty::get(brow[b + 64 * j]));
+  }
+  const uint32_t o[2] = {ordered(best[0]), ordered(best[1])};
+  Select sel(val[0], id[0], f.k, unordered(kth<2, 0>(o, f.k)));
+  for (int b = lane; b - lane < f.nb; b += 64 * U) {
+    float v[U];
+#pragma unroll
+    for (int j = 0; j < U; ++j) v[j] = b + 64 * j < f.nb ? rank_value<Ty>(brow[b + 64 * j]) : 0.0f;
+#pragma unroll
+    for (int j = 0; j < U; ++j) sel.feed(v[j], b + 64 * j, b + 64 * j < f.nb);
+  }
+  sel.cut();
+  // the blocks' elements: at least k reach the least of k maxima
+  const int nsel = sel.n;
+  float lowest = INFINITY;
+  for (int i = lane; i < nsel; i += 64) lowest = fminf(lowest, val[0][i]);
+  lowest = -wave_max(-lowest);
+  Select el(val[1], id[1], f.k, nsel < f.k ? -INFINITY : lowest);
+  for (int i = 0; i < nsel; i += U) {
+    float v[U];
+    int col[U];
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      col[j] = i + j < nsel ? id[0][i + j] * BLOCK + lane : f.V;
+      v[j] = col[j] < f.V ? rank_value<Ty>(row[col[j]]) : -INFINITY;
+    }
+#pragma unroll
+    for (int j = 0; j < U; ++j) el.feed(v[j], col[j], col[j] < f.V);
+  }
+  el.cut();
+}
+
+// Joins a row's slices; its outputs.  Four waves per row.
+//
+// Top alternatives, the usual case: each thread holds up to HELD block maxima
+// in registers; a value T that k of 256 (k <= 64) or 512 disjoint groups of
+// them reach is at most the k-th best, so the elements >= T of the blocks
+// >= T hold the answer.  There are few more than k of them, in any order:
+// (value, column) as one 64-bit key gives each its place by counting the
+// keys above it.  Rows where ties or masks leave too many (or a vocabulary of
+// more blocks than the registers hold) go through select_any.
+constexpr int HELD = 16, MAXBLK = 512, MAXCAND = 512;
 template <class Ty, bool TOP>
-__global__ __launch_bounds__(64) void logprobs_finish_kernel(FinishArgs f, LogprobPtrs q,
-                                                             const float4* __restrict__ part,
-                                                             const typename Ty::E* __restrict__ blocks) {
+__global__ __launch_bounds__(256) void logprobs_finish_kernel(FinishArgs f, LogprobPtrs q,
+                                                              const float4* __restrict__ part,
+                                                              const typename Ty::E* __restrict__ blocks) {
   typedef typename Ty::E E;
-  const int t = blockIdx.x, lane = threadIdx.x;
+  const int t = blockIdx.x, tid = threadIdx.x, lane = tid & 63;
   const E* row = static_cast<const E*>(q.logits) + (size_t)t * f.ld;
-  const Triple a = row_triple(part + (size_t)t * f.S, f.S, f.c);
+  const E* brow = TOP ? blocks + (size_t)t * f.nb : nullptr;
+  float held[HELD];
+  const bool few = f.nb <= HELD * 256;
+  if constexpr (TOP) {
+#pragma unroll
+    for (int i = 0; i < HELD; ++i) held[i] = few && i * 256 + tid < f.nb ? rank_value<Ty>(brow[i * 256 + tid]) : NAN;
+  }
+  const int lab = q.logp && tid == 0 ? q.labels[t] : -1;
+  const bool known = lab >= 0 && lab < f.V;
+  const float given = known ? Ty::get(row[lab]) : 0.0f;
+  Triple a{-INFINITY, 0.0f, 0.0f};
+  for (int i = lane; i < f.S; i += 64) {
+    const float4 p = part[(size_t)t * f.S + i];
+    a = join(a, Triple{p.x, p.y, p.z}, f.c);
+  }
+  a = wave_join(a, f.c);
   const bool empty = a.s == 0.0f;
   const float l = __logf(a.s);  // ln 0 = -inf for an empty row
-  if (lane == 0) {
+  if (tid == 0) {
     *reinterpret_cast<float2*>(q.stats + 2 * (size_t)t) = make_float2(a.m, l);
     if (q.entropy) q.entropy[t] = empty ? 0.0f : l - a.w * f.invtau / a.s;
-    if (q.logp) {
-      const int lab = q.labels[t];
-      float lp = lab == -1 ? 0.0f : NAN;
-      if (lab >= 0 && lab < f.V) lp = empty ? -INFINITY : (Ty::get(row[lab]) - a.m) * f.invtau - l;
-      q.logp[t] = lp;
-    }
+    if (q.logp)
+      q.logp[t] = lab == -1 ? 0.0f : !known ? NAN : empty ? -INFINITY : (given - a.m) * f.invtau - l;
   }
   if constexpr (TOP) {
+    constexpr int LOW = sizeof(E) == 2 ? 16 : 0;
+    __shared__ __align__(16) unsigned long long key[MAXCAND];
     __shared__ float val[2][QCAP];
     __shared__ int id[2][QCAP];
-    const E* brow = blocks + (size_t)t * f.nb;
-    // a value that at least k blocks reach: the k-th best of 128 interleaved
-    // groups of blocks
+    __shared__ uint32_t group[512];
+    __shared__ int cand_block[MAXBLK];
+    __shared__ float sh_floor;
+    __shared__ int nblk, ncand;
+    if (tid == 0) nblk = ncand = 0;
     float best[2] = {-INFINITY, -INFINITY};
-    for (int b = lane; b < f.nb; b += 128) {
-      best[0] = fmaxf(best[0], Ty::get(brow[b]));
-      if (b + 64 < f.nb) best[1] = fmaxf(best[1], Ty::get(brow[b + 64]));
-    }
-    const uint32_t o[2] = {ordered(best[0]), ordered(best[1])};
-    Select sel(val[0], id[0], f.k, unordered(kth<2>(o, f.k)));
-    for (int b = 0; b < f.nb; b += 64) {
-      const bool in = b + lane < f.nb;
-      sel.feed(in ? rank_value<Ty>(brow[b + lane]) : 0.0f, b + lane, in);
-    }
-    sel.cut();
+#pragma unroll
+    for (int i = 0; i < HELD; ++i) best[i & 1] = fmaxf(best[i & 1], held[i]);
+    group[tid] = ordered(f.k <= 64 ? fmaxf(best[0], best[1]) : best[0]);
+    if (f.k > 64) group[256 + tid] = ordered(best[1]);
     __syncthreads();
-    // their elements: at least k reach the least of k maxima
-    const int nsel = sel.n;
-    float lowest = INFINITY;
-    for (int i = lane; i < nsel; i += 64) lowest = fminf(lowest, val[0][i]);
+    if (tid < 64) {
+      uint32_t r;
+      if (f.k <= 64) {
+        uint32_t o[4];
 #pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) lowest = fminf(lowest, __shfl_xor(lowest, off));
-    Select el(val[1], id[1], f.k, nsel < f.k ? -INFINITY : lowest);
-    for (int i = 0; i < nsel; i += 8) {
-      float v[8];
-      int col[8];
+        for (int j = 0; j < 4; ++j) o[j] = group[64 * j + lane];
+        r = kth<4, LOW>(o, f.k);
+      } else {
+        uint32_t o[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        col[j] = i + j < nsel ? id[0][i + j] * BLOCK + lane : f.V;
-        v[j] = col[j] < f.V ? rank_value<Ty>(row[col[j]]) : -INFINITY;
+        for (int j = 0; j < 8; ++j) o[j] = group[64 * j + lane];
+        r = kth<8, LOW>(o, f.k);
       }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) el.feed(v[j], col[j], col[j] < f.V);
+      // (of a negative 16-bit value the lower half of the ordered form is ones)
+      if (tid == 0) sh_floor = r == 0u ? -INFINITY : unordered(LOW && !(r & 0x80000000u) ? r | 0xFFFFu : r);
     }
-    el.cut();
     __syncthreads();
-    // best first: an entry's place is the number of entries before it
+    const float floor = sh_floor;
 #pragma unroll
-    for (int h = 0; h < MAXTOP / 64; ++h) {
-      const int i = h * 64 + lane;
-      if (i < f.k) {
-        const float v = val[1][i];
-        int place = 0;
-        for (int j = 0; j < f.k; ++j) {
-          const float u = val[1][j];
-          place += (u > v || (u == v && j < i)) ? 1 : 0;
+    for (int i = 0; i < HELD; ++i)
+      if (held[i] >= floor) {  // (false for NaN: no block)
+        const int at = atomicAdd(&nblk, 1);
+        if (at < MAXBLK) cand_block[at] = i * 256 + tid;
+      }
+    __syncthreads();
+    const int n1 = nblk;
+    bool usual = few && n1 <= MAXBLK;
+    if (usual) {
+      constexpr int U = 8;
+      for (int i = tid >> 6; i < n1; i += 4 * U) {
+        float v[U];
+        int col[U];
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+          col[j] = i + 4 * j < n1 ? cand_block[i + 4 * j] * BLOCK + lane : f.V;
+          v[j] = col[j] < f.V ? rank_value<Ty>(row[col[j]]) : NAN;
         }
+#pragma unroll
+        for (int j = 0; j < U; ++j)
+          if (v[j] >= floor) {
+            const int at = atomicAdd(&ncand, 1);
+            if (at < MAXCAND) key[at] = (unsigned long long)ordered(v[j]) << 32 | (uint32_t)~col[j];
+          }
+      }
+      __syncthreads();
+      usual = ncand <= MAXCAND;
+    }
+    int n = usual ? ncand : f.k;
+    if (!usual) {
+      __syncthreads();
+      if (tid < 64) {
+        select_any<Ty>(f, row, brow, val, id);
+        for (int i = lane; i < f.k; i += 64)
+          key[i] = (unsigned long long)ordered(val[1][i]) << 32 | (uint32_t)~id[1][i];
+      }
+      __syncthreads();
+    }
+    // an even number of keys for the paired reads: 0 is below every key
+    if (tid == 0 && (n & 1)) key[n] = 0ull;
+    __syncthreads();
+    for (int i = tid; i < n; i += 256) {
+      const unsigned long long mine = key[i];
+      int place = 0;
+      for (int j = 0; j < n; j += 2) {
+        const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(key + j);
+        place += (o.x > mine ? 1 : 0) + (o.y > mine ? 1 : 0);
+      }
+      if (place < f.k) {
+        const float v = unordered((uint32_t)(mine >> 32));
         const size_t at = (size_t)t * f.k + place;
-        q.top_idx[at] = id[1][i];
+        q.top_idx[at] = (int)~(uint32_t)mine;
         q.top_logp[at] = l != l ? NAN : empty ? -INFINITY : (v - a.m) * f.invtau - l;
       }
     }
@@ -461,8 +577,7 @@ struct Teacher {
       mx = fmaxf(mx, v[i]);
     }
     bad = __ballot(b) != 0;
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) mx = fmaxf(mx, __shfl_xor(mx, off));
+    mx = wave_max(mx);
     any = mx != -INFINITY;
     float s = 0.0f, e[TI];
 #pragma unroll
@@ -471,8 +586,7 @@ struct Teacher {
       e[i] = exp2_hw(logq[i] * LOG2E);
       s += e[i];
     }
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) s += __shfl_xor(s, off);
+    s = wave_sum(s);
     const float ls = __logf(s);
 #pragma unroll
     for (int i = 0; i < TI; ++i) {
@@ -496,7 +610,12 @@ __global__ __launch_bounds__(64) void distill_finish_kernel(FinishArgs f, const 
   float x[TI];
 #pragma unroll
   for (int i = 0; i < TI; ++i) x[i] = te.ix[i] >= 0 ? Ty::get(row[te.ix[i]]) : 0.0f;
-  const Triple a = row_triple(part + (size_t)t * f.S, f.S, f.c);
+  Triple a{-INFINITY, 0.0f, 0.0f};
+  for (int i = threadIdx.x; i < f.S; i += 64) {
+    const float4 p = part[(size_t)t * f.S + i];
+    a = join(a, Triple{p.x, p.y, p.z}, f.c);
+  }
+  a = wave_join(a, f.c);
   const float l = __logf(a.s);
   float sum = 0.0f;
 #pragma unroll
@@ -505,8 +624,7 @@ __global__ __launch_bounds__(64) void distill_finish_kernel(FinishArgs f, const 
       const float lp = a.s == 0.0f ? -INFINITY : (x[i] - a.m) * f.invtau - l;
       sum = fmaf(te.q[i], te.logq[i] - lp, sum);
     }
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) sum += __shfl_xor(sum, off);
+  sum = wave_sum(sum);
   if (threadIdx.x == 0) {
     loss[t] = te.bad ? NAN : sum;
     *reinterpret_cast<float2*>(stats + 2 * (size_t)t) = make_float2(a.m, l);
@@ -573,8 +691,9 @@ __device__ __forceinline__ void bwd_columns(const typename Ty::E* row, typename 
       float x[VE], o[VE];
       Ty::unpack(v[u], x);
       if constexpr (ACC) Ty::unpack(old[u], o);
+      grad(x, i0);
 #pragma unroll
-      for (int j = 0; j < VE; ++j) x[j] = grad(x[j], i0 + j) + (ACC ? o[j] : 0.0f);
+      for (int j = 0; j < VE; ++j) x[j] += ACC ? o[j] : 0.0f;
       store16(out + i0, Ty::pack(x));
     }
   }
@@ -583,14 +702,20 @@ __device__ __forceinline__ void bwd_columns(const typename Ty::E* row, typename 
     if (i0 + VE <= hi) {
       Ty::unpack(load16(row + i0), x);
       if constexpr (ACC) Ty::unpack(load16(out + i0), o);
+      grad(x, i0);
 #pragma unroll
-      for (int j = 0; j < VE; ++j) x[j] = grad(x[j], i0 + j) + (ACC ? o[j] : 0.0f);
+      for (int j = 0; j < VE; ++j) x[j] += ACC ? o[j] : 0.0f;
       store16(out + i0, Ty::pack(x));
     } else {
-      for (int i = i0; i < hi; ++i) {
-        const float v = grad(Ty::get(row[i]), i) + (ACC ? Ty::get(out[i]) : 0.0f);
-        out[i] = Ty::put(v);
+#pragma unroll
+      for (int j = 0; j < VE; ++j) {
+        x[j] = i0 + j < hi ? Ty::get(row[i0 + j]) : 0.0f;
+        o[j] = ACC && i0 + j < hi ? Ty::get(out[i0 + j]) : 0.0f;
       }
+      grad(x, i0);
+#pragma unroll
+      for (int j = 0; j < VE; ++j)
+        if (i0 + j < hi) out[i0 + j] = Ty::put(x[j] + o[j]);
     }
   }
 }
@@ -619,8 +744,14 @@ __global__ __launch_bounds__(256) void logprobs_bwd_kernel(BwdArgs b, LogprobGra
   else if (st.y == -INFINITY) fill = FILL_ZERO;
   const RowGrad g{st.x, b.c, st.y * LOG2E, -ge * LN2 * b.invtau, -fmaf(ge, H, gl) * b.invtau};
   const float at = gl * b.invtau;
-  bwd_columns<Ty, ACC>(row, out, lo, hi, fill,
-                       [&](float x, int i) { return g(x) + (i == lab ? at : 0.0f); });
+  bwd_columns<Ty, ACC>(row, out, lo, hi, fill, [&](float (&x)[Ty::VE], int i0) {
+#pragma unroll
+    for (int j = 0; j < Ty::VE; ++j) x[j] = g(x[j]);
+    if ((unsigned)(lab - i0) < (unsigned)Ty::VE) {
+#pragma unroll
+      for (int j = 0; j < Ty::VE; ++j) x[j] += lab - i0 == j ? at : 0.0f;
+    }
+  });
 }
 
 template <class Ty, bool ACC>
@@ -630,8 +761,8 @@ __global__ __launch_bounds__(256) void distill_bwd_kernel(BwdArgs b, const typen
                                                           const float* __restrict__ stats,
                                                           const float* __restrict__ g_loss, typename Ty::E* d_logits) {
   typedef typename Ty::E E;
-  __shared__ int lidx[64 * TI];
-  __shared__ float lq[64 * TI];
+  __shared__ __align__(16) int lidx[64 * TI + 4];
+  __shared__ __align__(16) float lq[64 * TI + 4];
   const int t = blockIdx.x / b.S, sl = blockIdx.x % b.S, tid = threadIdx.x;
   const E* row = logits + (size_t)t * b.ld;
   E* out = d_logits + (size_t)t * b.ldg;
@@ -640,32 +771,49 @@ __global__ __launch_bounds__(256) void distill_bwd_kernel(BwdArgs b, const typen
   const float g = g_loss[t];
   // (each wave computes the list; all get the same)
   const Teacher te(idx + (size_t)t * b.k, teacher + (size_t)t * b.k, b.k, b.V, b.invtau);
-  if (tid < 64) {
-#pragma unroll
-    for (int i = 0; i < TI; ++i) {
-      lidx[tid + 64 * i] = te.ix[i];
-      lq[tid + 64 * i] = te.q[i];
-    }
-  }
   int fill = FILL_NONE;
   if (g == 0.0f) fill = FILL_ZERO;
   else if (te.bad) fill = FILL_NAN;
   else if (!te.any || st.y == -INFINITY) fill = FILL_ZERO;
-  __syncthreads();
   const RowGrad r{st.x, b.c, st.y * LOG2E, 0.0f, g * b.invtau};
-  // the listed columns of this slice, one per thread: p - sum of their q.
-  // Read before anything is written (d_logits may be logits)
-  const int mine = lidx[tid];
-  const bool listed = fill == FILL_NONE && mine >= lo && mine < hi;
+  // the entries of this slice, in list order
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < TI; ++i) {
+    const bool in = te.ix[i] >= lo && te.ix[i] < hi;
+    const unsigned long long mask = __ballot(in);
+    if (in && tid < 64) {
+      lidx[n + below(mask)] = te.ix[i];
+      lq[n + below(mask)] = te.q[i];
+    }
+    n += __popcll(mask);
+  }
+  if (tid < 4) lidx[n + tid] = -1;  // up to a multiple of four
+  __syncthreads();
+  // one entry per thread: the column's gradient p - sum of its q.  Read
+  // before anything is written (d_logits may be logits)
+  const bool listed = fill == FILL_NONE && tid < n;
+  const int mine = listed ? lidx[tid] : 0;
   float v = 0.0f;
   if (listed) {
+    v = exp2_hw(r.log2p(Ty::get(row[mine])));
     float q = 0.0f;
-    for (int j = 0; j < b.k; ++j) q += lidx[j] == mine ? lq[j] : 0.0f;
-    v = (exp2_hw(r.log2p(Ty::get(row[mine]))) - q) * r.gb;
+    for (int j = 0; j < n; j += 4) {
+      const int4 li = *reinterpret_cast<const int4*>(lidx + j);
+      const float4 qi = *reinterpret_cast<const float4*>(lq + j);
+      q += li.x == mine ? qi.x : 0.0f;
+      q += li.y == mine ? qi.y : 0.0f;
+      q += li.z == mine ? qi.z : 0.0f;
+      q += li.w == mine ? qi.w : 0.0f;
+    }
+    v = (v - q) * r.gb;
     if constexpr (ACC) v += Ty::get(out[mine]);
   }
   __syncthreads();
-  bwd_columns<Ty, ACC>(row, out, lo, hi, fill, [&](float x, int) { return exp2_hw(r.log2p(x)) * r.gb; });
+  bwd_columns<Ty, ACC>(row, out, lo, hi, fill, [&](float (&x)[Ty::VE], int) {
+#pragma unroll
+    for (int j = 0; j < Ty::VE; ++j) x[j] = exp2_hw(r.log2p(x[j])) * r.gb;
+  });
   __syncthreads();  // the slice's own writes come before the listed columns'
   if (listed) out[mine] = Ty::put(v);
 }
@@ -714,11 +862,11 @@ void logprobs_launch(const VocabDims& d, const LogprobPtrs& q, char* ws, hipStre
   if (d.k > 0) {
     if (q.entropy) stats_launch<Ty, true, true>(d, s, q.logits, ws, st);
     else stats_launch<Ty, false, true>(d, s, q.logits, ws, st);
-    hipLaunchKernelGGL((logprobs_finish_kernel<Ty, true>), dim3(d.T), dim3(64), 0, st, f, q, part, blocks);
+    hipLaunchKernelGGL((logprobs_finish_kernel<Ty, true>), dim3(d.T), dim3(256), 0, st, f, q, part, blocks);
   } else {
     if (q.entropy) stats_launch<Ty, true, false>(d, s, q.logits, ws, st);
     else stats_launch<Ty, false, false>(d, s, q.logits, ws, st);
-    hipLaunchKernelGGL((logprobs_finish_kernel<Ty, false>), dim3(d.T), dim3(64), 0, st, f, q, part, blocks);
+    hipLaunchKernelGGL((logprobs_finish_kernel<Ty, false>), dim3(d.T), dim3(256), 0, st, f, q, part, blocks);
   }
 }
 
