@@ -11,12 +11,10 @@
 //
 // Forward: vocab_stats_kernel reads every logit once (the operator is bound
 // by that read) and leaves one triple per slice of a row and, for the top
-// alternatives, the maximum of every 64 consecutive columns;
-// logprobs_finish_kernel / distill_finish_kernel join a row's slices.  The k
-// largest logits all lie in the k best of the 64-column blocks (order: larger
-// maximum, then lower block): a block outside has k blocks before it, each
-// with an element that beats all of its own.  So only k blocks of a row are
-// read again.
+// alternatives, the maximum of every block of 64 columns;
+// logprobs_finish_kernel / distill_finish_kernel join a row's slices.  Any
+// value that k blocks reach is at most the k-th best logit, so only the
+// blocks that reach such a value are read again.
 //
 // Backward: one read and one write per logit with (m, l) from the forward.
 //
@@ -24,6 +22,8 @@
 // allows); only a row's last, partial vector is read by elements, so nothing
 // outside a row is touched.
 #include <math.h>
+
+#include <type_traits>
 
 #include "oft_device.h"
 #include "oft_launch.h"
@@ -41,7 +41,6 @@ constexpr float LOWEST = -1000.0f;
 // the same for x - m where it meets a weight that is 0 from far above it on
 // (tau <= 2^20), so that a sum of masks at the type's lowest value stays finite
 constexpr float FAR = -1.0e30f;
-constexpr int BLOCK = 64;  // columns per stored maximum
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef u32x4 u32x4_row __attribute__((aligned(2), may_alias));  // 16 bytes of a row
@@ -154,21 +153,47 @@ constexpr int fwd_tile() {
   return 256 * FU * Ty::VE;
 }
 
-// one step: FU vectors per thread, x[u VE + j] is column base + (u 256 + tid) VE + j
-template <class Ty, bool ENT, bool TOP>
-__device__ __forceinline__ void fwd_step(const float (&x)[FU * Ty::VE], int base, int V, float c, Triple& a,
-                                         typename Ty::E* blocks) {
-  constexpr int VE = Ty::VE, N = FU * VE;
-  float vm[FU];
-#pragma unroll
-  for (int u = 0; u < FU; ++u) {
-    vm[u] = x[u * VE];
-#pragma unroll
-    for (int j = 1; j < VE; ++j) vm[u] = fmaxf(vm[u], x[u * VE + j]);
+// Order of the top alternatives as an unsigned number: larger value first,
+// -0 as +0, NaN as -inf.
+__device__ __forceinline__ uint32_t ordered(float v) {
+  const uint32_t b = __builtin_bit_cast(uint32_t, (v == v ? v : -INFINITY) + 0.0f);
+  return b ^ ((uint32_t)((int)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float unordered(uint32_t o) {
+  return __builtin_bit_cast(float, (o & 0x80000000u) ? o ^ 0x80000000u : ~o);
+}
+
+// Block maxima of a row, as `ordered` numbers: the upper half of it says all
+// for bf16.  A block is 64 columns of one step of the forward pass: the 16
+// columns of each of its FU vectors that RUN neighbouring lanes hold.
+template <class Ty>
+struct Blocks {
+  typedef std::conditional_t<sizeof(typename Ty::E) == 2, uint16_t, uint32_t> Key;
+  static constexpr int BITS = 8 * sizeof(Key);
+  static constexpr int RUN = 16 / Ty::VE;                 // lanes
+  static constexpr int PER_TILE = 256 / RUN;              // blocks of a step
+  static constexpr int VECS = FU * RUN;                   // 16-byte vectors of a block
+  static constexpr int TILE = fwd_tile<Ty>();
+  static __device__ __forceinline__ uint32_t key(float v) { return ordered(v) >> (32 - BITS); }
+  // first column of vector i of block b
+  static __device__ __forceinline__ int column(int b, int i) {
+    return b / PER_TILE * TILE + i / RUN * (256 * Ty::VE) + b % PER_TILE * 16 + i % RUN * Ty::VE;
   }
-  float bm = vm[0];
+};
+
+// one step: FU vectors per thread, x[u VE + j] is column base + (u 256 + tid)
+// VE + j; block: where the thread's block maximum goes (its first lane stores)
+template <class Ty, bool ENT, bool TOP>
+__device__ __forceinline__ void fwd_step(const float (&x)[FU * Ty::VE], float c, Triple& a,
+                                         typename Blocks<Ty>::Key* block) {
+  constexpr int N = FU * Ty::VE;
+  float m0 = x[0], m1 = x[1];
 #pragma unroll
-  for (int u = 1; u < FU; ++u) bm = fmaxf(bm, vm[u]);
+  for (int i = 2; i < N; i += 4) {
+    m0 = fmaxf(fmaxf(m0, x[i]), x[i + 1]);
+    if (i + 2 < N) m1 = fmaxf(fmaxf(m1, x[i + 2]), x[i + 3]);
+  }
+  const float bm = fmaxf(m0, m1);
   a = moved(a, fmaxf(a.m, bm), c);
   const float ref = a.m == -INFINITY ? 0.0f : a.m;
   float s[2] = {0.0f, 0.0f}, w[2] = {0.0f, 0.0f};
@@ -177,44 +202,43 @@ __device__ __forceinline__ void fwd_step(const float (&x)[FU * Ty::VE], int base
     const float d = x[i] - ref;
     const float e = exp2_hw(c * d);
     s[i & 1] += e;
-    if constexpr (ENT) w[i & 1] = fmaf(e, fmaxf(d, FAR), w[i & 1]);
+    if constexpr (ENT) w[i & 1] = fmaf(e, d, w[i & 1]);
+  }
+  if constexpr (ENT) {
+    // a masked logit gives 0 * -inf: that step once more with d clamped, which
+    // costs an instruction per logit that steps without one are spared
+    if (__builtin_amdgcn_ballot_w64(w[0] + w[1] != w[0] + w[1]) != 0) {
+      w[0] = w[1] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float d = x[i] - ref;
+        w[i & 1] = fmaf(exp2_hw(c * d), fmaxf(d, FAR), w[i & 1]);
+      }
+    }
   }
   a.s += s[0] + s[1];
   a.w += w[0] + w[1];
   if constexpr (TOP) {
-    // 64 columns are 64 / VE neighbouring lanes of one vector
-    constexpr int G = BLOCK / VE;
-    const int lane = threadIdx.x & 63;
-    float mine = -INFINITY;
-#pragma unroll
-    for (int u = 0; u < FU; ++u) {
-      float v = fmaxf(vm[u], dpp<PAIR>(vm[u]));
-      v = fmaxf(v, dpp<QUAD>(v));
-      v = fmaxf(v, dpp<EIGHT>(v));
-      if constexpr (G == 16) v = fmaxf(v, dpp<ROW>(v));
-      mine = (lane % G) == u ? v : mine;
-    }
-    // lane u of a group stores the block of vector u
-    if (lane % G < FU) {
-      const int b = (base + ((lane % G) * 256 + threadIdx.x - lane % G) * VE) / BLOCK;
-      if (b * BLOCK < V) blocks[b] = Ty::put(mine);
-    }
+    float v = fmaxf(bm, dpp<PAIR>(bm));
+    if constexpr (Blocks<Ty>::RUN == 4) v = fmaxf(v, dpp<QUAD>(v));
+    if (threadIdx.x % Blocks<Ty>::RUN == 0) *block = (typename Blocks<Ty>::Key)Blocks<Ty>::key(v);
   }
 }
 
 // part[t S + sl]: the triple of columns [sl slice, (sl + 1) slice) of row t;
-// blocks: the maxima of the row's 64-column blocks, nb per row
+// blocks: the maxima of the row's blocks, nb per row
 template <class Ty, bool ENT, bool TOP>
 __global__ __launch_bounds__(256) void vocab_stats_kernel(const typename Ty::E* __restrict__ logits, long ld, int V,
                                                           int S, int slice, float c, float4* __restrict__ part,
-                                                          typename Ty::E* __restrict__ blocks, int nb) {
+                                                          typename Blocks<Ty>::Key* __restrict__ blocks, int nb) {
   typedef typename Ty::E E;
+  typedef Blocks<Ty> B;
   constexpr int VE = Ty::VE, TILE = fwd_tile<Ty>();
   __shared__ float sh[4][3];
   const int t = blockIdx.x / S, sl = blockIdx.x % S, tid = threadIdx.x;
   const E* row = logits + (size_t)t * ld;
-  E* brow = TOP ? blocks + (size_t)t * nb : nullptr;
   const int lo = sl * slice, hi = min(V, lo + slice);
+  typename B::Key* block = TOP ? blocks + (size_t)t * nb + lo / TILE * B::PER_TILE + tid / B::RUN : nullptr;
   Triple a{-INFINITY, 0.0f, 0.0f};
   float x[FU * VE];
   int base = lo;
@@ -224,7 +248,8 @@ __global__ __launch_bounds__(256) void vocab_stats_kernel(const typename Ty::E* 
     for (int u = 0; u < FU; ++u) v[u] = load16(row + base + (u * 256 + tid) * VE);
 #pragma unroll
     for (int u = 0; u < FU; ++u) Ty::unpack(v[u], x + u * VE);
-    fwd_step<Ty, ENT, TOP>(x, base, V, c, a, brow);
+    fwd_step<Ty, ENT, TOP>(x, c, a, block);
+    if constexpr (TOP) block += B::PER_TILE;
   }
   if (base < hi) {
 #pragma unroll
@@ -237,7 +262,7 @@ __global__ __launch_bounds__(256) void vocab_stats_kernel(const typename Ty::E* 
         for (int j = 0; j < VE; ++j) x[u * VE + j] = i0 + j < hi ? Ty::get(row[i0 + j]) : -INFINITY;
       }
     }
-    fwd_step<Ty, ENT, TOP>(x, base, V, c, a, brow);
+    fwd_step<Ty, ENT, TOP>(x, c, a, block);
   }
   a = wave_join(a, c);
   if ((tid & 63) == 0) {
@@ -252,31 +277,26 @@ __global__ __launch_bounds__(256) void vocab_stats_kernel(const typename Ty::E* 
   }
 }
 
-// ---------------------------------------------------------- top alternatives
-__device__ __forceinline__ uint32_t ordered(float v) {  // unsigned order of values
-  const uint32_t b = __builtin_bit_cast(uint32_t, v + 0.0f);  // -0 as +0
-  return b ^ ((uint32_t)((int)b >> 31) | 0x80000000u);
-}
-__device__ __forceinline__ float unordered(uint32_t o) {
-  return __builtin_bit_cast(float, (o & 0x80000000u) ? o ^ 0x80000000u : ~o);
+// a row's triple from its slices, in every lane of the wave
+__device__ __forceinline__ Triple row_triple(const float4* part, int S, float c) {
+  Triple a{-INFINITY, 0.0f, 0.0f};
+  for (int i = threadIdx.x; i < S; i += 64) {
+    const float4 p = part[i];
+    a = join(a, Triple{p.x, p.y, p.z}, c);
+  }
+  return wave_join(a, c);
 }
 
+// ---------------------------------------------------------- top alternatives
 __device__ __forceinline__ int below(unsigned long long mask) {  // set bits of lower lanes
   return __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
 }
 
-template <class Ty>
-__device__ __forceinline__ float rank_value(typename Ty::E v) {  // NaN ranks as -inf
-  const float f = Ty::get(v);
-  return f != f ? -INFINITY : f;
-}
-
-// k-th largest of the N lane values (in `ordered` form), two bits a step.
-// Values of 16 bits (LOW = 16) are told apart by their upper half.
-template <int N, int LOW>
-__device__ __forceinline__ uint32_t kth(const uint32_t (&o)[N], int k) {
+// k-th largest of the N values per lane (numbers of BITS bits), two bits a step
+template <int N, int BITS>
+__device__ __forceinline__ uint32_t kth(const uint32_t* o, int k) {
   uint32_t r = 0;
-  for (int bit = 30; bit >= LOW; bit -= 2) {
+  for (int bit = BITS - 2; bit >= 0; bit -= 2) {
     int n1 = 0, n2 = 0, n3 = 0;
     const uint32_t t1 = r | (1u << bit), t2 = r | (2u << bit), t3 = r | (3u << bit);
 #pragma unroll
@@ -297,73 +317,91 @@ __device__ __forceinline__ void wave_lds() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// A wave's selection of the k best of a stream of (value, id), ids ascending:
-// candidates wait in LDS in order of id; when the list is full it is cut to
-// its k best, whose last value is then what a later candidate must exceed.
-// Right for any input, whatever its ties.
-constexpr int QCAP = 512, MAXTOP = 128;
-struct Select {
-  float* val;  // [QCAP] in LDS
-  int* id;     // [QCAP]
-  int k, n;
-  float floor;  // a candidate must reach it, or exceed it once `strict`
-  bool strict;
+// A candidate as one number: value first, then the lower column; no two of a
+// row are equal.
+__device__ __forceinline__ unsigned long long candidate(uint32_t order, int col) {
+  return (unsigned long long)order << 32 | (uint32_t)~col;
+}
 
-  __device__ __forceinline__ Select(float* v, int* i, int kk, float f)
-      : val(v), id(i), k(kk), n(0), floor(f), strict(false) {}
-
-  __device__ __forceinline__ void feed(float v, int i, bool ok) {
-    const bool take = ok && (strict ? v > floor : v >= floor);
-    const unsigned long long mask = __ballot(take);
-    if (mask == 0) return;
-    if (take) {
-      const int at = n + below(mask);
-      val[at] = v;
-      id[at] = i;
-    }
-    n += __popcll(mask);
-    if (n > QCAP - 64) cut();
+// The k best of a whole row, whatever its ties: one wave reads it in order of
+// columns, candidates wait in LDS, and a full list is cut to its k best, whose
+// last one a later candidate must exceed (an equal value has a higher column).
+// list: [QCAP], of which the first k are the result.  `order`: a number that
+// at least k logits reach.
+constexpr int QCAP = 1024;
+__device__ int cut(unsigned long long* list, int n, int k, uint32_t& floor) {
+  wave_lds();
+  if (n <= k) return n;
+  constexpr int N = QCAP / 64;
+  const int lane = threadIdx.x & 63;
+  unsigned long long e[N];
+  uint32_t o[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    e[j] = j * 64 + lane < n ? list[j * 64 + lane] : 0ull;
+    o[j] = (uint32_t)(e[j] >> 32);
   }
+  const uint32_t last = kth<N, 32>(o, k);
+  int above = 0;
+#pragma unroll
+  for (int j = 0; j < N; ++j) above += __popcll(__ballot(o[j] > last));
+  int ties = k - above, m = 0;
+  wave_lds();
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const bool tie = o[j] == last;  // (0 is no entry and below any)
+    const unsigned long long eq = __ballot(tie);
+    const bool keep = o[j] > last || (tie && below(eq) < ties);
+    const unsigned long long mask = __ballot(keep);
+    if (keep) list[m + below(mask)] = e[j];
+    m += __popcll(mask);
+    ties -= min(ties, (int)__popcll(eq));
+  }
+  floor = last + 1;
+  wave_lds();
+  return m;
+}
 
-  // keep the k best, in order of id
-  __device__ void cut() {
-    wave_lds();
-    if (n <= k) return;
-    constexpr int N = QCAP / 64;
-    const int lane = threadIdx.x & 63;
-    uint32_t o[N];
-    int ids[N];
+template <class Ty>
+__device__ void select_row(const typename Ty::E* row, int V, int k, uint32_t floor, unsigned long long* list) {
+  constexpr int VE = Ty::VE, U = 4;
+  static_assert(64 * VE <= QCAP / 2, "a vector per lane fits behind a list that is not cut");
+  const int lane = threadIdx.x & 63;
+  int n = 0;
+  for (int base = 0; base < V; base += 64 * VE * U) {
+    float x[U][VE];
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-      const bool in = j * 64 + lane < n;
-      o[j] = in ? ordered(val[j * 64 + lane]) : 0u;
-      ids[j] = in ? id[j * 64 + lane] : 0;
-    }
-    const uint32_t last = kth<N, 0>(o, k);
-    int above = 0;
+    for (int u = 0; u < U; ++u) {
+      const int i0 = base + (u * 64 + lane) * VE;
+      if (i0 + VE <= V) {
+        Ty::unpack(load16(row + i0), x[u]);
+      } else {
 #pragma unroll
-    for (int j = 0; j < N; ++j) above += __popcll(__ballot(o[j] > last));
-    int ties = k - above, m = 0;
-    wave_lds();
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-      const bool tie = o[j] == last && j * 64 + lane < n;
-      const unsigned long long eq = __ballot(tie);
-      const bool keep = o[j] > last || (tie && below(eq) < ties);
-      const unsigned long long mask = __ballot(keep);
-      if (keep) {
-        val[m + below(mask)] = unordered(o[j]);
-        id[m + below(mask)] = ids[j];
+        for (int j = 0; j < VE; ++j) x[u][j] = i0 + j < V ? Ty::get(row[i0 + j]) : 0.0f;
       }
-      m += __popcll(mask);
-      ties -= min(ties, (int)__popcll(eq));
     }
-    n = m;
-    floor = unordered(last);
-    strict = true;
-    wave_lds();
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i0 = base + (u * 64 + lane) * VE;
+      bool take[VE];
+      int at = n, more = 0;
+#pragma unroll
+      for (int j = 0; j < VE; ++j) {
+        take[j] = i0 + j < V && ordered(x[u][j]) >= floor;
+        const unsigned long long mask = __ballot(take[j]);
+        at += below(mask);
+        more += __popcll(mask);
+      }
+      if (more == 0) continue;
+#pragma unroll
+      for (int j = 0; j < VE; ++j)
+        if (take[j]) list[at++] = candidate(ordered(x[u][j]), i0 + j);
+      n += more;
+      if (n > QCAP / 2) n = cut(list, n, k, floor);
+    }
   }
-};
+  cut(list, n, k, floor);
+}
 
 struct FinishArgs {
   int V, k, S, nb;
@@ -371,174 +409,157 @@ struct FinishArgs {
   float c, invtau;
 };
 
-// Top alternatives of a row by one wave: the k best blocks, then the k best of
-// their elements.  val, id: [2][QCAP]; the result is val[1], id[1] in order
-// of column, at least k of them.
-template <class Ty>
-__device__ void select_any(const FinishArgs& f, const typename Ty::E* row, const typename Ty::E* brow,
-                           float (*val)[QCAP], int (*id)[QCAP]) {
-  constexpr int U = 8;  // loads in flight
-  const int lane = threadIdx.x & 63;
-  // a value that at least k blocks reach: the k-th best of 128 interleaved
-  // groups of blocks
-  float best[2] = {-INFINITY, -INFINITY};
-  for (int b = lane; b < f.nb; b += 64 * U) {
-#pragma unroll
-    for (int j = 0; j < U; ++j)
-      if (b + 64 * j < f.nb) best[j & 1] = fmaxf(best[j & 1], Ty::get(brow[b + 64 * j]));
-  }
-  const uint32_t o[2] = {ordered(best[0]), ordered(best[1])};
-  Select sel(val[0], id[0], f.k, unordered(kth<2, 0>(o, f.k)));
-  for (int b = lane; b - lane < f.nb; b += 64 * U) {
-    float v[U];
-#pragma unroll
-    for (int j = 0; j < U; ++j) v[j] = b + 64 * j < f.nb ? rank_value<Ty>(brow[b + 64 * j]) : 0.0f;
-#pragma unroll
-    for (int j = 0; j < U; ++j) sel.feed(v[j], b + 64 * j, b + 64 * j < f.nb);
-  }
-  sel.cut();
-  // the blocks' elements: at least k reach the least of k maxima
-  const int nsel = sel.n;
-  float lowest = INFINITY;
-  for (int i = lane; i < nsel; i += 64) lowest = fminf(lowest, val[0][i]);
-  lowest = -wave_max(-lowest);
-  Select el(val[1], id[1], f.k, nsel < f.k ? -INFINITY : lowest);
-  for (int i = 0; i < nsel; i += U) {
-    float v[U];
-    int col[U];
-#pragma unroll
-    for (int j = 0; j < U; ++j) {
-      col[j] = i + j < nsel ? id[0][i + j] * BLOCK + lane : f.V;
-      v[j] = col[j] < f.V ? rank_value<Ty>(row[col[j]]) : -INFINITY;
-    }
-#pragma unroll
-    for (int j = 0; j < U; ++j) el.feed(v[j], col[j], col[j] < f.V);
-  }
-  el.cut();
-}
-
-// Joins a row's slices; its outputs.  Four waves per row.
+// Joins a row's slices; its outputs.  One wave per row.
 //
-// Top alternatives, the usual case: each thread holds up to HELD block maxima
-// in registers; a value T that k of 256 (k <= 64) or 512 disjoint groups of
-// them reach is at most the k-th best, so the elements >= T of the blocks
-// >= T hold the answer.  There are few more than k of them, in any order:
-// (value, column) as one 64-bit key gives each its place by counting the
-// keys above it.  Rows where ties or masks leave too many (or a vocabulary of
-// more blocks than the registers hold) go through select_any.
-constexpr int HELD = 16, MAXBLK = 512, MAXCAND = 512;
+// Top alternatives, the usual case: each lane holds up to HELD vectors of
+// block maxima; a number t that k of 128, 256 or 512 disjoint groups of them
+// reach (4 groups and more for each alternative) leaves few more than k blocks
+// and elements, and the place of each of those is the number of candidates
+// above it.  Rows where ties or masks leave too many, or with more blocks than
+// the registers hold, go through select_row.
+constexpr int MAXBLK = 256, MAXCAND = 512;
 template <class Ty, bool TOP>
-__global__ __launch_bounds__(256) void logprobs_finish_kernel(FinishArgs f, LogprobPtrs q,
-                                                              const float4* __restrict__ part,
-                                                              const typename Ty::E* __restrict__ blocks) {
+__global__ __launch_bounds__(64) void logprobs_finish_kernel(FinishArgs f, LogprobPtrs q,
+                                                             const float4* __restrict__ part,
+                                                             const typename Blocks<Ty>::Key* __restrict__ blocks) {
   typedef typename Ty::E E;
-  const int t = blockIdx.x, tid = threadIdx.x, lane = tid & 63;
+  typedef Blocks<Ty> B;
+  constexpr int VE = Ty::VE, HELD = TOP ? (sizeof(E) == 2 ? 8 : 16) : 0, KV = 16 / sizeof(typename B::Key);
+  const int t = blockIdx.x, lane = threadIdx.x;
   const E* row = static_cast<const E*>(q.logits) + (size_t)t * f.ld;
-  const E* brow = TOP ? blocks + (size_t)t * f.nb : nullptr;
-  float held[HELD];
-  const bool few = f.nb <= HELD * 256;
+  u32x4 held[HELD + 1];
+  const int nvec = TOP ? f.nb / KV : 0;
   if constexpr (TOP) {
+    const u32x4* bv = reinterpret_cast<const u32x4*>(blocks + (size_t)t * f.nb);
 #pragma unroll
-    for (int i = 0; i < HELD; ++i) held[i] = few && i * 256 + tid < f.nb ? rank_value<Ty>(brow[i * 256 + tid]) : NAN;
+    for (int i = 0; i < HELD; ++i) held[i] = i * 64 + lane < nvec ? bv[i * 64 + lane] : u32x4{0, 0, 0, 0};
   }
-  const int lab = q.logp && tid == 0 ? q.labels[t] : -1;
+  const int lab = q.logp ? q.labels[t] : -1;
   const bool known = lab >= 0 && lab < f.V;
   const float given = known ? Ty::get(row[lab]) : 0.0f;
-  Triple a{-INFINITY, 0.0f, 0.0f};
-  for (int i = lane; i < f.S; i += 64) {
-    const float4 p = part[(size_t)t * f.S + i];
-    a = join(a, Triple{p.x, p.y, p.z}, f.c);
-  }
-  a = wave_join(a, f.c);
+  const Triple a = row_triple(part + (size_t)t * f.S, f.S, f.c);
   const bool empty = a.s == 0.0f;
   const float l = __logf(a.s);  // ln 0 = -inf for an empty row
-  if (tid == 0) {
+  if (lane == 0) {
     *reinterpret_cast<float2*>(q.stats + 2 * (size_t)t) = make_float2(a.m, l);
     if (q.entropy) q.entropy[t] = empty ? 0.0f : l - a.w * f.invtau / a.s;
     if (q.logp)
       q.logp[t] = lab == -1 ? 0.0f : !known ? NAN : empty ? -INFINITY : (given - a.m) * f.invtau - l;
   }
   if constexpr (TOP) {
-    constexpr int LOW = sizeof(E) == 2 ? 16 : 0;
-    __shared__ __align__(16) unsigned long long key[MAXCAND];
-    __shared__ float val[2][QCAP];
-    __shared__ int id[2][QCAP];
-    __shared__ uint32_t group[512];
-    __shared__ int cand_block[MAXBLK];
-    __shared__ float sh_floor;
-    __shared__ int nblk, ncand;
-    if (tid == 0) nblk = ncand = 0;
-    float best[2] = {-INFINITY, -INFINITY};
+    __shared__ __align__(16) unsigned long long list[QCAP];
+    __shared__ int cand[MAXBLK];
+    __shared__ int count[2];
+    if (lane < 2) count[lane] = 0;
+    // the best of each of eight groups per lane
+    uint32_t g[8];
+    if constexpr (KV == 8) {
+      typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 #pragma unroll
-    for (int i = 0; i < HELD; ++i) best[i & 1] = fmaxf(best[i & 1], held[i]);
-    group[tid] = ordered(f.k <= 64 ? fmaxf(best[0], best[1]) : best[0]);
-    if (f.k > 64) group[256 + tid] = ordered(best[1]);
-    __syncthreads();
-    if (tid < 64) {
-      uint32_t r;
-      if (f.k <= 64) {
-        uint32_t o[4];
+      for (int d = 0; d < 4; ++d) {
+        uint32_t w0 = held[0][d];
+        u16x2 m = __builtin_bit_cast(u16x2, w0);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) o[j] = group[64 * j + lane];
-        r = kth<4, LOW>(o, f.k);
-      } else {
-        uint32_t o[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = group[64 * j + lane];
-        r = kth<8, LOW>(o, f.k);
+        for (int i = 1; i < HELD; ++i) {
+          const uint32_t w = held[i][d];
+          m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, w));
+        }
+        g[2 * d] = m[0];
+        g[2 * d + 1] = m[1];
       }
-      // (of a negative 16-bit value the lower half of the ordered form is ones)
-      if (tid == 0) sh_floor = r == 0u ? -INFINITY : unordered(LOW && !(r & 0x80000000u) ? r | 0xFFFFu : r);
+    } else {
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        g[d] = held[0][d];
+        g[4 + d] = held[1][d];
+#pragma unroll
+        for (int i = 2; i < HELD; i += 2) {
+          g[d] = max(g[d], (uint32_t)held[i][d]);
+          g[4 + d] = max(g[4 + d], (uint32_t)held[i + 1][d]);
+        }
+      }
     }
-    __syncthreads();
-    const float floor = sh_floor;
+    uint32_t floor;
+    if (f.k > 64) {
+      floor = kth<8, B::BITS>(g, f.k);
+    } else {
 #pragma unroll
-    for (int i = 0; i < HELD; ++i)
-      if (held[i] >= floor) {  // (false for NaN: no block)
-        const int at = atomicAdd(&nblk, 1);
-        if (at < MAXBLK) cand_block[at] = i * 256 + tid;
+      for (int j = 0; j < 4; ++j) g[j] = max(g[j], g[4 + j]);
+      if (f.k > 24) {
+        floor = kth<4, B::BITS>(g, f.k);
+      } else {
+        g[0] = max(g[0], g[2]);
+        g[1] = max(g[1], g[3]);
+        floor = kth<2, B::BITS>(g, f.k);
       }
-    __syncthreads();
-    const int n1 = nblk;
-    bool usual = few && n1 <= MAXBLK;
+    }
+    wave_lds();
+    bool usual = nvec <= HELD * 64;
+    floor = max(floor, 1u);  // (fewer than k groups: every block is above 0)
+#pragma unroll
+    for (int i = 0; i < HELD; ++i) {
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        const uint32_t w = held[i][d];
+        const int b = (i * 64 + lane) * KV + d * (KV / 4);
+        const uint32_t k0 = KV == 8 ? w & 0xFFFFu : w, k1 = KV == 8 ? w >> 16 : 0u;
+        if (max(k0, k1) >= floor) {
+          if (k0 >= floor) {
+            const int at = atomicAdd(&count[0], 1);
+            if (at < MAXBLK) cand[at] = b;
+          }
+          if (k1 >= floor) {
+            const int at = atomicAdd(&count[0], 1);
+            if (at < MAXBLK) cand[at] = b + 1;
+          }
+        }
+      }
+    }
+    wave_lds();
+    const int n1 = count[0];
+    usual = usual && n1 <= MAXBLK;
+    int n = 0;
     if (usual) {
-      constexpr int U = 8;
-      for (int i = tid >> 6; i < n1; i += 4 * U) {
-        float v[U];
+      constexpr int U = 4;
+      for (int i = lane; i - lane < n1 * B::VECS; i += 64 * U) {
+        float x[U][VE];
         int col[U];
 #pragma unroll
-        for (int j = 0; j < U; ++j) {
-          col[j] = i + 4 * j < n1 ? cand_block[i + 4 * j] * BLOCK + lane : f.V;
-          v[j] = col[j] < f.V ? rank_value<Ty>(row[col[j]]) : NAN;
+        for (int u = 0; u < U; ++u) {
+          const int at = i + 64 * u;
+          col[u] = at < n1 * B::VECS ? B::column(cand[at / B::VECS], at % B::VECS) : f.V;
+          if (col[u] + VE <= f.V) {
+            Ty::unpack(load16(row + col[u]), x[u]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < VE; ++j) x[u][j] = col[u] + j < f.V ? Ty::get(row[col[u] + j]) : 0.0f;
+          }
         }
 #pragma unroll
-        for (int j = 0; j < U; ++j)
-          if (v[j] >= floor) {
-            const int at = atomicAdd(&ncand, 1);
-            if (at < MAXCAND) key[at] = (unsigned long long)ordered(v[j]) << 32 | (uint32_t)~col[j];
-          }
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int j = 0; j < VE; ++j)
+            if (B::key(x[u][j]) >= floor && col[u] + j < f.V) {
+              const int at = atomicAdd(&count[1], 1);
+              if (at < MAXCAND) list[at] = candidate(ordered(x[u][j]), col[u] + j);
+            }
       }
-      __syncthreads();
-      usual = ncand <= MAXCAND;
+      wave_lds();
+      n = count[1];
+      usual = n <= MAXCAND && n >= f.k;
     }
-    int n = usual ? ncand : f.k;
     if (!usual) {
-      __syncthreads();
-      if (tid < 64) {
-        select_any<Ty>(f, row, brow, val, id);
-        for (int i = lane; i < f.k; i += 64)
-          key[i] = (unsigned long long)ordered(val[1][i]) << 32 | (uint32_t)~id[1][i];
-      }
-      __syncthreads();
+      select_row<Ty>(row, f.V, f.k, floor << (32 - B::BITS), list);
+      n = f.k;
     }
-    // an even number of keys for the paired reads: 0 is below every key
-    if (tid == 0 && (n & 1)) key[n] = 0ull;
-    __syncthreads();
-    for (int i = tid; i < n; i += 256) {
-      const unsigned long long mine = key[i];
+    // an even number of candidates for the paired reads: 0 is below each
+    if (lane == 0 && (n & 1)) list[n] = 0ull;
+    wave_lds();
+    for (int i = lane; i < n; i += 64) {
+      const unsigned long long mine = list[i];
       int place = 0;
       for (int j = 0; j < n; j += 2) {
-        const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(key + j);
+        const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(list + j);
         place += (o.x > mine ? 1 : 0) + (o.y > mine ? 1 : 0);
       }
       if (place < f.k) {
@@ -610,12 +631,7 @@ __global__ __launch_bounds__(64) void distill_finish_kernel(FinishArgs f, const 
   float x[TI];
 #pragma unroll
   for (int i = 0; i < TI; ++i) x[i] = te.ix[i] >= 0 ? Ty::get(row[te.ix[i]]) : 0.0f;
-  Triple a{-INFINITY, 0.0f, 0.0f};
-  for (int i = threadIdx.x; i < f.S; i += 64) {
-    const float4 p = part[(size_t)t * f.S + i];
-    a = join(a, Triple{p.x, p.y, p.z}, f.c);
-  }
-  a = wave_join(a, f.c);
+  const Triple a = row_triple(part + (size_t)t * f.S, f.S, f.c);
   const float l = __logf(a.s);
   float sum = 0.0f;
 #pragma unroll
@@ -834,11 +850,15 @@ Split split(int T, int V, int tile) {
 Split fwd_split(const VocabDims& d) { return split(d.T, d.V, d.f32 ? fwd_tile<F32>() : fwd_tile<Bf16>()); }
 Split bwd_split(const VocabDims& d) { return split(d.T, d.V, d.f32 ? bwd_tile<F32>() : bwd_tile<Bf16>()); }
 
-int blocks_of(int V) { return (V + BLOCK - 1) / BLOCK; }
+template <class Ty>
+int blocks_of(int V) {
+  return (V + fwd_tile<Ty>() - 1) / fwd_tile<Ty>() * Blocks<Ty>::PER_TILE;
+}
 size_t part_bytes(const VocabDims& d) { return (size_t)d.T * fwd_split(d).S * sizeof(float4); }
 
+template <class Ty>
 FinishArgs finish_args(const VocabDims& d, int S) {
-  return FinishArgs{d.V, d.k, S, blocks_of(d.V), d.ld, d.invtau * LOG2E, d.invtau};
+  return FinishArgs{d.V, d.k, S, blocks_of<Ty>(d.V), d.ld, d.invtau * LOG2E, d.invtau};
 }
 BwdArgs bwd_args(const VocabDims& d) {
   const Split s = bwd_split(d);
@@ -850,23 +870,24 @@ void stats_launch(const VocabDims& d, const Split& s, const void* logits, char* 
   typedef typename Ty::E E;
   hipLaunchKernelGGL((vocab_stats_kernel<Ty, ENT, TOP>), dim3((size_t)d.T * s.S), dim3(256), 0, st,
                      static_cast<const E*>(logits), d.ld, d.V, s.S, s.slice, d.invtau * LOG2E,
-                     reinterpret_cast<float4*>(ws), reinterpret_cast<E*>(ws + part_bytes(d)), blocks_of(d.V));
+                     reinterpret_cast<float4*>(ws),
+                     reinterpret_cast<typename Blocks<Ty>::Key*>(ws + part_bytes(d)), blocks_of<Ty>(d.V));
 }
 
 template <class Ty>
 void logprobs_launch(const VocabDims& d, const LogprobPtrs& q, char* ws, hipStream_t st) {
   const Split s = fwd_split(d);
   const float4* part = reinterpret_cast<const float4*>(ws);
-  const typename Ty::E* blocks = reinterpret_cast<const typename Ty::E*>(ws + part_bytes(d));
-  const FinishArgs f = finish_args(d, s.S);
+  const auto* blocks = reinterpret_cast<const typename Blocks<Ty>::Key*>(ws + part_bytes(d));
+  const FinishArgs f = finish_args<Ty>(d, s.S);
   if (d.k > 0) {
     if (q.entropy) stats_launch<Ty, true, true>(d, s, q.logits, ws, st);
     else stats_launch<Ty, false, true>(d, s, q.logits, ws, st);
-    hipLaunchKernelGGL((logprobs_finish_kernel<Ty, true>), dim3(d.T), dim3(256), 0, st, f, q, part, blocks);
+    hipLaunchKernelGGL((logprobs_finish_kernel<Ty, true>), dim3(d.T), dim3(64), 0, st, f, q, part, blocks);
   } else {
     if (q.entropy) stats_launch<Ty, true, false>(d, s, q.logits, ws, st);
     else stats_launch<Ty, false, false>(d, s, q.logits, ws, st);
-    hipLaunchKernelGGL((logprobs_finish_kernel<Ty, false>), dim3(d.T), dim3(256), 0, st, f, q, part, blocks);
+    hipLaunchKernelGGL((logprobs_finish_kernel<Ty, false>), dim3(d.T), dim3(64), 0, st, f, q, part, blocks);
   }
 }
 
@@ -875,7 +896,7 @@ void distill_launch(const VocabDims& d, const void* logits, const int* idx, cons
                     float* stats, char* ws, hipStream_t st) {
   const Split s = fwd_split(d);
   stats_launch<Ty, false, false>(d, s, logits, ws, st);
-  hipLaunchKernelGGL((distill_finish_kernel<Ty>), dim3(d.T), dim3(64), 0, st, finish_args(d, s.S),
+  hipLaunchKernelGGL((distill_finish_kernel<Ty>), dim3(d.T), dim3(64), 0, st, finish_args<Ty>(d, s.S),
                      static_cast<const typename Ty::E*>(logits), idx, teacher, reinterpret_cast<const float4*>(ws), loss,
                      stats);
 }
@@ -900,7 +921,8 @@ void distill_bwd_launch(const VocabDims& d, const void* logits, const int* idx, 
 }  // namespace
 
 size_t vocab_ws_bytes(const VocabDims& d) {
-  return part_bytes(d) + (d.k > 0 ? (size_t)d.T * blocks_of(d.V) * (d.f32 ? 4 : 2) : 0);
+  const size_t maxima = (size_t)(d.f32 ? blocks_of<F32>(d.V) * 4 : blocks_of<Bf16>(d.V) * 2);
+  return part_bytes(d) + (d.k > 0 ? d.T * maxima : 0);
 }
 
 hipError_t launch_token_logprobs(const VocabDims& d, const LogprobPtrs& q, char* ws, hipStream_t st) {
