@@ -2,12 +2,15 @@
 // tokens with entropy and top alternatives, distillation from a teacher's
 // top logits, and their gradients.
 //
-// With x a row, m its maximum and c = log2(e) / tau:
-//   e_i = 2^(c (x_i - m)), s = sum e_i, w = sum e_i (x_i - m),
-//   l = ln s, log p_i = (x_i - m) / tau - l, H = l - w / (tau s).
+// With x a row, m its maximum, c = log2(e) / tau and R = c m as rounded:
+//   e_i = 2^(c x_i - R) (one fused multiply-add, so its rounding is relative
+//   to the small difference, and R is a reference like any other),
+//   s = sum e_i, w = sum e_i (c x_i - R),
+//   l = ln s - (c m - R) ln 2, H = (log2 s - w / s) ln 2,
+//   log p_i = (x_i - m) / tau - l.
 // A sum over part of a row is the triple (m, s, w) with its own m; moving it
-// to a larger maximum M multiplies s by f = 2^(c (m - M)) and turns w into
-// f (w + s (m - M)).
+// to a larger maximum multiplies s by f = 2^d, d the difference of the two
+// references, and turns w into f (w + s d).
 //
 // Forward: vocab_stats_kernel reads every logit once (the operator is bound
 // by that read) and leaves one triple per slice of a row and, for the top
@@ -35,13 +38,9 @@ namespace {
 
 constexpr float LOG2E = 1.44269504088896340736f;
 constexpr float LN2 = 0.69314718055994530942f;
-// clamp of z and log p where they are multiplied by p: p is 0 in fp32 far
-// above it, and 0 times it is 0 (0 times -inf would be NaN)
+// clamp of base-2 exponents where they meet their own 2^x: that is 0 in fp32
+// far above it, and 0 times it is 0 (0 times -inf would be NaN)
 constexpr float LOWEST = -1000.0f;
-// the same for x - m where it meets a weight that is 0 from far above it on
-// (tau <= 2^20), so that a sum of masks at the type's lowest value stays finite
-constexpr float FAR = -1.0e30f;
-
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef u32x4 u32x4_row __attribute__((aligned(2), may_alias));  // 16 bytes of a row
 
@@ -126,11 +125,31 @@ struct Triple {
   float m, s, w;
 };
 
+// R of a maximum; 0 for an empty set.  From 2^20 on, where the rounding of
+// c m is no longer small against 1 (masks at the type's lowest value alone in
+// a part of a row), the reference is c m itself: 2^(c (x - m)).
+__device__ __forceinline__ float reference(float m, float c) { return m == -INFINITY ? 0.0f : c * m; }
+__device__ __forceinline__ bool beyond(float R) { return !(fabsf(R) < 0x1p20f); }
+// c m less the reference
+__device__ __forceinline__ float rounding(float m, float R, float c) {
+  return m == -INFINITY || beyond(R) ? 0.0f : fmaf(c, m, -R);
+}
+
 // the triple moved to the maximum M >= m; an empty set has s = 0
 __device__ __forceinline__ Triple moved(const Triple& a, float M, float c) {
-  const float d = a.s == 0.0f ? 0.0f : a.m - M;
-  const float f = exp2_hw(c * d);
-  return Triple{M, a.s * f, f * fmaf(a.s, fmaxf(d, FAR), a.w)};
+  const float Ra = reference(a.m, c), RM = reference(M, c);
+  float d = beyond(Ra) || beyond(RM) ? c * (a.m - M) + (rounding(M, RM, c) - rounding(a.m, Ra, c)) : Ra - RM;
+  d = a.s == 0.0f ? 0.0f : d;
+  const float f = exp2_hw(d);
+  return Triple{M, a.s * f, f * fmaf(a.s, fmaxf(d, LOWEST), a.w)};
+}
+
+// l of a row's triple: -inf for an empty row
+__device__ __forceinline__ float log_sum(const Triple& a, float c) {
+  return (__builtin_amdgcn_logf(a.s) - rounding(a.m, reference(a.m, c), c)) * LN2;
+}
+__device__ __forceinline__ float entropy_of(const Triple& a) {
+  return a.s == 0.0f ? 0.0f : (__builtin_amdgcn_logf(a.s) - a.w / a.s) * LN2;
 }
 
 __device__ __forceinline__ Triple join(const Triple& a, const Triple& b, float c) {
@@ -182,10 +201,11 @@ struct Blocks {
 };
 
 // one step: FU vectors per thread, x[u VE + j] is column base + (u 256 + tid)
-// VE + j; block: where the thread's block maximum goes (its first lane stores)
-template <class Ty, bool ENT, bool TOP>
+// VE + j; again(u, y) reads vector u once more; block: where the thread's
+// block maximum goes (its first lane stores)
+template <class Ty, bool ENT, bool TOP, class F>
 __device__ __forceinline__ void fwd_step(const float (&x)[FU * Ty::VE], float c, Triple& a,
-                                         typename Blocks<Ty>::Key* block) {
+                                         typename Blocks<Ty>::Key* block, F again) {
   constexpr int N = FU * Ty::VE;
   float m0 = x[0], m1 = x[1];
 #pragma unroll
@@ -195,29 +215,41 @@ __device__ __forceinline__ void fwd_step(const float (&x)[FU * Ty::VE], float c,
   }
   const float bm = fmaxf(m0, m1);
   a = moved(a, fmaxf(a.m, bm), c);
-  const float ref = a.m == -INFINITY ? 0.0f : a.m;
+  const float R = reference(a.m, c);
   float s[2] = {0.0f, 0.0f}, w[2] = {0.0f, 0.0f};
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const float d = x[i] - ref;
-    const float e = exp2_hw(c * d);
+    const float z = fmaf(x[i], c, -R);
+    const float e = exp2_hw(z);
     s[i & 1] += e;
-    if constexpr (ENT) w[i & 1] = fmaf(e, d, w[i & 1]);
+    if constexpr (ENT) w[i & 1] = fmaf(e, z, w[i & 1]);
   }
-  if constexpr (ENT) {
-    // a masked logit gives 0 * -inf: that step once more with d clamped, which
-    // costs an instruction per logit that steps without one are spared
-    if (__builtin_amdgcn_ballot_w64(w[0] + w[1] != w[0] + w[1]) != 0) {
-      w[0] = w[1] = 0.0f;
+  float sum = s[0] + s[1], sumw = w[0] + w[1];
+  // (the sums stay on this side of the branch: their terms would hold registers)
+  asm volatile("" : "+v"(sum), "+v"(sumw));
+  // Some lane has a masked logit (0 * -inf in w) or a far reference:
+  // the wave's step once more with neither, from a second read, so that steps
+  // without them are spared the instructions and x need not outlive its sums.
+  if (__ballot((ENT && sumw != sumw) || beyond(R)) != 0) {
+    // (in the same order, so that l does not depend on whether H is wanted)
+    s[0] = s[1] = w[0] = w[1] = 0.0f;
+#pragma unroll 1
+    for (int u = 0; u < FU; ++u) {
+      float y[Ty::VE];
+      again(u, y);
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const float d = x[i] - ref;
-        w[i & 1] = fmaf(exp2_hw(c * d), fmaxf(d, FAR), w[i & 1]);
+      for (int j = 0; j < Ty::VE; ++j) {
+        const float z = beyond(R) ? c * (y[j] - a.m) : fmaf(y[j], c, -R);
+        const float e = exp2_hw(z);
+        s[j & 1] += e;
+        w[j & 1] = fmaf(e, fmaxf(z, LOWEST), w[j & 1]);
       }
     }
+    sum = s[0] + s[1];
+    sumw = w[0] + w[1];
   }
-  a.s += s[0] + s[1];
-  a.w += w[0] + w[1];
+  a.s += sum;
+  a.w += sumw;
   if constexpr (TOP) {
     float v = fmaxf(bm, dpp<PAIR>(bm));
     if constexpr (Blocks<Ty>::RUN == 4) v = fmaxf(v, dpp<QUAD>(v));
@@ -248,21 +280,24 @@ __global__ __launch_bounds__(256) void vocab_stats_kernel(const typename Ty::E* 
     for (int u = 0; u < FU; ++u) v[u] = load16(row + base + (u * 256 + tid) * VE);
 #pragma unroll
     for (int u = 0; u < FU; ++u) Ty::unpack(v[u], x + u * VE);
-    fwd_step<Ty, ENT, TOP>(x, c, a, block);
+    fwd_step<Ty, ENT, TOP>(x, c, a, block, [&](int u, float* y) {
+      Ty::unpack(load16(row + base + (u * 256 + tid) * VE), y);
+    });
     if constexpr (TOP) block += B::PER_TILE;
   }
   if (base < hi) {
-#pragma unroll
-    for (int u = 0; u < FU; ++u) {
+    const auto vec = [&](int u, float* y) {
       const int i0 = base + (u * 256 + tid) * VE;
       if (i0 + VE <= hi) {
-        Ty::unpack(load16(row + i0), x + u * VE);
+        Ty::unpack(load16(row + i0), y);
       } else {
 #pragma unroll
-        for (int j = 0; j < VE; ++j) x[u * VE + j] = i0 + j < hi ? Ty::get(row[i0 + j]) : -INFINITY;
+        for (int j = 0; j < VE; ++j) y[j] = i0 + j < hi ? Ty::get(row[i0 + j]) : -INFINITY;
       }
-    }
-    fwd_step<Ty, ENT, TOP>(x, c, a, block);
+    };
+#pragma unroll
+    for (int u = 0; u < FU; ++u) vec(u, x + u * VE);
+    fwd_step<Ty, ENT, TOP>(x, c, a, block, vec);
   }
   a = wave_join(a, c);
   if ((tid & 63) == 0) {
@@ -280,7 +315,7 @@ __global__ __launch_bounds__(256) void vocab_stats_kernel(const typename Ty::E* 
 // a row's triple from its slices, in every lane of the wave
 __device__ __forceinline__ Triple row_triple(const float4* part, int S, float c) {
   Triple a{-INFINITY, 0.0f, 0.0f};
-  for (int i = threadIdx.x; i < S; i += 64) {
+  for (int i = threadIdx.x & 63; i < S; i += 64) {
     const float4 p = part[i];
     a = join(a, Triple{p.x, p.y, p.z}, c);
   }
@@ -409,49 +444,58 @@ struct FinishArgs {
   float c, invtau;
 };
 
-// Joins a row's slices; its outputs.  One wave per row.
+// Joins a row's slices; its outputs.  W waves per row.
 //
-// Top alternatives, the usual case: each lane holds up to HELD vectors of
+// Top alternatives, the usual case: each thread holds up to HELD vectors of
 // block maxima; a number t that k of 128, 256 or 512 disjoint groups of them
 // reach (4 groups and more for each alternative) leaves few more than k blocks
 // and elements, and the place of each of those is the number of candidates
 // above it.  Rows where ties or masks leave too many, or with more blocks than
 // the registers hold, go through select_row.
 constexpr int MAXBLK = 256, MAXCAND = 512;
-template <class Ty, bool TOP>
-__global__ __launch_bounds__(64) void logprobs_finish_kernel(FinishArgs f, LogprobPtrs q,
-                                                             const float4* __restrict__ part,
-                                                             const typename Blocks<Ty>::Key* __restrict__ blocks) {
+
+template <int W>
+__device__ __forceinline__ void row_sync() {
+  if constexpr (W == 1) wave_lds();
+  else __syncthreads();
+}
+
+template <class Ty, bool TOP, int W>
+__global__ __launch_bounds__(64 * W, W == 1 ? 6 : 4) void logprobs_finish_kernel(FinishArgs f, LogprobPtrs q,
+                                                                 const float4* __restrict__ part,
+                                                                 const typename Blocks<Ty>::Key* __restrict__ blocks) {
   typedef typename Ty::E E;
   typedef Blocks<Ty> B;
-  constexpr int VE = Ty::VE, HELD = TOP ? (sizeof(E) == 2 ? 8 : 16) : 0, KV = 16 / sizeof(typename B::Key);
-  const int t = blockIdx.x, lane = threadIdx.x;
+  constexpr int VE = Ty::VE, NT = 64 * W, KV = 16 / sizeof(typename B::Key);
+  constexpr int HELD = TOP ? 4096 / KV / NT : 0;  // 4096 blocks: 262144 columns
+  const int t = blockIdx.x, tid = threadIdx.x, lane = tid & 63;
   const E* row = static_cast<const E*>(q.logits) + (size_t)t * f.ld;
   u32x4 held[HELD + 1];
   const int nvec = TOP ? f.nb / KV : 0;
   if constexpr (TOP) {
     const u32x4* bv = reinterpret_cast<const u32x4*>(blocks + (size_t)t * f.nb);
 #pragma unroll
-    for (int i = 0; i < HELD; ++i) held[i] = i * 64 + lane < nvec ? bv[i * 64 + lane] : u32x4{0, 0, 0, 0};
+    for (int i = 0; i < HELD; ++i) held[i] = i * NT + tid < nvec ? bv[i * NT + tid] : u32x4{0, 0, 0, 0};
   }
   const int lab = q.logp ? q.labels[t] : -1;
   const bool known = lab >= 0 && lab < f.V;
   const float given = known ? Ty::get(row[lab]) : 0.0f;
   const Triple a = row_triple(part + (size_t)t * f.S, f.S, f.c);
   const bool empty = a.s == 0.0f;
-  const float l = __logf(a.s);  // ln 0 = -inf for an empty row
-  if (lane == 0) {
+  const float l = log_sum(a, f.c);
+  if (tid == 0) {
     *reinterpret_cast<float2*>(q.stats + 2 * (size_t)t) = make_float2(a.m, l);
-    if (q.entropy) q.entropy[t] = empty ? 0.0f : l - a.w * f.invtau / a.s;
+    if (q.entropy) q.entropy[t] = entropy_of(a);
     if (q.logp)
       q.logp[t] = lab == -1 ? 0.0f : !known ? NAN : empty ? -INFINITY : (given - a.m) * f.invtau - l;
   }
   if constexpr (TOP) {
     __shared__ __align__(16) unsigned long long list[QCAP];
     __shared__ int cand[MAXBLK];
+    __shared__ uint32_t group[W == 1 ? 1 : 512];
     __shared__ int count[2];
-    if (lane < 2) count[lane] = 0;
-    // the best of each of eight groups per lane
+    if (tid < 2) count[tid] = 0;
+    // the best of each of eight groups per thread
     uint32_t g[8];
     if constexpr (KV == 8) {
       typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
@@ -479,29 +523,41 @@ __global__ __launch_bounds__(64) void logprobs_finish_kernel(FinishArgs f, Logpr
         }
       }
     }
+    if constexpr (W > 1) {
+      // two groups per thread (joined for k <= 64), eight or four per lane of
+      // the wave that counts; every wave counts, to the same number
+      static_assert(W == 4, "512 groups of 256 threads");
+#pragma unroll
+      for (int j = 0; j < 4; ++j) g[j] = max(g[j], g[4 + j]);
+      g[0] = max(g[0], g[2]);
+      g[1] = max(g[1], g[3]);
+      group[tid] = f.k > 64 ? g[0] : max(g[0], g[1]);
+      group[NT + tid] = g[1];
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < 8; ++j) g[j] = group[64 * j + lane];
+    } else if (f.k <= 64) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) g[j] = max(g[j], g[4 + j]);
+    }
     uint32_t floor;
     if (f.k > 64) {
       floor = kth<8, B::BITS>(g, f.k);
+    } else if (f.k > 24) {
+      floor = kth<4, B::BITS>(g, f.k);
     } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) g[j] = max(g[j], g[4 + j]);
-      if (f.k > 24) {
-        floor = kth<4, B::BITS>(g, f.k);
-      } else {
-        g[0] = max(g[0], g[2]);
-        g[1] = max(g[1], g[3]);
-        floor = kth<2, B::BITS>(g, f.k);
-      }
+      g[0] = max(g[0], g[2]);
+      g[1] = max(g[1], g[3]);
+      floor = kth<2, B::BITS>(g, f.k);
     }
-    wave_lds();
-    bool usual = nvec <= HELD * 64;
     floor = max(floor, 1u);  // (fewer than k groups: every block is above 0)
+    row_sync<W>();
 #pragma unroll
     for (int i = 0; i < HELD; ++i) {
 #pragma unroll
       for (int d = 0; d < 4; ++d) {
         const uint32_t w = held[i][d];
-        const int b = (i * 64 + lane) * KV + d * (KV / 4);
+        const int b = (i * NT + tid) * KV + d * (KV / 4);
         const uint32_t k0 = KV == 8 ? w & 0xFFFFu : w, k1 = KV == 8 ? w >> 16 : 0u;
         if (max(k0, k1) >= floor) {
           if (k0 >= floor) {
@@ -515,47 +571,53 @@ __global__ __launch_bounds__(64) void logprobs_finish_kernel(FinishArgs f, Logpr
         }
       }
     }
-    wave_lds();
+    row_sync<W>();
     const int n1 = count[0];
-    usual = usual && n1 <= MAXBLK;
+    bool usual = nvec <= HELD * NT && n1 <= MAXBLK;
     int n = 0;
     if (usual) {
       constexpr int U = 4;
-      for (int i = lane; i - lane < n1 * B::VECS; i += 64 * U) {
+      // key(x) >= floor as a comparison of numbers; false for NaN, which a row
+      // of few others leaves to select_row
+      const uint32_t o = floor << (32 - B::BITS);
+      const float least = o <= 0x007FFFFFu ? -INFINITY : unordered(o);
+      for (int i = tid; i - lane < n1 * B::VECS; i += NT * U) {
         float x[U][VE];
         int col[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          const int at = i + 64 * u;
+          const int at = i + NT * u;
           col[u] = at < n1 * B::VECS ? B::column(cand[at / B::VECS], at % B::VECS) : f.V;
           if (col[u] + VE <= f.V) {
             Ty::unpack(load16(row + col[u]), x[u]);
           } else {
 #pragma unroll
-            for (int j = 0; j < VE; ++j) x[u][j] = col[u] + j < f.V ? Ty::get(row[col[u] + j]) : 0.0f;
+            for (int j = 0; j < VE; ++j) x[u][j] = col[u] + j < f.V ? Ty::get(row[col[u] + j]) : NAN;
           }
         }
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
           for (int j = 0; j < VE; ++j)
-            if (B::key(x[u][j]) >= floor && col[u] + j < f.V) {
+            if (x[u][j] >= least) {
               const int at = atomicAdd(&count[1], 1);
               if (at < MAXCAND) list[at] = candidate(ordered(x[u][j]), col[u] + j);
             }
       }
-      wave_lds();
+      row_sync<W>();
       n = count[1];
       usual = n <= MAXCAND && n >= f.k;
     }
     if (!usual) {
-      select_row<Ty>(row, f.V, f.k, floor << (32 - B::BITS), list);
+      row_sync<W>();
+      if (tid < 64) select_row<Ty>(row, f.V, f.k, floor << (32 - B::BITS), list);
       n = f.k;
+      row_sync<W>();
     }
     // an even number of candidates for the paired reads: 0 is below each
-    if (lane == 0 && (n & 1)) list[n] = 0ull;
-    wave_lds();
-    for (int i = lane; i < n; i += 64) {
+    if (tid == 0 && (n & 1)) list[n] = 0ull;
+    row_sync<W>();
+    for (int i = tid; i < n; i += NT) {
       const unsigned long long mine = list[i];
       int place = 0;
       for (int j = 0; j < n; j += 2) {
@@ -632,7 +694,7 @@ __global__ __launch_bounds__(64) void distill_finish_kernel(FinishArgs f, const 
 #pragma unroll
   for (int i = 0; i < TI; ++i) x[i] = te.ix[i] >= 0 ? Ty::get(row[te.ix[i]]) : 0.0f;
   const Triple a = row_triple(part + (size_t)t * f.S, f.S, f.c);
-  const float l = __logf(a.s);
+  const float l = log_sum(a, f.c);
   float sum = 0.0f;
 #pragma unroll
   for (int i = 0; i < TI; ++i)
@@ -850,6 +912,8 @@ Split split(int T, int V, int tile) {
 Split fwd_split(const VocabDims& d) { return split(d.T, d.V, d.f32 ? fwd_tile<F32>() : fwd_tile<Bf16>()); }
 Split bwd_split(const VocabDims& d) { return split(d.T, d.V, d.f32 ? bwd_tile<F32>() : bwd_tile<Bf16>()); }
 
+constexpr int FEW_ROWS = 1024;
+
 template <class Ty>
 int blocks_of(int V) {
   return (V + fwd_tile<Ty>() - 1) / fwd_tile<Ty>() * Blocks<Ty>::PER_TILE;
@@ -883,11 +947,15 @@ void logprobs_launch(const VocabDims& d, const LogprobPtrs& q, char* ws, hipStre
   if (d.k > 0) {
     if (q.entropy) stats_launch<Ty, true, true>(d, s, q.logits, ws, st);
     else stats_launch<Ty, false, true>(d, s, q.logits, ws, st);
-    hipLaunchKernelGGL((logprobs_finish_kernel<Ty, true>), dim3(d.T), dim3(64), 0, st, f, q, part, blocks);
+    // few rows: four waves each, for the latency of one (FEW_ROWS)
+    if (d.T <= FEW_ROWS)
+      hipLaunchKernelGGL((logprobs_finish_kernel<Ty, true, 4>), dim3(d.T), dim3(256), 0, st, f, q, part, blocks);
+    else
+      hipLaunchKernelGGL((logprobs_finish_kernel<Ty, true, 1>), dim3(d.T), dim3(64), 0, st, f, q, part, blocks);
   } else {
     if (q.entropy) stats_launch<Ty, true, false>(d, s, q.logits, ws, st);
     else stats_launch<Ty, false, false>(d, s, q.logits, ws, st);
-    hipLaunchKernelGGL((logprobs_finish_kernel<Ty, false>), dim3(d.T), dim3(64), 0, st, f, q, part, blocks);
+    hipLaunchKernelGGL((logprobs_finish_kernel<Ty, false, 1>), dim3(d.T), dim3(64), 0, st, f, q, part, blocks);
   }
 }
 
