@@ -26,6 +26,7 @@
 // outside a row is touched.
 #include <math.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "oft_device.h"
@@ -90,6 +91,12 @@ template <class E>
 __device__ __forceinline__ u32x4 load16(const E* p) {
   return *reinterpret_cast<const u32x4_row*>(p);
 }
+// a vector that is read once: it need not displace what the caches hold
+// (4096 x 151936 bf16 rows summed in 180 instead of 203 us)
+template <class E>
+__device__ __forceinline__ u32x4 stream16(const E* p) {
+  return __builtin_nontemporal_load(reinterpret_cast<const u32x4_row*>(p));
+}
 template <class E>
 __device__ __forceinline__ void store16(E* p, const u32x4& v) {
   *reinterpret_cast<u32x4_row*>(p) = v;
@@ -118,6 +125,13 @@ __device__ __forceinline__ float wave_max(float v) {
   v = fmaxf(v, dpp<EIGHT>(v));
   v = fmaxf(v, dpp<ROW>(v));
   return fmaxf(fmaxf(lane_value(v, 0), lane_value(v, 16)), fmaxf(lane_value(v, 32), lane_value(v, 48)));
+}
+
+// LDS of one wave, written and read by its lanes
+__device__ __forceinline__ void wave_lds() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
 // ------------------------------------------------------------------ triples
@@ -183,29 +197,83 @@ __device__ __forceinline__ float unordered(uint32_t o) {
 }
 
 // Block maxima of a row, as `ordered` numbers: the upper half of it says all
-// for bf16.  A block is 64 columns of one step of the forward pass: the 16
+// for bf16.  A block is 64 columns of one step of the forward pass: the 64 / FU
 // columns of each of its FU vectors that RUN neighbouring lanes hold.
 template <class Ty>
 struct Blocks {
   typedef std::conditional_t<sizeof(typename Ty::E) == 2, uint16_t, uint32_t> Key;
   static constexpr int BITS = 8 * sizeof(Key);
-  static constexpr int RUN = 16 / Ty::VE;                 // lanes
+  static constexpr int RUN = 64 / FU / Ty::VE;            // lanes
   static constexpr int PER_TILE = 256 / RUN;              // blocks of a step
   static constexpr int VECS = FU * RUN;                   // 16-byte vectors of a block
   static constexpr int TILE = fwd_tile<Ty>();
   static __device__ __forceinline__ uint32_t key(float v) { return ordered(v) >> (32 - BITS); }
   // first column of vector i of block b
   static __device__ __forceinline__ int column(int b, int i) {
-    return b / PER_TILE * TILE + i / RUN * (256 * Ty::VE) + b % PER_TILE * 16 + i % RUN * Ty::VE;
+    return b / PER_TILE * TILE + i / RUN * (256 * Ty::VE) + b % PER_TILE * (64 / FU) + i % RUN * Ty::VE;
+  }
+};
+
+// a block's maximum, from its lanes' own maxima
+template <class Ty>
+__device__ __forceinline__ typename Blocks<Ty>::Key block_key(float v) {
+  if constexpr (Blocks<Ty>::RUN >= 2) v = fmaxf(v, dpp<PAIR>(v));
+  if constexpr (Blocks<Ty>::RUN == 4) v = fmaxf(v, dpp<QUAD>(v));
+  return (typename Blocks<Ty>::Key)Blocks<Ty>::key(v);
+}
+
+// What becomes of the block maxima of a workgroup's steps.
+// Nothing:
+struct KeepNone {
+  __device__ __forceinline__ void add(float) {}
+  __device__ __forceinline__ void flush() {}
+};
+// they stay in LDS, the whole row's:
+template <class Ty>
+struct KeepRow {
+  typedef typename Blocks<Ty>::Key Key;
+  Key* lds;  // the next step's PER_TILE keys
+  __device__ __forceinline__ void add(float v) {
+    const Key k = block_key<Ty>(v);
+    if (threadIdx.x % Blocks<Ty>::RUN == 0) lds[threadIdx.x / Blocks<Ty>::RUN] = k;
+    lds += Blocks<Ty>::PER_TILE;
+  }
+  __device__ __forceinline__ void flush() {}
+};
+// or they go to memory: a wave's keys of KEPT steps, 64 bytes each, wait in
+// LDS and leave as one 16-byte store per lane
+constexpr int KEPT = 16;
+template <class Ty>
+struct KeepOut {
+  typedef typename Blocks<Ty>::Key Key;
+  static constexpr int PW = 64 / Blocks<Ty>::RUN, PV = 16 / sizeof(Key);  // keys of a wave's step, of a vector
+  static_assert(PW == 4 * PV, "four vectors a step");
+  Key* lds;  // this wave's [KEPT][PW]
+  Key* out;  // this wave's first key of the first step kept
+  int n;     // steps kept
+
+  __device__ __forceinline__ void add(float v) {
+    const Key k = block_key<Ty>(v);
+    const int lane = threadIdx.x & 63;
+    if (lane % Blocks<Ty>::RUN == 0) lds[n * PW + lane / Blocks<Ty>::RUN] = k;
+    if (++n == KEPT) flush();
+  }
+  __device__ __forceinline__ void flush() {
+    wave_lds();
+    const int step = (threadIdx.x & 63) / 4, part = threadIdx.x % 4;
+    if (step < n)
+      *reinterpret_cast<u32x4*>(out + step * Blocks<Ty>::PER_TILE + part * PV) =
+          *reinterpret_cast<const u32x4*>(lds + step * PW + part * PV);
+    wave_lds();
+    out += n * Blocks<Ty>::PER_TILE;
+    n = 0;
   }
 };
 
 // one step: FU vectors per thread, x[u VE + j] is column base + (u 256 + tid)
-// VE + j; again(u, y) reads vector u once more; block: where the thread's
-// block maximum goes (its first lane stores)
-template <class Ty, bool ENT, bool TOP, class F>
-__device__ __forceinline__ void fwd_step(const float (&x)[FU * Ty::VE], float c, Triple& a,
-                                         typename Blocks<Ty>::Key* block, F again) {
+// VE + j; again(u, y) reads vector u once more.  Returns the thread's maximum.
+template <class Ty, bool ENT, class F>
+__device__ __forceinline__ float fwd_step(const float (&x)[FU * Ty::VE], float c, Triple& a, F again) {
   constexpr int N = FU * Ty::VE;
   float m0 = x[0], m1 = x[1];
 #pragma unroll
@@ -250,11 +318,77 @@ __device__ __forceinline__ void fwd_step(const float (&x)[FU * Ty::VE], float c,
   }
   a.s += sum;
   a.w += sumw;
-  if constexpr (TOP) {
-    float v = fmaxf(bm, dpp<PAIR>(bm));
-    if constexpr (Blocks<Ty>::RUN == 4) v = fmaxf(v, dpp<QUAD>(v));
-    if (threadIdx.x % Blocks<Ty>::RUN == 0) *block = (typename Blocks<Ty>::Key)Blocks<Ty>::key(v);
+  return bm;
+}
+
+// one vector, with masked logits and any reference: a row's last, partial step
+template <class Ty, bool ENT>
+__device__ __forceinline__ float fwd_vector(const float* x, float c, Triple& a) {
+  float bm = x[0];
+#pragma unroll
+  for (int j = 1; j < Ty::VE; ++j) bm = fmaxf(bm, x[j]);
+  a = moved(a, fmaxf(a.m, bm), c);
+  const float R = reference(a.m, c);
+  const bool far = beyond(R);
+#pragma unroll
+  for (int j = 0; j < Ty::VE; ++j) {
+    const float z = far ? c * (x[j] - a.m) : fmaf(x[j], c, -R);
+    const float e = exp2_hw(z);
+    a.s += e;
+    if constexpr (ENT) a.w = fmaf(e, fmaxf(z, LOWEST), a.w);
   }
+  return bm;
+}
+
+// The triple of columns [lo, hi) of a row by a workgroup, the same in every
+// thread; lo starts a step.
+template <class Ty, bool ENT, class K>
+__device__ __forceinline__ Triple slice_triple(const typename Ty::E* row, int lo, int hi, float c, K& keep) {
+  constexpr int VE = Ty::VE, TILE = fwd_tile<Ty>();
+  __shared__ float sh[4][3];
+  const int tid = threadIdx.x;
+  Triple a{-INFINITY, 0.0f, 0.0f};
+  float x[FU * VE];
+  int base = lo;
+  for (; base + TILE <= hi; base += TILE) {
+    u32x4 v[FU];
+#pragma unroll
+    for (int u = 0; u < FU; ++u) v[u] = stream16(row + base + (u * 256 + tid) * VE);
+#pragma unroll
+    for (int u = 0; u < FU; ++u) Ty::unpack(v[u], x + u * VE);
+    keep.add(fwd_step<Ty, ENT>(x, c, a, [&](int u, float* y) {
+      Ty::unpack(load16(row + base + (u * 256 + tid) * VE), y);
+    }));
+  }
+  if (base < hi) {
+#pragma unroll
+    for (int u = 0; u < FU; ++u) {
+      const int i0 = base + (u * 256 + tid) * VE;
+      if (i0 + VE <= hi) {
+        Ty::unpack(stream16(row + i0), x + u * VE);
+      } else {
+#pragma unroll
+        for (int j = 0; j < VE; ++j) x[u * VE + j] = i0 + j < hi ? Ty::get(row[i0 + j]) : -INFINITY;
+      }
+    }
+    float bm = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < FU; ++u)
+      if (base + (u * 256 + (tid & ~63)) * VE < hi) bm = fmaxf(bm, fwd_vector<Ty, ENT>(x + u * VE, c, a));
+    keep.add(bm);
+  }
+  keep.flush();
+  a = wave_join(a, c);
+  if ((tid & 63) == 0) {
+    sh[tid >> 6][0] = a.m;
+    sh[tid >> 6][1] = a.s;
+    sh[tid >> 6][2] = a.w;
+  }
+  __syncthreads();
+  a = Triple{sh[0][0], sh[0][1], sh[0][2]};
+#pragma unroll
+  for (int i = 1; i < 4; ++i) a = join(a, Triple{sh[i][0], sh[i][1], sh[i][2]}, c);
+  return a;
 }
 
 // part[t S + sl]: the triple of columns [sl slice, (sl + 1) slice) of row t;
@@ -263,53 +397,21 @@ template <class Ty, bool ENT, bool TOP>
 __global__ __launch_bounds__(256) void vocab_stats_kernel(const typename Ty::E* __restrict__ logits, long ld, int V,
                                                           int S, int slice, float c, float4* __restrict__ part,
                                                           typename Blocks<Ty>::Key* __restrict__ blocks, int nb) {
-  typedef typename Ty::E E;
   typedef Blocks<Ty> B;
-  constexpr int VE = Ty::VE, TILE = fwd_tile<Ty>();
-  __shared__ float sh[4][3];
+  typedef typename B::Key Key;
   const int t = blockIdx.x / S, sl = blockIdx.x % S, tid = threadIdx.x;
-  const E* row = logits + (size_t)t * ld;
   const int lo = sl * slice, hi = min(V, lo + slice);
-  typename B::Key* block = TOP ? blocks + (size_t)t * nb + lo / TILE * B::PER_TILE + tid / B::RUN : nullptr;
-  Triple a{-INFINITY, 0.0f, 0.0f};
-  float x[FU * VE];
-  int base = lo;
-  for (; base + TILE <= hi; base += TILE) {
-    u32x4 v[FU];
-#pragma unroll
-    for (int u = 0; u < FU; ++u) v[u] = load16(row + base + (u * 256 + tid) * VE);
-#pragma unroll
-    for (int u = 0; u < FU; ++u) Ty::unpack(v[u], x + u * VE);
-    fwd_step<Ty, ENT, TOP>(x, c, a, block, [&](int u, float* y) {
-      Ty::unpack(load16(row + base + (u * 256 + tid) * VE), y);
-    });
-    if constexpr (TOP) block += B::PER_TILE;
+  Triple a;
+  if constexpr (TOP) {
+    __shared__ __align__(16) Key kept[4][KEPT * KeepOut<Ty>::PW];
+    KeepOut<Ty> keep{kept[tid >> 6],
+                     blocks + (size_t)t * nb + lo / fwd_tile<Ty>() * B::PER_TILE + (tid & ~63) / B::RUN, 0};
+    a = slice_triple<Ty, ENT>(logits + (size_t)t * ld, lo, hi, c, keep);
+  } else {
+    KeepNone keep;
+    a = slice_triple<Ty, ENT>(logits + (size_t)t * ld, lo, hi, c, keep);
   }
-  if (base < hi) {
-    const auto vec = [&](int u, float* y) {
-      const int i0 = base + (u * 256 + tid) * VE;
-      if (i0 + VE <= hi) {
-        Ty::unpack(load16(row + i0), y);
-      } else {
-#pragma unroll
-        for (int j = 0; j < VE; ++j) y[j] = i0 + j < hi ? Ty::get(row[i0 + j]) : -INFINITY;
-      }
-    };
-#pragma unroll
-    for (int u = 0; u < FU; ++u) vec(u, x + u * VE);
-    fwd_step<Ty, ENT, TOP>(x, c, a, block, vec);
-  }
-  a = wave_join(a, c);
-  if ((tid & 63) == 0) {
-    sh[tid >> 6][0] = a.m;
-    sh[tid >> 6][1] = a.s;
-    sh[tid >> 6][2] = a.w;
-  }
-  __syncthreads();
-  if (tid == 0) {
-    for (int i = 1; i < 4; ++i) a = join(a, Triple{sh[i][0], sh[i][1], sh[i][2]}, c);
-    part[blockIdx.x] = make_float4(a.m, a.s, a.w, 0.0f);
-  }
+  if (tid == 0) part[blockIdx.x] = make_float4(a.m, a.s, a.w, 0.0f);
 }
 
 // a row's triple from its slices, in every lane of the wave
@@ -343,13 +445,6 @@ __device__ __forceinline__ uint32_t kth(const uint32_t* o, int k) {
     r = n3 >= k ? t3 : n2 >= k ? t2 : n1 >= k ? t1 : r;
   }
   return r;
-}
-
-// LDS of one wave, written and read by its lanes
-__device__ __forceinline__ void wave_lds() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
 // A candidate as one number: value first, then the lower column; no two of a
@@ -453,6 +548,7 @@ struct FinishArgs {
 // above it.  Rows where ties or masks leave too many, or with more blocks than
 // the registers hold, go through select_row.
 constexpr int MAXBLK = 256, MAXCAND = 512;
+constexpr int MAXKEYS = 4096;  // 262144 columns
 
 template <int W>
 __device__ __forceinline__ void row_sync() {
@@ -460,41 +556,38 @@ __device__ __forceinline__ void row_sync() {
   else __syncthreads();
 }
 
+// keys: the block maxima of the row, in LDS or memory; list: [QCAP] in LDS,
+// which may be where the keys are
 template <class Ty, bool TOP, int W>
-__global__ __launch_bounds__(64 * W, W == 1 ? 6 : 4) void logprobs_finish_kernel(FinishArgs f, LogprobPtrs q,
-                                                                 const float4* __restrict__ part,
-                                                                 const typename Blocks<Ty>::Key* __restrict__ blocks) {
+__device__ __forceinline__ void logprobs_finish(const FinishArgs& f, const LogprobPtrs& q, int t, const Triple& a,
+                                                const u32x4* keys, unsigned long long* list) {
   typedef typename Ty::E E;
   typedef Blocks<Ty> B;
   constexpr int VE = Ty::VE, NT = 64 * W, KV = 16 / sizeof(typename B::Key);
-  constexpr int HELD = TOP ? 4096 / KV / NT : 0;  // 4096 blocks: 262144 columns
-  const int t = blockIdx.x, tid = threadIdx.x, lane = tid & 63;
+  constexpr int HELD = TOP ? MAXKEYS / KV / NT : 0;
+  const int tid = threadIdx.x, lane = tid & 63;
   const E* row = static_cast<const E*>(q.logits) + (size_t)t * f.ld;
-  u32x4 held[HELD + 1];
-  const int nvec = TOP ? f.nb / KV : 0;
-  if constexpr (TOP) {
-    const u32x4* bv = reinterpret_cast<const u32x4*>(blocks + (size_t)t * f.nb);
-#pragma unroll
-    for (int i = 0; i < HELD; ++i) held[i] = i * NT + tid < nvec ? bv[i * NT + tid] : u32x4{0, 0, 0, 0};
-  }
-  const int lab = q.logp ? q.labels[t] : -1;
-  const bool known = lab >= 0 && lab < f.V;
-  const float given = known ? Ty::get(row[lab]) : 0.0f;
-  const Triple a = row_triple(part + (size_t)t * f.S, f.S, f.c);
   const bool empty = a.s == 0.0f;
   const float l = log_sum(a, f.c);
   if (tid == 0) {
     *reinterpret_cast<float2*>(q.stats + 2 * (size_t)t) = make_float2(a.m, l);
     if (q.entropy) q.entropy[t] = entropy_of(a);
-    if (q.logp)
-      q.logp[t] = lab == -1 ? 0.0f : !known ? NAN : empty ? -INFINITY : (given - a.m) * f.invtau - l;
+    if (q.logp) {
+      const int lab = q.labels[t];
+      float lp = lab == -1 ? 0.0f : NAN;
+      if (lab >= 0 && lab < f.V) lp = empty ? -INFINITY : (Ty::get(row[lab]) - a.m) * f.invtau - l;
+      q.logp[t] = lp;
+    }
   }
   if constexpr (TOP) {
-    __shared__ __align__(16) unsigned long long list[QCAP];
     __shared__ int cand[MAXBLK];
     __shared__ uint32_t group[W == 1 ? 1 : 512];
     __shared__ int count[2];
     if (tid < 2) count[tid] = 0;
+    u32x4 held[HELD];
+    const int nvec = f.nb / KV;
+#pragma unroll
+    for (int i = 0; i < HELD; ++i) held[i] = i * NT + tid < nvec ? keys[i * NT + tid] : u32x4{0, 0, 0, 0};
     // the best of each of eight groups per thread
     uint32_t g[8];
     if constexpr (KV == 8) {
@@ -634,6 +727,42 @@ __global__ __launch_bounds__(64 * W, W == 1 ? 6 : 4) void logprobs_finish_kernel
   }
 }
 
+template <class Ty, bool TOP, int W>
+__global__ __launch_bounds__(64 * W, W == 1 ? 6 : 4) void logprobs_finish_kernel(
+    FinishArgs f, LogprobPtrs q, const float4* __restrict__ part,
+    const typename Blocks<Ty>::Key* __restrict__ blocks) {
+  const int t = blockIdx.x;
+  const Triple a = row_triple(part + (size_t)t * f.S, f.S, f.c);
+  if constexpr (TOP) {
+    __shared__ __align__(16) unsigned long long list[QCAP];
+    logprobs_finish<Ty, true, W>(f, q, t, a, reinterpret_cast<const u32x4*>(blocks + (size_t)t * f.nb), list);
+  } else {
+    logprobs_finish<Ty, false, W>(f, q, t, a, nullptr, nullptr);
+  }
+}
+
+// A whole row by one workgroup, for rows enough to fill the chip: no triples
+// and no block maxima through memory (writing 20 MB of them beside a read of
+// 1.2 GB took 25 us).
+template <class Ty, bool ENT, bool TOP>
+__global__ __launch_bounds__(256, 6) void logprobs_row_kernel(FinishArgs f, LogprobPtrs q) {
+  typedef typename Blocks<Ty>::Key Key;
+  const int t = blockIdx.x;
+  const typename Ty::E* row = static_cast<const typename Ty::E*>(q.logits) + (size_t)t * f.ld;
+  if constexpr (TOP) {
+    __shared__ __align__(16) Key kept[MAXKEYS];
+    static_assert(sizeof(kept) >= QCAP * 8, "the list of candidates takes the keys' place");
+    KeepRow<Ty> keep{kept};
+    const Triple a = slice_triple<Ty, ENT>(row, 0, f.V, f.c, keep);
+    logprobs_finish<Ty, true, 4>(f, q, t, a, reinterpret_cast<const u32x4*>(kept),
+                                 reinterpret_cast<unsigned long long*>(kept));
+  } else {
+    KeepNone keep;
+    const Triple a = slice_triple<Ty, ENT>(row, 0, f.V, f.c, keep);
+    logprobs_finish<Ty, false, 4>(f, q, t, a, nullptr, nullptr);
+  }
+}
+
 // ------------------------------------------------------------------ teacher
 // A row's teacher list over one wave: entry lane + 64 i in register i.
 // ix -1: an entry without weight.  bad: an entry is out of range, NaN or
@@ -680,20 +809,18 @@ struct Teacher {
   }
 };
 
-// one wave per row
+struct DistillPtrs {
+  const void* logits;
+  const int* idx;
+  const float* teacher;
+  float* loss;
+  float* stats;
+};
+
+// by one wave
 template <class Ty>
-__global__ __launch_bounds__(64) void distill_finish_kernel(FinishArgs f, const typename Ty::E* __restrict__ logits,
-                                                            const int* __restrict__ idx,
-                                                            const float* __restrict__ teacher,
-                                                            const float4* __restrict__ part, float* __restrict__ loss,
-                                                            float* __restrict__ stats) {
-  const int t = blockIdx.x;
-  const typename Ty::E* row = logits + (size_t)t * f.ld;
-  const Teacher te(idx + (size_t)t * f.k, teacher + (size_t)t * f.k, f.k, f.V, f.invtau);
-  float x[TI];
-#pragma unroll
-  for (int i = 0; i < TI; ++i) x[i] = te.ix[i] >= 0 ? Ty::get(row[te.ix[i]]) : 0.0f;
-  const Triple a = row_triple(part + (size_t)t * f.S, f.S, f.c);
+__device__ __forceinline__ void distill_finish(const FinishArgs& f, const DistillPtrs& q, int t, const Teacher& te,
+                                               const float (&x)[TI], const Triple& a) {
   const float l = log_sum(a, f.c);
   float sum = 0.0f;
 #pragma unroll
@@ -704,9 +831,39 @@ __global__ __launch_bounds__(64) void distill_finish_kernel(FinishArgs f, const 
     }
   sum = wave_sum(sum);
   if (threadIdx.x == 0) {
-    loss[t] = te.bad ? NAN : sum;
-    *reinterpret_cast<float2*>(stats + 2 * (size_t)t) = make_float2(a.m, l);
+    q.loss[t] = te.bad ? NAN : sum;
+    *reinterpret_cast<float2*>(q.stats + 2 * (size_t)t) = make_float2(a.m, l);
   }
+}
+
+template <class Ty>
+__device__ __forceinline__ Teacher teacher_row(const FinishArgs& f, const DistillPtrs& q, int t, float (&x)[TI]) {
+  const typename Ty::E* row = static_cast<const typename Ty::E*>(q.logits) + (size_t)t * f.ld;
+  const Teacher te(q.idx + (size_t)t * f.k, q.teacher + (size_t)t * f.k, f.k, f.V, f.invtau);
+#pragma unroll
+  for (int i = 0; i < TI; ++i) x[i] = te.ix[i] >= 0 ? Ty::get(row[te.ix[i]]) : 0.0f;
+  return te;
+}
+
+template <class Ty>
+__global__ __launch_bounds__(64) void distill_finish_kernel(FinishArgs f, DistillPtrs q,
+                                                            const float4* __restrict__ part) {
+  const int t = blockIdx.x;
+  float x[TI];
+  const Teacher te = teacher_row<Ty>(f, q, t, x);
+  distill_finish<Ty>(f, q, t, te, x, row_triple(part + (size_t)t * f.S, f.S, f.c));
+}
+
+template <class Ty>
+__global__ __launch_bounds__(256) void distill_row_kernel(FinishArgs f, DistillPtrs q) {
+  const int t = blockIdx.x;
+  KeepNone keep;
+  const Triple a = slice_triple<Ty, false>(static_cast<const typename Ty::E*>(q.logits) + (size_t)t * f.ld, 0, f.V, f.c,
+                                           keep);
+  if (threadIdx.x >= 64) return;
+  float x[TI];
+  const Teacher te = teacher_row<Ty>(f, q, t, x);
+  distill_finish<Ty>(f, q, t, te, x, a);
 }
 
 // ----------------------------------------------------------------- backward
@@ -897,35 +1054,49 @@ __global__ __launch_bounds__(256) void distill_bwd_kernel(BwdArgs b, const typen
 }
 
 // --------------------------------------------------------------- host side
-// Slices of a row: enough workgroups to fill the chip several times over, at
-// least a tile each.
+// Slices of a row: `want` workgroups, at least a tile each.
 struct Split {
   int S, slice;
 };
-Split split(int T, int V, int tile) {
+Split split(int T, int V, int tile, long want) {
   const long tiles = ((long)V + tile - 1) / tile;
-  const long want = (8192 + T - 1) / T;
-  const long S = want < tiles ? want : tiles;
+  const long S = std::min((want + T - 1) / T, tiles);
   const long per = (tiles + S - 1) / S;
   return Split{(int)((tiles + per - 1) / per), (int)(per * tile)};
 }
-Split fwd_split(const VocabDims& d) { return split(d.T, d.V, d.f32 ? fwd_tile<F32>() : fwd_tile<Bf16>()); }
-Split bwd_split(const VocabDims& d) { return split(d.T, d.V, d.f32 ? bwd_tile<F32>() : bwd_tile<Bf16>()); }
-
-constexpr int FEW_ROWS = 1024;
-
+#ifndef WANT
+#define WANT 4096
+#endif
+#ifndef ROWS
+#define ROWS 1024
+#endif
+constexpr int MANY_ROWS = ROWS;
 template <class Ty>
 int blocks_of(int V) {
   return (V + fwd_tile<Ty>() - 1) / fwd_tile<Ty>() * Blocks<Ty>::PER_TILE;
 }
-size_t part_bytes(const VocabDims& d) { return (size_t)d.T * fwd_split(d).S * sizeof(float4); }
+// a workgroup per row, with its block maxima in LDS where they are wanted
+template <class Ty>
+bool whole_rows(const VocabDims& d, bool top) {
+  return d.T >= MANY_ROWS && (!top || blocks_of<Ty>(d.V) <= MAXKEYS);
+}
+template <class Ty>
+Split fwd_split(const VocabDims& d) {
+  return split(d.T, d.V, fwd_tile<Ty>(), WANT);
+}
+template <class Ty>
+size_t part_bytes(const VocabDims& d) {
+  return (size_t)d.T * fwd_split<Ty>(d).S * sizeof(float4);
+}
+constexpr int FEW_ROWS = 1024;
 
 template <class Ty>
 FinishArgs finish_args(const VocabDims& d, int S) {
   return FinishArgs{d.V, d.k, S, blocks_of<Ty>(d.V), d.ld, d.invtau * LOG2E, d.invtau};
 }
+template <class Ty>
 BwdArgs bwd_args(const VocabDims& d) {
-  const Split s = bwd_split(d);
+  const Split s = split(d.T, d.V, bwd_tile<Ty>(), 8192);
   return BwdArgs{d.V, d.k, s.S, s.slice, d.ld, d.ldg, d.invtau * LOG2E, d.invtau};
 }
 
@@ -935,43 +1106,48 @@ void stats_launch(const VocabDims& d, const Split& s, const void* logits, char* 
   hipLaunchKernelGGL((vocab_stats_kernel<Ty, ENT, TOP>), dim3((size_t)d.T * s.S), dim3(256), 0, st,
                      static_cast<const E*>(logits), d.ld, d.V, s.S, s.slice, d.invtau * LOG2E,
                      reinterpret_cast<float4*>(ws),
-                     reinterpret_cast<typename Blocks<Ty>::Key*>(ws + part_bytes(d)), blocks_of<Ty>(d.V));
+                     reinterpret_cast<typename Blocks<Ty>::Key*>(ws + part_bytes<Ty>(d)), blocks_of<Ty>(d.V));
+}
+
+template <class Ty, bool ENT, bool TOP>
+void logprobs_launch(const VocabDims& d, const LogprobPtrs& q, char* ws, hipStream_t st) {
+  if (whole_rows<Ty>(d, TOP)) {
+    hipLaunchKernelGGL((logprobs_row_kernel<Ty, ENT, TOP>), dim3(d.T), dim3(256), 0, st, finish_args<Ty>(d, 1), q);
+    return;
+  }
+  const Split s = fwd_split<Ty>(d);
+  const float4* part = reinterpret_cast<const float4*>(ws);
+  const auto* blocks = reinterpret_cast<const typename Blocks<Ty>::Key*>(ws + part_bytes<Ty>(d));
+  const FinishArgs f = finish_args<Ty>(d, s.S);
+  stats_launch<Ty, ENT, TOP>(d, s, q.logits, ws, st);
+  // few rows: four waves each, for the latency of one
+  if (TOP && d.T <= FEW_ROWS)
+    hipLaunchKernelGGL((logprobs_finish_kernel<Ty, TOP, 4>), dim3(d.T), dim3(256), 0, st, f, q, part, blocks);
+  else
+    hipLaunchKernelGGL((logprobs_finish_kernel<Ty, TOP, 1>), dim3(d.T), dim3(64), 0, st, f, q, part, blocks);
 }
 
 template <class Ty>
 void logprobs_launch(const VocabDims& d, const LogprobPtrs& q, char* ws, hipStream_t st) {
-  const Split s = fwd_split(d);
-  const float4* part = reinterpret_cast<const float4*>(ws);
-  const auto* blocks = reinterpret_cast<const typename Blocks<Ty>::Key*>(ws + part_bytes(d));
-  const FinishArgs f = finish_args<Ty>(d, s.S);
-  if (d.k > 0) {
-    if (q.entropy) stats_launch<Ty, true, true>(d, s, q.logits, ws, st);
-    else stats_launch<Ty, false, true>(d, s, q.logits, ws, st);
-    // few rows: four waves each, for the latency of one (FEW_ROWS)
-    if (d.T <= FEW_ROWS)
-      hipLaunchKernelGGL((logprobs_finish_kernel<Ty, true, 4>), dim3(d.T), dim3(256), 0, st, f, q, part, blocks);
-    else
-      hipLaunchKernelGGL((logprobs_finish_kernel<Ty, true, 1>), dim3(d.T), dim3(64), 0, st, f, q, part, blocks);
-  } else {
-    if (q.entropy) stats_launch<Ty, true, false>(d, s, q.logits, ws, st);
-    else stats_launch<Ty, false, false>(d, s, q.logits, ws, st);
-    hipLaunchKernelGGL((logprobs_finish_kernel<Ty, false, 1>), dim3(d.T), dim3(64), 0, st, f, q, part, blocks);
-  }
+  if (d.k > 0) q.entropy ? logprobs_launch<Ty, true, true>(d, q, ws, st) : logprobs_launch<Ty, false, true>(d, q, ws, st);
+  else q.entropy ? logprobs_launch<Ty, true, false>(d, q, ws, st) : logprobs_launch<Ty, false, false>(d, q, ws, st);
 }
 
 template <class Ty>
-void distill_launch(const VocabDims& d, const void* logits, const int* idx, const float* teacher, float* loss,
-                    float* stats, char* ws, hipStream_t st) {
-  const Split s = fwd_split(d);
-  stats_launch<Ty, false, false>(d, s, logits, ws, st);
-  hipLaunchKernelGGL((distill_finish_kernel<Ty>), dim3(d.T), dim3(64), 0, st, finish_args<Ty>(d, s.S),
-                     static_cast<const typename Ty::E*>(logits), idx, teacher, reinterpret_cast<const float4*>(ws), loss,
-                     stats);
+void distill_launch(const VocabDims& d, const DistillPtrs& q, char* ws, hipStream_t st) {
+  if (whole_rows<Ty>(d, false)) {
+    hipLaunchKernelGGL((distill_row_kernel<Ty>), dim3(d.T), dim3(256), 0, st, finish_args<Ty>(d, 1), q);
+    return;
+  }
+  const Split s = fwd_split<Ty>(d);
+  stats_launch<Ty, false, false>(d, s, q.logits, ws, st);
+  hipLaunchKernelGGL((distill_finish_kernel<Ty>), dim3(d.T), dim3(64), 0, st, finish_args<Ty>(d, s.S), q,
+                     reinterpret_cast<const float4*>(ws));
 }
 
 template <class Ty>
 void logprobs_bwd_launch(const VocabDims& d, const LogprobGradPtrs& q, hipStream_t st) {
-  const BwdArgs b = bwd_args(d);
+  const BwdArgs b = bwd_args<Ty>(d);
   auto* f = d.accumulate ? logprobs_bwd_kernel<Ty, true> : logprobs_bwd_kernel<Ty, false>;
   hipLaunchKernelGGL(f, dim3((size_t)d.T * b.S), dim3(256), 0, st, b, q);
 }
@@ -980,7 +1156,7 @@ template <class Ty>
 void distill_bwd_launch(const VocabDims& d, const void* logits, const int* idx, const float* teacher,
                         const float* stats, const float* g_loss, void* d_logits, hipStream_t st) {
   typedef typename Ty::E E;
-  const BwdArgs b = bwd_args(d);
+  const BwdArgs b = bwd_args<Ty>(d);
   auto* f = d.accumulate ? distill_bwd_kernel<Ty, true> : distill_bwd_kernel<Ty, false>;
   hipLaunchKernelGGL(f, dim3((size_t)d.T * b.S), dim3(256), 0, st, b, static_cast<const E*>(logits), idx, teacher,
                      stats, g_loss, static_cast<E*>(d_logits));
@@ -988,10 +1164,12 @@ void distill_bwd_launch(const VocabDims& d, const void* logits, const int* idx, 
 
 }  // namespace
 
-size_t vocab_ws_bytes(const VocabDims& d) {
-  const size_t maxima = (size_t)(d.f32 ? blocks_of<F32>(d.V) * 4 : blocks_of<Bf16>(d.V) * 2);
-  return part_bytes(d) + (d.k > 0 ? d.T * maxima : 0);
+template <class Ty>
+static size_t ws_bytes_of(const VocabDims& d) {
+  if (whole_rows<Ty>(d, d.k > 0)) return 0;  // (then a distillation's rows are whole too)
+  return part_bytes<Ty>(d) + (d.k > 0 ? (size_t)d.T * blocks_of<Ty>(d.V) * sizeof(typename Blocks<Ty>::Key) : 0);
 }
+size_t vocab_ws_bytes(const VocabDims& d) { return d.f32 ? ws_bytes_of<F32>(d) : ws_bytes_of<Bf16>(d); }
 
 hipError_t launch_token_logprobs(const VocabDims& d, const LogprobPtrs& q, char* ws, hipStream_t st) {
   ProfScope prof(st, "vocab.logprobs");
@@ -1008,8 +1186,8 @@ hipError_t launch_token_logprobs_bwd(const VocabDims& d, const LogprobGradPtrs& 
 hipError_t launch_distill(const VocabDims& d, const void* logits, const int* idx, const float* teacher, float* loss,
                           float* stats, char* ws, hipStream_t st) {
   ProfScope prof(st, "vocab.distill");
-  d.f32 ? distill_launch<F32>(d, logits, idx, teacher, loss, stats, ws, st)
-        : distill_launch<Bf16>(d, logits, idx, teacher, loss, stats, ws, st);
+  const DistillPtrs q{logits, idx, teacher, loss, stats};
+  d.f32 ? distill_launch<F32>(d, q, ws, st) : distill_launch<Bf16>(d, q, ws, st);
   return hipGetLastError();
 }
 
