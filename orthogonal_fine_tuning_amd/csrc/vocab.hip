@@ -21,9 +21,11 @@
 //
 // Backward: one read and one write per logit with (m, l) from the forward.
 //
-// Rows start anywhere (16-byte loads at element alignment, which gfx950
-// allows); only a row's last, partial vector is read by elements, so nothing
-// outside a row is touched.
+// Rows start anywhere: gfx950 takes 16-byte loads at any 4-byte address at full
+// speed (at 2-byte ones 30 % slower, 126 for 96 us at 2048 x 151935 bf16).  So
+// a bf16 row at an odd element is taken from one element earlier: positions
+// are columns + skew, and position 0 is no column.  Only a row's partial
+// vectors are read by elements, so nothing outside a row is touched.
 #include <math.h>
 
 #include <algorithm>
@@ -100,6 +102,12 @@ __device__ __forceinline__ u32x4 stream16(const E* p) {
 template <class E>
 __device__ __forceinline__ void store16(E* p, const u32x4& v) {
   *reinterpret_cast<u32x4_row*>(p) = v;
+}
+
+// elements that a row is taken early
+template <class Ty>
+__device__ __forceinline__ int skew_of(const typename Ty::E* row) {
+  return sizeof(typename Ty::E) == 2 ? (int)(reinterpret_cast<uintptr_t>(row) >> 1 & 1) : 0;
 }
 
 // value of another lane of the same 16 (DPP)
@@ -208,8 +216,8 @@ struct Blocks {
   static constexpr int VECS = FU * RUN;                   // 16-byte vectors of a block
   static constexpr int TILE = fwd_tile<Ty>();
   static __device__ __forceinline__ uint32_t key(float v) { return ordered(v) >> (32 - BITS); }
-  // first column of vector i of block b
-  static __device__ __forceinline__ int column(int b, int i) {
+  // first position of vector i of block b
+  static __device__ __forceinline__ int position(int b, int i) {
     return b / PER_TILE * TILE + i / RUN * (256 * Ty::VE) + b % PER_TILE * (64 / FU) + i % RUN * Ty::VE;
   }
 };
@@ -270,7 +278,7 @@ struct KeepOut {
   }
 };
 
-// one step: FU vectors per thread, x[u VE + j] is column base + (u 256 + tid)
+// one step: FU vectors per thread, x[u VE + j] is position base + (u 256 + tid)
 // VE + j; again(u, y) reads vector u once more.  Returns the thread's maximum.
 template <class Ty, bool ENT, class F>
 __device__ __forceinline__ float fwd_step(const float (&x)[FU * Ty::VE], float c, Triple& a, F again) {
@@ -340,37 +348,53 @@ __device__ __forceinline__ float fwd_vector(const float* x, float c, Triple& a) 
   return bm;
 }
 
-// The triple of columns [lo, hi) of a row by a workgroup, the same in every
+// vector at position i0 of a row's positions [skew, hi), -inf elsewhere; `row`
+// is where position 0 would be
+template <class Ty>
+__device__ __forceinline__ void read_vector(const typename Ty::E* row, int i0, int skew, int hi, float* y) {
+  constexpr int VE = Ty::VE;
+  if (i0 >= skew && i0 + VE <= hi) {
+    Ty::unpack(stream16(row + i0), y);
+  } else {
+#pragma unroll
+    for (int j = 0; j < VE; ++j) y[j] = i0 + j >= skew && i0 + j < hi ? Ty::get(row[i0 + j]) : -INFINITY;
+  }
+}
+
+// The triple of positions [lo, hi) of a row by a workgroup, the same in every
 // thread; lo starts a step.
 template <class Ty, bool ENT, class K>
-__device__ __forceinline__ Triple slice_triple(const typename Ty::E* row, int lo, int hi, float c, K& keep) {
+__device__ __forceinline__ Triple slice_triple(const typename Ty::E* row, int skew, int lo, int hi, float c, K& keep) {
   constexpr int VE = Ty::VE, TILE = fwd_tile<Ty>();
   __shared__ float sh[4][3];
   const int tid = threadIdx.x;
   Triple a{-INFINITY, 0.0f, 0.0f};
   float x[FU * VE];
   int base = lo;
-  for (; base + TILE <= hi; base += TILE) {
-    u32x4 v[FU];
+  u32x4 v[FU];
+  if (base + TILE <= hi) {
 #pragma unroll
-    for (int u = 0; u < FU; ++u) v[u] = stream16(row + base + (u * 256 + tid) * VE);
+    for (int u = 0; u < FU; ++u)
+      if (u > 0 || lo + tid > 0 || skew == 0) v[u] = stream16(row + base + (u * 256 + tid) * VE);
+    if (skew != 0 && lo + tid == 0) {  // position 0 is no column: -inf before the row's first seven
+      const u32x4 f = load16(row + 1);
+      v[0] = u32x4{f[0] << 16 | 0xFF80u, f[1] << 16 | f[0] >> 16, f[2] << 16 | f[1] >> 16, f[3] << 16 | f[2] >> 16};
+    }
+  }
+  for (; base + TILE <= hi; base += TILE) {
 #pragma unroll
     for (int u = 0; u < FU; ++u) Ty::unpack(v[u], x + u * VE);
-    keep.add(fwd_step<Ty, ENT>(x, c, a, [&](int u, float* y) {
-      Ty::unpack(load16(row + base + (u * 256 + tid) * VE), y);
-    }));
+    // the next step's loads fly during this one's sums
+    if (base + 2 * TILE <= hi) {
+#pragma unroll
+      for (int u = 0; u < FU; ++u) v[u] = stream16(row + base + TILE + (u * 256 + tid) * VE);
+    }
+    keep.add(fwd_step<Ty, ENT>(
+        x, c, a, [&](int u, float* y) { read_vector<Ty>(row, base + (u * 256 + tid) * VE, skew, hi, y); }));
   }
   if (base < hi) {
 #pragma unroll
-    for (int u = 0; u < FU; ++u) {
-      const int i0 = base + (u * 256 + tid) * VE;
-      if (i0 + VE <= hi) {
-        Ty::unpack(stream16(row + i0), x + u * VE);
-      } else {
-#pragma unroll
-        for (int j = 0; j < VE; ++j) x[u * VE + j] = i0 + j < hi ? Ty::get(row[i0 + j]) : -INFINITY;
-      }
-    }
+    for (int u = 0; u < FU; ++u) read_vector<Ty>(row, base + (u * 256 + tid) * VE, skew, hi, x + u * VE);
     float bm = -INFINITY;
 #pragma unroll
     for (int u = 0; u < FU; ++u)
@@ -391,8 +415,8 @@ __device__ __forceinline__ Triple slice_triple(const typename Ty::E* row, int lo
   return a;
 }
 
-// part[t S + sl]: the triple of columns [sl slice, (sl + 1) slice) of row t;
-// blocks: the maxima of the row's blocks, nb per row
+// part[t S + sl]: the triple of positions [sl slice, (sl + 1) slice) of row t;
+// blocks: the maxima of the row's blocks, rows of them nb apart
 template <class Ty, bool ENT, bool TOP>
 __global__ __launch_bounds__(256) void vocab_stats_kernel(const typename Ty::E* __restrict__ logits, long ld, int V,
                                                           int S, int slice, float c, float4* __restrict__ part,
@@ -400,16 +424,19 @@ __global__ __launch_bounds__(256) void vocab_stats_kernel(const typename Ty::E* 
   typedef Blocks<Ty> B;
   typedef typename B::Key Key;
   const int t = blockIdx.x / S, sl = blockIdx.x % S, tid = threadIdx.x;
-  const int lo = sl * slice, hi = min(V, lo + slice);
+  const typename Ty::E* row = logits + (size_t)t * ld;
+  const int skew = skew_of<Ty>(row);
+  row -= skew;
+  const int lo = sl * slice, hi = min(V + skew, lo + slice);
   Triple a;
   if constexpr (TOP) {
     __shared__ __align__(16) Key kept[4][KEPT * KeepOut<Ty>::PW];
     KeepOut<Ty> keep{kept[tid >> 6],
                      blocks + (size_t)t * nb + lo / fwd_tile<Ty>() * B::PER_TILE + (tid & ~63) / B::RUN, 0};
-    a = slice_triple<Ty, ENT>(logits + (size_t)t * ld, lo, hi, c, keep);
+    a = slice_triple<Ty, ENT>(row, skew, lo, hi, c, keep);
   } else {
     KeepNone keep;
-    a = slice_triple<Ty, ENT>(logits + (size_t)t * ld, lo, hi, c, keep);
+    a = slice_triple<Ty, ENT>(row, skew, lo, hi, c, keep);
   }
   if (tid == 0) part[blockIdx.x] = make_float4(a.m, a.s, a.w, 0.0f);
 }
@@ -585,7 +612,8 @@ __device__ __forceinline__ void logprobs_finish(const FinishArgs& f, const Logpr
     __shared__ int count[2];
     if (tid < 2) count[tid] = 0;
     u32x4 held[HELD];
-    const int nvec = f.nb / KV;
+    const int skew = skew_of<Ty>(row), end = f.V + skew;
+    const int nvec = (end + B::TILE - 1) / B::TILE * B::PER_TILE / KV;
 #pragma unroll
     for (int i = 0; i < HELD; ++i) held[i] = i * NT + tid < nvec ? keys[i * NT + tid] : u32x4{0, 0, 0, 0};
     // the best of each of eight groups per thread
@@ -676,16 +704,19 @@ __device__ __forceinline__ void logprobs_finish(const FinishArgs& f, const Logpr
       const float least = o <= 0x007FFFFFu ? -INFINITY : unordered(o);
       for (int i = tid; i - lane < n1 * B::VECS; i += NT * U) {
         float x[U][VE];
-        int col[U];
+        int pos[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const int at = i + NT * u;
-          col[u] = at < n1 * B::VECS ? B::column(cand[at / B::VECS], at % B::VECS) : f.V;
-          if (col[u] + VE <= f.V) {
-            Ty::unpack(load16(row + col[u]), x[u]);
+          pos[u] = at < n1 * B::VECS ? B::position(cand[at / B::VECS], at % B::VECS) : end;
+          if (pos[u] >= skew && pos[u] + VE <= end) {
+            Ty::unpack(load16(row + (pos[u] - skew)), x[u]);
           } else {
 #pragma unroll
-            for (int j = 0; j < VE; ++j) x[u][j] = col[u] + j < f.V ? Ty::get(row[col[u] + j]) : NAN;
+            for (int j = 0; j < VE; ++j) {
+              const int col = pos[u] + j - skew;
+              x[u][j] = col >= 0 && col < f.V ? Ty::get(row[col]) : NAN;
+            }
           }
         }
 #pragma unroll
@@ -694,7 +725,7 @@ __device__ __forceinline__ void logprobs_finish(const FinishArgs& f, const Logpr
           for (int j = 0; j < VE; ++j)
             if (x[u][j] >= least) {
               const int at = atomicAdd(&count[1], 1);
-              if (at < MAXCAND) list[at] = candidate(ordered(x[u][j]), col[u] + j);
+              if (at < MAXCAND) list[at] = candidate(ordered(x[u][j]), pos[u] + j - skew);
             }
       }
       row_sync<W>();
@@ -749,16 +780,18 @@ __global__ __launch_bounds__(256, 6) void logprobs_row_kernel(FinishArgs f, Logp
   typedef typename Blocks<Ty>::Key Key;
   const int t = blockIdx.x;
   const typename Ty::E* row = static_cast<const typename Ty::E*>(q.logits) + (size_t)t * f.ld;
+  const int skew = skew_of<Ty>(row);
+  row -= skew;
   if constexpr (TOP) {
     __shared__ __align__(16) Key kept[MAXKEYS];
     static_assert(sizeof(kept) >= QCAP * 8, "the list of candidates takes the keys' place");
     KeepRow<Ty> keep{kept};
-    const Triple a = slice_triple<Ty, ENT>(row, 0, f.V, f.c, keep);
+    const Triple a = slice_triple<Ty, ENT>(row, skew, 0, f.V + skew, f.c, keep);
     logprobs_finish<Ty, true, 4>(f, q, t, a, reinterpret_cast<const u32x4*>(kept),
                                  reinterpret_cast<unsigned long long*>(kept));
   } else {
     KeepNone keep;
-    const Triple a = slice_triple<Ty, ENT>(row, 0, f.V, f.c, keep);
+    const Triple a = slice_triple<Ty, ENT>(row, skew, 0, f.V + skew, f.c, keep);
     logprobs_finish<Ty, false, 4>(f, q, t, a, nullptr, nullptr);
   }
 }
@@ -857,9 +890,10 @@ __global__ __launch_bounds__(64) void distill_finish_kernel(FinishArgs f, Distil
 template <class Ty>
 __global__ __launch_bounds__(256) void distill_row_kernel(FinishArgs f, DistillPtrs q) {
   const int t = blockIdx.x;
+  const typename Ty::E* row = static_cast<const typename Ty::E*>(q.logits) + (size_t)t * f.ld;
+  const int skew = skew_of<Ty>(row);
   KeepNone keep;
-  const Triple a = slice_triple<Ty, false>(static_cast<const typename Ty::E*>(q.logits) + (size_t)t * f.ld, 0, f.V, f.c,
-                                           keep);
+  const Triple a = slice_triple<Ty, false>(row - skew, skew, 0, f.V + skew, f.c, keep);
   if (threadIdx.x >= 64) return;
   float x[TI];
   const Teacher te = teacher_row<Ty>(f, q, t, x);
@@ -889,30 +923,58 @@ struct RowGrad {
 
 enum { FILL_NONE = 0, FILL_ZERO = 1, FILL_NAN = 2 };
 
-// columns [lo, hi) of a row: the gradient, or the same value everywhere
+// Positions [lo, hi) of a row (from `skew` on, where lo is 0): the gradient,
+// or the same value everywhere.  row, out: where position 0 would be.
 template <class Ty, bool ACC, class F>
-__device__ __forceinline__ void bwd_columns(const typename Ty::E* row, typename Ty::E* out, int lo, int hi, int fill,
-                                            F grad) {
-  typedef typename Ty::E E;
+__device__ __forceinline__ void bwd_columns(const typename Ty::E* row, typename Ty::E* out, int skew, int lo, int hi,
+                                            int fill, F grad) {
   constexpr int VE = Ty::VE, TILE = bwd_tile<Ty>();
   const int tid = threadIdx.x;
   if (fill == FILL_ZERO && ACC) return;  // adds nothing
-  if (fill != FILL_NONE) {
-    const float v = fill == FILL_ZERO ? 0.0f : NAN;
-    float f[VE];
+  // vectors of [from, to), partial ones by elements
+  const auto guarded = [&](int from, int to) {
+    for (int i0 = from + tid * VE; i0 < to; i0 += 256 * VE) {
+      float x[VE], o[VE];
+      const bool whole = i0 >= skew && i0 + VE <= hi;
+      if (fill != FILL_NONE) {
 #pragma unroll
-    for (int j = 0; j < VE; ++j) f[j] = v;
-    const u32x4 p = Ty::pack(f);
-    for (int i0 = lo + tid * VE; i0 < hi; i0 += 256 * VE) {
-      if (i0 + VE <= hi) {
-        store16(out + i0, p);
+        for (int j = 0; j < VE; ++j) {
+          x[j] = fill == FILL_ZERO ? 0.0f : NAN;
+          o[j] = 0.0f;
+        }
+      } else if (whole) {
+        Ty::unpack(load16(row + i0), x);
+        if constexpr (ACC) Ty::unpack(load16(out + i0), o);
+        grad(x, i0);
       } else {
-        for (int j = 0; i0 + j < hi; ++j) out[i0 + j] = Ty::put(v);
+#pragma unroll
+        for (int j = 0; j < VE; ++j) {
+          const bool in = i0 + j >= skew && i0 + j < hi;
+          x[j] = in ? Ty::get(row[i0 + j]) : 0.0f;
+          o[j] = ACC && in ? Ty::get(out[i0 + j]) : 0.0f;
+        }
+        grad(x, i0);
+      }
+#pragma unroll
+      for (int j = 0; j < VE; ++j) x[j] += ACC ? o[j] : 0.0f;
+      if (whole) {
+        store16(out + i0, Ty::pack(x));
+      } else {
+#pragma unroll
+        for (int j = 0; j < VE; ++j)
+          if (i0 + j >= skew && i0 + j < hi) out[i0 + j] = Ty::put(x[j]);
       }
     }
+  };
+  if (fill != FILL_NONE) {
+    guarded(lo, hi);
     return;
   }
   int base = lo;
+  if (skew != 0 && lo == 0) {
+    guarded(0, min(TILE, hi));
+    base = TILE;
+  }
   for (; base + TILE <= hi; base += TILE) {
     u32x4 v[BU], old[BU];
 #pragma unroll
@@ -932,27 +994,7 @@ __device__ __forceinline__ void bwd_columns(const typename Ty::E* row, typename 
       store16(out + i0, Ty::pack(x));
     }
   }
-  for (int i0 = base + tid * VE; i0 < hi; i0 += 256 * VE) {
-    float x[VE], o[VE];
-    if (i0 + VE <= hi) {
-      Ty::unpack(load16(row + i0), x);
-      if constexpr (ACC) Ty::unpack(load16(out + i0), o);
-      grad(x, i0);
-#pragma unroll
-      for (int j = 0; j < VE; ++j) x[j] += ACC ? o[j] : 0.0f;
-      store16(out + i0, Ty::pack(x));
-    } else {
-#pragma unroll
-      for (int j = 0; j < VE; ++j) {
-        x[j] = i0 + j < hi ? Ty::get(row[i0 + j]) : 0.0f;
-        o[j] = ACC && i0 + j < hi ? Ty::get(out[i0 + j]) : 0.0f;
-      }
-      grad(x, i0);
-#pragma unroll
-      for (int j = 0; j < VE; ++j)
-        if (i0 + j < hi) out[i0 + j] = Ty::put(x[j] + o[j]);
-    }
-  }
+  guarded(base, hi);
 }
 
 struct BwdArgs {
@@ -967,7 +1009,8 @@ __global__ __launch_bounds__(256) void logprobs_bwd_kernel(BwdArgs b, LogprobGra
   const int t = blockIdx.x / b.S, sl = blockIdx.x % b.S;
   const E* row = static_cast<const E*>(q.logits) + (size_t)t * b.ld;
   E* out = static_cast<E*>(q.d_logits) + (size_t)t * b.ldg;
-  const int lo = sl * b.slice, hi = min(b.V, lo + b.slice);
+  const int skew = skew_of<Ty>(row);
+  const int lo = sl * b.slice, hi = min(b.V + skew, lo + b.slice);
   const float2 st = *reinterpret_cast<const float2*>(q.stats + 2 * (size_t)t);
   const int lab = q.labels ? q.labels[t] : -1;
   const float gl = lab == -1 ? 0.0f : q.g_logp[t];
@@ -979,12 +1022,13 @@ __global__ __launch_bounds__(256) void logprobs_bwd_kernel(BwdArgs b, LogprobGra
   else if (st.y == -INFINITY) fill = FILL_ZERO;
   const RowGrad g{st.x, b.c, st.y * LOG2E, -ge * LN2 * b.invtau, -fmaf(ge, H, gl) * b.invtau};
   const float at = gl * b.invtau;
-  bwd_columns<Ty, ACC>(row, out, lo, hi, fill, [&](float (&x)[Ty::VE], int i0) {
+  bwd_columns<Ty, ACC>(row - skew, out - skew, skew, lo, hi, fill, [&](float (&x)[Ty::VE], int i0) {
 #pragma unroll
     for (int j = 0; j < Ty::VE; ++j) x[j] = g(x[j]);
-    if ((unsigned)(lab - i0) < (unsigned)Ty::VE) {
+    const int here = lab + skew - i0;
+    if ((unsigned)here < (unsigned)Ty::VE) {
 #pragma unroll
-      for (int j = 0; j < Ty::VE; ++j) x[j] += lab - i0 == j ? at : 0.0f;
+      for (int j = 0; j < Ty::VE; ++j) x[j] += here == j ? at : 0.0f;
     }
   });
 }
@@ -1001,7 +1045,8 @@ __global__ __launch_bounds__(256) void distill_bwd_kernel(BwdArgs b, const typen
   const int t = blockIdx.x / b.S, sl = blockIdx.x % b.S, tid = threadIdx.x;
   const E* row = logits + (size_t)t * b.ld;
   E* out = d_logits + (size_t)t * b.ldg;
-  const int lo = sl * b.slice, hi = min(b.V, lo + b.slice);
+  const int skew = skew_of<Ty>(row);
+  const int lo = sl * b.slice, hi = min(b.V + skew, lo + b.slice);
   const float2 st = *reinterpret_cast<const float2*>(stats + 2 * (size_t)t);
   const float g = g_loss[t];
   // (each wave computes the list; all get the same)
@@ -1015,7 +1060,7 @@ __global__ __launch_bounds__(256) void distill_bwd_kernel(BwdArgs b, const typen
   int n = 0;
 #pragma unroll
   for (int i = 0; i < TI; ++i) {
-    const bool in = te.ix[i] >= lo && te.ix[i] < hi;
+    const bool in = te.ix[i] >= 0 && te.ix[i] + skew >= lo && te.ix[i] + skew < hi;
     const unsigned long long mask = __ballot(in);
     if (in && tid < 64) {
       lidx[n + below(mask)] = te.ix[i];
@@ -1045,7 +1090,7 @@ __global__ __launch_bounds__(256) void distill_bwd_kernel(BwdArgs b, const typen
     if constexpr (ACC) v += Ty::get(out[mine]);
   }
   __syncthreads();
-  bwd_columns<Ty, ACC>(row, out, lo, hi, fill, [&](float (&x)[Ty::VE], int) {
+  bwd_columns<Ty, ACC>(row - skew, out - skew, skew, lo, hi, fill, [&](float (&x)[Ty::VE], int) {
 #pragma unroll
     for (int j = 0; j < Ty::VE; ++j) x[j] = exp2_hw(r.log2p(x[j])) * r.gb;
   });
@@ -1054,6 +1099,12 @@ __global__ __launch_bounds__(256) void distill_bwd_kernel(BwdArgs b, const typen
 }
 
 // --------------------------------------------------------------- host side
+// positions of a row at most
+template <class Ty>
+int positions(const VocabDims& d) {
+  return d.V + (sizeof(typename Ty::E) == 2 ? 1 : 0);
+}
+
 // Slices of a row: `want` workgroups, at least a tile each.
 struct Split {
   int S, slice;
@@ -1064,25 +1115,29 @@ Split split(int T, int V, int tile, long want) {
   const long per = (tiles + S - 1) / S;
   return Split{(int)((tiles + per - 1) / per), (int)(per * tile)};
 }
-#ifndef WANT
-#define WANT 4096
-#endif
-#ifndef ROWS
-#define ROWS 1024
-#endif
-constexpr int MANY_ROWS = ROWS;
+constexpr long WANT = 4096;
 template <class Ty>
-int blocks_of(int V) {
-  return (V + fwd_tile<Ty>() - 1) / fwd_tile<Ty>() * Blocks<Ty>::PER_TILE;
+int blocks_of(const VocabDims& d) {
+  return (positions<Ty>(d) + fwd_tile<Ty>() - 1) / fwd_tile<Ty>() * Blocks<Ty>::PER_TILE;
 }
-// a workgroup per row, with its block maxima in LDS where they are wanted
+// A workgroup per row, with its block maxima in LDS where they are wanted:
+// from MANY_ROWS on, and for rows of few steps, where one launch costs less
+// than a row's slices gain.  Measured (bf16, us, whole row / slices): 151936
+// columns, 20 alternatives, 1 row 20.4 / 13.8, 64 rows 22.8 / 17.1, 200 rows
+// 24.9 / 24.6, 400 rows 31.4 / 33.7, 4096 rows 203 / 231; without alternatives
+// 64 rows 17.3 / 13.1, 200 rows 19.1 / 18.5, 4096 rows 190 / 191; 32003 columns
+// (4 steps), 20 alternatives, 1 row 13.0 / 13.8, 400 rows 18.0 / 23.6.  fp32,
+// 50021 columns (13 steps): 1 row with alternatives 15.3 / 13.8, without
+// 10.7 / 12.8.
+constexpr int MANY_ROWS = 200, FEW_STEPS = 16, FEW_STEPS_TOP = 8;
 template <class Ty>
 bool whole_rows(const VocabDims& d, bool top) {
-  return d.T >= MANY_ROWS && (!top || blocks_of<Ty>(d.V) <= MAXKEYS);
+  if (top && blocks_of<Ty>(d) > MAXKEYS) return false;
+  return d.T >= MANY_ROWS || d.V <= (top ? FEW_STEPS_TOP : FEW_STEPS) * fwd_tile<Ty>();
 }
 template <class Ty>
 Split fwd_split(const VocabDims& d) {
-  return split(d.T, d.V, fwd_tile<Ty>(), WANT);
+  return split(d.T, positions<Ty>(d), fwd_tile<Ty>(), WANT);
 }
 template <class Ty>
 size_t part_bytes(const VocabDims& d) {
@@ -1092,11 +1147,11 @@ constexpr int FEW_ROWS = 1024;
 
 template <class Ty>
 FinishArgs finish_args(const VocabDims& d, int S) {
-  return FinishArgs{d.V, d.k, S, blocks_of<Ty>(d.V), d.ld, d.invtau * LOG2E, d.invtau};
+  return FinishArgs{d.V, d.k, S, blocks_of<Ty>(d), d.ld, d.invtau * LOG2E, d.invtau};
 }
 template <class Ty>
 BwdArgs bwd_args(const VocabDims& d) {
-  const Split s = split(d.T, d.V, bwd_tile<Ty>(), 8192);
+  const Split s = split(d.T, positions<Ty>(d), bwd_tile<Ty>(), 8192);
   return BwdArgs{d.V, d.k, s.S, s.slice, d.ld, d.ldg, d.invtau * LOG2E, d.invtau};
 }
 
@@ -1106,7 +1161,7 @@ void stats_launch(const VocabDims& d, const Split& s, const void* logits, char* 
   hipLaunchKernelGGL((vocab_stats_kernel<Ty, ENT, TOP>), dim3((size_t)d.T * s.S), dim3(256), 0, st,
                      static_cast<const E*>(logits), d.ld, d.V, s.S, s.slice, d.invtau * LOG2E,
                      reinterpret_cast<float4*>(ws),
-                     reinterpret_cast<typename Blocks<Ty>::Key*>(ws + part_bytes<Ty>(d)), blocks_of<Ty>(d.V));
+                     reinterpret_cast<typename Blocks<Ty>::Key*>(ws + part_bytes<Ty>(d)), blocks_of<Ty>(d));
 }
 
 template <class Ty, bool ENT, bool TOP>
@@ -1167,7 +1222,7 @@ void distill_bwd_launch(const VocabDims& d, const void* logits, const int* idx, 
 template <class Ty>
 static size_t ws_bytes_of(const VocabDims& d) {
   if (whole_rows<Ty>(d, d.k > 0)) return 0;  // (then a distillation's rows are whole too)
-  return part_bytes<Ty>(d) + (d.k > 0 ? (size_t)d.T * blocks_of<Ty>(d.V) * sizeof(typename Blocks<Ty>::Key) : 0);
+  return part_bytes<Ty>(d) + (d.k > 0 ? (size_t)d.T * blocks_of<Ty>(d) * sizeof(typename Blocks<Ty>::Key) : 0);
 }
 size_t vocab_ws_bytes(const VocabDims& d) { return d.f32 ? ws_bytes_of<F32>(d) : ws_bytes_of<Bf16>(d); }
 
