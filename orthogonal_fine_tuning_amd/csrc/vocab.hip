@@ -456,9 +456,11 @@ __device__ __forceinline__ int below(unsigned long long mask) {  // set bits of 
   return __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
 }
 
-// k-th largest of the N values per lane (numbers of BITS bits), two bits a step
+// The largest number of few low bits that at least k and at most k + slack of
+// the N values per lane (of BITS bits) reach; the k-th largest itself where
+// ties allow no such number.  Two bits a step.
 template <int N, int BITS>
-__device__ __forceinline__ uint32_t kth(const uint32_t* o, int k) {
+__device__ __forceinline__ uint32_t kth(const uint32_t* o, int k, int slack) {
   uint32_t r = 0;
   for (int bit = BITS - 2; bit >= 0; bit -= 2) {
     int n1 = 0, n2 = 0, n3 = 0;
@@ -470,6 +472,8 @@ __device__ __forceinline__ uint32_t kth(const uint32_t* o, int k) {
       n3 += __popcll(__ballot(o[j] >= t3));
     }
     r = n3 >= k ? t3 : n2 >= k ? t2 : n1 >= k ? t1 : r;
+    const int n = n3 >= k ? n3 : n2 >= k ? n2 : n1;
+    if (n >= k && n <= k + slack) break;
   }
   return r;
 }
@@ -498,7 +502,7 @@ __device__ int cut(unsigned long long* list, int n, int k, uint32_t& floor) {
     e[j] = j * 64 + lane < n ? list[j * 64 + lane] : 0ull;
     o[j] = (uint32_t)(e[j] >> 32);
   }
-  const uint32_t last = kth<N, 32>(o, k);
+  const uint32_t last = kth<N, 32>(o, k, 0);
   int above = 0;
 #pragma unroll
   for (int j = 0; j < N; ++j) above += __popcll(__ballot(o[j] > last));
@@ -566,10 +570,10 @@ struct FinishArgs {
   float c, invtau;
 };
 
-// Joins a row's slices; its outputs.  W waves per row.
+// A row's outputs from its triple, by a workgroup of 256 threads.
 //
 // Top alternatives, the usual case: each thread holds up to HELD vectors of
-// block maxima; a number t that k of 128, 256 or 512 disjoint groups of them
+// block maxima; a number that k of 128, 256 or 512 disjoint groups of them
 // reach (4 groups and more for each alternative) leaves few more than k blocks
 // and elements, and the place of each of those is the number of candidates
 // above it.  Rows where ties or masks leave too many, or with more blocks than
@@ -577,38 +581,46 @@ struct FinishArgs {
 constexpr int MAXBLK = 256, MAXCAND = 512;
 constexpr int MAXKEYS = 4096;  // 262144 columns
 
-template <int W>
-__device__ __forceinline__ void row_sync() {
-  if constexpr (W == 1) wave_lds();
-  else __syncthreads();
+// a row's given token: read at a kernel's start, since its two dependent loads
+// would otherwise end the row's critical path
+struct Given {
+  int label;
+  float x;
+};
+template <class Ty>
+__device__ __forceinline__ Given given_of(const FinishArgs& f, const LogprobPtrs& q, int t) {
+  Given g{-1, 0.0f};
+  if (q.labels) g.label = q.labels[t];
+  if (g.label >= 0 && g.label < f.V)
+    g.x = Ty::get((static_cast<const typename Ty::E*>(q.logits) + (size_t)t * f.ld)[g.label]);
+  return g;
 }
 
 // keys: the block maxima of the row, in LDS or memory; list: [QCAP] in LDS,
 // which may be where the keys are
-template <class Ty, bool TOP, int W>
-__device__ __forceinline__ void logprobs_finish(const FinishArgs& f, const LogprobPtrs& q, int t, const Triple& a,
-                                                const u32x4* keys, unsigned long long* list) {
+template <class Ty, bool TOP>
+__device__ __forceinline__ void logprobs_finish(const FinishArgs& f, const LogprobPtrs& q, int t, const Given& g,
+                                                const Triple& a, const u32x4* keys, unsigned long long* list) {
   typedef typename Ty::E E;
   typedef Blocks<Ty> B;
-  constexpr int VE = Ty::VE, NT = 64 * W, KV = 16 / sizeof(typename B::Key);
+  constexpr int VE = Ty::VE, NT = 256, KV = 16 / sizeof(typename B::Key);
   constexpr int HELD = TOP ? MAXKEYS / KV / NT : 0;
   const int tid = threadIdx.x, lane = tid & 63;
   const E* row = static_cast<const E*>(q.logits) + (size_t)t * f.ld;
   const bool empty = a.s == 0.0f;
   const float l = log_sum(a, f.c);
-  if (tid == 0) {
+  if (tid == NT - 1) {
     *reinterpret_cast<float2*>(q.stats + 2 * (size_t)t) = make_float2(a.m, l);
     if (q.entropy) q.entropy[t] = entropy_of(a);
     if (q.logp) {
-      const int lab = q.labels[t];
-      float lp = lab == -1 ? 0.0f : NAN;
-      if (lab >= 0 && lab < f.V) lp = empty ? -INFINITY : (Ty::get(row[lab]) - a.m) * f.invtau - l;
+      float lp = g.label == -1 ? 0.0f : NAN;
+      if (g.label >= 0 && g.label < f.V) lp = empty ? -INFINITY : (g.x - a.m) * f.invtau - l;
       q.logp[t] = lp;
     }
   }
   if constexpr (TOP) {
     __shared__ int cand[MAXBLK];
-    __shared__ uint32_t group[W == 1 ? 1 : 512];
+    __shared__ uint32_t group[512];
     __shared__ int count[2];
     if (tid < 2) count[tid] = 0;
     u32x4 held[HELD];
@@ -617,7 +629,7 @@ __device__ __forceinline__ void logprobs_finish(const FinishArgs& f, const Logpr
 #pragma unroll
     for (int i = 0; i < HELD; ++i) held[i] = i * NT + tid < nvec ? keys[i * NT + tid] : u32x4{0, 0, 0, 0};
     // the best of each of eight groups per thread
-    uint32_t g[8];
+    uint32_t best[8];
     if constexpr (KV == 8) {
       typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 #pragma unroll
@@ -629,124 +641,157 @@ __device__ __forceinline__ void logprobs_finish(const FinishArgs& f, const Logpr
           const uint32_t w = held[i][d];
           m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, w));
         }
-        g[2 * d] = m[0];
-        g[2 * d + 1] = m[1];
+        best[2 * d] = m[0];
+        best[2 * d + 1] = m[1];
       }
     } else {
 #pragma unroll
       for (int d = 0; d < 4; ++d) {
-        g[d] = held[0][d];
-        g[4 + d] = held[1][d];
+        best[d] = held[0][d];
+        best[4 + d] = held[1][d];
 #pragma unroll
         for (int i = 2; i < HELD; i += 2) {
-          g[d] = max(g[d], (uint32_t)held[i][d]);
-          g[4 + d] = max(g[4 + d], (uint32_t)held[i + 1][d]);
+          best[d] = max(best[d], (uint32_t)held[i][d]);
+          best[4 + d] = max(best[4 + d], (uint32_t)held[i + 1][d]);
         }
       }
     }
-    if constexpr (W > 1) {
-      // two groups per thread (joined for k <= 64), eight or four per lane of
-      // the wave that counts; every wave counts, to the same number
-      static_assert(W == 4, "512 groups of 256 threads");
+    // 512 groups in all, 8, 4 or 2 of a thread as fewer or more of them hold
+    // vectors; each wave counts in all of them, to the same number
+    const int shift = nvec <= 64 && KV == 8 ? 3 : nvec <= 128 ? 2 : 1;
+    if (shift <= 2) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) g[j] = max(g[j], g[4 + j]);
-      g[0] = max(g[0], g[2]);
-      g[1] = max(g[1], g[3]);
-      group[tid] = f.k > 64 ? g[0] : max(g[0], g[1]);
-      group[NT + tid] = g[1];
-      __syncthreads();
-#pragma unroll
-      for (int j = 0; j < 8; ++j) g[j] = group[64 * j + lane];
-    } else if (f.k <= 64) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) g[j] = max(g[j], g[4 + j]);
+      for (int j = 0; j < 4; ++j) best[j] = max(best[j], best[4 + j]);
     }
+    if (shift == 1) {
+      best[0] = max(best[0], best[2]);
+      best[1] = max(best[1], best[3]);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < 1 << shift && tid < 512 >> shift) group[(tid << shift) + j] = best[j];
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) best[j] = group[64 * j + lane];
+    if (f.k <= 64) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) best[j] = max(best[j], best[4 + j]);
+    }
+    const int slack = f.k / 8 + 4;  // a few more candidates for fewer steps
     uint32_t floor;
     if (f.k > 64) {
-      floor = kth<8, B::BITS>(g, f.k);
+      floor = kth<8, B::BITS>(best, f.k, slack);
     } else if (f.k > 24) {
-      floor = kth<4, B::BITS>(g, f.k);
+      floor = kth<4, B::BITS>(best, f.k, slack);
     } else {
-      g[0] = max(g[0], g[2]);
-      g[1] = max(g[1], g[3]);
-      floor = kth<2, B::BITS>(g, f.k);
+      best[0] = max(best[0], best[2]);
+      best[1] = max(best[1], best[3]);
+      floor = kth<2, B::BITS>(best, f.k, slack);
     }
     floor = max(floor, 1u);  // (fewer than k groups: every block is above 0)
-    row_sync<W>();
+    __syncthreads();
+    // a thread's finds enter the lists together: one counter update each
+    const auto found = [&](auto&& each) {
+      int more = 0;
 #pragma unroll
-    for (int i = 0; i < HELD; ++i) {
+      for (int i = 0; i < HELD; ++i) {
 #pragma unroll
-      for (int d = 0; d < 4; ++d) {
-        const uint32_t w = held[i][d];
-        const int b = (i * NT + tid) * KV + d * (KV / 4);
-        const uint32_t k0 = KV == 8 ? w & 0xFFFFu : w, k1 = KV == 8 ? w >> 16 : 0u;
-        if (max(k0, k1) >= floor) {
-          if (k0 >= floor) {
-            const int at = atomicAdd(&count[0], 1);
-            if (at < MAXBLK) cand[at] = b;
-          }
-          if (k1 >= floor) {
-            const int at = atomicAdd(&count[0], 1);
-            if (at < MAXBLK) cand[at] = b + 1;
+        for (int d = 0; d < 4; ++d) {
+          const uint32_t w = held[i][d];
+          const int b = (i * NT + tid) * KV + d * (KV / 4);
+          if constexpr (KV == 8) {
+            more += each((w & 0xFFFFu) >= floor, b) + each((w >> 16) >= floor, b + 1);
+          } else {
+            more += each(w >= floor, b);
           }
         }
       }
+      return more;
+    };
+    const int blocks = found([](bool in, int) { return in ? 1 : 0; });
+    if (blocks > 0) {
+      int at = atomicAdd(&count[0], blocks);
+      found([&](bool in, int b) {
+        if (in) {
+          if (at < MAXBLK) cand[at] = b;
+          ++at;
+        }
+        return 0;
+      });
     }
-    row_sync<W>();
+    __syncthreads();
     const int n1 = count[0];
     bool usual = nvec <= HELD * NT && n1 <= MAXBLK;
     int n = 0;
     if (usual) {
-      constexpr int U = 4;
       // key(x) >= floor as a comparison of numbers; false for NaN, which a row
       // of few others leaves to select_row
       const uint32_t o = floor << (32 - B::BITS);
       const float least = o <= 0x007FFFFFu ? -INFINITY : unordered(o);
-      for (int i = tid; i - lane < n1 * B::VECS; i += NT * U) {
-        float x[U][VE];
-        int pos[U];
+      const auto gather = [&](auto width) {
+        constexpr int U = decltype(width)::value;  // vectors in flight per thread
+        for (int i = tid; i - lane < n1 * B::VECS; i += NT * U) {
+          u32x4 x[U];
+          int pos[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int at = i + NT * u;
-          pos[u] = at < n1 * B::VECS ? B::position(cand[at / B::VECS], at % B::VECS) : end;
-          if (pos[u] >= skew && pos[u] + VE <= end) {
-            Ty::unpack(load16(row + (pos[u] - skew)), x[u]);
-          } else {
+          for (int u = 0; u < U; ++u) {
+            const int at = i + NT * u;
+            pos[u] = at < n1 * B::VECS ? B::position(cand[at / B::VECS], at % B::VECS) : end;
+            if (pos[u] >= skew && pos[u] + VE <= end) {
+              x[u] = load16(row + (pos[u] - skew));
+            } else {
+              float y[VE];
 #pragma unroll
-            for (int j = 0; j < VE; ++j) {
-              const int col = pos[u] + j - skew;
-              x[u][j] = col >= 0 && col < f.V ? Ty::get(row[col]) : NAN;
+              for (int j = 0; j < VE; ++j) {
+                const int col = pos[u] + j - skew;
+                y[j] = col >= 0 && col < f.V ? Ty::get(row[col]) : NAN;
+              }
+              x[u] = Ty::pack(y);
+            }
+          }
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            float y[VE];
+            Ty::unpack(x[u], y);
+            int more = 0;
+#pragma unroll
+            for (int j = 0; j < VE; ++j) more += y[j] >= least ? 1 : 0;
+            if (more > 0) {
+              int at = atomicAdd(&count[1], more);
+#pragma unroll
+              for (int j = 0; j < VE; ++j)
+                if (y[j] >= least) {
+                  if (at < MAXCAND) list[at] = candidate(ordered(y[j]), pos[u] + j - skew);
+                  ++at;
+                }
             }
           }
         }
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-          for (int j = 0; j < VE; ++j)
-            if (x[u][j] >= least) {
-              const int at = atomicAdd(&count[1], 1);
-              if (at < MAXCAND) list[at] = candidate(ordered(x[u][j]), pos[u] + j - skew);
-            }
-      }
-      row_sync<W>();
+      };
+      if (n1 * B::VECS <= NT) gather(std::integral_constant<int, 1>{});
+      else gather(std::integral_constant<int, 4>{});
+      __syncthreads();
       n = count[1];
       usual = n <= MAXCAND && n >= f.k;
     }
     if (!usual) {
-      row_sync<W>();
+      __syncthreads();
       if (tid < 64) select_row<Ty>(row, f.V, f.k, floor << (32 - B::BITS), list);
       n = f.k;
-      row_sync<W>();
+      __syncthreads();
     }
-    // an even number of candidates for the paired reads: 0 is below each
-    if (tid == 0 && (n & 1)) list[n] = 0ull;
-    row_sync<W>();
+    // up to a multiple of eight for the reads below: 0 is below each candidate
+    if (tid < 8 && n + tid < ((n + 7) & ~7)) list[n + tid] = 0ull;
+    __syncthreads();
     for (int i = tid; i < n; i += NT) {
       const unsigned long long mine = list[i];
       int place = 0;
-      for (int j = 0; j < n; j += 2) {
-        const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(list + j);
-        place += (o.x > mine ? 1 : 0) + (o.y > mine ? 1 : 0);
+      for (int j = 0; j < n; j += 8) {
+#pragma unroll
+        for (int h = 0; h < 8; h += 2) {
+          const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(list + j + h);
+          place += (o.x > mine ? 1 : 0) + (o.y > mine ? 1 : 0);
+        }
       }
       if (place < f.k) {
         const float v = unordered((uint32_t)(mine >> 32));
@@ -758,17 +803,18 @@ __device__ __forceinline__ void logprobs_finish(const FinishArgs& f, const Logpr
   }
 }
 
-template <class Ty, bool TOP, int W>
-__global__ __launch_bounds__(64 * W, W == 1 ? 6 : 4) void logprobs_finish_kernel(
+template <class Ty, bool TOP>
+__global__ __launch_bounds__(256, 4) void logprobs_finish_kernel(
     FinishArgs f, LogprobPtrs q, const float4* __restrict__ part,
     const typename Blocks<Ty>::Key* __restrict__ blocks) {
   const int t = blockIdx.x;
+  const Given g = given_of<Ty>(f, q, t);
   const Triple a = row_triple(part + (size_t)t * f.S, f.S, f.c);
   if constexpr (TOP) {
     __shared__ __align__(16) unsigned long long list[QCAP];
-    logprobs_finish<Ty, true, W>(f, q, t, a, reinterpret_cast<const u32x4*>(blocks + (size_t)t * f.nb), list);
+    logprobs_finish<Ty, true>(f, q, t, g, a, reinterpret_cast<const u32x4*>(blocks + (size_t)t * f.nb), list);
   } else {
-    logprobs_finish<Ty, false, W>(f, q, t, a, nullptr, nullptr);
+    logprobs_finish<Ty, false>(f, q, t, g, a, nullptr, nullptr);
   }
 }
 
@@ -782,17 +828,18 @@ __global__ __launch_bounds__(256, 6) void logprobs_row_kernel(FinishArgs f, Logp
   const typename Ty::E* row = static_cast<const typename Ty::E*>(q.logits) + (size_t)t * f.ld;
   const int skew = skew_of<Ty>(row);
   row -= skew;
+  const Given g = given_of<Ty>(f, q, t);
   if constexpr (TOP) {
     __shared__ __align__(16) Key kept[MAXKEYS];
     static_assert(sizeof(kept) >= QCAP * 8, "the list of candidates takes the keys' place");
     KeepRow<Ty> keep{kept};
     const Triple a = slice_triple<Ty, ENT>(row, skew, 0, f.V + skew, f.c, keep);
-    logprobs_finish<Ty, true, 4>(f, q, t, a, reinterpret_cast<const u32x4*>(kept),
+    logprobs_finish<Ty, true>(f, q, t, g, a, reinterpret_cast<const u32x4*>(kept),
                                  reinterpret_cast<unsigned long long*>(kept));
   } else {
     KeepNone keep;
     const Triple a = slice_triple<Ty, ENT>(row, skew, 0, f.V + skew, f.c, keep);
-    logprobs_finish<Ty, false, 4>(f, q, t, a, nullptr, nullptr);
+    logprobs_finish<Ty, false>(f, q, t, g, a, nullptr, nullptr);
   }
 }
 
@@ -1129,7 +1176,7 @@ int blocks_of(const VocabDims& d) {
 // (4 steps), 20 alternatives, 1 row 13.0 / 13.8, 400 rows 18.0 / 23.6.  fp32,
 // 50021 columns (13 steps): 1 row with alternatives 15.3 / 13.8, without
 // 10.7 / 12.8.
-constexpr int MANY_ROWS = 200, FEW_STEPS = 16, FEW_STEPS_TOP = 8;
+constexpr int MANY_ROWS = 200, FEW_STEPS = 8, FEW_STEPS_TOP = 4;
 template <class Ty>
 bool whole_rows(const VocabDims& d, bool top) {
   if (top && blocks_of<Ty>(d) > MAXKEYS) return false;
@@ -1143,8 +1190,6 @@ template <class Ty>
 size_t part_bytes(const VocabDims& d) {
   return (size_t)d.T * fwd_split<Ty>(d).S * sizeof(float4);
 }
-constexpr int FEW_ROWS = 1024;
-
 template <class Ty>
 FinishArgs finish_args(const VocabDims& d, int S) {
   return FinishArgs{d.V, d.k, S, blocks_of<Ty>(d), d.ld, d.invtau * LOG2E, d.invtau};
@@ -1175,11 +1220,7 @@ void logprobs_launch(const VocabDims& d, const LogprobPtrs& q, char* ws, hipStre
   const auto* blocks = reinterpret_cast<const typename Blocks<Ty>::Key*>(ws + part_bytes<Ty>(d));
   const FinishArgs f = finish_args<Ty>(d, s.S);
   stats_launch<Ty, ENT, TOP>(d, s, q.logits, ws, st);
-  // few rows: four waves each, for the latency of one
-  if (TOP && d.T <= FEW_ROWS)
-    hipLaunchKernelGGL((logprobs_finish_kernel<Ty, TOP, 4>), dim3(d.T), dim3(256), 0, st, f, q, part, blocks);
-  else
-    hipLaunchKernelGGL((logprobs_finish_kernel<Ty, TOP, 1>), dim3(d.T), dim3(64), 0, st, f, q, part, blocks);
+  hipLaunchKernelGGL((logprobs_finish_kernel<Ty, TOP>), dim3(d.T), dim3(256), 0, st, f, q, part, blocks);
 }
 
 template <class Ty>
