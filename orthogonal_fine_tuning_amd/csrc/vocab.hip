@@ -576,8 +576,8 @@ struct FinishArgs {
 // block maxima; a number that k of 128, 256 or 512 disjoint groups of them
 // reach (4 groups and more for each alternative) leaves few more than k blocks
 // and elements, and the place of each of those is the number of candidates
-// above it.  Rows where ties or masks leave too many, or with more blocks than
-// the registers hold, go through select_row.
+// above it.  Rows whose many candidates are no ties, or with more blocks than the
+// registers hold, go through select_row.
 constexpr int MAXBLK = 256, MAXCAND = 512;
 constexpr int MAXKEYS = 4096;  // 262144 columns
 
@@ -622,7 +622,6 @@ __device__ __forceinline__ void logprobs_finish(const FinishArgs& f, const Logpr
     __shared__ int cand[MAXBLK];
     __shared__ uint32_t group[512];
     __shared__ int count[2];
-    if (tid < 2) count[tid] = 0;
     u32x4 held[HELD];
     const int skew = skew_of<Ty>(row), end = f.V + skew;
     const int nvec = (end + B::TILE - 1) / B::TILE * B::PER_TILE / KV;
@@ -689,44 +688,50 @@ __device__ __forceinline__ void logprobs_finish(const FinishArgs& f, const Logpr
       floor = kth<2, B::BITS>(best, f.k, slack);
     }
     floor = max(floor, 1u);  // (fewer than k groups: every block is above 0)
-    __syncthreads();
-    // a thread's finds enter the lists together: one counter update each
-    const auto found = [&](auto&& each) {
-      int more = 0;
+    // First the candidates that reach the floor.  If they are too many, those
+    // above it: where ties did it (a masked or constant row) they are few, and
+    // the lowest columns at the floor itself complete them.
+    bool done = false;
+    int n = 0;
+    for (uint32_t lo = floor; lo <= floor + 1 && !done; ++lo) {
+      __syncthreads();
+      if (tid < 2) count[tid] = 0;
+      __syncthreads();
+      // a thread's finds enter the lists together: one counter update each
+      const auto found = [&](auto&& each) {
+        int more = 0;
 #pragma unroll
-      for (int i = 0; i < HELD; ++i) {
+        for (int i = 0; i < HELD; ++i) {
 #pragma unroll
-        for (int d = 0; d < 4; ++d) {
-          const uint32_t w = held[i][d];
-          const int b = (i * NT + tid) * KV + d * (KV / 4);
-          if constexpr (KV == 8) {
-            more += each((w & 0xFFFFu) >= floor, b) + each((w >> 16) >= floor, b + 1);
-          } else {
-            more += each(w >= floor, b);
+          for (int d = 0; d < 4; ++d) {
+            const uint32_t w = held[i][d];
+            const int b = (i * NT + tid) * KV + d * (KV / 4);
+            if constexpr (KV == 8) {
+              more += each((w & 0xFFFFu) >= lo, b) + each((w >> 16) >= lo, b + 1);
+            } else {
+              more += each(w >= lo, b);
+            }
           }
         }
+        return more;
+      };
+      const int blocks = found([](bool in, int) { return in ? 1 : 0; });
+      if (blocks > 0) {
+        int at = atomicAdd(&count[0], blocks);
+        found([&](bool in, int b) {
+          if (in) {
+            if (at < MAXBLK) cand[at] = b;
+            ++at;
+          }
+          return 0;
+        });
       }
-      return more;
-    };
-    const int blocks = found([](bool in, int) { return in ? 1 : 0; });
-    if (blocks > 0) {
-      int at = atomicAdd(&count[0], blocks);
-      found([&](bool in, int b) {
-        if (in) {
-          if (at < MAXBLK) cand[at] = b;
-          ++at;
-        }
-        return 0;
-      });
-    }
-    __syncthreads();
-    const int n1 = count[0];
-    bool usual = nvec <= HELD * NT && n1 <= MAXBLK;
-    int n = 0;
-    if (usual) {
-      // key(x) >= floor as a comparison of numbers; false for NaN, which a row
-      // of few others leaves to select_row
-      const uint32_t o = floor << (32 - B::BITS);
+      __syncthreads();
+      const int n1 = count[0];
+      if (nvec > HELD * NT || n1 > MAXBLK) continue;
+      // key(x) >= lo as a comparison of numbers (false for NaN, which ranks as
+      // -inf: a row with few others finds it at the floor)
+      const uint32_t o = lo << (32 - B::BITS);
       const float least = o <= 0x007FFFFFu ? -INFINITY : unordered(o);
       const auto gather = [&](auto width) {
         constexpr int U = decltype(width)::value;  // vectors in flight per thread
@@ -772,9 +777,37 @@ __device__ __forceinline__ void logprobs_finish(const FinishArgs& f, const Logpr
       else gather(std::integral_constant<int, 4>{});
       __syncthreads();
       n = count[1];
-      usual = n <= MAXCAND && n >= f.k;
+      done = n <= MAXCAND && (n >= f.k || lo > floor);
     }
-    if (!usual) {
+    // at the floor itself, in order of columns
+    for (int base = 0; done && n < f.k && base < f.V; base += NT * VE) {
+      const int c0 = base + tid * VE;
+      int hit = 0, at = 0, total = 0;
+#pragma unroll
+      for (int j = 0; j < VE; ++j) {
+        const bool in = c0 + j < f.V && B::key(Ty::get(row[c0 + j])) == floor;
+        const unsigned long long mask = __ballot(in);
+        hit |= in ? 1 << j : 0;
+        at += below(mask);
+        total += __popcll(mask);
+      }
+      if (lane == 0) cand[tid >> 6] = total;
+      __syncthreads();
+      total = 0;
+      for (int w = 0; w < 4; ++w) {
+        if (w == tid >> 6) at += total;
+        total += cand[w];
+      }
+#pragma unroll
+      for (int j = 0; j < VE; ++j)
+        if (hit >> j & 1) {
+          if (n + at < f.k) list[n + at] = candidate(ordered(Ty::get(row[c0 + j])), c0 + j);
+          ++at;
+        }
+      n = min(f.k, n + total);
+      __syncthreads();
+    }
+    if (!done || n < f.k) {
       __syncthreads();
       if (tid < 64) select_row<Ty>(row, f.V, f.k, floor << (32 - B::BITS), list);
       n = f.k;
