@@ -93,15 +93,15 @@ template <class E>
 __device__ __forceinline__ u32x4 load16(const E* p) {
   return *reinterpret_cast<const u32x4_row*>(p);
 }
-// a vector that is read once: it need not displace what the caches hold
-// (4096 x 151936 bf16 rows summed in 180 instead of 203 us)
+// a vector that is read or written once: it need not displace what the caches
+// hold (4096 x 151936 bf16 rows summed in 180 instead of 203 us)
 template <class E>
 __device__ __forceinline__ u32x4 stream16(const E* p) {
   return __builtin_nontemporal_load(reinterpret_cast<const u32x4_row*>(p));
 }
 template <class E>
-__device__ __forceinline__ void store16(E* p, const u32x4& v) {
-  *reinterpret_cast<u32x4_row*>(p) = v;
+__device__ __forceinline__ void stream16(E* p, const u32x4& v) {
+  __builtin_nontemporal_store(v, reinterpret_cast<u32x4_row*>(p));
 }
 
 // elements that a row is taken early
@@ -877,10 +877,11 @@ __global__ __launch_bounds__(256, 6) void logprobs_row_kernel(FinishArgs f, Logp
 }
 
 // ------------------------------------------------------------------ teacher
-// A row's teacher list over one wave: entry lane + 64 i in register i.
+// A row's teacher list over one wave: entry lane + 64 i in register i < TI (1 or
+// 4: lists of up to 64 or 256).
 // ix -1: an entry without weight.  bad: an entry is out of range, NaN or
 // +inf; any: some entry has weight.
-constexpr int TI = 4;
+template <int TI>
 struct Teacher {
   int ix[TI];
   float q[TI], logq[TI];
@@ -931,8 +932,8 @@ struct DistillPtrs {
 };
 
 // by one wave
-template <class Ty>
-__device__ __forceinline__ void distill_finish(const FinishArgs& f, const DistillPtrs& q, int t, const Teacher& te,
+template <class Ty, int TI>
+__device__ __forceinline__ void distill_finish(const FinishArgs& f, const DistillPtrs& q, int t, const Teacher<TI>& te,
                                                const float (&x)[TI], const Triple& a) {
   const float l = log_sum(a, f.c);
   float sum = 0.0f;
@@ -949,25 +950,25 @@ __device__ __forceinline__ void distill_finish(const FinishArgs& f, const Distil
   }
 }
 
-template <class Ty>
-__device__ __forceinline__ Teacher teacher_row(const FinishArgs& f, const DistillPtrs& q, int t, float (&x)[TI]) {
+template <class Ty, int TI>
+__device__ __forceinline__ Teacher<TI> teacher_row(const FinishArgs& f, const DistillPtrs& q, int t, float (&x)[TI]) {
   const typename Ty::E* row = static_cast<const typename Ty::E*>(q.logits) + (size_t)t * f.ld;
-  const Teacher te(q.idx + (size_t)t * f.k, q.teacher + (size_t)t * f.k, f.k, f.V, f.invtau);
+  const Teacher<TI> te(q.idx + (size_t)t * f.k, q.teacher + (size_t)t * f.k, f.k, f.V, f.invtau);
 #pragma unroll
   for (int i = 0; i < TI; ++i) x[i] = te.ix[i] >= 0 ? Ty::get(row[te.ix[i]]) : 0.0f;
   return te;
 }
 
-template <class Ty>
+template <class Ty, int TI>
 __global__ __launch_bounds__(64) void distill_finish_kernel(FinishArgs f, DistillPtrs q,
                                                             const float4* __restrict__ part) {
   const int t = blockIdx.x;
   float x[TI];
-  const Teacher te = teacher_row<Ty>(f, q, t, x);
-  distill_finish<Ty>(f, q, t, te, x, row_triple(part + (size_t)t * f.S, f.S, f.c));
+  const Teacher<TI> te = teacher_row<Ty, TI>(f, q, t, x);
+  distill_finish<Ty, TI>(f, q, t, te, x, row_triple(part + (size_t)t * f.S, f.S, f.c));
 }
 
-template <class Ty>
+template <class Ty, int TI>
 __global__ __launch_bounds__(256) void distill_row_kernel(FinishArgs f, DistillPtrs q) {
   const int t = blockIdx.x;
   const typename Ty::E* row = static_cast<const typename Ty::E*>(q.logits) + (size_t)t * f.ld;
@@ -976,8 +977,8 @@ __global__ __launch_bounds__(256) void distill_row_kernel(FinishArgs f, DistillP
   const Triple a = slice_triple<Ty, false>(row - skew, skew, 0, f.V + skew, f.c, keep);
   if (threadIdx.x >= 64) return;
   float x[TI];
-  const Teacher te = teacher_row<Ty>(f, q, t, x);
-  distill_finish<Ty>(f, q, t, te, x, a);
+  const Teacher<TI> te = teacher_row<Ty, TI>(f, q, t, x);
+  distill_finish<Ty, TI>(f, q, t, te, x, a);
 }
 
 // ----------------------------------------------------------------- backward
@@ -985,9 +986,17 @@ __global__ __launch_bounds__(256) void distill_row_kernel(FinishArgs f, DistillP
 // log2 p = c (x - m) - l log2 e:
 //   logprobs  ga = -g_H ln 2 / tau, gb = -(g_logp + g_H H) / tau
 //   distill   ga = 0, gb = g / tau (the listed columns follow)
-constexpr int BU = 4;  // vectors per thread and step
+//
+// A workgroup has one tile of a row, BU vectors a thread: loaded at once,
+// computed, stored, with nothing kept in the caches.  Time goes by the bytes
+// (4096 x 151936 bf16, read and written, us): 477 with cached loads and
+// stores and two slices a row, 401 streamed with a tile of 4 vectors, 381
+// of 2, 408 of 1.  The distillation's workgroups also read the teacher's
+// list, which 3 vectors repay better (192 us at half the rows; 210 of 2, 198
+// of 4).
+constexpr int BU_LOGPROBS = 2, BU_DISTILL = 3;
 
-template <class Ty>
+template <class Ty, int BU>
 constexpr int bwd_tile() {
   return 256 * BU * Ty::VE;
 }
@@ -1001,31 +1010,58 @@ struct RowGrad {
   }
 };
 
-enum { FILL_NONE = 0, FILL_ZERO = 1, FILL_NAN = 2 };
+// A workgroup's tile of a row: positions [lo, hi), from `skew` on where lo is
+// 0; row, out: where position 0 would be.
+template <class Ty, int BU, bool ACC>
+struct Tile {
+  typedef typename Ty::E E;
+  static constexpr int VE = Ty::VE, SIZE = bwd_tile<Ty, BU>();
+  const E* row;
+  E* out;
+  int skew, lo, hi;
+  u32x4 v[BU], old[ACC ? BU : 1];
 
-// Positions [lo, hi) of a row (from `skew` on, where lo is 0): the gradient,
-// or the same value everywhere.  row, out: where position 0 would be.
-template <class Ty, bool ACC, class F>
-__device__ __forceinline__ void bwd_columns(const typename Ty::E* row, typename Ty::E* out, int skew, int lo, int hi,
-                                            int fill, F grad) {
-  constexpr int VE = Ty::VE, TILE = bwd_tile<Ty>();
-  const int tid = threadIdx.x;
-  if (fill == FILL_ZERO && ACC) return;  // adds nothing
-  // vectors of [from, to), partial ones by elements
-  const auto guarded = [&](int from, int to) {
-    for (int i0 = from + tid * VE; i0 < to; i0 += 256 * VE) {
-      float x[VE], o[VE];
-      const bool whole = i0 >= skew && i0 + VE <= hi;
-      if (fill != FILL_NONE) {
+  __device__ __forceinline__ Tile(const E* r, E* o, int sk, int l, int V)
+      : row(r - sk), out(o - sk), skew(sk), lo(l), hi(min(V + sk, l + SIZE)) {}
+  __device__ __forceinline__ int first(int u) const { return lo + (u * 256 + (int)threadIdx.x) * VE; }
+  __device__ __forceinline__ bool whole(int i0) const { return i0 >= skew && i0 + VE <= hi; }
+
+  // no partial vector in the tile: known to all its threads alike, so that the
+  // loads stand in no branch of their own
+  __device__ __forceinline__ bool full() const { return lo >= skew && lo + SIZE <= hi; }
+
+  __device__ __forceinline__ void load() {
+    if (!full()) return;
 #pragma unroll
-        for (int j = 0; j < VE; ++j) {
-          x[j] = fill == FILL_ZERO ? 0.0f : NAN;
-          o[j] = 0.0f;
-        }
-      } else if (whole) {
-        Ty::unpack(load16(row + i0), x);
-        if constexpr (ACC) Ty::unpack(load16(out + i0), o);
-        grad(x, i0);
+    for (int u = 0; u < BU; ++u) {
+      v[u] = stream16(row + first(u));
+      if constexpr (ACC) old[u] = stream16(out + first(u));
+    }
+  }
+
+  // grad(x, i0): the gradient of the vector at position i0 in place of x
+  template <class F>
+  __device__ __forceinline__ void store(F grad) {
+    if (full()) {
+#pragma unroll
+      for (int u = 0; u < BU; ++u) {
+        float x[VE], o[VE];
+        Ty::unpack(v[u], x);
+        if constexpr (ACC) Ty::unpack(old[u], o);
+        grad(x, first(u));
+#pragma unroll
+        for (int j = 0; j < VE; ++j) x[j] += ACC ? o[j] : 0.0f;
+        stream16(out + first(u), Ty::pack(x));
+      }
+      return;
+    }
+#pragma unroll 1
+    for (int u = 0; u < BU; ++u) {
+      const int i0 = first(u);
+      float x[VE], o[VE];
+      if (whole(i0)) {
+        Ty::unpack(stream16(row + i0), x);
+        if constexpr (ACC) Ty::unpack(stream16(out + i0), o);
       } else {
 #pragma unroll
         for (int j = 0; j < VE; ++j) {
@@ -1033,52 +1069,51 @@ __device__ __forceinline__ void bwd_columns(const typename Ty::E* row, typename 
           x[j] = in ? Ty::get(row[i0 + j]) : 0.0f;
           o[j] = ACC && in ? Ty::get(out[i0 + j]) : 0.0f;
         }
-        grad(x, i0);
       }
+      grad(x, i0);
 #pragma unroll
       for (int j = 0; j < VE; ++j) x[j] += ACC ? o[j] : 0.0f;
-      if (whole) {
-        store16(out + i0, Ty::pack(x));
+      if (whole(i0)) {
+        stream16(out + i0, Ty::pack(x));
       } else {
 #pragma unroll
         for (int j = 0; j < VE; ++j)
           if (i0 + j >= skew && i0 + j < hi) out[i0 + j] = Ty::put(x[j]);
       }
     }
-  };
-  if (fill != FILL_NONE) {
-    guarded(lo, hi);
-    return;
   }
-  int base = lo;
-  if (skew != 0 && lo == 0) {
-    guarded(0, min(TILE, hi));
-    base = TILE;
-  }
-  for (; base + TILE <= hi; base += TILE) {
-    u32x4 v[BU], old[BU];
+
+  // the same value everywhere (zeros add nothing)
+  __device__ __forceinline__ void fill(float value) {
+    if (ACC && value == 0.0f) return;
+    float x[VE];
 #pragma unroll
+    for (int j = 0; j < VE; ++j) x[j] = value;
+#pragma unroll 1
     for (int u = 0; u < BU; ++u) {
-      v[u] = load16(row + base + (u * 256 + tid) * VE);
-      if constexpr (ACC) old[u] = load16(out + base + (u * 256 + tid) * VE);
-    }
+      const int i0 = first(u);
+      if (whole(i0)) {
+        stream16(out + i0, Ty::pack(x));
+      } else {
 #pragma unroll
-    for (int u = 0; u < BU; ++u) {
-      const int i0 = base + (u * 256 + tid) * VE;
-      float x[VE], o[VE];
-      Ty::unpack(v[u], x);
-      if constexpr (ACC) Ty::unpack(old[u], o);
-      grad(x, i0);
-#pragma unroll
-      for (int j = 0; j < VE; ++j) x[j] += ACC ? o[j] : 0.0f;
-      store16(out + i0, Ty::pack(x));
+        for (int j = 0; j < VE; ++j)
+          if (i0 + j >= skew && i0 + j < hi) out[i0 + j] = Ty::put(value);
+      }
     }
   }
-  guarded(base, hi);
-}
+};
+
+enum { ZEROS = 1, NANS = 2 };  // a row of one value
+
+// row and tile of a workgroup, in scalar registers
+struct Place {
+  int t, tile;
+  __device__ __forceinline__ explicit Place(int S)
+      : t(__builtin_amdgcn_readfirstlane((int)(blockIdx.x / (unsigned)S))), tile((int)blockIdx.x - t * S) {}
+};
 
 struct BwdArgs {
-  int V, k, S, slice;
+  int V, k, S;
   long ld, ldg;
   float c, invtau;
 };
@@ -1086,23 +1121,24 @@ struct BwdArgs {
 template <class Ty, bool ACC>
 __global__ __launch_bounds__(256) void logprobs_bwd_kernel(BwdArgs b, LogprobGradPtrs q) {
   typedef typename Ty::E E;
-  const int t = blockIdx.x / b.S, sl = blockIdx.x % b.S;
+  typedef Tile<Ty, BU_LOGPROBS, ACC> Part;
+  const Place at_tile(b.S);
+  const int t = at_tile.t;
   const E* row = static_cast<const E*>(q.logits) + (size_t)t * b.ld;
-  E* out = static_cast<E*>(q.d_logits) + (size_t)t * b.ldg;
   const int skew = skew_of<Ty>(row);
-  const int lo = sl * b.slice, hi = min(b.V + skew, lo + b.slice);
+  Part part(row, static_cast<E*>(q.d_logits) + (size_t)t * b.ldg, skew, at_tile.tile * Part::SIZE, b.V);
   const float2 st = *reinterpret_cast<const float2*>(q.stats + 2 * (size_t)t);
+  // (each load on its own: none waits for another's value)
   const int lab = q.labels ? q.labels[t] : -1;
-  const float gl = lab == -1 ? 0.0f : q.g_logp[t];
-  const float ge = q.g_entropy ? q.g_entropy[t] : 0.0f;
-  const float H = ge != 0.0f ? q.entropy[t] : 0.0f;
-  int fill = FILL_NONE;
-  if (gl == 0.0f && ge == 0.0f) fill = FILL_ZERO;
-  else if (lab < -1 || lab >= b.V) fill = FILL_NAN;
-  else if (st.y == -INFINITY) fill = FILL_ZERO;
+  const float given = q.g_logp ? q.g_logp[t] : 0.0f, gl = lab == -1 ? 0.0f : given;
+  const float ge = q.g_entropy ? q.g_entropy[t] : 0.0f, ent = q.g_entropy ? q.entropy[t] : 0.0f;
+  const int same = gl == 0.0f && ge == 0.0f ? ZEROS : lab < -1 || lab >= b.V ? NANS : st.y == -INFINITY ? ZEROS : 0;
+  if (same != 0) return part.fill(same == ZEROS ? 0.0f : NAN);
+  part.load();
+  const float H = ge != 0.0f ? ent : 0.0f;
   const RowGrad g{st.x, b.c, st.y * LOG2E, -ge * LN2 * b.invtau, -fmaf(ge, H, gl) * b.invtau};
   const float at = gl * b.invtau;
-  bwd_columns<Ty, ACC>(row - skew, out - skew, skew, lo, hi, fill, [&](float (&x)[Ty::VE], int i0) {
+  part.store([&](float (&x)[Ty::VE], int i0) {
 #pragma unroll
     for (int j = 0; j < Ty::VE; ++j) x[j] = g(x[j]);
     const int here = lab + skew - i0;
@@ -1113,34 +1149,34 @@ __global__ __launch_bounds__(256) void logprobs_bwd_kernel(BwdArgs b, LogprobGra
   });
 }
 
-template <class Ty, bool ACC>
+template <class Ty, int TI, bool ACC>
 __global__ __launch_bounds__(256) void distill_bwd_kernel(BwdArgs b, const typename Ty::E* logits,
                                                           const int* __restrict__ idx,
                                                           const float* __restrict__ teacher,
                                                           const float* __restrict__ stats,
                                                           const float* __restrict__ g_loss, typename Ty::E* d_logits) {
   typedef typename Ty::E E;
+  typedef Tile<Ty, BU_DISTILL, ACC> Part;
   __shared__ __align__(16) int lidx[64 * TI + 4];
   __shared__ __align__(16) float lq[64 * TI + 4];
-  const int t = blockIdx.x / b.S, sl = blockIdx.x % b.S, tid = threadIdx.x;
+  const Place at_tile(b.S);
+  const int t = at_tile.t, tid = threadIdx.x;
   const E* row = logits + (size_t)t * b.ld;
   E* out = d_logits + (size_t)t * b.ldg;
   const int skew = skew_of<Ty>(row);
-  const int lo = sl * b.slice, hi = min(b.V + skew, lo + b.slice);
-  const float2 st = *reinterpret_cast<const float2*>(stats + 2 * (size_t)t);
+  Part part(row, out, skew, at_tile.tile * Part::SIZE, b.V);
   const float g = g_loss[t];
+  const float2 st = *reinterpret_cast<const float2*>(stats + 2 * (size_t)t);
   // (each wave computes the list; all get the same)
-  const Teacher te(idx + (size_t)t * b.k, teacher + (size_t)t * b.k, b.k, b.V, b.invtau);
-  int fill = FILL_NONE;
-  if (g == 0.0f) fill = FILL_ZERO;
-  else if (te.bad) fill = FILL_NAN;
-  else if (!te.any || st.y == -INFINITY) fill = FILL_ZERO;
+  const Teacher<TI> te(idx + (size_t)t * b.k, teacher + (size_t)t * b.k, b.k, b.V, b.invtau);
+  const int same = g == 0.0f ? ZEROS : te.bad ? NANS : !te.any || st.y == -INFINITY ? ZEROS : 0;
+  if (same != 0) return part.fill(same == ZEROS ? 0.0f : NAN);
   const RowGrad r{st.x, b.c, st.y * LOG2E, 0.0f, g * b.invtau};
-  // the entries of this slice, in list order
+  // the entries of this tile, in list order
   int n = 0;
 #pragma unroll
   for (int i = 0; i < TI; ++i) {
-    const bool in = te.ix[i] >= 0 && te.ix[i] + skew >= lo && te.ix[i] + skew < hi;
+    const bool in = te.ix[i] >= 0 && te.ix[i] + skew >= part.lo && te.ix[i] + skew < part.hi;
     const unsigned long long mask = __ballot(in);
     if (in && tid < 64) {
       lidx[n + below(mask)] = te.ix[i];
@@ -1152,10 +1188,9 @@ __global__ __launch_bounds__(256) void distill_bwd_kernel(BwdArgs b, const typen
   __syncthreads();
   // one entry per thread: the column's gradient p - sum of its q.  Read
   // before anything is written (d_logits may be logits)
-  const bool listed = fill == FILL_NONE && tid < n;
-  const int mine = listed ? lidx[tid] : 0;
+  const int mine = tid < n ? lidx[tid] : 0;
   float v = 0.0f;
-  if (listed) {
+  if (tid < n) {
     v = exp2_hw(r.log2p(Ty::get(row[mine])));
     float q = 0.0f;
     for (int j = 0; j < n; j += 4) {
@@ -1170,12 +1205,13 @@ __global__ __launch_bounds__(256) void distill_bwd_kernel(BwdArgs b, const typen
     if constexpr (ACC) v += Ty::get(out[mine]);
   }
   __syncthreads();
-  bwd_columns<Ty, ACC>(row - skew, out - skew, skew, lo, hi, fill, [&](float (&x)[Ty::VE], int) {
+  part.load();  // (ahead of a barrier they would only be waited for there)
+  part.store([&](float (&x)[Ty::VE], int) {
 #pragma unroll
     for (int j = 0; j < Ty::VE; ++j) x[j] = exp2_hw(r.log2p(x[j])) * r.gb;
   });
-  __syncthreads();  // the slice's own writes come before the listed columns'
-  if (listed) out[mine] = Ty::put(v);
+  __syncthreads();  // the tile's own writes come before the listed columns'
+  if (tid < n) out[mine] = Ty::put(v);
 }
 
 // --------------------------------------------------------------- host side
@@ -1227,10 +1263,10 @@ template <class Ty>
 FinishArgs finish_args(const VocabDims& d, int S) {
   return FinishArgs{d.V, d.k, S, blocks_of<Ty>(d), d.ld, d.invtau * LOG2E, d.invtau};
 }
-template <class Ty>
+template <class Ty, int BU>
 BwdArgs bwd_args(const VocabDims& d) {
-  const Split s = split(d.T, positions<Ty>(d), bwd_tile<Ty>(), 8192);
-  return BwdArgs{d.V, d.k, s.S, s.slice, d.ld, d.ldg, d.invtau * LOG2E, d.invtau};
+  const int tile = bwd_tile<Ty, BU>();
+  return BwdArgs{d.V, d.k, (positions<Ty>(d) + tile - 1) / tile, d.ld, d.ldg, d.invtau * LOG2E, d.invtau};
 }
 
 template <class Ty, bool ENT, bool TOP>
@@ -1262,33 +1298,42 @@ void logprobs_launch(const VocabDims& d, const LogprobPtrs& q, char* ws, hipStre
   else q.entropy ? logprobs_launch<Ty, true, false>(d, q, ws, st) : logprobs_launch<Ty, false, false>(d, q, ws, st);
 }
 
-template <class Ty>
+template <class Ty, int TI>
 void distill_launch(const VocabDims& d, const DistillPtrs& q, char* ws, hipStream_t st) {
   if (whole_rows<Ty>(d, false)) {
-    hipLaunchKernelGGL((distill_row_kernel<Ty>), dim3(d.T), dim3(256), 0, st, finish_args<Ty>(d, 1), q);
+    hipLaunchKernelGGL((distill_row_kernel<Ty, TI>), dim3(d.T), dim3(256), 0, st, finish_args<Ty>(d, 1), q);
     return;
   }
   const Split s = fwd_split<Ty>(d);
   stats_launch<Ty, false, false>(d, s, q.logits, ws, st);
-  hipLaunchKernelGGL((distill_finish_kernel<Ty>), dim3(d.T), dim3(64), 0, st, finish_args<Ty>(d, s.S), q,
+  hipLaunchKernelGGL((distill_finish_kernel<Ty, TI>), dim3(d.T), dim3(64), 0, st, finish_args<Ty>(d, s.S), q,
                      reinterpret_cast<const float4*>(ws));
 }
 
 template <class Ty>
 void logprobs_bwd_launch(const VocabDims& d, const LogprobGradPtrs& q, hipStream_t st) {
-  const BwdArgs b = bwd_args<Ty>(d);
+  const BwdArgs b = bwd_args<Ty, BU_LOGPROBS>(d);
   auto* f = d.accumulate ? logprobs_bwd_kernel<Ty, true> : logprobs_bwd_kernel<Ty, false>;
   hipLaunchKernelGGL(f, dim3((size_t)d.T * b.S), dim3(256), 0, st, b, q);
 }
 
-template <class Ty>
+template <class Ty, int TI>
 void distill_bwd_launch(const VocabDims& d, const void* logits, const int* idx, const float* teacher,
                         const float* stats, const float* g_loss, void* d_logits, hipStream_t st) {
   typedef typename Ty::E E;
-  const BwdArgs b = bwd_args<Ty>(d);
-  auto* f = d.accumulate ? distill_bwd_kernel<Ty, true> : distill_bwd_kernel<Ty, false>;
+  const BwdArgs b = bwd_args<Ty, BU_DISTILL>(d);
+  auto* f = d.accumulate ? distill_bwd_kernel<Ty, TI, true> : distill_bwd_kernel<Ty, TI, false>;
   hipLaunchKernelGGL(f, dim3((size_t)d.T * b.S), dim3(256), 0, st, b, static_cast<const E*>(logits), idx, teacher,
                      stats, g_loss, static_cast<E*>(d_logits));
+}
+
+// f(type, entries of a teacher list per lane)
+template <class F>
+void teacher_shape(const VocabDims& d, F&& f) {
+  using One = std::integral_constant<int, 1>;
+  using Four = std::integral_constant<int, 4>;
+  if (d.f32) d.k <= 64 ? f(F32{}, One{}) : f(F32{}, Four{});
+  else d.k <= 64 ? f(Bf16{}, One{}) : f(Bf16{}, Four{});
 }
 
 }  // namespace
@@ -1316,15 +1361,16 @@ hipError_t launch_distill(const VocabDims& d, const void* logits, const int* idx
                           float* stats, char* ws, hipStream_t st) {
   ProfScope prof(st, "vocab.distill");
   const DistillPtrs q{logits, idx, teacher, loss, stats};
-  d.f32 ? distill_launch<F32>(d, q, ws, st) : distill_launch<Bf16>(d, q, ws, st);
+  teacher_shape(d, [&](auto ty, auto ti) { distill_launch<decltype(ty), decltype(ti)::value>(d, q, ws, st); });
   return hipGetLastError();
 }
 
 hipError_t launch_distill_bwd(const VocabDims& d, const void* logits, const int* idx, const float* teacher,
                               const float* stats, const float* g_loss, void* d_logits, hipStream_t st) {
   ProfScope prof(st, "vocab.distill_bwd");
-  d.f32 ? distill_bwd_launch<F32>(d, logits, idx, teacher, stats, g_loss, d_logits, st)
-        : distill_bwd_launch<Bf16>(d, logits, idx, teacher, stats, g_loss, d_logits, st);
+  teacher_shape(d, [&](auto ty, auto ti) {
+    distill_bwd_launch<decltype(ty), decltype(ti)::value>(d, logits, idx, teacher, stats, g_loss, d_logits, st);
+  });
   return hipGetLastError();
 }
 
