@@ -93,15 +93,17 @@ template <class E>
 __device__ __forceinline__ u32x4 load16(const E* p) {
   return *reinterpret_cast<const u32x4_row*>(p);
 }
-// a vector that is read or written once: it need not displace what the caches
-// hold (4096 x 151936 bf16 rows summed in 180 instead of 203 us)
-template <class E>
+// a vector that is read or written once; NT: it need not displace what the
+// caches hold (STREAM_BYTES below)
+template <bool NT, class E>
 __device__ __forceinline__ u32x4 stream16(const E* p) {
-  return __builtin_nontemporal_load(reinterpret_cast<const u32x4_row*>(p));
+  const u32x4_row* v = reinterpret_cast<const u32x4_row*>(p);
+  return NT ? __builtin_nontemporal_load(v) : *v;
 }
-template <class E>
+template <bool NT, class E>
 __device__ __forceinline__ void stream16(E* p, const u32x4& v) {
-  __builtin_nontemporal_store(v, reinterpret_cast<u32x4_row*>(p));
+  if constexpr (NT) __builtin_nontemporal_store(v, reinterpret_cast<u32x4_row*>(p));
+  else *reinterpret_cast<u32x4_row*>(p) = v;
 }
 
 // elements that a row is taken early
@@ -350,11 +352,11 @@ __device__ __forceinline__ float fwd_vector(const float* x, float c, Triple& a) 
 
 // vector at position i0 of a row's positions [skew, hi), -inf elsewhere; `row`
 // is where position 0 would be
-template <class Ty>
+template <class Ty, bool NT>
 __device__ __forceinline__ void read_vector(const typename Ty::E* row, int i0, int skew, int hi, float* y) {
   constexpr int VE = Ty::VE;
   if (i0 >= skew && i0 + VE <= hi) {
-    Ty::unpack(stream16(row + i0), y);
+    Ty::unpack(stream16<NT>(row + i0), y);
   } else {
 #pragma unroll
     for (int j = 0; j < VE; ++j) y[j] = i0 + j >= skew && i0 + j < hi ? Ty::get(row[i0 + j]) : -INFINITY;
@@ -363,7 +365,7 @@ __device__ __forceinline__ void read_vector(const typename Ty::E* row, int i0, i
 
 // The triple of positions [lo, hi) of a row by a workgroup, the same in every
 // thread; lo starts a step.
-template <class Ty, bool ENT, class K>
+template <class Ty, bool ENT, bool NT, class K>
 __device__ __forceinline__ Triple slice_triple(const typename Ty::E* row, int skew, int lo, int hi, float c, K& keep) {
   constexpr int VE = Ty::VE, TILE = fwd_tile<Ty>();
   __shared__ float sh[4][3];
@@ -375,7 +377,7 @@ __device__ __forceinline__ Triple slice_triple(const typename Ty::E* row, int sk
   if (base + TILE <= hi) {
 #pragma unroll
     for (int u = 0; u < FU; ++u)
-      if (u > 0 || lo + tid > 0 || skew == 0) v[u] = stream16(row + base + (u * 256 + tid) * VE);
+      if (u > 0 || lo + tid > 0 || skew == 0) v[u] = stream16<NT>(row + base + (u * 256 + tid) * VE);
     if (skew != 0 && lo + tid == 0) {  // position 0 is no column: -inf before the row's first seven
       const u32x4 f = load16(row + 1);
       v[0] = u32x4{f[0] << 16 | 0xFF80u, f[1] << 16 | f[0] >> 16, f[2] << 16 | f[1] >> 16, f[3] << 16 | f[2] >> 16};
@@ -387,14 +389,14 @@ __device__ __forceinline__ Triple slice_triple(const typename Ty::E* row, int sk
     // the next step's loads fly during this one's sums
     if (base + 2 * TILE <= hi) {
 #pragma unroll
-      for (int u = 0; u < FU; ++u) v[u] = stream16(row + base + TILE + (u * 256 + tid) * VE);
+      for (int u = 0; u < FU; ++u) v[u] = stream16<NT>(row + base + TILE + (u * 256 + tid) * VE);
     }
     keep.add(fwd_step<Ty, ENT>(
-        x, c, a, [&](int u, float* y) { read_vector<Ty>(row, base + (u * 256 + tid) * VE, skew, hi, y); }));
+        x, c, a, [&](int u, float* y) { read_vector<Ty, NT>(row, base + (u * 256 + tid) * VE, skew, hi, y); }));
   }
   if (base < hi) {
 #pragma unroll
-    for (int u = 0; u < FU; ++u) read_vector<Ty>(row, base + (u * 256 + tid) * VE, skew, hi, x + u * VE);
+    for (int u = 0; u < FU; ++u) read_vector<Ty, NT>(row, base + (u * 256 + tid) * VE, skew, hi, x + u * VE);
     float bm = -INFINITY;
 #pragma unroll
     for (int u = 0; u < FU; ++u)
@@ -417,7 +419,7 @@ __device__ __forceinline__ Triple slice_triple(const typename Ty::E* row, int sk
 
 // part[t S + sl]: the triple of positions [sl slice, (sl + 1) slice) of row t;
 // blocks: the maxima of the row's blocks, rows of them nb apart
-template <class Ty, bool ENT, bool TOP>
+template <class Ty, bool ENT, bool TOP, bool NT>
 __global__ __launch_bounds__(256) void vocab_stats_kernel(const typename Ty::E* __restrict__ logits, long ld, int V,
                                                           int S, int slice, float c, float4* __restrict__ part,
                                                           typename Blocks<Ty>::Key* __restrict__ blocks, int nb) {
@@ -433,10 +435,10 @@ __global__ __launch_bounds__(256) void vocab_stats_kernel(const typename Ty::E* 
     __shared__ __align__(16) Key kept[4][KEPT * KeepOut<Ty>::PW];
     KeepOut<Ty> keep{kept[tid >> 6],
                      blocks + (size_t)t * nb + lo / fwd_tile<Ty>() * B::PER_TILE + (tid & ~63) / B::RUN, 0};
-    a = slice_triple<Ty, ENT>(row, skew, lo, hi, c, keep);
+    a = slice_triple<Ty, ENT, NT>(row, skew, lo, hi, c, keep);
   } else {
     KeepNone keep;
-    a = slice_triple<Ty, ENT>(row, skew, lo, hi, c, keep);
+    a = slice_triple<Ty, ENT, NT>(row, skew, lo, hi, c, keep);
   }
   if (tid == 0) part[blockIdx.x] = make_float4(a.m, a.s, a.w, 0.0f);
 }
@@ -854,7 +856,7 @@ __global__ __launch_bounds__(256, 4) void logprobs_finish_kernel(
 // A whole row by one workgroup, for rows enough to fill the chip: no triples
 // and no block maxima through memory (writing 20 MB of them beside a read of
 // 1.2 GB took 25 us).
-template <class Ty, bool ENT, bool TOP>
+template <class Ty, bool ENT, bool TOP, bool NT>
 __global__ __launch_bounds__(256, 6) void logprobs_row_kernel(FinishArgs f, LogprobPtrs q) {
   typedef typename Blocks<Ty>::Key Key;
   const int t = blockIdx.x;
@@ -866,12 +868,12 @@ __global__ __launch_bounds__(256, 6) void logprobs_row_kernel(FinishArgs f, Logp
     __shared__ __align__(16) Key kept[MAXKEYS];
     static_assert(sizeof(kept) >= QCAP * 8, "the list of candidates takes the keys' place");
     KeepRow<Ty> keep{kept};
-    const Triple a = slice_triple<Ty, ENT>(row, skew, 0, f.V + skew, f.c, keep);
+    const Triple a = slice_triple<Ty, ENT, NT>(row, skew, 0, f.V + skew, f.c, keep);
     logprobs_finish<Ty, true>(f, q, t, g, a, reinterpret_cast<const u32x4*>(kept),
                                  reinterpret_cast<unsigned long long*>(kept));
   } else {
     KeepNone keep;
-    const Triple a = slice_triple<Ty, ENT>(row, skew, 0, f.V + skew, f.c, keep);
+    const Triple a = slice_triple<Ty, ENT, NT>(row, skew, 0, f.V + skew, f.c, keep);
     logprobs_finish<Ty, false>(f, q, t, g, a, nullptr, nullptr);
   }
 }
@@ -968,13 +970,13 @@ __global__ __launch_bounds__(64) void distill_finish_kernel(FinishArgs f, Distil
   distill_finish<Ty, TI>(f, q, t, te, x, row_triple(part + (size_t)t * f.S, f.S, f.c));
 }
 
-template <class Ty, int TI>
+template <class Ty, int TI, bool NT>
 __global__ __launch_bounds__(256) void distill_row_kernel(FinishArgs f, DistillPtrs q) {
   const int t = blockIdx.x;
   const typename Ty::E* row = static_cast<const typename Ty::E*>(q.logits) + (size_t)t * f.ld;
   const int skew = skew_of<Ty>(row);
   KeepNone keep;
-  const Triple a = slice_triple<Ty, false>(row - skew, skew, 0, f.V + skew, f.c, keep);
+  const Triple a = slice_triple<Ty, false, NT>(row - skew, skew, 0, f.V + skew, f.c, keep);
   if (threadIdx.x >= 64) return;
   float x[TI];
   const Teacher<TI> te = teacher_row<Ty, TI>(f, q, t, x);
@@ -1012,7 +1014,7 @@ struct RowGrad {
 
 // A workgroup's tile of a row: positions [lo, hi), from `skew` on where lo is
 // 0; row, out: where position 0 would be.
-template <class Ty, int BU, bool ACC>
+template <class Ty, int BU, bool ACC, bool NT>
 struct Tile {
   typedef typename Ty::E E;
   static constexpr int VE = Ty::VE, SIZE = bwd_tile<Ty, BU>();
@@ -1034,8 +1036,8 @@ struct Tile {
     if (!full()) return;
 #pragma unroll
     for (int u = 0; u < BU; ++u) {
-      v[u] = stream16(row + first(u));
-      if constexpr (ACC) old[u] = stream16(out + first(u));
+      v[u] = stream16<NT>(row + first(u));
+      if constexpr (ACC) old[u] = stream16<NT>(out + first(u));
     }
   }
 
@@ -1051,7 +1053,7 @@ struct Tile {
         grad(x, first(u));
 #pragma unroll
         for (int j = 0; j < VE; ++j) x[j] += ACC ? o[j] : 0.0f;
-        stream16(out + first(u), Ty::pack(x));
+        stream16<NT>(out + first(u), Ty::pack(x));
       }
       return;
     }
@@ -1060,8 +1062,8 @@ struct Tile {
       const int i0 = first(u);
       float x[VE], o[VE];
       if (whole(i0)) {
-        Ty::unpack(stream16(row + i0), x);
-        if constexpr (ACC) Ty::unpack(stream16(out + i0), o);
+        Ty::unpack(stream16<NT>(row + i0), x);
+        if constexpr (ACC) Ty::unpack(stream16<NT>(out + i0), o);
       } else {
 #pragma unroll
         for (int j = 0; j < VE; ++j) {
@@ -1074,7 +1076,7 @@ struct Tile {
 #pragma unroll
       for (int j = 0; j < VE; ++j) x[j] += ACC ? o[j] : 0.0f;
       if (whole(i0)) {
-        stream16(out + i0, Ty::pack(x));
+        stream16<NT>(out + i0, Ty::pack(x));
       } else {
 #pragma unroll
         for (int j = 0; j < VE; ++j)
@@ -1093,7 +1095,7 @@ struct Tile {
     for (int u = 0; u < BU; ++u) {
       const int i0 = first(u);
       if (whole(i0)) {
-        stream16(out + i0, Ty::pack(x));
+        stream16<NT>(out + i0, Ty::pack(x));
       } else {
 #pragma unroll
         for (int j = 0; j < VE; ++j)
@@ -1118,10 +1120,10 @@ struct BwdArgs {
   float c, invtau;
 };
 
-template <class Ty, bool ACC>
+template <class Ty, bool ACC, bool NT>
 __global__ __launch_bounds__(256) void logprobs_bwd_kernel(BwdArgs b, LogprobGradPtrs q) {
   typedef typename Ty::E E;
-  typedef Tile<Ty, BU_LOGPROBS, ACC> Part;
+  typedef Tile<Ty, BU_LOGPROBS, ACC, NT> Part;
   const Place at_tile(b.S);
   const int t = at_tile.t;
   const E* row = static_cast<const E*>(q.logits) + (size_t)t * b.ld;
@@ -1149,14 +1151,14 @@ __global__ __launch_bounds__(256) void logprobs_bwd_kernel(BwdArgs b, LogprobGra
   });
 }
 
-template <class Ty, int TI, bool ACC>
+template <class Ty, int TI, bool ACC, bool NT>
 __global__ __launch_bounds__(256) void distill_bwd_kernel(BwdArgs b, const typename Ty::E* logits,
                                                           const int* __restrict__ idx,
                                                           const float* __restrict__ teacher,
                                                           const float* __restrict__ stats,
                                                           const float* __restrict__ g_loss, typename Ty::E* d_logits) {
   typedef typename Ty::E E;
-  typedef Tile<Ty, BU_DISTILL, ACC> Part;
+  typedef Tile<Ty, BU_DISTILL, ACC, NT> Part;
   __shared__ __align__(16) int lidx[64 * TI + 4];
   __shared__ __align__(16) float lq[64 * TI + 4];
   const Place at_tile(b.S);
@@ -1263,49 +1265,69 @@ template <class Ty>
 FinishArgs finish_args(const VocabDims& d, int S) {
   return FinishArgs{d.V, d.k, S, blocks_of<Ty>(d), d.ld, d.invtau * LOG2E, d.invtau};
 }
+// Logits of more bytes than this (and their gradients) are streamed past the
+// caches; 256 MB of them in front of the memory keep fewer for whoever comes
+// next.  Measured, bf16, 151936 columns, us kept / streamed, logits just
+// written by another kernel: 256 rows (78 MB) distillation 16.5 / 21.3, policy
+// gradient 23.3 / 23.5; 512 rows (156 MB) 23.0 / 25.8 and 48.3 / 38.4; 1024
+// rows (311 MB) 63.2 / 52.7 and 100.3 / 80.2.
+constexpr long STREAM_BYTES = 128L << 20;
+bool streamed(const VocabDims& d) { return (long)d.T * d.V * (d.f32 ? 4 : 2) > STREAM_BYTES; }
+// f(true_type) or f(false_type)
+template <class F>
+void choose(bool b, F&& f) {
+  b ? f(std::true_type{}) : f(std::false_type{});
+}
+
 template <class Ty, int BU>
 BwdArgs bwd_args(const VocabDims& d) {
   const int tile = bwd_tile<Ty, BU>();
   return BwdArgs{d.V, d.k, (positions<Ty>(d) + tile - 1) / tile, d.ld, d.ldg, d.invtau * LOG2E, d.invtau};
 }
 
-template <class Ty, bool ENT, bool TOP>
+template <class Ty, bool ENT, bool TOP, bool NT>
 void stats_launch(const VocabDims& d, const Split& s, const void* logits, char* ws, hipStream_t st) {
   typedef typename Ty::E E;
-  hipLaunchKernelGGL((vocab_stats_kernel<Ty, ENT, TOP>), dim3((size_t)d.T * s.S), dim3(256), 0, st,
+  hipLaunchKernelGGL((vocab_stats_kernel<Ty, ENT, TOP, NT>), dim3((size_t)d.T * s.S), dim3(256), 0, st,
                      static_cast<const E*>(logits), d.ld, d.V, s.S, s.slice, d.invtau * LOG2E,
                      reinterpret_cast<float4*>(ws),
                      reinterpret_cast<typename Blocks<Ty>::Key*>(ws + part_bytes<Ty>(d)), blocks_of<Ty>(d));
 }
 
-template <class Ty, bool ENT, bool TOP>
+template <class Ty, bool ENT, bool TOP, bool NT>
 void logprobs_launch(const VocabDims& d, const LogprobPtrs& q, char* ws, hipStream_t st) {
   if (whole_rows<Ty>(d, TOP)) {
-    hipLaunchKernelGGL((logprobs_row_kernel<Ty, ENT, TOP>), dim3(d.T), dim3(256), 0, st, finish_args<Ty>(d, 1), q);
+    hipLaunchKernelGGL((logprobs_row_kernel<Ty, ENT, TOP, NT>), dim3(d.T), dim3(256), 0, st, finish_args<Ty>(d, 1),
+                       q);
     return;
   }
   const Split s = fwd_split<Ty>(d);
   const float4* part = reinterpret_cast<const float4*>(ws);
   const auto* blocks = reinterpret_cast<const typename Blocks<Ty>::Key*>(ws + part_bytes<Ty>(d));
   const FinishArgs f = finish_args<Ty>(d, s.S);
-  stats_launch<Ty, ENT, TOP>(d, s, q.logits, ws, st);
+  stats_launch<Ty, ENT, TOP, NT>(d, s, q.logits, ws, st);
   hipLaunchKernelGGL((logprobs_finish_kernel<Ty, TOP>), dim3(d.T), dim3(256), 0, st, f, q, part, blocks);
 }
 
 template <class Ty>
 void logprobs_launch(const VocabDims& d, const LogprobPtrs& q, char* ws, hipStream_t st) {
-  if (d.k > 0) q.entropy ? logprobs_launch<Ty, true, true>(d, q, ws, st) : logprobs_launch<Ty, false, true>(d, q, ws, st);
-  else q.entropy ? logprobs_launch<Ty, true, false>(d, q, ws, st) : logprobs_launch<Ty, false, false>(d, q, ws, st);
+  choose(q.entropy != nullptr, [&](auto ent) {
+    choose(d.k > 0, [&](auto top) {
+      choose(streamed(d), [&](auto nt) {
+        logprobs_launch<Ty, decltype(ent)::value, decltype(top)::value, decltype(nt)::value>(d, q, ws, st);
+      });
+    });
+  });
 }
 
-template <class Ty, int TI>
+template <class Ty, int TI, bool NT>
 void distill_launch(const VocabDims& d, const DistillPtrs& q, char* ws, hipStream_t st) {
   if (whole_rows<Ty>(d, false)) {
-    hipLaunchKernelGGL((distill_row_kernel<Ty, TI>), dim3(d.T), dim3(256), 0, st, finish_args<Ty>(d, 1), q);
+    hipLaunchKernelGGL((distill_row_kernel<Ty, TI, NT>), dim3(d.T), dim3(256), 0, st, finish_args<Ty>(d, 1), q);
     return;
   }
   const Split s = fwd_split<Ty>(d);
-  stats_launch<Ty, false, false>(d, s, q.logits, ws, st);
+  stats_launch<Ty, false, false, NT>(d, s, q.logits, ws, st);
   hipLaunchKernelGGL((distill_finish_kernel<Ty, TI>), dim3(d.T), dim3(64), 0, st, finish_args<Ty>(d, s.S), q,
                      reinterpret_cast<const float4*>(ws));
 }
@@ -1313,8 +1335,12 @@ void distill_launch(const VocabDims& d, const DistillPtrs& q, char* ws, hipStrea
 template <class Ty>
 void logprobs_bwd_launch(const VocabDims& d, const LogprobGradPtrs& q, hipStream_t st) {
   const BwdArgs b = bwd_args<Ty, BU_LOGPROBS>(d);
-  auto* f = d.accumulate ? logprobs_bwd_kernel<Ty, true> : logprobs_bwd_kernel<Ty, false>;
-  hipLaunchKernelGGL(f, dim3((size_t)d.T * b.S), dim3(256), 0, st, b, q);
+  choose(d.accumulate, [&](auto acc) {
+    choose(streamed(d), [&](auto nt) {
+      hipLaunchKernelGGL((logprobs_bwd_kernel<Ty, decltype(acc)::value, decltype(nt)::value>),
+                         dim3((size_t)d.T * b.S), dim3(256), 0, st, b, q);
+    });
+  });
 }
 
 template <class Ty, int TI>
@@ -1322,9 +1348,13 @@ void distill_bwd_launch(const VocabDims& d, const void* logits, const int* idx, 
                         const float* stats, const float* g_loss, void* d_logits, hipStream_t st) {
   typedef typename Ty::E E;
   const BwdArgs b = bwd_args<Ty, BU_DISTILL>(d);
-  auto* f = d.accumulate ? distill_bwd_kernel<Ty, TI, true> : distill_bwd_kernel<Ty, TI, false>;
-  hipLaunchKernelGGL(f, dim3((size_t)d.T * b.S), dim3(256), 0, st, b, static_cast<const E*>(logits), idx, teacher,
-                     stats, g_loss, static_cast<E*>(d_logits));
+  choose(d.accumulate, [&](auto acc) {
+    choose(streamed(d), [&](auto nt) {
+      hipLaunchKernelGGL((distill_bwd_kernel<Ty, TI, decltype(acc)::value, decltype(nt)::value>),
+                         dim3((size_t)d.T * b.S), dim3(256), 0, st, b, static_cast<const E*>(logits), idx, teacher,
+                         stats, g_loss, static_cast<E*>(d_logits));
+    });
+  });
 }
 
 // f(type, entries of a teacher list per lane)
@@ -1361,7 +1391,11 @@ hipError_t launch_distill(const VocabDims& d, const void* logits, const int* idx
                           float* stats, char* ws, hipStream_t st) {
   ProfScope prof(st, "vocab.distill");
   const DistillPtrs q{logits, idx, teacher, loss, stats};
-  teacher_shape(d, [&](auto ty, auto ti) { distill_launch<decltype(ty), decltype(ti)::value>(d, q, ws, st); });
+  teacher_shape(d, [&](auto ty, auto ti) {
+    choose(streamed(d), [&](auto nt) {
+      distill_launch<decltype(ty), decltype(ti)::value, decltype(nt)::value>(d, q, ws, st);
+    });
+  });
   return hipGetLastError();
 }
 
