@@ -354,7 +354,7 @@ int32_t oft_logprob_diff(int32_t T, int32_t V, const float* logits_actor, const 
  * OFT_EUNSUPPORTED) and k <= V (else OFT_ESHAPE); oft_distill_topk and its
  * backward: 1 <= k <= OFT_MAX_TEACHER (else OFT_EUNSUPPORTED);
  * oft_token_logprobs_bwd ignores k.  Size range (else OFT_EUNSUPPORTED):
- * T <= 2^22, V <= 2^24, T ld and T ld_grad < 2^40. */
+ * T <= 2^22, V <= 2^24, T V <= 2^34, T ld and T ld_grad < 2^40. */
 typedef struct {
   int32_t T, V;       /* rows, vocabulary                                    */
   int32_t dtype;      /* of logits and d_logits                              */

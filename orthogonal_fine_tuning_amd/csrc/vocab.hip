@@ -527,41 +527,35 @@ __device__ int cut(unsigned long long* list, int n, int k, uint32_t& floor) {
 
 template <class Ty>
 __device__ void select_row(const typename Ty::E* row, int V, int k, uint32_t floor, unsigned long long* list) {
-  constexpr int VE = Ty::VE, U = 4;
+  constexpr int VE = Ty::VE;
   static_assert(64 * VE <= QCAP / 2, "a vector per lane fits behind a list that is not cut");
   const int lane = threadIdx.x & 63;
   int n = 0;
-  for (int base = 0; base < V; base += 64 * VE * U) {
-    float x[U][VE];
+#pragma unroll 1
+  for (int base = 0; base < V; base += 64 * VE) {
+    float x[VE];
+    const int i0 = base + lane * VE;
+    if (i0 + VE <= V) {
+      Ty::unpack(load16(row + i0), x);
+    } else {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i0 = base + (u * 64 + lane) * VE;
-      if (i0 + VE <= V) {
-        Ty::unpack(load16(row + i0), x[u]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < VE; ++j) x[u][j] = i0 + j < V ? Ty::get(row[i0 + j]) : 0.0f;
-      }
+      for (int j = 0; j < VE; ++j) x[j] = i0 + j < V ? Ty::get(row[i0 + j]) : 0.0f;
     }
+    int hit = 0, at = n, more = 0;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i0 = base + (u * 64 + lane) * VE;
-      bool take[VE];
-      int at = n, more = 0;
-#pragma unroll
-      for (int j = 0; j < VE; ++j) {
-        take[j] = i0 + j < V && ordered(x[u][j]) >= floor;
-        const unsigned long long mask = __ballot(take[j]);
-        at += below(mask);
-        more += __popcll(mask);
-      }
-      if (more == 0) continue;
-#pragma unroll
-      for (int j = 0; j < VE; ++j)
-        if (take[j]) list[at++] = candidate(ordered(x[u][j]), i0 + j);
-      n += more;
-      if (n > QCAP / 2) n = cut(list, n, k, floor);
+    for (int j = 0; j < VE; ++j) {
+      const bool take = i0 + j < V && ordered(x[j]) >= floor;
+      const unsigned long long mask = __ballot(take);
+      hit |= take ? 1 << j : 0;
+      at += below(mask);
+      more += __popcll(mask);
     }
+    if (more == 0) continue;
+#pragma unroll
+    for (int j = 0; j < VE; ++j)
+      if (hit >> j & 1) list[at++] = candidate(ordered(x[j]), i0 + j);
+    n += more;
+    if (n > QCAP / 2) n = cut(list, n, k, floor);
   }
   cut(list, n, k, floor);
 }
@@ -990,13 +984,12 @@ __global__ __launch_bounds__(256) void distill_row_kernel(FinishArgs f, DistillP
 //   distill   ga = 0, gb = g / tau (the listed columns follow)
 //
 // A workgroup has one tile of a row, BU vectors a thread: loaded at once,
-// computed, stored, with nothing kept in the caches.  Time goes by the bytes
-// (4096 x 151936 bf16, read and written, us): 477 with cached loads and
-// stores and two slices a row, 401 streamed with a tile of 4 vectors, 381
-// of 2, 408 of 1.  The distillation's workgroups also read the teacher's
-// list, which 3 vectors repay better (192 us at half the rows; 210 of 2, 198
-// of 4).
-constexpr int BU_LOGPROBS = 2, BU_DISTILL = 3;
+// computed, stored.  Time goes by the bytes (4096 x 151936 bf16, read and
+// written, us): 477 with two slices a row, cached, 449 with a tile a workgroup,
+// 401 of 4 vectors streamed, 381 of 2, 408 of 1.  The distillation's
+// workgroups also read the teacher's list, which 4 vectors repay better (198 us
+// at half the rows; 210 of 2).
+constexpr int BU_LOGPROBS = 2, BU_DISTILL = 4;
 
 template <class Ty, int BU>
 constexpr int bwd_tile() {

@@ -25,7 +25,9 @@ int32_t validate_vocab(const oft_vocab_desc* d) {
   // (a NaN temperature fails the comparison)
   if (!(d->temperature >= 0x1p-20f && d->temperature <= 0x1p20f)) return OFT_EINVAL;
   if (d->dtype != OFT_DT_BF16 && d->dtype != OFT_DT_F32) return OFT_EDTYPE;
-  if (d->T > (1 << 22) || d->V > (1 << 24)) return OFT_EUNSUPPORTED;
+  // a backward workgroup takes 2048 elements or more of a row: at most 2^24 of
+  // them, what a launch can hold of 256 threads each
+  if (d->T > (1 << 22) || d->V > (1 << 24) || (int64_t)d->T * d->V > (1LL << 34)) return OFT_EUNSUPPORTED;
   // (the first two comparisons keep the products inside 64 bits)
   if (d->ld >= (1LL << 40) || d->ld_grad >= (1LL << 40)) return OFT_EUNSUPPORTED;
   if (d->T * d->ld >= (1LL << 40) || d->T * d->ld_grad >= (1LL << 40)) return OFT_EUNSUPPORTED;

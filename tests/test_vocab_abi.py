@@ -50,6 +50,8 @@ def _query(d):
     (dict(T=(1 << 22) + 1), _lib.OFT_EUNSUPPORTED),
     (dict(V=1 << 24, ld=1 << 24, ld_grad=1 << 24), _lib.OFT_OK),
     (dict(V=(1 << 24) + 1, ld=1 << 25, ld_grad=1 << 25), _lib.OFT_EUNSUPPORTED),
+    (dict(T=1 << 20, V=1 << 14, ld=1 << 14, ld_grad=1 << 14), _lib.OFT_OK),
+    (dict(T=(1 << 20) + 1, V=1 << 14, ld=1 << 14, ld_grad=1 << 14), _lib.OFT_EUNSUPPORTED),
     (dict(T=2, ld=(1 << 39) - 1), _lib.OFT_OK),
     (dict(T=2, ld=1 << 39), _lib.OFT_EUNSUPPORTED),
     (dict(T=2, ld_grad=1 << 39), _lib.OFT_EUNSUPPORTED),
