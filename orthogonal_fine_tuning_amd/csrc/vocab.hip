@@ -684,12 +684,14 @@ __device__ __forceinline__ void logprobs_finish(const FinishArgs& f, const Logpr
       floor = kth<2, B::BITS>(best, f.k, slack);
     }
     floor = max(floor, 1u);  // (fewer than k groups: every block is above 0)
-    // First the candidates that reach the floor.  If they are too many, those
-    // above it: where ties did it (a masked or constant row) they are few, and
-    // the lowest columns at the floor itself complete them.
+    // First the candidates that reach the floor.  If their blocks hold too many,
+    // those that reach a higher one, from the blocks' vectors in 512 groups.
+    // Then those above the floor: where ties did it (a masked or constant row)
+    // they are few, and the lowest columns at the floor itself complete them.
     bool done = false;
     int n = 0;
-    for (uint32_t lo = floor; lo <= floor + 1 && !done; ++lo) {
+    uint32_t lo = floor;
+    for (int step = 0; step < 3 && !done; ++step) {
       __syncthreads();
       if (tid < 2) count[tid] = 0;
       __syncthreads();
@@ -724,7 +726,11 @@ __device__ __forceinline__ void logprobs_finish(const FinishArgs& f, const Logpr
       }
       __syncthreads();
       const int n1 = count[0];
-      if (nvec > HELD * NT || n1 > MAXBLK) continue;
+      if (nvec > HELD * NT || n1 > MAXBLK) {
+        lo = floor + 1;
+        continue;
+      }
+      best[0] = best[1] = 0;
       // key(x) >= lo as a comparison of numbers (false for NaN, which ranks as
       // -inf: a row with few others finds it at the floor)
       const uint32_t o = lo << (32 - B::BITS);
@@ -755,8 +761,13 @@ __device__ __forceinline__ void logprobs_finish(const FinishArgs& f, const Logpr
             float y[VE];
             Ty::unpack(x[u], y);
             int more = 0;
+            float top = y[0];
 #pragma unroll
-            for (int j = 0; j < VE; ++j) more += y[j] >= least ? 1 : 0;
+            for (int j = 0; j < VE; ++j) {
+              more += y[j] >= least ? 1 : 0;
+              top = fmaxf(top, y[j]);
+            }
+            best[u & 1] = max(best[u & 1], pos[u] < end ? B::key(top) : 0u);
             if (more > 0) {
               int at = atomicAdd(&count[1], more);
 #pragma unroll
@@ -774,6 +785,18 @@ __device__ __forceinline__ void logprobs_finish(const FinishArgs& f, const Logpr
       __syncthreads();
       n = count[1];
       done = n <= MAXCAND && (n >= f.k || lo > floor);
+      if (done) break;
+      if (step == 0 && n > MAXCAND) {
+        group[tid] = best[0];
+        group[NT + tid] = best[1];
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) best[j] = group[64 * j + lane];
+        floor = max(floor, kth<8, B::BITS>(best, f.k, slack));
+        lo = floor;
+      } else {
+        lo = floor + 1;
+      }
     }
     // at the floor itself, in order of columns
     for (int base = 0; done && n < f.k && base < f.V; base += NT * VE) {
@@ -936,8 +959,10 @@ __device__ __forceinline__ void distill_finish(const FinishArgs& f, const Distil
 #pragma unroll
   for (int i = 0; i < TI; ++i)
     if (te.ix[i] >= 0) {
-      const float lp = a.s == 0.0f ? -INFINITY : (x[i] - a.m) * f.invtau - l;
-      sum = fmaf(te.q[i], te.logq[i] - lp, sum);
+      // q (log q - log p), the far end of log p kept in range by its q (a
+      // listed column may be masked at the type's lowest value)
+      const float far = te.q[i] * f.invtau * (x[i] - a.m);
+      sum += a.s == 0.0f ? INFINITY : fmaf(te.q[i], te.logq[i] + l, -far);
     }
   sum = wave_sum(sum);
   if (threadIdx.x == 0) {

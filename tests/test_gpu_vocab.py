@@ -7,7 +7,7 @@ from oft_inputs import DenseConfig, make_dense
 from oracle import dense as odense
 from oracle import vocab
 from tests.helpers import dev, err, host
-from tests.vocab_cases import ALL_KINDS, Bounds, check, rows
+from tests.vocab_cases import ALL_KINDS, MORE_KINDS, Bounds, check, rows
 
 pytestmark = pytest.mark.gpu
 
@@ -236,7 +236,7 @@ def test_optional_parts_and_zero_alternatives(dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("V,pad", [(1000, 0), (4097, 3)])
+@pytest.mark.parametrize("V,pad", [(1000, 0), (4097, 3), (4097, 0), (13001, 2)])
 def test_gradient_in_place_and_accumulated(dtype, V, pad):
     """In place: bit for bit the gradient written elsewhere.  Accumulated:
     one rounding of the sum; rows without a gradient stay as they are."""
@@ -373,6 +373,92 @@ def test_gradient_against_differences_of_the_loss(which):
     tol = 3 * noise + 2 * (np.abs(host(dv)) * np.abs(step)).sum(axis=1) * 2.0 ** -16 + beyond * 1.01
     assert np.all(np.abs(diff - want) <= tol), (np.abs(diff - want) / tol).max()
     assert np.abs(diff).max() > 5 * tol.max()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T,V,k,pad", [(205, 40001, 20, 0), (207, 33333, 128, 2), (19, 9000, 128, 1)])
+def test_rows_enough_to_take_whole(T, V, k, pad, dtype):
+    """Rows of several steps, one workgroup each, with every kind of row;
+    and few rows with nearly as many alternatives as blocks of columns."""
+    import torch
+    import orthogonal_fine_tuning_amd as oft
+
+    c = _c(T, V, k, pad=pad, gpad=pad, tau=0.8)
+    rng = np.random.default_rng(T)
+    x = rows(T, V, dtype, T, ALL_KINDS)
+    labels = _labels(rng, T, V)
+    xv, got = _logprobs(c, dtype, x, labels)
+    b = Bounds(x, np.float64(np.float32(0.8)))
+    _check_logprobs(c, x, labels, got, b)
+    idx, val = _teacher_case(rng, x, min(256, 2 * k), True)
+    d, xv, loss, stats = _distill(c, dtype, x, idx, val)
+    check(host(loss), vocab.distill(x, idx, val, b.tau), b.teacher(idx, val)[0], "loss")
+    assert torch.equal(stats.view(torch.int32), got["stats"].view(torch.int32))
+    g = rng.normal(0, 1, T).astype(np.float32)
+    _, dv = _view(np.full((T, V), 3.0, np.float32), dtype, d.ld_grad, 0, 77.0)
+    oft.oft_distill_topk_bwd(d, xv, dev(idx), dev(val), stats, dev(g), dv)
+    torch.cuda.synchronize()
+    ref = vocab.distill_grad(x, idx, val, g, b.tau)
+    check(host(dv.float()), ref, b.distill_grad(ref, idx, val, g, dtype), "d_logits")
+
+
+@pytest.mark.parametrize("T,V", [(8, 10007), (210, 10007), (8, 70001)])
+@pytest.mark.parametrize("tau", [1.0, 2.0 ** -20, 2.0 ** 20, 0.01, 300.0])
+def test_temperatures_and_far_references(T, V, tau):
+    """The smallest and largest temperature, and rows whose scaled maximum
+    crosses the border between the two forms of a sum's reference."""
+    import torch
+    import orthogonal_fine_tuning_amd as oft
+
+    c = _c(T, V, 9, tau=tau)
+    x = rows(T, V, "f32", 5, MORE_KINDS)
+    rng = np.random.default_rng(1)
+    labels = vocab.top(x, 3)[np.arange(T), rng.integers(0, 3, T)].astype(np.int32)
+    xv, got = _logprobs(c, "f32", x, labels)
+    b = Bounds(x, tau)
+    _check_logprobs(c, x, labels, got, b)
+    gl, ge = rng.normal(0, 1, T).astype(np.float32), rng.normal(0, 1, T).astype(np.float32)
+    dv = torch.empty((T, V), device="cuda")
+    oft.oft_token_logprobs_bwd(_desc(c, "f32"), xv, dev(labels), got["stats"], dev(gl), dv, entropy=got["entropy"],
+                               g_entropy=dev(ge))
+    torch.cuda.synchronize()
+    ref = vocab.logprobs_grad(x, labels, gl, ge, tau)
+    check(host(dv), ref, b.grad(ref, gl, ge, "f32"), "d_logits")
+
+
+def test_streamed_rows_equal_kept_ones():
+    """A call large enough to pass the caches by, bit for bit its rows in
+    smaller calls that do not, forward and backward."""
+    import torch
+    import orthogonal_fine_tuning_amd as oft
+
+    T, V, k, part = 690, 120011, 20, 230  # 166 MB of bf16 against 55 MB
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = (2.5 * torch.randn((T, V), generator=g, device="cuda")).to(torch.bfloat16)
+    lab = torch.randint(0, V, (T,), generator=g, device="cuda", dtype=torch.int32)
+    up = torch.randn(T, generator=g, device="cuda")
+
+    def run(a, b):
+        n = b - a
+        d = oft.vocab_desc(n, V, k=k, temperature=0.9)
+        o = dict(logp=_f32(n), stats=_f32(n, 2), entropy=_f32(n),
+                 top_idx=torch.zeros((n, k), dtype=torch.int32, device="cuda"), top_logp=_f32(n, k))
+        oft.oft_token_logprobs(d, x[a:b], lab[a:b].clone(), **o, **_ws(d))
+        gr = torch.empty((n, V), dtype=torch.bfloat16, device="cuda")
+        dg = torch.empty_like(gr)
+        oft.oft_token_logprobs_bwd(d, x[a:b], lab[a:b].clone(), o["stats"], up[a:b].clone(), gr, entropy=o["entropy"],
+                                   g_entropy=up[a:b].clone())
+        loss, st = _f32(n), _f32(n, 2)
+        oft.oft_distill_topk(d, x[a:b], o["top_idx"], o["top_logp"], loss, st, **_ws(d))
+        oft.oft_distill_topk_bwd(d, x[a:b], o["top_idx"], o["top_logp"], st, up[a:b].clone(), dg)
+        torch.cuda.synchronize()
+        return {**o, "grad": gr, "loss": loss, "dgrad": dg}
+
+    whole = run(0, T)
+    for a in range(0, T, part):
+        small = run(a, a + part)
+        for name in small:
+            assert torch.equal(whole[name][a:a + part], small[name]), (name, a)
 
 
 def test_deterministic_and_independent_of_other_rows():

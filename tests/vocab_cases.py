@@ -71,11 +71,18 @@ def rows(T, V, dtype, seed, kinds=None):
             r[-1] = 30.0
         elif kind == "peak_first":
             r[0] = 30.0
+        elif kind == "border":
+            # c x crosses 2^20 at temperature 1, where the reference of the
+            # sums changes its form
+            r += 2.0 ** 20 * np.log(2.0)
+        elif kind == "narrow":
+            r[:] = 3.0 + r * 1e-6
         elif kind != "plain":
             raise ValueError(kind)
     return as_type(x, dtype)
 
 
+MORE_KINDS = ["border", "narrow", "plain", "masked"]
 ALL_KINDS = ["plain", "ties", "constant", "zeros", "masked", "lowest", "all_lowest", "empty", "one", "nan", "all_nan",
              "inf", "wide", "shifted", "up", "down", "peak_last", "peak_first"]
 
