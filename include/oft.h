@@ -349,12 +349,13 @@ int32_t oft_logprob_diff(int32_t T, int32_t V, const float* logits_actor, const 
 #define OFT_NO_LABEL (-1)   /* a row (teacher entry) without a token      */
 
 /* Constraints: T >= 0 (T == 0 is a no-op), V >= 1, ld >= V, ld_grad >= V,
- * 2^-20 <= temperature <= 2^20, accumulate in {0, 1} (else OFT_EINVAL); dtype OFT_DT_BF16 or OFT_DT_F32 (else
- * OFT_EDTYPE).  oft_token_logprobs: 0 <= k <= OFT_MAX_TOP (else
- * OFT_EUNSUPPORTED) and k <= V (else OFT_ESHAPE); oft_distill_topk and its
- * backward: 1 <= k <= OFT_MAX_TEACHER (else OFT_EUNSUPPORTED);
- * oft_token_logprobs_bwd ignores k.  Size range (else OFT_EUNSUPPORTED):
- * T <= 2^22, V <= 2^24, T V <= 2^34, T ld and T ld_grad < 2^40. */
+ * 2^-20 <= temperature <= 2^20, accumulate in {0, 1} (else OFT_EINVAL); dtype
+ * OFT_DT_BF16 or OFT_DT_F32 (else OFT_EDTYPE).  oft_token_logprobs:
+ * 0 <= k <= OFT_MAX_TOP (else OFT_EUNSUPPORTED) and k <= V (else OFT_ESHAPE);
+ * oft_distill_topk and its backward: 1 <= k <= OFT_MAX_TEACHER (else
+ * OFT_EUNSUPPORTED); oft_token_logprobs_bwd ignores k.  Size range (else
+ * OFT_EUNSUPPORTED): T <= 2^22, V <= 2^24, T V <= 2^34, T ld and
+ * T ld_grad < 2^40. */
 typedef struct {
   int32_t T, V;       /* rows, vocabulary                                    */
   int32_t dtype;      /* of logits and d_logits                              */
@@ -395,8 +396,8 @@ int32_t oft_token_logprobs(const oft_vocab_desc* d, const void* logits, const in
  * with label OFT_NO_LABEL has g_logp 0 whatever the array holds; a row whose
  * gradients are both 0 gets exactly 0 without being read, and a row with
  * another label outside [0, V) gets NaN.  d_logits may be logits itself
- * (same pointer, ld_grad == ld, accumulate == 0); any other overlap of the
- * two is OFT_EINVAL. */
+ * (same pointer, ld_grad == ld, accumulate == 0); any other overlap of their
+ * address ranges, rows between the other's rows included, is OFT_EINVAL. */
 int32_t oft_token_logprobs_bwd(const oft_vocab_desc* d, const void* logits, const int32_t* labels_or_null,
                                const float* stats, const float* entropy_or_null, const float* g_logp_or_null,
                                const float* g_entropy_or_null, void* d_logits, void* stream);

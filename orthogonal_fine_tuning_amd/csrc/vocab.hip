@@ -12,14 +12,18 @@
 // to a larger maximum multiplies s by f = 2^d, d the difference of the two
 // references, and turns w into f (w + s d).
 //
-// Forward: vocab_stats_kernel reads every logit once (the operator is bound
-// by that read) and leaves one triple per slice of a row and, for the top
-// alternatives, the maximum of every block of 64 columns;
-// logprobs_finish_kernel / distill_finish_kernel join a row's slices.  Any
-// value that k blocks reach is at most the k-th best logit, so only the
-// blocks that reach such a value are read again.
+// Forward: every logit is read once, which bounds large calls (4096 x 151936
+// bf16: 187 us for the distillation loss, 6.7 TB/s; 199 us with entropy and 20
+// alternatives).  A workgroup takes a whole row (logprobs_row_kernel,
+// distill_row_kernel), or a slice of one where rows are few:
+// vocab_stats_kernel leaves a triple per slice, logprobs_finish_kernel and
+// distill_finish_kernel join them.  For the top alternatives the pass also
+// keeps the maximum of every block of 64 columns: any value that k blocks
+// reach is at most the k-th best logit, so only the blocks that reach such a
+// value are read again.
 //
-// Backward: one read and one write per logit with (m, l) from the forward.
+// Backward: one read and one write per logit with (m, l) from the forward
+// (4096 x 151936 bf16: 390 us, 6.2 TB/s both ways).
 //
 // Rows start anywhere: gfx950 takes 16-byte loads at any 4-byte address at full
 // speed (at 2-byte ones 30 % slower, 126 for 96 us at 2048 x 151935 bf16).  So
@@ -418,7 +422,8 @@ __device__ __forceinline__ Triple slice_triple(const typename Ty::E* row, int sk
 }
 
 // part[t S + sl]: the triple of positions [sl slice, (sl + 1) slice) of row t;
-// blocks: the maxima of the row's blocks, rows of them nb apart
+// blocks: the maxima of the row's blocks, rows of them nb apart.  (One row of
+// 151936 bf16 columns, 19 slices: 4.4 us; 64 rows 7.6 us.)
 template <class Ty, bool ENT, bool TOP, bool NT>
 __global__ __launch_bounds__(256) void vocab_stats_kernel(const typename Ty::E* __restrict__ logits, long ld, int V,
                                                           int S, int slice, float c, float4* __restrict__ part,
@@ -489,8 +494,8 @@ __device__ __forceinline__ unsigned long long candidate(uint32_t order, int col)
 // The k best of a whole row, whatever its ties: one wave reads it in order of
 // columns, candidates wait in LDS, and a full list is cut to its k best, whose
 // last one a later candidate must exceed (an equal value has a higher column).
-// list: [QCAP], of which the first k are the result.  `order`: a number that
-// at least k logits reach.
+// list: [QCAP], of which the first k are the result.  floor: an `ordered`
+// number that at least k logits reach.
 constexpr int QCAP = 1024;
 __device__ int cut(unsigned long long* list, int n, int k, uint32_t& floor) {
   wave_lds();
@@ -574,6 +579,10 @@ struct FinishArgs {
 // and elements, and the place of each of those is the number of candidates
 // above it.  Rows whose many candidates are no ties, or with more blocks than the
 // registers hold, go through select_row.
+//
+// Latency bounds it, not bytes: the joining kernel takes 6.4 us for 1 and for 64
+// rows of 151936 columns and 20 alternatives, a chain of dependent trips to
+// memory (triples and maxima, then the chosen blocks) and the selection between.
 constexpr int MAXBLK = 256, MAXCAND = 512;
 constexpr int MAXKEYS = 4096;  // 262144 columns
 
@@ -1258,13 +1267,15 @@ int blocks_of(const VocabDims& d) {
 }
 // A workgroup per row, with its block maxima in LDS where they are wanted:
 // from MANY_ROWS on, and for rows of few steps, where one launch costs less
-// than a row's slices gain.  Measured (bf16, us, whole row / slices): 151936
-// columns, 20 alternatives, 1 row 20.4 / 13.8, 64 rows 22.8 / 17.1, 200 rows
-// 24.9 / 24.6, 400 rows 31.4 / 33.7, 4096 rows 203 / 231; without alternatives
-// 64 rows 17.3 / 13.1, 200 rows 19.1 / 18.5, 4096 rows 190 / 191; 32003 columns
-// (4 steps), 20 alternatives, 1 row 13.0 / 13.8, 400 rows 18.0 / 23.6.  fp32,
-// 50021 columns (13 steps): 1 row with alternatives 15.3 / 13.8, without
-// 10.7 / 12.8.
+// than a row's slices gain.  Measured (bf16, us, whole row / slices, the time
+// of a call, which two launches hold at 12.5 or more): 151936 columns, 20
+// alternatives, 1 row 20.4 / 13.8, 64 rows 22.8 / 17.1, 200 rows 24.9 / 24.6,
+// 400 rows 31.4 / 33.7, 4096 rows 203 / 231; without alternatives 64 rows
+// 17.3 / 13.1, 200 rows 19.1 / 18.5, 4096 rows 190 / 191; 32003 columns (4
+// steps), 20 alternatives, 1 row 13.0 / 13.8, 400 rows 18.0 / 23.6.  FEW_STEPS
+// goes by the kernels' own time: a whole row takes 3.5 us and 0.55 more a step,
+// the two kernels of its slices 8.5 to 9 (with alternatives 12, and the whole
+// row its selection on top).
 constexpr int MANY_ROWS = 200, FEW_STEPS = 8, FEW_STEPS_TOP = 4;
 template <class Ty>
 bool whole_rows(const VocabDims& d, bool top) {

@@ -211,3 +211,31 @@ def test_graph_replay_and_side_stream():
         torch.cuda.synchronize()
         for name in ("counts", "tokens", "loss", "mean_prob", "d_logits"):
             assert torch.equal(a[name], e[name]), (r, name)
+
+
+def test_more_sequences_and_experts_than_one_grid_dimension():
+    """A million sequences of one token: their finishing workgroups, 17 to a
+    sequence, are more threads than one dimension of a grid holds.  With one
+    pair to a token the loss is E p of its expert."""
+    import torch
+    import orthogonal_fine_tuning_amd as oft
+
+    S, E = 1_000_000, 544
+    d = oft.moe_desc(S, E, 1, 64, 64, 32, 32, 16)
+    n = oft.oft_moe_balance_workspace_bytes(d, 1)
+    g = torch.Generator(device="cuda").manual_seed(4)
+    x = torch.randn((S, E), generator=g, device="cuda")
+    idx = torch.randint(0, E, (S, 1), generator=g, device="cuda", dtype=torch.int32)
+    counts = torch.full((S, E), -7, dtype=torch.int32, device="cuda")
+    tokens, loss = torch.full((S,), -7, dtype=torch.int32, device="cuda"), torch.full((S,), -7.0, device="cuda")
+    oft.oft_moe_balance(d, 1, x, idx, counts, tokens, loss, ws=torch.empty(n, dtype=torch.uint8, device="cuda"),
+                        ws_bytes=n)
+    torch.cuda.synchronize()
+    assert bool((tokens == 1).all()) and bool((counts.sum(1) == 1).all())
+    assert torch.equal(counts.argmax(1), idx[:, 0].long())
+    for a in range(0, S, 100_000):
+        at = slice(a, a + 100_000)
+        want = E * torch.softmax(x[at].double(), 1).gather(1, idx[at].long())[:, 0]
+        # as in _check: |z| <= 16 (the maximum less the minimum of E normal values)
+        tol = want * (10 * 16 + E / 16 + 16 + E / 64 + 24) * U
+        assert bool(((loss[at].double() - want).abs() <= tol).all()), a
