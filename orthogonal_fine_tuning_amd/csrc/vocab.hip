@@ -13,7 +13,7 @@
 // references, and turns w into f (w + s d).
 //
 // Forward: every logit is read once, which bounds large calls (4096 x 151936
-// bf16: 187 us for the distillation loss, 6.7 TB/s; 199 us with entropy and 20
+// bf16: 187 us for the distillation loss, 6.7 TB/s; 198 us with entropy and 20
 // alternatives).  A workgroup takes a whole row (logprobs_row_kernel,
 // distill_row_kernel), or a slice of one where rows are few:
 // vocab_stats_kernel leaves a triple per slice, logprobs_finish_kernel and
@@ -117,28 +117,33 @@ __device__ __forceinline__ int skew_of(const typename Ty::E* row) {
 }
 
 // value of another lane of the same 16 (DPP)
-template <int CTRL>
-__device__ __forceinline__ float dpp(float v) {
-  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
+template <int CTRL, class T>
+__device__ __forceinline__ T dpp(T v) {
+  return __builtin_bit_cast(T, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
 }
 constexpr int PAIR = 0xB1, QUAD = 0x4E, EIGHT = 0x141, ROW = 0x140;  // lanes ^ 1, ^ 2, 7 - i of 8, 15 - i of 16
-__device__ __forceinline__ float lane_value(float v, int l) {
-  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), l));
+template <class T>
+__device__ __forceinline__ T lane_value(T v, int l) {
+  return __builtin_bit_cast(T, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), l));
 }
 // over the wave's 64 lanes (all active), the same bits in every lane
-__device__ __forceinline__ float wave_sum(float v) {
+template <class T>
+__device__ __forceinline__ T wave_sum(T v) {
   v += dpp<PAIR>(v);
   v += dpp<QUAD>(v);
   v += dpp<EIGHT>(v);
   v += dpp<ROW>(v);
   return (lane_value(v, 0) + lane_value(v, 16)) + (lane_value(v, 32) + lane_value(v, 48));
 }
-__device__ __forceinline__ float wave_max(float v) {
-  v = fmaxf(v, dpp<PAIR>(v));
-  v = fmaxf(v, dpp<QUAD>(v));
-  v = fmaxf(v, dpp<EIGHT>(v));
-  v = fmaxf(v, dpp<ROW>(v));
-  return fmaxf(fmaxf(lane_value(v, 0), lane_value(v, 16)), fmaxf(lane_value(v, 32), lane_value(v, 48)));
+__device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); }
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return a > b ? a : b; }
+template <class T>
+__device__ __forceinline__ T wave_max(T v) {
+  v = larger(v, dpp<PAIR>(v));
+  v = larger(v, dpp<QUAD>(v));
+  v = larger(v, dpp<EIGHT>(v));
+  v = larger(v, dpp<ROW>(v));
+  return larger(larger(lane_value(v, 0), lane_value(v, 16)), larger(lane_value(v, 32), lane_value(v, 48)));
 }
 
 // LDS of one wave, written and read by its lanes
@@ -465,24 +470,69 @@ __device__ __forceinline__ int below(unsigned long long mask) {  // set bits of 
 
 // The largest number of few low bits that at least k and at most k + slack of
 // the N values per lane (of BITS bits) reach; the k-th largest itself where
-// ties allow no such number.  Two bits a step.
+// ties allow no such number.  Two bits a step, after a first one from the
+// largest value's upper eight (a factor of four each): three steps of eight at
+// usual rows.
 template <int N, int BITS>
 __device__ __forceinline__ uint32_t kth(const uint32_t* o, int k, int slack) {
-  uint32_t r = 0;
-  for (int bit = BITS - 2; bit >= 0; bit -= 2) {
-    int n1 = 0, n2 = 0, n3 = 0;
-    const uint32_t t1 = r | (1u << bit), t2 = r | (2u << bit), t3 = r | (3u << bit);
+  uint32_t top = o[0];
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-      n1 += __popcll(__ballot(o[j] >= t1));
-      n2 += __popcll(__ballot(o[j] >= t2));
-      n3 += __popcll(__ballot(o[j] >= t3));
+  for (int j = 1; j < N; ++j) top = max(top, o[j]);
+  top = wave_max(top) >> (BITS - 8);
+  bool guess = top >= 3;
+  uint32_t r = guess ? (top - 3) << (BITS - 8) : 0;
+  int bit = guess ? BITS - 8 : BITS - 2;
+  while (bit >= 0) {
+    const uint32_t t1 = r + (1u << bit), t2 = r + (2u << bit), t3 = r + (3u << bit);
+    int n1 = 0, n2 = 0, n3 = 0;
+    if constexpr (N == 8) {  // (three counts of up to 512 in one sum)
+      uint32_t c1 = 0, c2 = 0, c3 = 0;
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        c1 += o[j] >= t1 ? 1 : 0;
+        c2 += o[j] >= t2 ? 1 : 0;
+        c3 += o[j] >= t3 ? 1 : 0;
+      }
+      const uint32_t c = wave_sum(c1 | c2 << 10 | c3 << 20);
+      n1 = (int)(c & 1023), n2 = (int)(c >> 10 & 1023), n3 = (int)(c >> 20);
+    } else {
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        n1 += __popcll(__ballot(o[j] >= t1));
+        n2 += __popcll(__ballot(o[j] >= t2));
+        n3 += __popcll(__ballot(o[j] >= t3));
+      }
     }
+    if (guess && n1 < k) {
+      guess = false;
+      r = 0;
+      bit = BITS - 2;
+      continue;
+    }
+    guess = false;
     r = n3 >= k ? t3 : n2 >= k ? t2 : n1 >= k ? t1 : r;
     const int n = n3 >= k ? n3 : n2 >= k ? n2 : n1;
     if (n >= k && n <= k + slack) break;
+    bit -= 2;
   }
   return r;
+}
+
+// y[j], by halving (bits are chosen by a mask: a choice of elements by j would
+// put y into memory)
+template <int N>
+__device__ __forceinline__ float element(const float (&y)[N], int j) {
+  if constexpr (N == 1) {
+    return y[0];
+  } else {
+    const uint32_t odd = 0u - (uint32_t)(j & 1);
+    float h[N / 2];
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i)
+      h[i] = __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, y[2 * i + 1]) & odd) |
+                                           (__builtin_bit_cast(uint32_t, y[2 * i]) & ~odd));
+    return element<N / 2>(h, j >> 1);
+  }
 }
 
 // A candidate as one number: value first, then the lower column; no two of a
@@ -580,10 +630,14 @@ struct FinishArgs {
 // above it.  Rows whose many candidates are no ties, or with more blocks than the
 // registers hold, go through select_row.
 //
-// Latency bounds it, not bytes: the joining kernel takes 6.4 us for 1 and for 64
+// Latency bounds it, not bytes: the joining kernel takes 5.3 us for 1 and for 64
 // rows of 151936 columns and 20 alternatives, a chain of dependent trips to
 // memory (triples and maxima, then the chosen blocks) and the selection between.
-constexpr int MAXBLK = 256, MAXCAND = 512;
+// In cycles of one wave, with 20 / 128 alternatives: 2700 to the triple, 1700 to
+// the groups, 1200 / 2600 the floor, 1100 / 1300 the blocks that reach it, 1200 /
+// 5000 their elements, 3100 / 6500 the places.  (With lists that all waves
+// filled through one counter: 4200 / 18600 for the elements, 6.4 us in all.)
+constexpr int WAVE_BLOCKS = 128, WAVE_LIST = QCAP / 4, LISTED = 512;
 constexpr int MAXKEYS = 4096;  // 262144 columns
 
 // a row's given token: read at a kernel's start, since its two dependent loads
@@ -624,14 +678,17 @@ __device__ __forceinline__ void logprobs_finish(const FinishArgs& f, const Logpr
     }
   }
   if constexpr (TOP) {
-    __shared__ int cand[MAXBLK];
+    __shared__ uint16_t cand[4][WAVE_BLOCKS];
     __shared__ uint32_t group[512];
-    __shared__ int count[2];
+    __shared__ int count[3][4], ties[4];
+    constexpr int OVER = 1 << 24;
+    // (waves interleaved by vectors: neighbouring columns are often good together)
+    const int place = lane * 4 + (tid >> 6);
     u32x4 held[HELD];
     const int skew = skew_of<Ty>(row), end = f.V + skew;
     const int nvec = (end + B::TILE - 1) / B::TILE * B::PER_TILE / KV;
 #pragma unroll
-    for (int i = 0; i < HELD; ++i) held[i] = i * NT + tid < nvec ? keys[i * NT + tid] : u32x4{0, 0, 0, 0};
+    for (int i = 0; i < HELD; ++i) held[i] = i * NT + place < nvec ? keys[i * NT + place] : u32x4{0, 0, 0, 0};
     // the best of each of eight groups per thread
     uint32_t best[8];
     if constexpr (KV == 8) {
@@ -673,7 +730,7 @@ __device__ __forceinline__ void logprobs_finish(const FinishArgs& f, const Logpr
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (j < 1 << shift && tid < 512 >> shift) group[(tid << shift) + j] = best[j];
+      if (j < 1 << shift && place < 512 >> shift) group[(place << shift) + j] = best[j];
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < 8; ++j) best[j] = group[64 * j + lane];
@@ -697,105 +754,100 @@ __device__ __forceinline__ void logprobs_finish(const FinishArgs& f, const Logpr
     // those that reach a higher one, from the blocks' vectors in 512 groups.
     // Then those above the floor: where ties did it (a masked or constant row)
     // they are few, and the lowest columns at the floor itself complete them.
+    // Each wave reads the blocks it holds the maxima of, into a list of its own.
+    const int wave = tid >> 6;
+    unsigned long long* mine = list + wave * WAVE_LIST;
+    int c[4];  // entries of the waves' lists
     bool done = false;
     int n = 0;
     uint32_t lo = floor;
-    for (int step = 0; step < 3 && !done; ++step) {
-      __syncthreads();
-      if (tid < 2) count[tid] = 0;
-      __syncthreads();
-      // a thread's finds enter the lists together: one counter update each
-      const auto found = [&](auto&& each) {
-        int more = 0;
+    for (int step = 0; step < 3; ++step) {
+      int nb = 0, nc = 0;
+      uint32_t hits = 0;  // bit e: the e-th maximum held
+      const uint32_t high = lo << (32 - B::BITS);
 #pragma unroll
-        for (int i = 0; i < HELD; ++i) {
-#pragma unroll
-          for (int d = 0; d < 4; ++d) {
-            const uint32_t w = held[i][d];
-            const int b = (i * NT + tid) * KV + d * (KV / 4);
-            if constexpr (KV == 8) {
-              more += each((w & 0xFFFFu) >= lo, b) + each((w >> 16) >= lo, b + 1);
-            } else {
-              more += each(w >= lo, b);
-            }
-          }
-        }
-        return more;
-      };
-      const int blocks = found([](bool in, int) { return in ? 1 : 0; });
-      if (blocks > 0) {
-        int at = atomicAdd(&count[0], blocks);
-        found([&](bool in, int b) {
-          if (in) {
-            if (at < MAXBLK) cand[at] = b;
-            ++at;
-          }
-          return 0;
-        });
+      for (int e = 0; e < HELD * KV; ++e) {
+        const uint32_t w = held[e / KV][e % KV * 4 / KV];
+        hits |= (KV == 8 && e % 2 == 0 ? w << 16 : w) >= high ? 1u << e : 0u;
       }
-      __syncthreads();
-      const int n1 = count[0];
-      if (nvec > HELD * NT || n1 > MAXBLK) {
-        lo = floor + 1;
-        continue;
+      for (unsigned long long mask; (mask = __ballot(hits != 0)) != 0; hits &= hits - 1) {
+        const int at = nb + below(mask), e = __builtin_ctz(hits | 1u << 31);
+        if (hits != 0 && at < WAVE_BLOCKS) cand[wave][at] = (uint16_t)((e / KV * NT + place) * KV + e % KV);
+        nb += __popcll(mask);
       }
-      best[0] = best[1] = 0;
-      // key(x) >= lo as a comparison of numbers (false for NaN, which ranks as
-      // -inf: a row with few others finds it at the floor)
-      const uint32_t o = lo << (32 - B::BITS);
-      const float least = o <= 0x007FFFFFu ? -INFINITY : unordered(o);
-      const auto gather = [&](auto width) {
-        constexpr int U = decltype(width)::value;  // vectors in flight per thread
-        for (int i = tid; i - lane < n1 * B::VECS; i += NT * U) {
+      wave_lds();
+      const int nv = nb * B::VECS;
+      // f(vector, position) for the blocks' vectors, 64 at a time; NaN where
+      // there is no column
+      const auto each = [&](auto&& f_) {
+        constexpr int U = 4;  // vectors in flight per lane
+        for (int base = 0; base < nv; base += 64 * U) {
           u32x4 x[U];
           int pos[U];
 #pragma unroll
           for (int u = 0; u < U; ++u) {
-            const int at = i + NT * u;
-            pos[u] = at < n1 * B::VECS ? B::position(cand[at / B::VECS], at % B::VECS) : end;
-            if (pos[u] >= skew && pos[u] + VE <= end) {
-              x[u] = load16(row + (pos[u] - skew));
-            } else {
-              float y[VE];
-#pragma unroll
-              for (int j = 0; j < VE; ++j) {
-                const int col = pos[u] + j - skew;
-                y[j] = col >= 0 && col < f.V ? Ty::get(row[col]) : NAN;
-              }
-              x[u] = Ty::pack(y);
-            }
+            if (base + 64 * u >= nv) break;
+            const int at = base + 64 * u + lane;
+            pos[u] = at < nv ? B::position(cand[wave][at / B::VECS], at % B::VECS) : end;
+            x[u] = u32x4{~0u, ~0u, ~0u, ~0u};
+            if (pos[u] >= skew && pos[u] + VE <= end) x[u] = load16(row + (pos[u] - skew));
           }
 #pragma unroll
           for (int u = 0; u < U; ++u) {
+            if (base + 64 * u >= nv) break;
             float y[VE];
             Ty::unpack(x[u], y);
-            int more = 0;
-            float top = y[0];
+            if (__ballot(pos[u] < end && (pos[u] < skew || pos[u] + VE > end)) != 0) {
 #pragma unroll
-            for (int j = 0; j < VE; ++j) {
-              more += y[j] >= least ? 1 : 0;
-              top = fmaxf(top, y[j]);
+              for (int j = 0; j < VE; ++j) {
+                const int col = pos[u] + j - skew;
+                if (pos[u] < skew || pos[u] + VE > end) y[j] = col >= 0 && col < f.V ? Ty::get(row[col]) : NAN;
+              }
             }
-            best[u & 1] = max(best[u & 1], pos[u] < end ? B::key(top) : 0u);
-            if (more > 0) {
-              int at = atomicAdd(&count[1], more);
-#pragma unroll
-              for (int j = 0; j < VE; ++j)
-                if (y[j] >= least) {
-                  if (at < MAXCAND) list[at] = candidate(ordered(y[j]), pos[u] + j - skew);
-                  ++at;
-                }
-            }
+            f_(y, pos[u]);
           }
         }
       };
-      if (n1 * B::VECS <= NT) gather(std::integral_constant<int, 1>{});
-      else gather(std::integral_constant<int, 4>{});
+      // key(x) >= lo as a comparison of numbers (false for NaN, which ranks as
+      // -inf: a row with few others finds it at the floor)
+      const float least = high <= 0x007FFFFFu ? -INFINITY : unordered(high);
+      const bool over = nvec > HELD * NT || nb > WAVE_BLOCKS;
+      if (!over) {
+        each([&](const float (&y)[VE], int pos) {
+          uint32_t in = 0;
+#pragma unroll
+          for (int j = 0; j < VE; ++j) in |= y[j] >= least ? 1u << j : 0u;
+          // (most lanes with any have one: the loop runs once or twice)
+          for (unsigned long long mask; (mask = __ballot(in != 0)) != 0; in &= in - 1) {
+            const int at = nc + below(mask), j = __builtin_ctz(in | 1u << 31);
+            if (in != 0 && at < WAVE_LIST) mine[at] = candidate(ordered(element(y, j)), pos + j - skew);
+            nc += __popcll(mask);
+          }
+        });
+      }
+      if (lane == 0) count[step][wave] = over ? OVER : nc;
       __syncthreads();
-      n = count[1];
-      done = n <= MAXCAND && (n >= f.k || lo > floor);
+      n = 0;
+      int most = 0;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        c[w] = count[step][w];
+        n += c[w];
+        most = max(most, c[w]);
+      }
+      const bool fits = most <= WAVE_LIST && n <= LISTED;
+      done = fits && (n >= f.k || lo > floor);
       if (done) break;
-      if (step == 0 && n > MAXCAND) {
+      if (step == 0 && !fits && most < OVER) {
+        best[0] = best[1] = 0;
+        each([&](const float (&y)[VE], int pos) {
+          float top = y[0];
+#pragma unroll
+          for (int j = 1; j < VE; ++j) top = fmaxf(top, y[j]);
+          const uint32_t key = pos < end ? B::key(top) : 0u;
+          if (pos / VE & 1) best[1] = max(best[1], key);
+          else best[0] = max(best[0], key);
+        });
         group[tid] = best[0];
         group[NT + tid] = best[1];
         __syncthreads();
@@ -807,7 +859,9 @@ __device__ __forceinline__ void logprobs_finish(const FinishArgs& f, const Logpr
         lo = floor + 1;
       }
     }
-    // at the floor itself, in order of columns
+    // at the floor itself, in order of columns, behind the last list
+    unsigned long long* last = list + 3 * WAVE_LIST + c[3] - n;
+    c[3] -= n;
     for (int base = 0; done && n < f.k && base < f.V; base += NT * VE) {
       const int c0 = base + tid * VE;
       int hit = 0, at = 0, total = 0;
@@ -819,45 +873,75 @@ __device__ __forceinline__ void logprobs_finish(const FinishArgs& f, const Logpr
         at += below(mask);
         total += __popcll(mask);
       }
-      if (lane == 0) cand[tid >> 6] = total;
+      if (lane == 0) ties[wave] = total;
       __syncthreads();
       total = 0;
       for (int w = 0; w < 4; ++w) {
-        if (w == tid >> 6) at += total;
-        total += cand[w];
+        if (w == wave) at += total;
+        total += ties[w];
       }
 #pragma unroll
       for (int j = 0; j < VE; ++j)
         if (hit >> j & 1) {
-          if (n + at < f.k) list[n + at] = candidate(ordered(Ty::get(row[c0 + j])), c0 + j);
+          if (n + at < f.k) last[n + at] = candidate(ordered(Ty::get(row[c0 + j])), c0 + j);
           ++at;
         }
       n = min(f.k, n + total);
       __syncthreads();
     }
+    c[3] += n;
     if (!done || n < f.k) {
       __syncthreads();
       if (tid < 64) select_row<Ty>(row, f.V, f.k, floor << (32 - B::BITS), list);
-      n = f.k;
-      __syncthreads();
+      c[0] = n = f.k;
+      c[1] = c[2] = c[3] = 0;
     }
-    // up to a multiple of eight for the reads below: 0 is below each candidate
-    if (tid < 8 && n + tid < ((n + 7) & ~7)) list[n + tid] = 0ull;
+    // Places: each wave counts, for all candidates, those of its own list above
+    // them.  The lists go up to multiples of eight (0 is below each candidate).
+    uint32_t* places = group;
+    places[tid] = places[NT + tid] = 0;
+#pragma unroll
+    for (int w = 0; w < 4; ++w)
+      if (tid >> 3 == w && c[w] + (tid & 7) < ((c[w] + 7) & ~7)) list[w * WAVE_LIST + c[w] + (tid & 7)] = 0ull;
+    __syncthreads();
+    const auto entry = [&](int i) {
+      const int w1 = c[0], w2 = w1 + c[1], w3 = w2 + c[2];
+      return list[i < w1 ? i : i < w2 ? i - w1 + WAVE_LIST : i < w3 ? i - w2 + 2 * WAVE_LIST : i - w3 + 3 * WAVE_LIST];
+    };
+    const int own = wave == 0 ? c[0] : wave == 1 ? c[1] : wave == 2 ? c[2] : c[3];
+    const auto count_above = [&](auto width) {
+      constexpr int R = decltype(width)::value;  // candidates per lane
+      for (int base = 0; base < n; base += 64 * R) {
+        unsigned long long e[R];
+        int above[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          e[r] = base + 64 * r + lane < n ? entry(base + 64 * r + lane) : 0ull;
+          above[r] = 0;
+        }
+        for (int j = 0; j < own; j += 8) {
+#pragma unroll
+          for (int h = 0; h < 8; h += 2) {
+            const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(mine + j + h);
+#pragma unroll
+            for (int r = 0; r < R; ++r) above[r] += (o.x > e[r] ? 1 : 0) + (o.y > e[r] ? 1 : 0);
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+          if (base + 64 * r + lane < n && above[r] > 0) atomicAdd(&places[base + 64 * r + lane], above[r]);
+      }
+    };
+    if (n <= 64) count_above(std::integral_constant<int, 1>{});
+    else count_above(std::integral_constant<int, 3>{});
     __syncthreads();
     for (int i = tid; i < n; i += NT) {
-      const unsigned long long mine = list[i];
-      int place = 0;
-      for (int j = 0; j < n; j += 8) {
-#pragma unroll
-        for (int h = 0; h < 8; h += 2) {
-          const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(list + j + h);
-          place += (o.x > mine ? 1 : 0) + (o.y > mine ? 1 : 0);
-        }
-      }
-      if (place < f.k) {
-        const float v = unordered((uint32_t)(mine >> 32));
-        const size_t at = (size_t)t * f.k + place;
-        q.top_idx[at] = (int)~(uint32_t)mine;
+      const int rank = (int)places[i];
+      const unsigned long long e = entry(i);
+      if (rank < f.k) {
+        const float v = unordered((uint32_t)(e >> 32));
+        const size_t at = (size_t)t * f.k + rank;
+        q.top_idx[at] = (int)~(uint32_t)e;
         q.top_logp[at] = l != l ? NAN : empty ? -INFINITY : (v - a.m) * f.invtau - l;
       }
     }
@@ -881,9 +965,10 @@ __global__ __launch_bounds__(256, 4) void logprobs_finish_kernel(
 
 // A whole row by one workgroup, for rows enough to fill the chip: no triples
 // and no block maxima through memory (writing 20 MB of them beside a read of
-// 1.2 GB took 25 us).
+// 1.2 GB took 25 us).  (Six workgroups a CU of fp32 would spill a register.)
 template <class Ty, bool ENT, bool TOP, bool NT>
-__global__ __launch_bounds__(256, 6) void logprobs_row_kernel(FinishArgs f, LogprobPtrs q) {
+__global__ __launch_bounds__(256, sizeof(typename Ty::E) == 2 ? 6 : 5) void logprobs_row_kernel(FinishArgs f,
+                                                                                               LogprobPtrs q) {
   typedef typename Blocks<Ty>::Key Key;
   const int t = blockIdx.x;
   const typename Ty::E* row = static_cast<const typename Ty::E*>(q.logits) + (size_t)t * f.ld;
@@ -1266,21 +1351,21 @@ int blocks_of(const VocabDims& d) {
   return (positions<Ty>(d) + fwd_tile<Ty>() - 1) / fwd_tile<Ty>() * Blocks<Ty>::PER_TILE;
 }
 // A workgroup per row, with its block maxima in LDS where they are wanted:
-// from MANY_ROWS on, and for rows of few steps, where one launch costs less
-// than a row's slices gain.  Measured (bf16, us, whole row / slices, the time
-// of a call, which two launches hold at 12.5 or more): 151936 columns, 20
-// alternatives, 1 row 20.4 / 13.8, 64 rows 22.8 / 17.1, 200 rows 24.9 / 24.6,
-// 400 rows 31.4 / 33.7, 4096 rows 203 / 231; without alternatives 64 rows
-// 17.3 / 13.1, 200 rows 19.1 / 18.5, 4096 rows 190 / 191; 32003 columns (4
-// steps), 20 alternatives, 1 row 13.0 / 13.8, 400 rows 18.0 / 23.6.  FEW_STEPS
-// goes by the kernels' own time: a whole row takes 3.5 us and 0.55 more a step,
-// the two kernels of its slices 8.5 to 9 (with alternatives 12, and the whole
-// row its selection on top).
-constexpr int MANY_ROWS = 200, FEW_STEPS = 8, FEW_STEPS_TOP = 4;
+// from MANY_ROWS on, and for short rows, where one launch costs less than a
+// row's slices gain.  Measured (us, whole row / slices, the time of a call,
+// which two launches hold at 13 or more; on the GPU alone the slices of few
+// rows take 8.5 and with alternatives 10): bf16 of 151936 columns with 20
+// alternatives 1 row 18.9 / 14.9, 64 rows 20.7 / 15.8, 200 rows 23.2 / 23.4,
+// 400 rows 30.4 / 32.9, 4096 rows 202 / 234; without 64 rows 16.2 / 13.7, 200
+// rows 20.1 / 17.7, 400 rows 26.3 / 27.8; of 32003 columns with 20
+// alternatives 1 row 10.5 / 14.6, 400 rows 18.4 / 20.8; fp32 of 50021 columns
+// without 1 row 9.0 / 13.3, 57 rows 9.5 / 14.2, with 20 alternatives 12.3 /
+// 14.7 and 13.5 / 14.8.
+constexpr int MANY_ROWS = 200, SHORT = 65536, SHORT_TOP = 32768;
 template <class Ty>
 bool whole_rows(const VocabDims& d, bool top) {
   if (top && blocks_of<Ty>(d) > MAXKEYS) return false;
-  return d.T >= MANY_ROWS || d.V <= (top ? FEW_STEPS_TOP : FEW_STEPS) * fwd_tile<Ty>();
+  return d.T >= MANY_ROWS || d.V <= (top ? SHORT_TOP : SHORT);
 }
 template <class Ty>
 Split fwd_split(const VocabDims& d) {
