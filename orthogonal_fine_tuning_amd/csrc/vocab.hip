@@ -995,24 +995,32 @@ __global__ __launch_bounds__(256, sizeof(typename Ty::E) == 2 ? 6 : 5) void logp
 // ix -1: an entry without weight.  bad: an entry is out of range, NaN or
 // +inf; any: some entry has weight.
 template <int TI>
+struct Listed {  // as given: read ahead of what hides their way from memory
+  int ix[TI];
+  float v[TI];
+  __device__ __forceinline__ Listed(const int* idx, const float* val, int k) {
+#pragma unroll
+    for (int i = 0; i < TI; ++i) {
+      const int at = (threadIdx.x & 63) + 64 * i;
+      ix[i] = at < k ? idx[at] : -1;
+      v[i] = at < k ? val[at] : -INFINITY;
+    }
+  }
+};
+template <int TI>
 struct Teacher {
   int ix[TI];
   float q[TI], logq[TI];
   bool bad, any;
 
-  __device__ __forceinline__ Teacher(const int* idx, const float* val, int k, int V, float invtau) {
-    const int lane = threadIdx.x & 63;
+  __device__ __forceinline__ Teacher(const Listed<TI>& given, int V, float invtau) {
     float v[TI], mx = -INFINITY;
     bool b = false;
 #pragma unroll
     for (int i = 0; i < TI; ++i) {
-      ix[i] = -1;
-      v[i] = -INFINITY;
-      if (lane + 64 * i < k) {
-        ix[i] = idx[lane + 64 * i];
-        if (ix[i] != -1) v[i] = val[lane + 64 * i];
-        b |= ix[i] < -1 || ix[i] >= V || v[i] != v[i] || v[i] == INFINITY;
-      }
+      ix[i] = given.ix[i];
+      v[i] = ix[i] == -1 ? -INFINITY : given.v[i];
+      b |= ix[i] < -1 || ix[i] >= V || v[i] != v[i] || v[i] == INFINITY;
       mx = fmaxf(mx, v[i]);
     }
     bad = __ballot(b) != 0;
@@ -1065,10 +1073,15 @@ __device__ __forceinline__ void distill_finish(const FinishArgs& f, const Distil
   }
 }
 
+template <int TI>
+__device__ __forceinline__ Listed<TI> listed_row(const FinishArgs& f, const DistillPtrs& q, int t) {
+  return Listed<TI>(q.idx + (size_t)t * f.k, q.teacher + (size_t)t * f.k, f.k);
+}
 template <class Ty, int TI>
-__device__ __forceinline__ Teacher<TI> teacher_row(const FinishArgs& f, const DistillPtrs& q, int t, float (&x)[TI]) {
+__device__ __forceinline__ Teacher<TI> teacher_row(const FinishArgs& f, const DistillPtrs& q, int t,
+                                                   const Listed<TI>& given, float (&x)[TI]) {
   const typename Ty::E* row = static_cast<const typename Ty::E*>(q.logits) + (size_t)t * f.ld;
-  const Teacher<TI> te(q.idx + (size_t)t * f.k, q.teacher + (size_t)t * f.k, f.k, f.V, f.invtau);
+  const Teacher<TI> te(given, f.V, f.invtau);
 #pragma unroll
   for (int i = 0; i < TI; ++i) x[i] = te.ix[i] >= 0 ? Ty::get(row[te.ix[i]]) : 0.0f;
   return te;
@@ -1079,7 +1092,7 @@ __global__ __launch_bounds__(64) void distill_finish_kernel(FinishArgs f, Distil
                                                             const float4* __restrict__ part) {
   const int t = blockIdx.x;
   float x[TI];
-  const Teacher<TI> te = teacher_row<Ty, TI>(f, q, t, x);
+  const Teacher<TI> te = teacher_row<Ty, TI>(f, q, t, listed_row<TI>(f, q, t), x);
   distill_finish<Ty, TI>(f, q, t, te, x, row_triple(part + (size_t)t * f.S, f.S, f.c));
 }
 
@@ -1088,11 +1101,12 @@ __global__ __launch_bounds__(256) void distill_row_kernel(FinishArgs f, DistillP
   const int t = blockIdx.x;
   const typename Ty::E* row = static_cast<const typename Ty::E*>(q.logits) + (size_t)t * f.ld;
   const int skew = skew_of<Ty>(row);
+  const Listed<TI> given = listed_row<TI>(f, q, t);
   KeepNone keep;
   const Triple a = slice_triple<Ty, false, NT>(row - skew, skew, 0, f.V + skew, f.c, keep);
   if (threadIdx.x >= 64) return;
   float x[TI];
-  const Teacher<TI> te = teacher_row<Ty, TI>(f, q, t, x);
+  const Teacher<TI> te = teacher_row<Ty, TI>(f, q, t, given, x);
   distill_finish<Ty, TI>(f, q, t, te, x, a);
 }
 
@@ -1282,7 +1296,7 @@ __global__ __launch_bounds__(256) void distill_bwd_kernel(BwdArgs b, const typen
   const float g = g_loss[t];
   const float2 st = *reinterpret_cast<const float2*>(stats + 2 * (size_t)t);
   // (each wave computes the list; all get the same)
-  const Teacher<TI> te(idx + (size_t)t * b.k, teacher + (size_t)t * b.k, b.k, b.V, b.invtau);
+  const Teacher<TI> te(Listed<TI>(idx + (size_t)t * b.k, teacher + (size_t)t * b.k, b.k), b.V, b.invtau);
   const int same = g == 0.0f ? ZEROS : te.bad ? NANS : !te.any || st.y == -INFINITY ? ZEROS : 0;
   if (same != 0) return part.fill(same == ZEROS ? 0.0f : NAN);
   const RowGrad r{st.x, b.c, st.y * LOG2E, 0.0f, g * b.invtau};
