@@ -7,7 +7,7 @@ from oft_inputs import DenseConfig, make_dense
 from oracle import dense as odense
 from oracle import vocab
 from tests.helpers import dev, err, host
-from tests.vocab_cases import ALL_KINDS, MORE_KINDS, Bounds, check, rows
+from tests.vocab_cases import ALL_KINDS, MORE_KINDS, Bounds, as_type, check, rows
 
 pytestmark = pytest.mark.gpu
 
@@ -400,6 +400,33 @@ def test_rows_enough_to_take_whole(T, V, k, pad, dtype):
     torch.cuda.synchronize()
     ref = vocab.distill_grad(x, idx, val, g, b.tau)
     check(host(dv.float()), ref, b.distill_grad(ref, idx, val, g, dtype), "d_logits")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T,V,k", [(6, 151936, 128), (7, 151935, 20), (204, 40001, 128), (12, 20000, 128)])
+def test_alternatives_in_clusters(T, V, k, dtype):
+    """The best columns next to each other or in the share of one wave, a few
+    or some hundred, apart or equal: the lists of candidates run over in one
+    wave, in all, or hold nearly all of them."""
+    rng = np.random.default_rng(V + k)
+    x = rng.normal(0, 2, (T, V)).astype(np.float32)
+    for t in range(T):
+        kind, n = t % 6, (400, 140, 60)[t // 6 % 3]
+        at = np.arange(n) + int(rng.integers(0, V - n))  # a run
+        if kind >= 3:
+            # 128 columns of every 2048, from a common offset: one wave's vectors
+            at = (np.arange(4)[:, None] * 2048 + np.arange(n // 4) + 512 * (kind - 3)).reshape(-1)
+        x[t, at] = 12.0 if kind % 3 == 1 else rng.uniform(9.0, 20.0, at.size)
+        if kind % 3 == 2:
+            x[t, at[::2]] = 12.0
+    x = as_type(x, dtype)
+    c = _c(T, V, k)
+    labels = _labels(rng, T, V)
+    _, got = _logprobs(c, dtype, x, labels)
+    assert np.array_equal(host(got["top_idx"]), vocab.top(x, k))
+    b = Bounds(x[:6], 1.0)
+    top = host(got["top_idx"])[:6]
+    check(host(got["top_logp"])[:6], np.take_along_axis(b.lp, top, 1), np.take_along_axis(b.lp_tol, top, 1), "top_logp")
 
 
 @pytest.mark.parametrize("T,V", [(8, 10007), (210, 10007), (8, 70001)])
