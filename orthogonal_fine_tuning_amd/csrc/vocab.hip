@@ -749,7 +749,10 @@ __device__ __forceinline__ void logprobs_finish(const FinishArgs& f, const Logpr
       best[1] = max(best[1], best[3]);
       floor = kth<2, B::BITS>(best, f.k, slack);
     }
-    floor = max(floor, 1u);  // (fewer than k groups: every block is above 0)
+    // (-inf and NaN rank alike, below any number, and each column reaches their
+    // key: the floor where fewer than k groups or numbers above it are left)
+    constexpr uint32_t LAST = 0x007FFFFFu >> (32 - B::BITS);
+    floor = max(floor, LAST);
     // First the candidates that reach the floor.  If their blocks hold too many,
     // those that reach a higher one, from the blocks' vectors in 512 groups.
     // Then those above the floor: where ties did it (a masked or constant row)
@@ -808,15 +811,20 @@ __device__ __forceinline__ void logprobs_finish(const FinishArgs& f, const Logpr
           }
         }
       };
-      // key(x) >= lo as a comparison of numbers (false for NaN, which ranks as
-      // -inf: a row with few others finds it at the floor)
-      const float least = high <= 0x007FFFFFu ? -INFINITY : unordered(high);
+      // key(x) >= lo as a comparison of numbers, false for NaN; at the last key
+      // every column takes part, NaN among them
+      const bool all = lo == LAST;
+      const float least = unordered(high);
       const bool over = nvec > HELD * NT || nb > WAVE_BLOCKS;
       if (!over) {
         each([&](const float (&y)[VE], int pos) {
           uint32_t in = 0;
+          if (all) {
+            in = (1u << max(min(end - pos, VE), 0)) - (1u << max(skew - pos, 0));
+          } else {
 #pragma unroll
-          for (int j = 0; j < VE; ++j) in |= y[j] >= least ? 1u << j : 0u;
+            for (int j = 0; j < VE; ++j) in |= y[j] >= least ? 1u << j : 0u;
+          }
           // (most lanes with any have one: the loop runs once or twice)
           for (unsigned long long mask; (mask = __ballot(in != 0)) != 0; in &= in - 1) {
             const int at = nc + below(mask), j = __builtin_ctz(in | 1u << 31);
