@@ -403,11 +403,15 @@ int32_t oft_token_logprobs_bwd(const oft_vocab_desc* d, const void* logits, cons
                                const float* g_entropy_or_null, void* d_logits, void* stream);
 
 /* Distillation from a teacher's top logits: teacher_idx int32 [T, k] names
- * columns, teacher_logits [T, k] holds the teacher's logits or
- * log-probabilities there (any shift per row; as oft_token_logprobs writes
- * top_idx and top_logp).  With q = softmax(teacher_logits / tau) over the
- * row's k entries,
+ * columns, teacher_logits [T, k] holds the teacher's logits there, up to a
+ * shift per row.  With q = softmax(teacher_logits / tau) over the row's k
+ * entries,
  *   loss[t] = sum_j q_j (log q_j - log p_{idx_j}).
+ * The call itself divides the list by tau, so that log-probabilities are a
+ * list only at temperature 1: the (top_idx, top_logp) of oft_token_logprobs
+ * with temperature 1, whatever tau is here.  Scored at another temperature
+ * tau', top_logp has to be multiplied by tau' first (as it stands, q would be
+ * the teacher's at tau tau').
  * An entry with index OFT_NO_LABEL, or at -inf, has q = 0; a row without any
  * other has loss 0 and gradient 0.  An index listed twice counts with both
  * its q.  Any other index outside [0, V) makes the row's loss NaN, as does a

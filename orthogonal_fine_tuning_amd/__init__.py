@@ -273,7 +273,9 @@ def oft_token_logprobs_bwd(desc, logits, labels, stats, g_logp, d_logits, entrop
 
 
 def oft_distill_topk(desc, logits, teacher_idx, teacher_logits, loss, stats, ws=None, ws_bytes=0, stream=None):
-    """Per-row loss against the teacher's renormalised top list."""
+    """Per-row loss against the teacher's renormalised top list.  The list is
+    divided by desc.temperature here: logits, or log-probabilities at
+    temperature 1 (top_logp of another temperature times that temperature)."""
     d, dev, listed = desc, logits.get_device(), (desc.T, desc.k)
     x = _rows("logits", logits, d, d.ld, dev)
     ti = _tensor("teacher_idx", teacher_idx, "int32", listed, dev)

@@ -5,9 +5,9 @@ import numpy as np
 import pytest
 
 from oracle import vocab
-from tests.helpers import host
-from tests.test_gpu_vocab import DTYPES, _c, _logprobs
-from tests.vocab_cases import NEG, Bounds, as_type, check
+from tests.helpers import dev, host
+from tests.test_gpu_vocab import DTYPES, _c, _f32, _logprobs, _ws
+from tests.vocab_cases import NEG, U, Bounds, as_type, check
 
 pytestmark = pytest.mark.gpu
 
@@ -59,3 +59,56 @@ def test_nan_ranks_as_minus_infinity_beside_it(c, dtype):
     b = Bounds(x, 1.0)
     check(host(got["top_logp"]), np.take_along_axis(b.lp, want, 1), np.take_along_axis(b.lp_tol, want, 1), "top_logp")
     check(host(got["entropy"]), b.H, b.H_tol, "entropy")
+
+
+# ------------------------------------------------ the temperature of a teacher
+@pytest.mark.parametrize("scored_at", [1.0, 0.7])
+@pytest.mark.parametrize("tau", [0.6, 1.5])
+def test_teacher_scored_and_distilled_at_other_temperatures(tau, scored_at):
+    """The list that the teacher's scoring wrote at temperature 1 (times the
+    temperature, if another one) against the teacher's own logits, divided by
+    tau once."""
+    import torch
+    import orthogonal_fine_tuning_amd as oft
+
+    print(f"[teacher] tau={tau} scored at {scored_at}", flush=True)
+    T, V, k = 40, 5003, 16
+    rng = np.random.default_rng(8)
+    teacher = as_type(rng.normal(0, 2.5, (T, V)).astype(np.float32), "bf16")
+    x = as_type((teacher + rng.normal(0, 0.7, (T, V))).astype(np.float32), "bf16")
+    _, got = _logprobs(_c(T, V, k, tau=scored_at), "bf16", teacher, np.zeros(T, np.int32))
+    idx = vocab.top(teacher, k)
+    assert np.array_equal(host(got["top_idx"]), idx)
+    values = got["top_logp"] * scored_at if scored_at != 1.0 else got["top_logp"]
+    d = oft.vocab_desc(T, V, k=k, temperature=tau)
+    xt = torch.from_numpy(x).to("cuda").to(torch.bfloat16)
+    loss, stats, dx = _f32(T), _f32(T, 2), torch.empty_like(xt)
+    g = rng.normal(0, 1, T).astype(np.float32)
+    oft.oft_distill_topk(d, xt, got["top_idx"], values, loss, stats, **_ws(d))
+    oft.oft_distill_topk_bwd(d, xt, got["top_idx"], values, stats, dev(g), dx)
+    torch.cuda.synchronize()
+    t32, s32 = np.float64(np.float32(tau)), np.float64(np.float32(scored_at))
+    b, bt = Bounds(x, t32), Bounds(teacher, s32)
+    raw = np.take_along_axis(teacher.astype(np.float64), idx, 1)
+    # what the list itself is off by: its log-probabilities' bound, and one
+    # rounding (and the factor's own) of the product
+    at = np.take_along_axis(bt.lp, idx, 1)
+    off = np.take_along_axis(bt.lp_tol, idx, 1) * s32 + (0.0 if scored_at == 1.0 else 2 * U * np.abs(at) * s32)
+    off = off.max(axis=1, keepdims=True) / t32
+    # d loss / d value = q (log q - log p - loss) / tau, d log q at most twice
+    # the values' own; 1 % for what the linear terms leave out (off is below 1e-5)
+    ref = vocab.distill(x, idx, raw, t32)
+    q, lq = vocab.teacher_probs(idx, raw, V, t32)
+    gap = np.abs(lq - np.take_along_axis(b.lp, idx, 1) - ref[:, None])
+    assert off.max() < 1e-5
+    tol = b.teacher(idx, raw)[0] + 1.01 * (q * gap * off).sum(axis=1)
+    check(host(loss), ref, tol, "loss")
+    # the same list as it stands is another teacher, by its weights (its loss
+    # may meet the right one's by chance: it does not grow or fall with tau)
+    if scored_at != 1.0:
+        assert (np.abs(vocab.teacher_probs(idx, at, V, t32)[0] - q).max(axis=1) > 1e3 * off[:, 0]).all()
+    gref = vocab.distill_grad(x, idx, raw, g, t32)
+    more = np.zeros((T, V))
+    np.put_along_axis(more, idx.astype(np.int64), q * 2.02 * off, 1)
+    more *= (np.abs(g) / t32)[:, None]
+    check(host(dx.float()), gref, b.distill_grad(gref, idx, raw, g, "bf16") + more * (1 + 2.0 ** -8), "d_logits")
