@@ -185,6 +185,12 @@ __device__ __forceinline__ float entropy_of(const Triple& a) {
   return a.s == 0.0f ? 0.0f : (__builtin_amdgcn_logf(a.s) - a.w / a.s) * LN2;
 }
 
+// k (x - m), also where the difference alone passes fp32's range
+__device__ __forceinline__ float scaled(float x, float m, float k) {
+  const float d = x - m;
+  return d == -INFINITY ? k * x - k * m : k * d;
+}
+
 __device__ __forceinline__ Triple join(const Triple& a, const Triple& b, float c) {
   const float M = fmaxf(a.m, b.m);
   const Triple x = moved(a, M, c), y = moved(b, M, c);
@@ -673,7 +679,7 @@ __device__ __forceinline__ void logprobs_finish(const FinishArgs& f, const Logpr
     if (q.entropy) q.entropy[t] = entropy_of(a);
     if (q.logp) {
       float lp = g.label == -1 ? 0.0f : NAN;
-      if (g.label >= 0 && g.label < f.V) lp = empty ? -INFINITY : (g.x - a.m) * f.invtau - l;
+      if (g.label >= 0 && g.label < f.V) lp = empty ? -INFINITY : scaled(g.x, a.m, f.invtau) - l;
       q.logp[t] = lp;
     }
   }
@@ -950,7 +956,7 @@ __device__ __forceinline__ void logprobs_finish(const FinishArgs& f, const Logpr
         const float v = unordered((uint32_t)(e >> 32));
         const size_t at = (size_t)t * f.k + rank;
         q.top_idx[at] = (int)~(uint32_t)e;
-        q.top_logp[at] = l != l ? NAN : empty ? -INFINITY : (v - a.m) * f.invtau - l;
+        q.top_logp[at] = l != l ? NAN : empty ? -INFINITY : scaled(v, a.m, f.invtau) - l;
       }
     }
   }
@@ -1071,7 +1077,7 @@ __device__ __forceinline__ void distill_finish(const FinishArgs& f, const Distil
     if (te.ix[i] >= 0) {
       // q (log q - log p), the far end of log p kept in range by its q (a
       // listed column may be masked at the type's lowest value)
-      const float far = te.q[i] * f.invtau * (x[i] - a.m);
+      const float far = scaled(x[i], a.m, te.q[i] * f.invtau);
       sum += a.s == 0.0f ? INFINITY : fmaf(te.q[i], te.logq[i] + l, -far);
     }
   sum = wave_sum(sum);

@@ -112,3 +112,42 @@ def test_teacher_scored_and_distilled_at_other_temperatures(tau, scored_at):
     np.put_along_axis(more, idx.astype(np.int64), q * 2.02 * off, 1)
     more *= (np.abs(g) / t32)[:, None]
     check(host(dx.float()), gref, b.distill_grad(gref, idx, raw, g, "bf16") + more * (1 + 2.0 ** -8), "d_logits")
+
+
+# ----------------------------------------------------- far ends of log p
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("tau", [1.0, 4.0, 2.0 ** 20])
+@pytest.mark.parametrize("T,V", [(6, 90), (6, 70001), (203, 2100)])
+def test_distances_to_the_maximum_beyond_fp32(T, V, tau, dtype):
+    """Finite logits of both signs near the type's range: x - m passes fp32's,
+    (x - m) / tau does not (from a temperature of 2 on)."""
+    print(f"[far] T={T} V={V} tau={tau} {dtype}", flush=True)
+    import torch
+    import orthogonal_fine_tuning_amd as oft
+
+    rng = np.random.default_rng(V)
+    x = rng.normal(0, 2.5, (T, V)).astype(np.float32)
+    x[:, ::7] = -3e38
+    x[::2, 3] = 3e38
+    x[1::2, 5:40] = rng.uniform(1e38, 3.3e38, (len(x[1::2]), 35))
+    x[1, 20:30] = NEG
+    x = as_type(x, dtype)
+    k = 60
+    labels = np.where(np.arange(T) % 3 == 0, 7, np.arange(T) % V).astype(np.int32)
+    xv, got = _logprobs(_c(T, V, k, tau=tau), dtype, x, labels)
+    b = Bounds(x, tau)
+    top = vocab.top(x, k)
+    assert np.array_equal(host(got["top_idx"]), top)
+    check(host(got["logp"]), vocab.given(b.lp, labels), b.lp_tol[np.arange(T), labels], "logp")
+    check(host(got["top_logp"]), np.take_along_axis(b.lp, top, 1), np.take_along_axis(b.lp_tol, top, 1), "top_logp")
+    check(host(got["entropy"]), b.H, b.H_tol, "entropy")
+    idx = np.concatenate([top[:, :5], np.tile(np.array([7, 14, 8], np.int32), (T, 1))], axis=1)
+    val = (rng.normal(0, 1, idx.shape) * tau).astype(np.float32)
+    d = oft.vocab_desc(T, V, oft.OFT_DT_F32 if dtype == "f32" else oft.OFT_DT_BF16, k=idx.shape[1], temperature=tau)
+    loss, stats, dx = _f32(T), _f32(T, 2), torch.empty_like(xv)
+    oft.oft_distill_topk(d, xv, dev(idx), dev(val), loss, stats, **_ws(d))
+    oft.oft_distill_topk_bwd(d, xv, dev(idx), dev(val), stats, torch.ones(T, device="cuda"), dx)
+    torch.cuda.synchronize()
+    check(host(loss), vocab.distill(x, idx, val, tau), b.teacher(idx, val)[0], "loss")
+    ref = vocab.distill_grad(x, idx, val, np.ones(T), tau)
+    check(host(dx.float()), ref, b.distill_grad(ref, idx, val, np.ones(T), dtype), "d_logits")
