@@ -412,10 +412,12 @@ int32_t oft_token_logprobs_bwd(const oft_vocab_desc* d, const void* logits, cons
  * with temperature 1, whatever tau is here.  Scored at another temperature
  * tau', top_logp has to be multiplied by tau' first (as it stands, q would be
  * the teacher's at tau tau').
- * An entry with index OFT_NO_LABEL, or at -inf, has q = 0; a row without any
- * other has loss 0 and gradient 0.  An index listed twice counts with both
- * its q.  Any other index outside [0, V) makes the row's loss NaN, as does a
- * NaN or +inf teacher value.  Errors as oft_token_logprobs. */
+ * An entry with index OFT_NO_LABEL, or at -inf, has q = 0 (one whose q is
+ * below 2^-126 may count as such); a row without any other has loss 0 and
+ * gradient 0.  A column at -inf with q > 0 makes the loss +inf.  An index
+ * listed twice counts with both its q.  Any other index outside [0, V) makes
+ * the row's loss NaN, as does a NaN or +inf teacher value.  Errors as
+ * oft_token_logprobs. */
 int32_t oft_distill_topk(const oft_vocab_desc* d, const void* logits, const int32_t* teacher_idx,
                          const float* teacher_logits, float* loss, float* stats, void* ws, size_t ws_bytes,
                          void* stream);

@@ -1076,9 +1076,10 @@ __device__ __forceinline__ void distill_finish(const FinishArgs& f, const Distil
   for (int i = 0; i < TI; ++i)
     if (te.ix[i] >= 0) {
       // q (log q - log p), the far end of log p kept in range by its q (a
-      // listed column may be masked at the type's lowest value)
+      // listed column may be masked at the type's lowest value; at -inf, as in
+      // an empty row, it is infinite however small q / tau)
       const float far = scaled(x[i], a.m, te.q[i] * f.invtau);
-      sum += a.s == 0.0f ? INFINITY : fmaf(te.q[i], te.logq[i] + l, -far);
+      sum += x[i] == -INFINITY && l == l ? INFINITY : fmaf(te.q[i], te.logq[i] + l, -far);
     }
   sum = wave_sum(sum);
   if (threadIdx.x == 0) {

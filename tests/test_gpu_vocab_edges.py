@@ -6,7 +6,7 @@ import pytest
 
 from oracle import vocab
 from tests.helpers import dev, host
-from tests.test_gpu_vocab import DTYPES, _c, _f32, _logprobs, _ws
+from tests.test_gpu_vocab import DTYPES, _c, _distill, _f32, _logprobs, _ws
 from tests.vocab_cases import NEG, U, Bounds, as_type, check
 
 pytestmark = pytest.mark.gpu
@@ -151,3 +151,29 @@ def test_distances_to_the_maximum_beyond_fp32(T, V, tau, dtype):
     check(host(loss), vocab.distill(x, idx, val, tau), b.teacher(idx, val)[0], "loss")
     ref = vocab.distill_grad(x, idx, val, np.ones(T), tau)
     check(host(dx.float()), ref, b.distill_grad(ref, idx, val, np.ones(T), dtype), "d_logits")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T,V", [(3, 300), (3, 70001), (201, 300)])
+def test_a_listed_column_of_little_weight_that_the_student_masks(T, V, dtype):
+    """255 equal entries and one just inside the smallest weight (its
+    exponential is 2^-125.5, its share of the sum 2^-133.5, and that over the
+    largest temperature 0 in fp32): masked by the student, the loss is infinite;
+    in a row with a NaN it is NaN, and with the entry unlisted finite."""
+    print(f"[little weight] T={T} V={V} {dtype}", flush=True)
+    tau, K = 2.0 ** 20, 256
+    rng = np.random.default_rng(1)
+    x = as_type(rng.normal(0, 2.5, (T, V)).astype(np.float32), dtype)
+    x[:, 299] = NEG
+    x[1, 298] = np.nan
+    idx = np.tile(np.append(np.arange(K - 1), 299).astype(np.int32), (T, 1))
+    val = np.zeros((T, K), np.float32)
+    val[:, -1] = -125.5 * np.log(2.0) * tau
+    idx[2, -1] = -1
+    q = vocab.teacher_probs(idx, val, V, tau)[0]
+    assert np.all(q[:2, -1] > 2.0 ** -134) and np.all(q[:2, -1] * 2.0 ** -20 < 2.0 ** -151)
+    _, _, loss, _ = _distill(_c(T, V, 1, tau=tau), dtype, x, idx, val)
+    b = Bounds(x, tau)
+    want = vocab.distill(x, idx, val, tau)
+    assert want[0] == np.inf and np.isnan(want[1]) and np.isfinite(want[2])
+    check(host(loss), want, b.teacher(idx, val)[0], "loss")
