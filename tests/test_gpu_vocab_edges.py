@@ -7,7 +7,7 @@ import pytest
 from oracle import vocab
 from tests.helpers import dev, host
 from tests.test_gpu_vocab import DTYPES, _c, _distill, _f32, _logprobs, _ws
-from tests.vocab_cases import NEG, U, Bounds, as_type, check
+from tests.vocab_cases import NEG, U, Bounds, as_type, check, rows
 
 pytestmark = pytest.mark.gpu
 
@@ -177,3 +177,115 @@ def test_a_listed_column_of_little_weight_that_the_student_masks(T, V, dtype):
     want = vocab.distill(x, idx, val, tau)
     assert want[0] == np.inf and np.isnan(want[1]) and np.isfinite(want[2])
     check(host(loss), want, b.teacher(idx, val)[0], "loss")
+
+
+# ------------------------------------------------------- rows and their calls
+def _everything(x, labels, idx, val, g, k, tau):
+    """Scoring, distillation and both gradients of some rows."""
+    import torch
+    import orthogonal_fine_tuning_amd as oft
+
+    T, V = x.shape
+    d = oft.vocab_desc(T, V, oft.OFT_DT_F32 if x.dtype == torch.float32 else oft.OFT_DT_BF16, k=k, temperature=tau)
+    o = dict(logp=_f32(T), entropy=_f32(T), stats=_f32(T, 2),
+             top_idx=torch.full((T, k), -5, dtype=torch.int32, device="cuda"), top_logp=_f32(T, k))
+    oft.oft_token_logprobs(d, x, labels, **o, **_ws(d))
+    d1, d2, loss, stats2 = torch.empty_like(x), torch.empty_like(x), _f32(T), _f32(T, 2)
+    oft.oft_token_logprobs_bwd(d, x, labels, o["stats"], g, d1, entropy=o["entropy"], g_entropy=g)
+    oft.oft_distill_topk(d, x, idx, val, loss, stats2, **_ws(d))
+    oft.oft_distill_topk_bwd(d, x, idx, val, stats2, g, d2)
+    torch.cuda.synchronize()
+    return {**o, "d_logits": d1, "loss": loss, "stats2": stats2, "distilled": d2}
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T,V", [(37, 30012), (37, 151936), (9, 300004)])
+def test_a_row_alone_and_in_any_order(T, V, dtype):
+    """Bit for bit the same results for a row among others, in another order
+    and by itself: whole rows, and rows in slices (as many for one row as for
+    all of these; rows of an even length start alike)."""
+    import torch
+
+    print(f"[any order] T={T} V={V} {dtype}", flush=True)
+    k, tau = 50, 0.9
+    rng = np.random.default_rng(V)
+    kinds = ["plain", "ties", "masked", "nan", "constant", "wide"]
+    x = torch.from_numpy(rows(T, V, dtype, 3, kinds)).to("cuda").to(torch.float32 if dtype == "f32" else torch.bfloat16)
+    labels, g = dev(rng.integers(0, V, T).astype(np.int32)), dev(rng.normal(0, 1, T).astype(np.float32))
+    idx = dev(rng.integers(0, V, (T, k)).astype(np.int32))
+    val = dev(rng.normal(0, 2, (T, k)).astype(np.float32))
+
+    def some(at):
+        return _everything(*(a[at].contiguous() for a in (x, labels, idx, val, g)), k, tau)
+
+    def same(name, a, b):
+        bits = {4: torch.int32, 2: torch.int16}[a.element_size()]
+        return torch.equal(a.contiguous().view(bits), b.contiguous().view(bits))
+
+    every = some(torch.arange(T, device="cuda"))
+    order = torch.from_numpy(rng.permutation(T)).to("cuda")
+    mixed = some(order)
+    for name in every:
+        assert same(name, mixed[name], every[name][order]), name
+    for t in range(0, T, 1 if V < 100000 else 4):
+        alone = some(torch.tensor([t], device="cuda"))
+        for name in every:
+            assert same(name, alone[name], every[name][t:t + 1]), (t, name)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_graphs_of_sliced_rows_with_a_shared_workspace(dtype):
+    """Scoring and distillation of rows in slices, captured into two graphs
+    that share the one workspace both of them write, replayed in turn and one
+    of them twice, with new logits and eager calls in between."""
+    import torch
+    import orthogonal_fine_tuning_amd as oft
+
+    T, V, k = 6, 70001, 20
+    dt = torch.float32 if dtype == "f32" else torch.bfloat16
+    d = oft.vocab_desc(T, V, oft.OFT_DT_F32 if dtype == "f32" else oft.OFT_DT_BF16, k=k)
+    n = oft.oft_vocab_workspace_bytes(d)
+    assert n > 0
+    ws, ws2 = (torch.full((n,), 0xA5, dtype=torch.uint8, device="cuda") for _ in range(2))
+    x = torch.empty((T, V), dtype=dt, device="cuda")
+    lab, g = torch.arange(T, dtype=torch.int32, device="cuda"), torch.ones(T, device="cuda")
+
+    def outs():
+        return dict(logp=_f32(T), entropy=_f32(T), stats=_f32(T, 2), top_logp=_f32(T, k), loss=_f32(T), stats2=_f32(T, 2),
+                    top_idx=torch.zeros((T, k), dtype=torch.int32, device="cuda"), d1=torch.empty_like(x),
+                    d2=torch.empty_like(x))
+
+    def score(o, w):
+        oft.oft_token_logprobs(d, x, lab, o["logp"], o["stats"], o["entropy"], o["top_idx"], o["top_logp"], ws=w, ws_bytes=n)
+        oft.oft_token_logprobs_bwd(d, x, lab, o["stats"], g, o["d1"], entropy=o["entropy"], g_entropy=g)
+
+    def distill(o, w):
+        oft.oft_distill_topk(d, x, o["top_idx"], o["top_logp"], o["loss"], o["stats2"], ws=w, ws_bytes=n)
+        oft.oft_distill_topk_bwd(d, x, o["top_idx"], o["top_logp"], o["stats2"], g, o["d2"])
+
+    a, e = outs(), outs()
+    x.copy_(torch.from_numpy(rows(T, V, dtype, 0)))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        score(a, ws)
+        torch.cuda.synchronize()
+        ws.fill_(0xA5)
+        distill(a, ws)
+    torch.cuda.synchronize()
+    assert bool((ws != 0xA5).any())  # the distillation's triples go through it too
+    g1, g2 = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g1):
+        score(a, ws)
+    with torch.cuda.graph(g2):
+        distill(a, ws)
+    for r in range(4):
+        x.copy_(torch.from_numpy(rows(T, V, dtype, r + 1, ["plain", "masked", "ties"])))
+        score(e, ws2)
+        distill(e, ws2)
+        torch.cuda.synchronize()
+        for graph in ((g1, g2), (g1, g2, g2), (g1, g1, g2), (g1, g2))[r]:
+            graph.replay()
+        torch.cuda.synchronize()
+        for name in a:
+            assert torch.equal(a[name], e[name]), (r, name)
