@@ -188,7 +188,7 @@ __device__ __forceinline__ float entropy_of(const Triple& a) {
 // k (x - m), also where the difference alone passes fp32's range
 __device__ __forceinline__ float scaled(float x, float m, float k) {
   const float d = x - m;
-  return d == -INFINITY ? k * x - k * m : k * d;
+  return d == -INFINITY && x > -INFINITY ? k * x - k * m : k * d;
 }
 
 __device__ __forceinline__ Triple join(const Triple& a, const Triple& b, float c) {

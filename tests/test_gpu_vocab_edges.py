@@ -289,3 +289,26 @@ def test_graphs_of_sliced_rows_with_a_shared_workspace(dtype):
         torch.cuda.synchronize()
         for name in a:
             assert torch.equal(a[name], e[name]), (r, name)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("tau", [0.5, 1.0, 2.0])
+@pytest.mark.parametrize("T,V", [(4, 31), (4, 70001), (201, 3000)])
+def test_masked_columns_below_a_row_of_lowest_values(T, V, tau, dtype):
+    """Columns at -inf where the maximum is the type's lowest value (and its
+    quotient by a small temperature passes fp32's range): log p is -inf."""
+    x = np.full((T, V), NEG, np.float32)
+    x[:, 5::9] = -3.3895314e38 if dtype == "bf16" else -3.4028235e38
+    labels = np.where(np.arange(T) % 2 == 0, 3, 5).astype(np.int32)
+    k = 20
+    _, got = _logprobs(_c(T, V, k, tau=tau), dtype, x, labels)
+    b, top = Bounds(x, tau), vocab.top(x, k)
+    assert np.array_equal(host(got["top_idx"]), top)
+    check(host(got["logp"]), vocab.given(b.lp, labels), b.lp_tol[np.arange(T), labels], "logp")
+    check(host(got["top_logp"]), np.take_along_axis(b.lp, top, 1), np.take_along_axis(b.lp_tol, top, 1), "top_logp")
+    check(host(got["entropy"]), b.H, b.H_tol, "entropy")
+    idx = np.tile(np.array([5, 14, 3], np.int32), (T, 1))
+    idx[::3, 2] = -1
+    val = np.zeros((T, 3), np.float32)
+    loss = _distill(_c(T, V, 1, tau=tau), dtype, x, idx, val)[2]
+    check(host(loss), vocab.distill(x, idx, val, tau), b.teacher(idx, val)[0], "loss")
