@@ -60,6 +60,9 @@
 extern "C" {
 #endif
 
+/* The losses on vocabulary logits and the router's balance loss came under
+ * version 8: a program that may meet an earlier library of that version looks
+ * their symbols up. */
 #define OFT_ABI_VERSION 8
 
 typedef enum {

@@ -1383,13 +1383,17 @@ int blocks_of(const VocabDims& d) {
 // from MANY_ROWS on, and for short rows, where one launch costs less than a
 // row's slices gain.  Measured (us, whole row / slices, the time of a call,
 // which two launches hold at 13 or more; on the GPU alone the slices of few
-// rows take 8.5 and with alternatives 10): bf16 of 151936 columns with 20
+// rows take 8.5 and with alternatives 10; the limits are the same for both
+// types and for calls with and without entropy): bf16 of 151936 columns with 20
 // alternatives 1 row 18.9 / 14.9, 64 rows 20.7 / 15.8, 200 rows 23.2 / 23.4,
 // 400 rows 30.4 / 32.9, 4096 rows 202 / 234; without 64 rows 16.2 / 13.7, 200
 // rows 20.1 / 17.7, 400 rows 26.3 / 27.8; of 32003 columns with 20
 // alternatives 1 row 10.5 / 14.6, 400 rows 18.4 / 20.8; fp32 of 50021 columns
 // without 1 row 9.0 / 13.3, 57 rows 9.5 / 14.2, with 20 alternatives 12.3 /
-// 14.7 and 13.5 / 14.8.
+// 14.7 and 13.5 / 14.8.  So the other side is the faster one for 200 to
+// somewhat less than 400 rows of 151936 columns without alternatives (2.4 us at
+// 200) and for fp32 rows of 50021 columns with them (2.4 us for 1 row, 1.3 for
+// 57).
 constexpr int MANY_ROWS = 200, SHORT = 65536, SHORT_TOP = 32768;
 template <class Ty>
 bool whole_rows(const VocabDims& d, bool top) {
