@@ -185,7 +185,8 @@ __device__ __forceinline__ float entropy_of(const Triple& a) {
   return a.s == 0.0f ? 0.0f : (__builtin_amdgcn_logf(a.s) - a.w / a.s) * LN2;
 }
 
-// k (x - m), also where the difference alone passes fp32's range
+// k (x - m), also where the difference of finite values alone passes fp32's
+// range (for x = -inf the two products could be infinite alike)
 __device__ __forceinline__ float scaled(float x, float m, float k) {
   const float d = x - m;
   return d == -INFINITY && x > -INFINITY ? k * x - k * m : k * d;
