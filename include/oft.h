@@ -60,9 +60,10 @@
 extern "C" {
 #endif
 
-/* The losses on vocabulary logits and the router's balance loss came under
- * version 8: a program that may meet an earlier library of that version looks
- * their symbols up. */
+/* The losses on vocabulary logits, the router's balance loss, the operators on
+ * adapters of many requests and the gradient clipping came under version 8: a
+ * program that may meet an earlier library of that version looks their symbols
+ * up. */
 #define OFT_ABI_VERSION 8
 
 typedef enum {
@@ -531,6 +532,149 @@ int32_t oft_moe_balance(const oft_moe_desc* d, int32_t seq_len, const float* log
 int32_t oft_moe_balance_bwd(const oft_moe_desc* d, int32_t seq_len, const float* logits,
                             const uint8_t* mask_or_null, const int32_t* counts, const int32_t* tokens,
                             const float* g_loss, float* d_logits, int32_t accumulate, void* stream);
+
+/* ---- adapters of many requests ----------------------------------------------
+ * One frozen projection, many adapters: a server's batch mixes requests that
+ * began under different versions of an adapter (the Synced article's
+ * "Technical details" section keeps requests in flight while a new version
+ * streams in) or that belong to different adapters altogether, and a training
+ * step may update several at once.  The shared projection runs once, by
+ * oft_linear_fwd_base (dx: oft_linear_bwd with R = I); the calls below add
+ * what each row's own adapter does, orthogonal (block rotations) or low-rank
+ * (the other family that the chooseai.io page's "Architectural advantages of
+ * OFT over LoRA" compares with).
+ *
+ * Rows are given their adapter by number: adapter int32 [T], 0 .. n - 1, any
+ * other value for a row that uses the base model alone.  oft_adapter_route
+ * sorts the rows once per batch; every call on that batch reads the result:
+ *   order    int32 [T]    rows by adapter, equal ones in their own order, rows
+ *                         without an adapter last
+ *   offsets  int32 [n+1]  adapter a's rows are order[offsets[a] ..
+ *                         offsets[a+1]); offsets[n] rows have an adapter
+ *   tiles    work lists for the other calls, of the size that
+ *            oft_adapter_rows_bytes gives
+ * Rows keep their places in x, y and the rest; nothing is gathered or moved.
+ * T and n of a call's descriptor have to be those of its rows (else
+ * OFT_ESHAPE).  T == 0 leaves nothing to write but zero gradients. */
+#define OFT_MAX_ADAPTERS 1024
+typedef struct {
+  int32_t T, n;     /* rows (at most 2^22), adapters (at most OFT_MAX_ADAPTERS) */
+  int32_t* order;
+  int32_t* offsets;
+  int32_t* tiles;
+} oft_adapter_rows;
+
+/* Sizes of `tiles` and of oft_adapter_route's workspace (0 up to 16384 rows).
+ * Errors here and below: OFT_EINVAL (T < 0, n < 1, null or misaligned
+ * pointers), OFT_EUNSUPPORTED (T > 2^22, n > OFT_MAX_ADAPTERS). */
+int32_t oft_adapter_rows_bytes(int32_t T, int32_t n, size_t* tiles_bytes, size_t* ws_bytes);
+int32_t oft_adapter_route(const int32_t* adapter, const oft_adapter_rows* rows, void* ws, size_t ws_bytes,
+                          void* stream);
+
+/* Low-rank updates beside a projection x [T, K] -> y [T, N], N = sum(seg): each
+ * segment s of a fused projection (columns c of y) has its own factors,
+ *   v[t, s r + j] = sum_k x[t, k] A[a, s r + j, k]
+ *   y[t, c]       = y_base[t, c] + scale[a] sum_j v[t, s r + j] B[a, c, j]
+ * with a the row's adapter; y = y_base and v = 0 in rows without one.
+ * A bf16 [n, n_seg r, K], B bf16 [n, N, r], scale fp32 [n].
+ * Constraints: r and n_seg at least 1 and K % 64 == 0, r % 8 == 0, every
+ * seg[s] % 16 == 0 (else OFT_ESHAPE); r <= OFT_MAX_RANK, n_seg <= 8, K and N <=
+ * 2^20 (else OFT_EUNSUPPORTED); dtype OFT_DT_BF16 or OFT_DT_F32.
+ * All sums are fp32, and a result is rounded once, to its own type: v and fp32
+ * rows enter the matrix products as bf16 parts that hold all their bits (16
+ * of them where the result is bf16).  A row's infinite or NaN values reach its
+ * own results and its adapter's gradients alone; there they may become NaN
+ * where the formula has an infinity. */
+#define OFT_MAX_RANK 128
+typedef struct {
+  int32_t T, n, K, N;
+  int32_t r;      /* rank of each segment's update                  */
+  int32_t dtype;  /* of x, y_base, y, dx_base and dx (dy is bf16)   */
+  int32_t n_seg;
+  int32_t seg[OFT_MAX_SEGMENTS];
+} oft_lowrank_desc;
+
+int32_t oft_lowrank_workspace_bytes(const oft_lowrank_desc* d, int32_t pass, size_t* bytes);
+
+/* y_base is what the shared projection wrote; y may be y_base itself (same
+ * pointer), any other overlap of them, or of y and x, is OFT_EINVAL.
+ * v_or_null [T, n_seg r] fp32 is kept for the backward when given. */
+int32_t oft_lowrank_fwd(const oft_lowrank_desc* d, const oft_adapter_rows* rows, const void* x, const uint16_t* A,
+                        const uint16_t* B, const float* scale, const void* y_base, void* y, float* v_or_null, void* ws,
+                        size_t ws_bytes, void* stream);
+
+/* Backward of <dy, y>, dy [T, N] bf16 and v as the forward wrote it:
+ *   u[t, s r + j] = sum_{c in s} dy[t, c] B[a, c, j]
+ *   dx[t]      = dx_base[t] + scale[a] sum_j u[t, j] A[a, j]
+ *   dA[a, j]   = scale[a] sum_{rows t of a} u[t, j] x[t]          fp32
+ *   dB[a, c, j] = scale[a] sum_{rows t of a} dy[t, c] v[t, s r + j]  fp32
+ * dx_base (what the shared projection's backward wrote) may be NULL, for
+ * zeros, or dx itself; any other overlap of dx with dx_base, x or dy is
+ * OFT_EINVAL.  dA and dB are 0 for an adapter without rows.  Each gradient may
+ * be NULL; x is needed for dA, v for dB, A for dx, B for dx and dA. */
+int32_t oft_lowrank_bwd(const oft_lowrank_desc* d, const oft_adapter_rows* rows, const uint16_t* dy, const void* x,
+                        const float* v, const uint16_t* A, const uint16_t* B, const float* scale,
+                        const void* dx_base_or_null, void* dx_or_null, float* dA_or_null, float* dB_or_null, void* ws,
+                        size_t ws_bytes, void* stream);
+
+/* Block rotations after a projection with output z [T, N]: in every block j of
+ * b channels, with a the row's adapter,
+ *   y[t, blk j] = R[a, j] z[t, blk j];  y = z in rows without an adapter.
+ * R_ops bf16 [n, N/b, 2, b, b] and R_f32 [n, N/b, b, b] as cayley_build writes
+ * them for the n N/b blocks of all adapters together.  Segments of a fused
+ * projection need no mention: their blocks follow each other.
+ * Constraints: b in {16, 32} and N <= 2^20 (else OFT_EUNSUPPORTED),
+ * N % 32 == 0 (else OFT_ESHAPE); dtype OFT_DT_BF16 or OFT_DT_F32.
+ * Sums are fp32 and a result is rounded once; fp32 rows enter the matrix
+ * products with all their bits (oft_linear_fwd rounds its z to bf16 there). */
+typedef struct {
+  int32_t T, n, N, b;
+  int32_t dtype;  /* of z, y and y_saved (dy and dz are bf16) */
+} oft_rotate_desc;
+
+/* The forward needs no workspace. */
+int32_t oft_rotate_workspace_bytes(const oft_rotate_desc* d, int32_t pass, size_t* bytes);
+
+/* y may be z itself; any other overlap is OFT_EINVAL. */
+int32_t oft_rotate_fwd(const oft_rotate_desc* d, const oft_adapter_rows* rows, const void* z, const uint16_t* R_ops,
+                       void* y, void* stream);
+
+/* Backward of <dy, y>, dy [T, N] bf16 and y_saved the forward's output:
+ *   dz[t, blk j] = R[a, j]^T dy[t, blk j]  (dy in rows without an adapter),
+ *   dq [n, N/b, b(b-1)/2] fp32, packed like cayley_build's parameters, as
+ *   oft_linear_bwd forms it from each adapter's own rows (0 without any).
+ * dz is what the shared projection's backward takes.  Either may be NULL; dz
+ * may be dy itself, any other overlap of dz with dy or y_saved is OFT_EINVAL.
+ * y_saved and R_f32 are needed for dq, R_ops for dz. */
+int32_t oft_rotate_bwd(const oft_rotate_desc* d, const oft_adapter_rows* rows, const uint16_t* dy, const void* y_saved,
+                       const float* R_f32, const uint16_t* R_ops, uint16_t* dz_or_null, float* dq_or_null, void* ws,
+                       size_t ws_bytes, void* stream);
+
+/* ---- global gradient norm and clipping -------------------------------------
+ * What a training step does between the adapters' gradients (dq, dA, dB of
+ * every layer) and its optimiser:
+ *   sumsq = sum of g^2 over the m tensors (fp64: no finite g overflows)
+ *   norm = sqrt(sumsq), coefficient = min(1, max_norm / (norm + 1e-6))
+ *   out[i] = coefficient grads[i]
+ * in two calls, so that sumsq can be reduced over GPUs that hold different
+ * gradients in between.  grads, numel and out are HOST arrays of m device
+ * addresses, element counts and addresses, read during the call; a captured
+ * call replays with the addresses of its capture.  All tensors have one dtype
+ * (OFT_DT_BF16 or OFT_DT_F32), need only their element's alignment, and may be
+ * empty (their address is then not looked at).  out[i] is grads[i] itself or
+ * lies apart from it (else OFT_EINVAL); no out may overlap another's tensors.
+ * Gradients in place with coefficient 1 are not written.  sumsq: device fp64;
+ * stats: device fp32 [2] = (norm, coefficient), 8-byte aligned.  An infinite
+ * norm has coefficient 0, a NaN among the gradients makes all of it NaN.
+ * Deterministic.  Errors: OFT_EINVAL (m < 0, a negative count, max_norm
+ * negative or NaN, null or misaligned pointers), OFT_EDTYPE, OFT_EUNSUPPORTED
+ * (m > OFT_MAX_GRADS, 2^40 elements or more), OFT_EWORKSPACE. */
+#define OFT_MAX_GRADS 65536
+int32_t oft_grad_workspace_bytes(int32_t m, const int64_t* numel, int32_t dtype, size_t* bytes);
+int32_t oft_grad_sumsq(int32_t m, const void* const* grads, const int64_t* numel, int32_t dtype, double* sumsq,
+                       void* ws, size_t ws_bytes, void* stream);
+int32_t oft_grad_clip(int32_t m, const void* const* grads, const int64_t* numel, int32_t dtype, const double* sumsq,
+                      float max_norm, void* const* out, float* stats, void* stream);
 
 #ifdef __cplusplus
 }

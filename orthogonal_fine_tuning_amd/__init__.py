@@ -11,7 +11,8 @@ import ctypes as C
 from . import _lib
 from ._lib import (OFT_DT_BF16, OFT_DT_F32, OFT_PASS_BWD, OFT_PASS_FWD, OFT_W_BF16,
                    OFT_W_FP4_E2M1, OFT_W_FP8_E4M3, OFT_W_INT4, OFT_W_INT4_TILED, OFT_MAX_TEACHER, OFT_MAX_TOP,
-                   OFT_NO_LABEL, OftError, oft_linear_desc, oft_moe_desc, oft_moe_routing, oft_vocab_desc)
+                   OFT_MAX_ADAPTERS, OFT_MAX_GRADS, OFT_MAX_RANK, OFT_NO_LABEL, OftError, oft_adapter_rows,
+                   oft_linear_desc, oft_lowrank_desc, oft_moe_desc, oft_moe_routing, oft_rotate_desc, oft_vocab_desc)
 
 __all__ = [
     "OftError", "linear_desc", "moe_desc", "moe_routing", "cayley_build", "oft_dequant", "oft_pack_int4_tiled",
@@ -20,10 +21,15 @@ __all__ = [
     "oft_moe_workspace_bytes", "oft_moe_route", "oft_moe_router_bwd", "oft_moe_grouped_fwd", "oft_moe_grouped_fwd_base", "oft_moe_grouped_bwd", "abi_version",
     "vocab_desc", "oft_vocab_workspace_bytes", "oft_token_logprobs", "oft_token_logprobs_bwd", "oft_distill_topk",
     "oft_distill_topk_bwd", "oft_moe_balance_workspace_bytes", "oft_moe_balance", "oft_moe_balance_bwd",
+    "AdapterRows", "adapter_rows", "oft_adapter_rows_bytes", "oft_adapter_route", "lowrank_desc",
+    "oft_lowrank_workspace_bytes", "oft_lowrank_fwd", "oft_lowrank_bwd", "rotate_desc", "oft_rotate_workspace_bytes",
+    "oft_rotate_fwd", "oft_rotate_bwd", "GradList", "grad_list", "oft_grad_workspace_bytes", "oft_grad_sumsq",
+    "oft_grad_clip",
     "prof_enable", "prof_records",
     "OFT_DT_BF16", "OFT_DT_F32", "OFT_W_INT4", "OFT_W_FP8_E4M3", "OFT_W_BF16", "OFT_W_FP4_E2M1", "OFT_W_INT4_TILED",
     "OFT_PASS_FWD",
-    "OFT_PASS_BWD", "OFT_MAX_TOP", "OFT_MAX_TEACHER", "OFT_NO_LABEL",
+    "OFT_PASS_BWD", "OFT_MAX_TOP", "OFT_MAX_TEACHER", "OFT_NO_LABEL", "OFT_MAX_ADAPTERS", "OFT_MAX_RANK",
+    "OFT_MAX_GRADS",
 ]
 
 
@@ -337,6 +343,205 @@ def oft_moe_balance_bwd(desc, seq_len, logits, counts, tokens, g_loss, d_logits,
     g = _tensor("g_loss", g_loss, "float32", (S,), dev)
     dx = _tensor("d_logits", d_logits, "float32", (d.T, d.E), dev)
     _launch("oft_moe_balance_bwd", dev, stream, C.byref(d), int(seq_len), x, mk, cn, tk, g, dx, int(accumulate))
+
+
+# ---- adapters of many requests ---------------------------------------------
+# These calls check their tensors as those above do, against the descriptor
+# and on the GPU of the rows' order.
+class AdapterRows:
+    """A batch's rows sorted by adapter: order int32 [T], offsets int32 [n + 1]
+    and the work lists of the calls that run over them, with the workspace of
+    oft_adapter_route.  Calls that overlap on different streams may share one
+    that none of them writes."""
+
+    def __init__(self, T, n, order, offsets, tiles, ws):
+        self.T, self.n, self.order, self.offsets, self.tiles, self.ws = int(T), int(n), order, offsets, tiles, ws
+        dev = self.dev = offsets.get_device()
+        tiles_bytes, ws_bytes = oft_adapter_rows_bytes(T, n)
+        self.c = oft_adapter_rows()
+        self.c.T, self.c.n = self.T, self.n
+        self.c.order = _tensor("order", order, "int32", (self.T,), dev) or None
+        self.c.offsets = _tensor("offsets", offsets, "int32", (self.n + 1,), dev)
+        self.c.tiles = _buffer("tiles", tiles, tiles_bytes, dev)
+        self.ws_bytes = ws_bytes
+        self._ws = _buffer("ws", ws, ws_bytes, dev) if ws_bytes else None
+
+
+def _buffer(what, t, nbytes, dev):
+    if t.get_device() != dev or not t.is_contiguous() or t.numel() * t.element_size() < nbytes:
+        raise ValueError(f"{what}: want a contiguous tensor of at least {nbytes} bytes on the rows' GPU")
+    return t.data_ptr()
+
+
+def oft_adapter_rows_bytes(T, n):
+    """(bytes of the work lists, bytes of oft_adapter_route's workspace)."""
+    a, b = C.c_size_t(0), C.c_size_t(0)
+    _lib.check(_lib.load().oft_adapter_rows_bytes(int(T), int(n), C.byref(a), C.byref(b)), "oft_adapter_rows_bytes")
+    return a.value, b.value
+
+
+def adapter_rows(T, n, device="cuda") -> AdapterRows:
+    """AdapterRows with tensors of its own on `device`, for oft_adapter_route to fill."""
+    import torch
+
+    tiles, ws = oft_adapter_rows_bytes(T, n)
+    new = lambda k: torch.empty(k, dtype=torch.int32, device=device)  # noqa: E731
+    return AdapterRows(T, n, new(T), new(n + 1), new(tiles // 4), new((ws + 3) // 4))
+
+
+def oft_adapter_route(rows, adapter, stream=None):
+    """Sort the batch's rows by adapter int32 [T] (outside 0 .. n - 1: none)."""
+    a = _tensor("adapter", adapter, "int32", (rows.T,), rows.dev)
+    _launch("oft_adapter_route", rows.dev, stream, a or None, C.byref(rows.c), rows._ws, rows.ws_bytes)
+
+
+def lowrank_desc(T, n, K, segs, r, dtype=OFT_DT_BF16) -> oft_lowrank_desc:
+    d = oft_lowrank_desc()
+    d.T, d.n, d.K, d.N, d.r, d.dtype = int(T), int(n), int(K), int(sum(segs)), int(r), int(dtype)
+    d.n_seg = len(segs)
+    for i, s in enumerate(segs[:len(d.seg)]):
+        d.seg[i] = int(s)
+    return d
+
+
+def oft_lowrank_workspace_bytes(desc, pass_) -> int:
+    n = C.c_size_t(0)
+    _lib.check(_lib.load().oft_lowrank_workspace_bytes(C.byref(desc), pass_, C.byref(n)),
+               "oft_lowrank_workspace_bytes")
+    return n.value
+
+
+_BF16 = "bfloat16 int16 uint16"
+
+
+def _row_type(desc):
+    return "float32" if desc.dtype == OFT_DT_F32 else _BF16
+
+
+def _same_batch(desc, rows):
+    if desc.T != rows.T or desc.n != rows.n:
+        raise ValueError(f"rows: of {rows.T} rows and {rows.n} adapters, want {desc.T} and {desc.n}")
+
+
+def oft_lowrank_fwd(desc, rows, x, A, B, scale, y_base, y, v=None, ws=None, ws_bytes=0, stream=None):
+    """y = y_base + scale v B^T, v = x A^T, with each row's own factors; y may be y_base."""
+    d, dev, t = desc, rows.dev, _row_type(desc)
+    _same_batch(d, rows)
+    R = d.n_seg * d.r
+    _launch("oft_lowrank_fwd", dev, stream, C.byref(d), C.byref(rows.c), _tensor("x", x, t, (d.T, d.K), dev),
+            _tensor("A", A, _BF16, (d.n, R, d.K), dev), _tensor("B", B, _BF16, (d.n, d.N, d.r), dev),
+            _tensor("scale", scale, "float32", (d.n,), dev), _tensor("y_base", y_base, t, (d.T, d.N), dev),
+            _tensor("y", y, t, (d.T, d.N), dev), _maybe("v", v, "float32", (d.T, R), dev),
+            _workspace(ws, ws_bytes, dev), ws_bytes)
+
+
+def oft_lowrank_bwd(desc, rows, dy, x, v, A, B, scale, dx=None, dx_base=None, dA=None, dB=None, ws=None, ws_bytes=0,
+                    stream=None):
+    """dx (added to dx_base, which may be dx), dA and dB of <dy, y>."""
+    d, dev, t = desc, rows.dev, _row_type(desc)
+    _same_batch(d, rows)
+    R = d.n_seg * d.r
+    _launch("oft_lowrank_bwd", dev, stream, C.byref(d), C.byref(rows.c),
+            _tensor("dy", dy, _BF16, (d.T, d.N), dev), _maybe("x", x, t, (d.T, d.K), dev),
+            _maybe("v", v, "float32", (d.T, R), dev), _maybe("A", A, _BF16, (d.n, R, d.K), dev),
+            _maybe("B", B, _BF16, (d.n, d.N, d.r), dev), _tensor("scale", scale, "float32", (d.n,), dev),
+            _maybe("dx_base", dx_base, t, (d.T, d.K), dev), _maybe("dx", dx, t, (d.T, d.K), dev),
+            _maybe("dA", dA, "float32", (d.n, R, d.K), dev), _maybe("dB", dB, "float32", (d.n, d.N, d.r), dev),
+            _workspace(ws, ws_bytes, dev), ws_bytes)
+
+
+def rotate_desc(T, n, N, b, dtype=OFT_DT_BF16) -> oft_rotate_desc:
+    d = oft_rotate_desc()
+    d.T, d.n, d.N, d.b, d.dtype = int(T), int(n), int(N), int(b), int(dtype)
+    return d
+
+
+def oft_rotate_workspace_bytes(desc, pass_) -> int:
+    n = C.c_size_t(0)
+    _lib.check(_lib.load().oft_rotate_workspace_bytes(C.byref(desc), pass_, C.byref(n)), "oft_rotate_workspace_bytes")
+    return n.value
+
+
+def oft_rotate_fwd(desc, rows, z, R_ops, y, stream=None):
+    """y = R z in every block of channels, with each row's own R; y may be z."""
+    d, dev, t = desc, rows.dev, _row_type(desc)
+    _same_batch(d, rows)
+    _launch("oft_rotate_fwd", dev, stream, C.byref(d), C.byref(rows.c), _tensor("z", z, t, (d.T, d.N), dev),
+            _tensor("R_ops", R_ops, _BF16, (d.n, d.N // d.b, 2, d.b, d.b), dev), _tensor("y", y, t, (d.T, d.N), dev))
+
+
+def oft_rotate_bwd(desc, rows, dy, y_saved, R_f32, R_ops, dz=None, dq=None, ws=None, ws_bytes=0, stream=None):
+    """dz (may be dy) and dq of <dy, y>."""
+    d, dev = desc, rows.dev
+    _same_batch(d, rows)
+    nblk = d.N // d.b
+    _launch("oft_rotate_bwd", dev, stream, C.byref(d), C.byref(rows.c), _tensor("dy", dy, _BF16, (d.T, d.N), dev),
+            _maybe("y_saved", y_saved, _row_type(d), (d.T, d.N), dev),
+            _maybe("R_f32", R_f32, "float32", (d.n, nblk, d.b, d.b), dev),
+            _maybe("R_ops", R_ops, _BF16, (d.n, nblk, 2, d.b, d.b), dev), _maybe("dz", dz, _BF16, (d.T, d.N), dev),
+            _maybe("dq", dq, "float32", (d.n, nblk, d.b * (d.b - 1) // 2), dev), _workspace(ws, ws_bytes, dev), ws_bytes)
+
+
+# ---- global gradient norm and clipping --------------------------------------
+class GradList:
+    """Gradients and where their clipped values go, checked once: a program
+    whose gradients keep their addresses makes one and uses it every step."""
+
+    def __init__(self, grads, out=None):
+        import torch
+
+        self.grads, self.out = list(grads), list(grads if out is None else out)
+        self.m = len(self.grads)
+        if len(self.out) != self.m or self.m == 0:
+            raise ValueError(f"grad_list: {self.m} gradients, {len(self.out)} outputs: want as many, and one at least")
+        first = self.grads[0]
+        self.dev = first.get_device()
+        self.dtype = OFT_DT_F32 if first.dtype == torch.float32 else OFT_DT_BF16
+        kind = "float32" if self.dtype == OFT_DT_F32 else "bfloat16"
+        for g, o in zip(self.grads, self.out):
+            _tensor("grads", g, kind, g.shape, self.dev)
+            _tensor("out", o, kind, g.shape, self.dev)
+        at = lambda t: (t.data_ptr(), t.data_ptr() + t.numel() * t.element_size())  # noqa: E731
+        written = sorted(at(o) for o in self.out if o.numel())
+        for a, b in zip(written, written[1:]):
+            if b[0] < a[1]:
+                raise ValueError("grad_list: two outputs overlap")
+        apart = sorted([(at(g), 0) for g, o in zip(self.grads, self.out) if g.numel() and g.data_ptr() != o.data_ptr()] +
+                       [(w, 1) for w in written])
+        end = [0, 0]
+        for (lo, hi), kind_ in apart:
+            if lo < end[1 - kind_]:
+                raise ValueError("grad_list: an output overlaps a gradient that is not its own")
+            end[kind_] = max(end[kind_], hi)
+        self._grads = (C.c_void_p * self.m)(*[t.data_ptr() for t in self.grads])
+        self._out = (C.c_void_p * self.m)(*[t.data_ptr() for t in self.out])
+        self._numel = (C.c_int64 * self.m)(*[t.numel() for t in self.grads])
+
+
+def grad_list(grads, out=None) -> GradList:
+    """out: where the clipped gradients go (the gradients themselves if None)."""
+    return GradList(grads, out)
+
+
+def oft_grad_workspace_bytes(grads) -> int:
+    n = C.c_size_t(0)
+    _lib.check(_lib.load().oft_grad_workspace_bytes(grads.m, grads._numel, grads.dtype, C.byref(n)),
+               "oft_grad_workspace_bytes")
+    return n.value
+
+
+def oft_grad_sumsq(grads, sumsq, ws=None, ws_bytes=0, stream=None):
+    """sumsq fp64 [1]: the sum of the squares of all gradients of a GradList."""
+    _launch("oft_grad_sumsq", grads.dev, stream, grads.m, grads._grads, grads._numel, grads.dtype,
+            _tensor("sumsq", sumsq, "float64", (1,), grads.dev), _workspace(ws, ws_bytes, grads.dev), ws_bytes)
+
+
+def oft_grad_clip(grads, sumsq, max_norm, stats, stream=None):
+    """Scale the gradients so that their norm is at most max_norm; stats fp32
+    [2]: the norm before, and the coefficient."""
+    _launch("oft_grad_clip", grads.dev, stream, grads.m, grads._grads, grads._numel, grads.dtype,
+            _tensor("sumsq", sumsq, "float64", (1,), grads.dev), float(max_norm), grads._out,
+            _tensor("stats", stats, "float32", (2,), grads.dev))
 
 
 def oft_moe_workspace_bytes(desc, pass_) -> int:

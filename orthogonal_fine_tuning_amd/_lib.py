@@ -19,6 +19,7 @@ OFT_PASS_FWD, OFT_PASS_BWD = 0, 1
 OFT_MAX_SEGMENTS = 8
 OFT_NOALLOC_SCRATCH_BYTES = 128 << 20
 OFT_MAX_TOP, OFT_MAX_TEACHER, OFT_NO_LABEL = 128, 256, -1
+OFT_MAX_ADAPTERS, OFT_MAX_RANK, OFT_MAX_GRADS = 1024, 128, 65536
 
 
 class oft_linear_desc(C.Structure):
@@ -44,6 +45,20 @@ class oft_vocab_desc(C.Structure):
     _fields_ = [("T", C.c_int32), ("V", C.c_int32), ("dtype", C.c_int32), ("k", C.c_int32),
                 ("ld", C.c_int64), ("ld_grad", C.c_int64), ("temperature", C.c_float),
                 ("accumulate", C.c_int32)]
+
+
+class oft_adapter_rows(C.Structure):
+    _fields_ = [("T", C.c_int32), ("n", C.c_int32), ("order", C.c_void_p), ("offsets", C.c_void_p),
+                ("tiles", C.c_void_p)]
+
+
+class oft_lowrank_desc(C.Structure):
+    _fields_ = [("T", C.c_int32), ("n", C.c_int32), ("K", C.c_int32), ("N", C.c_int32), ("r", C.c_int32),
+                ("dtype", C.c_int32), ("n_seg", C.c_int32), ("seg", C.c_int32 * OFT_MAX_SEGMENTS)]
+
+
+class oft_rotate_desc(C.Structure):
+    _fields_ = [("T", C.c_int32), ("n", C.c_int32), ("N", C.c_int32), ("b", C.c_int32), ("dtype", C.c_int32)]
 
 
 _P = C.c_void_p
@@ -79,6 +94,20 @@ SIGNATURES = {
     "oft_moe_balance_workspace_bytes": (_I, [C.POINTER(oft_moe_desc), _I, C.POINTER(_SZ)]),
     "oft_moe_balance": (_I, [C.POINTER(oft_moe_desc), _I, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "oft_moe_balance_bwd": (_I, [C.POINTER(oft_moe_desc), _I, _P, _P, _P, _P, _P, _P, _I, _P]),
+    "oft_adapter_rows_bytes": (_I, [_I, _I, C.POINTER(_SZ), C.POINTER(_SZ)]),
+    "oft_adapter_route": (_I, [_P, C.POINTER(oft_adapter_rows), _P, _SZ, _P]),
+    "oft_lowrank_workspace_bytes": (_I, [C.POINTER(oft_lowrank_desc), _I, C.POINTER(_SZ)]),
+    "oft_lowrank_fwd": (_I, [C.POINTER(oft_lowrank_desc), C.POINTER(oft_adapter_rows), _P, _P, _P, _P, _P, _P, _P, _P,
+                             _SZ, _P]),
+    "oft_lowrank_bwd": (_I, [C.POINTER(oft_lowrank_desc), C.POINTER(oft_adapter_rows), _P, _P, _P, _P, _P, _P, _P, _P,
+                             _P, _P, _P, _SZ, _P]),
+    "oft_rotate_workspace_bytes": (_I, [C.POINTER(oft_rotate_desc), _I, C.POINTER(_SZ)]),
+    "oft_rotate_fwd": (_I, [C.POINTER(oft_rotate_desc), C.POINTER(oft_adapter_rows), _P, _P, _P, _P]),
+    "oft_rotate_bwd": (_I, [C.POINTER(oft_rotate_desc), C.POINTER(oft_adapter_rows), _P, _P, _P, _P, _P, _P, _P, _SZ,
+                            _P]),
+    "oft_grad_workspace_bytes": (_I, [_I, _P, _I, C.POINTER(_SZ)]),
+    "oft_grad_sumsq": (_I, [_I, _P, _P, _I, _P, _P, _SZ, _P]),
+    "oft_grad_clip": (_I, [_I, _P, _P, _I, _P, C.c_float, _P, _P, _P]),
     "oft_moe_workspace_bytes": (_I, [C.POINTER(oft_moe_desc), _I, C.POINTER(_SZ)]),
     "oft_moe_route": (_I, [C.POINTER(oft_moe_desc), _P, C.POINTER(oft_moe_routing), _P, _SZ, _P]),
     "oft_moe_grouped_fwd": (_I, [C.POINTER(oft_moe_desc), _P, _P, _P, _P, _P, _P, _P,
