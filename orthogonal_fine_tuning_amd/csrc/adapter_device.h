@@ -60,6 +60,20 @@ __device__ __forceinline__ void split_bf16x8(const float (&v)[8], uint4 (&o)[P])
   for (int p = 0; p < P; ++p) o[p] = make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
 }
 
+// 16-byte loads and stores; STREAM: past the caches, for rows that are read
+// and written once and do not fit them.
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+template <bool STREAM>
+__device__ __forceinline__ uint4 load16(const void* p) {
+  if constexpr (STREAM) return __builtin_bit_cast(uint4, __builtin_nontemporal_load(static_cast<const u32x4*>(p)));
+  else return *static_cast<const uint4*>(p);
+}
+template <bool STREAM>
+__device__ __forceinline__ void store16(void* p, const uint4& v) {
+  if constexpr (STREAM) __builtin_nontemporal_store(__builtin_bit_cast(u32x4, v), static_cast<u32x4*>(p));
+  else *static_cast<uint4*>(p) = v;
+}
+
 // Eight consecutive elements of a bf16 or fp32 row as P operands (P = 1 for
 // bf16, whose values are operands already; 3 for fp32).
 template <bool F32>
@@ -68,8 +82,13 @@ template <>
 struct Oct<false> {
   static constexpr int P = 1;
   uint4 u;
+  template <bool STREAM = false>
   __device__ __forceinline__ void load(const void* p, size_t at) {
-    u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at);
+    u = load16<STREAM>(static_cast<const uint16_t*>(p) + at);
+  }
+  template <bool STREAM = false>
+  __device__ __forceinline__ void store(void* p, size_t at) const {
+    store16<STREAM>(static_cast<uint16_t*>(p) + at, u);
   }
   __device__ __forceinline__ void zero() { u = zero4(); }
   __device__ __forceinline__ void parts(uint4 (&o)[1]) const { o[0] = u; }
@@ -78,10 +97,17 @@ template <>
 struct Oct<true> {
   static constexpr int P = 3;
   float4 a, b;
+  template <bool STREAM = false>
   __device__ __forceinline__ void load(const void* p, size_t at) {
-    const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
-    a = q[0];
-    b = q[1];
+    const float* q = static_cast<const float*>(p) + at;
+    a = __builtin_bit_cast(float4, load16<STREAM>(q));
+    b = __builtin_bit_cast(float4, load16<STREAM>(q + 4));
+  }
+  template <bool STREAM = false>
+  __device__ __forceinline__ void store(void* p, size_t at) const {
+    float* q = static_cast<float*>(p) + at;
+    store16<STREAM>(q, __builtin_bit_cast(uint4, a));
+    store16<STREAM>(q + 4, __builtin_bit_cast(uint4, b));
   }
   __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
   __device__ __forceinline__ void parts(uint4 (&o)[3]) const {
@@ -89,5 +115,38 @@ struct Oct<true> {
     split_bf16x8<3>(v, o);
   }
 };
+
+// A wave's own tile in LDS, 64 rows of 128 bytes, between the two ways in
+// which its lanes hold it: by rows (piece i: 16 bytes of row 8 i + lane / 8,
+// eight lanes to a row, as global memory is best read and written: a load
+// whose lanes follow each other down the rows takes the memory pipe four
+// times as long) and by operands (16 bytes of row 16 i + lane % 16, as matrix
+// steps take and leave them).  Chunks of a row are exchanged by bits of its
+// number, so that both ways touch all banks evenly.
+struct WaveTile {
+  static constexpr int BYTES = 64 * 128;
+  char* lds;
+  __device__ __forceinline__ uint4* at(int row, int chunk) const {
+    return reinterpret_cast<uint4*>(lds + row * 128 + 16 * (chunk ^ ((row >> 1) & 7)));
+  }
+  __device__ __forceinline__ uint4& by_row(int i, int lane) const { return *at(8 * i + (lane >> 3), lane & 7); }
+  __device__ __forceinline__ uint4& by_operand(int i, int chunk, int lane) const {
+    return *at(16 * i + (lane & 15), chunk);
+  }
+};
+// Between the accesses of different lanes to the wave's tile: LDS takes them
+// in order, the compiler must not exchange them.
+__device__ __forceinline__ void wave_order() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
+
+// The rows of a 64-row entry for the pieces of a tile (the last row again
+// past the end)
+__device__ __forceinline__ void tile_rows8(const RowLists& l, const int* order, const int4& e, int lane, int (&row)[8]) {
+  const int mine = row_at(l, order, e.y + min(lane, e.z - 1));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) row[i] = __shfl(mine, 8 * i + (lane >> 3));
+}
+
+// Rows of more bytes than this are streamed past the caches
+constexpr size_t STREAM_BYTES = (size_t)128 << 20;
 
 }  // namespace oft

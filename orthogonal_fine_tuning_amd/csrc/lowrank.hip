@@ -26,9 +26,13 @@ namespace oft {
 namespace {
 
 // ------------------------------------------------------------------- down
-// part[split][row][j] = sum over the split's columns of src[row] W[j], the
-// split sums added by whoever reads them.  A job is up to 64 of a segment's
-// output columns, or of all of them where the rows of src are whole.
+// v[row][j] = sum_k src[row][k] W[j][k]: a workgroup per 16 rows and up to 64
+// output columns of one segment (of all, where the rows of src are whole).
+// Its eight waves deal the columns of src among them, 64 at a time, so that a
+// long contraction is as many loads in flight and no second launch has to add
+// partial sums; the waves' sums are added through LDS in their order.  A
+// wave's step goes through its own part of LDS, from loads whose lanes run
+// along the rows to operands whose lanes run across them.
 struct DownArgs {
   RowLists l;
   RowOrder rows;
@@ -36,297 +40,392 @@ struct DownArgs {
   long lds;
   const uint16_t* w;
   long w_a;  // elements of an adapter's matrices
-  float* part;
-  int R;       // columns of part
-  int nsplit;
-  int n_seg, r, per;  // r output columns a segment (R when whole), `per` a job
+  float* v;
+  int R;             // columns of v
+  int r, per;        // r output columns a segment (R when whole), `per` a job
   int jobs_per_seg;
   bool whole;
   int K;
   int seg_at[MAX_SEG + 1];
 };
+constexpr int DW = 8;  // waves
 
-template <int TM, int NG, bool F32>
-__global__ __launch_bounds__(256) void down_kernel(DownArgs a) {
-  constexpr int P = Oct<F32>::P, XG = TM / 16;
-  __shared__ __attribute__((aligned(16))) float red[2][XG * NG * 4][64];
-  const int split = blockIdx.y, job = blockIdx.z;
+// LIST: LIST_16, or LIST_64 in four parts
+template <int LIST, int NG, bool F32>
+__global__ __launch_bounds__(64 * DW) void down_kernel(DownArgs a) {
+  constexpr int P = Oct<F32>::P, SUB = LIST == LIST_16 ? 1 : 4;
+  constexpr int XB = F32 ? 256 : 128, XI = 16 * XB / 1024;  // bytes of a row of x and step, loads of a lane
+  constexpr int WAVE = 16 * XB + 16 * NG * 128;             // bytes of a wave's step
+  __shared__ __attribute__((aligned(16))) char lds[DW * WAVE];
   int4 e;
-  if (!list_entry(a.l, a.rows.tiles, TM == 16 ? LIST_16 : LIST_64, blockIdx.x, e) || e.x < 0) return;
-  const int seg = job / a.jobs_per_seg, sub = job % a.jobs_per_seg;
-  const int col0 = a.whole ? 0 : a.seg_at[seg];
-  const int len = a.whole ? a.K : a.seg_at[seg + 1] - col0;
-  const int jw = sub * a.per, nj = min(a.per, a.r - jw);  // rows of this segment's matrix
-  const uint16_t* w = a.w + (size_t)e.x * a.w_a + (a.whole ? 0 : (size_t)a.r * col0) + (size_t)jw * len;
-
+  if (!list_entry(a.l, a.rows.tiles, LIST, blockIdx.x / SUB, e)) return;
+  e.y += 16 * (blockIdx.x % SUB);
+  e.z -= 16 * (blockIdx.x % SUB);
+  if (e.z <= 0) return;
+  e.z = min(e.z, 16);
+  const int job = blockIdx.y;
+  int seg = 0, col0 = 0, len = a.K;
+  if (!a.whole) {
+    seg = job / a.jobs_per_seg;
+    col0 = a.seg_at[seg];
+    len = a.seg_at[seg + 1] - col0;
+  }
+  const int jw = (job % a.jobs_per_seg) * a.per, nj = min(a.per, a.r - jw);  // rows of the segment's matrix
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int l16 = lane & 15, g = lane >> 4;
-  // the split's columns in steps of 64, dealt to the four waves in turn
-  const int steps = (len + 63) / 64, per = (steps + a.nsplit - 1) / a.nsplit;
-  const int s0 = split * per, s1 = min(steps, s0 + per);
 
-  size_t xrow[XG];
-  int row[XG];
+  if (e.x >= 0) {
+    const uint16_t* w = a.w + (size_t)e.x * a.w_a + (size_t)a.r * col0 + (size_t)jw * len;
+    constexpr int XL = XB / 16;  // lanes along a row of x
+    size_t xat[XI];
 #pragma unroll
-  for (int i = 0; i < XG; ++i) {
-    row[i] = row_at(a.l, a.rows.order, e.y + min(16 * i + l16, e.z - 1));
-    xrow[i] = (size_t)row[i] * a.lds + col0;
-  }
-  size_t wrow[NG];
+    for (int i = 0; i < XI; ++i)
+      xat[i] = (size_t)row_at(a.l, a.rows.order, e.y + min(i * (64 / XL) + lane / XL, e.z - 1)) * a.lds + col0 +
+               (F32 ? 4 : 8) * (lane % XL);
+    size_t wat[2 * NG];
 #pragma unroll
-  for (int j = 0; j < NG; ++j) wrow[j] = (size_t)min(16 * j + l16, nj - 1) * len;
+    for (int i = 0; i < 2 * NG; ++i) wat[i] = (size_t)min(8 * i + (lane >> 3), nj - 1) * len + 8 * (lane & 7);
+    const int xk = (F32 ? 4 : 8) * (lane % XL), wk = 8 * (lane & 7);
+    char* xs = lds + wave * WAVE;
+    char* ws = xs + 16 * XB;
+    // chunks of a row exchanged as in WaveTile, over the 256 bytes of two rows
+    // of bf16 or one of fp32
+    auto xput = [&](int i) {
+      const int r = i * (64 / XL) + lane / XL, c = lane % XL;
+      return reinterpret_cast<uint4*>(xs + r * XB + 16 * (F32 ? c ^ r : c ^ ((r >> 1) & 7)));
+    };
+    auto wput = [&](int r, int c) { return reinterpret_cast<uint4*>(ws + r * 128 + 16 * (c ^ ((r >> 1) & 7))); };
 
-  f32x4 acc[XG][NG];
+    f32x4 acc[NG];
 #pragma unroll
-  for (int i = 0; i < XG; ++i)
+    for (int j = 0; j < NG; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    uint4 x[XI], wv[2 * NG];
+    // (segments are multiples of 16: a lane's columns are inside or not)
+    auto load = [&](int s) {
+      const int k = 64 * s;
 #pragma unroll
-    for (int j = 0; j < NG; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-  Oct<F32> x[XG][2];
-  uint4 wv[NG][2];
-  // a lane's 16 columns of a step are contiguous: 32 bytes of bf16
-  auto load = [&](int s) {
+      for (int i = 0; i < XI; ++i)
+        x[i] = k + xk < len ? *reinterpret_cast<const uint4*>(static_cast<const char*>(a.src) + (xat[i] + k) * (F32 ? 4 : 2))
+                            : zero4();
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const int k = 64 * s + 16 * g + 8 * t;
-      const bool ok = k < len;  // (segments are multiples of 16)
+      for (int i = 0; i < 2 * NG; ++i) wv[i] = k + wk < len ? *reinterpret_cast<const uint4*>(w + wat[i] + k) : zero4();
+    };
+    const int steps = (len + 63) / 64;
+    int s = wave;
+    if (s < steps) load(s);
+    for (; s < steps; s += DW) {
+      wave_order();  // the last step's reads are before these writes
 #pragma unroll
-      for (int i = 0; i < XG; ++i) {
-        if (ok) x[i][t].load(a.src, xrow[i] + k);
-        else x[i][t].zero();
-      }
+      for (int i = 0; i < XI; ++i) *xput(i) = x[i];
 #pragma unroll
-      for (int j = 0; j < NG; ++j) wv[j][t] = ok ? *reinterpret_cast<const uint4*>(w + wrow[j] + k) : zero4();
-    }
-  };
-  int s = s0 + wave;
-  if (s < s1) load(s);
-  for (; s < s1; s += 4) {
-    Oct<F32> xc[XG][2];
-    uint4 wc[NG][2];
+      for (int i = 0; i < 2 * NG; ++i) *wput(8 * i + (lane >> 3), lane & 7) = wv[i];
+      if (s + DW < steps) load(s + DW);
+      wave_order();
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-#pragma unroll
-      for (int i = 0; i < XG; ++i) xc[i][t] = x[i][t];
-#pragma unroll
-      for (int j = 0; j < NG; ++j) wc[j][t] = wv[j][t];
-    }
-    if (s + 4 < s1) load(s + 4);
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int i = 0; i < XG; ++i) {
+      for (int t = 0; t < 2; ++t) {
         uint4 xp[P];
-        xc[i][t].parts(xp);
+        Oct<F32> o;
+        if constexpr (F32) {
+          o.a = *reinterpret_cast<const float4*>(xs + l16 * XB + 16 * ((8 * t + 2 * g) ^ l16));
+          o.b = *reinterpret_cast<const float4*>(xs + l16 * XB + 16 * ((8 * t + 2 * g + 1) ^ l16));
+        } else {
+          o.u = *reinterpret_cast<const uint4*>(xs + l16 * XB + 16 * ((4 * t + g) ^ ((l16 >> 1) & 7)));
+        }
+        o.parts(xp);
 #pragma unroll
-        for (int j = 0; j < NG; ++j)
+        for (int j = 0; j < NG; ++j) {
+          const bf16x8 wj = as_bf16x8(*wput(16 * j + l16, 4 * t + g));
 #pragma unroll
-          for (int p = P - 1; p >= 0; --p) acc[i][j] = mfma16(as_bf16x8(wc[j][t]), as_bf16x8(xp[p]), acc[i][j]);
-      }
-  }
-  // the four waves' sums, in a fixed order: (0 + 2) + (1 + 3)
-  if (wave >= 2) {
-#pragma unroll
-    for (int i = 0; i < XG; ++i)
-#pragma unroll
-      for (int j = 0; j < NG; ++j)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) red[wave - 2][(i * NG + j) * 4 + c][lane] = acc[i][j][c];
-  }
-  __syncthreads();
-  if (wave < 2) {
-#pragma unroll
-    for (int i = 0; i < XG; ++i)
-#pragma unroll
-      for (int j = 0; j < NG; ++j)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) acc[i][j][c] += red[wave][(i * NG + j) * 4 + c][lane];
-  }
-  __syncthreads();
-  if (wave == 1) {
-#pragma unroll
-    for (int i = 0; i < XG; ++i)
-#pragma unroll
-      for (int j = 0; j < NG; ++j)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) red[0][(i * NG + j) * 4 + c][lane] = acc[i][j][c];
-  }
-  __syncthreads();
-  if (wave != 0) return;
-  // lane: row l16 of each 16, four consecutive output columns
-#pragma unroll
-  for (int i = 0; i < XG; ++i) {
-    if (16 * i + l16 >= e.z) continue;
-    float* out = a.part + ((size_t)split * a.l.T + row[i]) * a.R + (a.whole ? 0 : seg * a.r) + jw;
-#pragma unroll
-    for (int j = 0; j < NG; ++j) {
-      const int c0 = 16 * j + 4 * g;
-      if (c0 < nj) {  // (ranks are multiples of 8)
-        float4 v;
-        v.x = acc[i][j][0] + red[0][(i * NG + j) * 4 + 0][lane];
-        v.y = acc[i][j][1] + red[0][(i * NG + j) * 4 + 1][lane];
-        v.z = acc[i][j][2] + red[0][(i * NG + j) * 4 + 2][lane];
-        v.w = acc[i][j][3] + red[0][(i * NG + j) * 4 + 3][lane];
-        *reinterpret_cast<float4*>(out + c0) = v;
+          for (int p = P - 1; p >= 0; --p) acc[j] = mfma16(wj, as_bf16x8(xp[p]), acc[j]);
+        }
       }
     }
+    __syncthreads();  // the sums take the steps' place
+    float4* red = reinterpret_cast<float4*>(lds);  // [wave][NG][64]
+#pragma unroll
+    for (int j = 0; j < NG; ++j)
+      red[(wave * NG + j) * 64 + lane] = make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
+    __syncthreads();
   }
+  // lane: row l16, four consecutive output columns of 16; rows without an
+  // adapter have v = 0
+  if (wave >= NG) return;
+  const int c0 = 16 * wave + 4 * g;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (e.x >= 0) {
+    const float4* red = reinterpret_cast<const float4*>(lds);
+#pragma unroll
+    for (int k = 0; k < DW; ++k) {
+      const float4 t = red[(k * NG + wave) * 64 + lane];
+      o.x += t.x;
+      o.y += t.y;
+      o.z += t.z;
+      o.w += t.w;
+    }
+  }
+  if (l16 < e.z && c0 < nj)  // (ranks are multiples of 8)
+    *reinterpret_cast<float4*>(a.v + (size_t)row_at(a.l, a.rows.order, e.y + l16) * a.R + seg * a.r + jw + c0) = o;
 }
 
 // --------------------------------------------------------------------- up
-// out[row][c] = base[row][c] + scale sum_k v[row][k] W[c][k]: a wave per 64
-// columns of one segment and TM rows.  The lane's operand row of W is column
-// 16 (l / 4 % 4) + 4 m + l % 4 of the 64 in matrix step m, so that its results
-// of the four steps are 16 consecutive columns of one row.
+// out[row][c] = base[row][c] + scale sum_k v[row][k] W[c][k]: a workgroup per
+// tile of rows and 256 columns of one segment, a wave per 64 of them.  The
+// tile's v is split into operands once, in LDS, 64 columns at a time.  The
+// columns that a matrix step's operand rows stand for are chosen so that a
+// lane's results are the 16 bytes of a row next to its neighbours': bf16
+// column 32 (m / 2) + 8 (i / 4) + 4 (m % 2) + i % 4 of the 64 for operand row i
+// of step m, fp32 16 m + i.
 struct UpArgs {
   RowLists l;
   RowOrder rows;
-  const float* part;  // [nsplit][T][R], summed here
-  int nsplit, R, r;   // r: the contraction, from column seg * r of part
+  const float* v;  // [T][R]
+  int R, r;        // r: the contraction, from column seg * r of v
   const uint16_t* w;  // [n][C][r]
   long w_a;
   const float* scale;
   const void* base;
   void* out;
-  int C;       // columns
-  float* v;    // [T][R], the summed part (NULL: not kept)
-  int n_seg, cblocks;
-  int seg_at[MAX_SEG + 1], block_at[MAX_SEG + 1];  // columns and 64-column blocks before each segment
+  int C;  // columns
+  int n_seg, blocks;
+  int seg_at[MAX_SEG + 1], block_at[MAX_SEG + 1];  // columns and 256-column blocks before each segment
 };
+constexpr int UC = 256, UK = 64, UROW = UK + 8;
 
 template <int TM, bool F32>
 __global__ __launch_bounds__(256) void up_kernel(UpArgs a) {
-  constexpr int P = F32 ? 3 : 2, XG = TM / 16;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  constexpr int P = F32 ? 3 : 2, XG = TM / 16, H = F32 ? 4 : 2;  // H: 16-byte pieces of a lane and row
+  __shared__ __attribute__((aligned(16))) uint16_t vs[P][TM][UROW];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int l16 = lane & 15, g = lane >> 4;
-  const int wgs = (a.cblocks + 3) / 4;
-  const int tile = blockIdx.x / wgs, cb = (blockIdx.x % wgs) * 4 + wave;
+  const int tile = blockIdx.x / a.blocks, cb = blockIdx.x % a.blocks;
   int4 e;
-  if (cb >= a.cblocks || !list_entry(a.l, a.rows.tiles, TM == 16 ? LIST_16 : LIST_64, tile, e)) return;
-  int seg = 0;
+  if (!list_entry(a.l, a.rows.tiles, TM == 16 ? LIST_16 : LIST_64, tile, e)) return;
+  int seg = 0, seg_lo = 0, seg_hi = a.seg_at[1], blk_lo = 0;
 #pragma unroll
-  for (int i = 1; i < MAX_SEG; ++i) seg += i < a.n_seg && cb >= a.block_at[i];
-  int seg_lo = 0, seg_hi = 0, blk_lo = 0;
-#pragma unroll
-  for (int i = 0; i < MAX_SEG; ++i)
-    if (i == seg) {
+  for (int i = 1; i < MAX_SEG; ++i)
+    if (i < a.n_seg && cb >= a.block_at[i]) {
+      seg = i;
       seg_lo = a.seg_at[i];
       seg_hi = a.seg_at[i + 1];
       blk_lo = a.block_at[i];
     }
-  const int n0 = seg_lo + 64 * (cb - blk_lo);
-  const bool col_ok = n0 + 16 * g < seg_hi;  // this lane's 16 columns (segments are multiples of 16)
+  const int n0 = seg_lo + UC * (cb - blk_lo) + 64 * wave;
+  // column of piece h within the 64
+  auto col = [&](int h) { return F32 ? 16 * h + 4 * g : 32 * h + 8 * g; };
 
-  Oct<F32> y[XG][2];
+  uint4 y[XG][H];
   size_t at[XG];
-  int row[XG];
 #pragma unroll
   for (int i = 0; i < XG; ++i) {
-    row[i] = row_at(a.l, a.rows.order, e.y + min(16 * i + l16, e.z - 1));
-    at[i] = (size_t)row[i] * a.C + n0 + 16 * g;
+    at[i] = (size_t)row_at(a.l, a.rows.order, e.y + min(16 * i + l16, e.z - 1)) * a.C + n0;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (col_ok && a.base != nullptr) y[i][h].load(a.base, at[i] + 8 * h);
-      else y[i][h].zero();
+    for (int h = 0; h < H; ++h) {
+      // (segments are multiples of 16: a piece is inside or not)
+      const bool ok = n0 + col(h) < seg_hi && a.base != nullptr;
+      y[i][h] = ok ? *reinterpret_cast<const uint4*>(static_cast<const char*>(a.base) + (at[i] + col(h)) * (F32 ? 4 : 2))
+                   : zero4();
     }
   }
+  auto store = [&](int i, int h, const uint4& u) {
+    if (16 * i + l16 < e.z && n0 + col(h) < seg_hi)
+      *reinterpret_cast<uint4*>(static_cast<char*>(a.out) + (at[i] + col(h)) * (F32 ? 4 : 2)) = u;
+  };
   if (e.x < 0) {  // rows of the base model
-    if (a.base != a.out && col_ok) {
+    if (a.base == a.out) return;
 #pragma unroll
-      for (int i = 0; i < XG; ++i)
-        if (16 * i + l16 < e.z)
+    for (int i = 0; i < XG; ++i)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if constexpr (F32) {
-              float4* o = reinterpret_cast<float4*>(static_cast<float*>(a.out) + at[i] + 8 * h);
-              o[0] = y[i][h].a;
-              o[1] = y[i][h].b;
-            } else {
-              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at[i] + 8 * h) = y[i][h].u;
-            }
-          }
-    }
-    if (a.v != nullptr && n0 == seg_lo) {
-      for (int k = 8 * g; k < a.r; k += 32)
-#pragma unroll
-        for (int i = 0; i < XG; ++i)
-          if (16 * i + l16 < e.z) {
-            float4* o = reinterpret_cast<float4*>(a.v + (size_t)row[i] * a.R + seg * a.r + k);
-            o[0] = o[1] = make_float4(0.f, 0.f, 0.f, 0.f);
-          }
-    }
+      for (int h = 0; h < H; ++h) store(i, h, y[i][h]);
     return;
   }
   const uint16_t* w = a.w + (size_t)e.x * a.w_a;
   size_t wrow[4];
 #pragma unroll
-  for (int m = 0; m < 4; ++m) wrow[m] = (size_t)min(n0 + 16 * (l16 >> 2) + 4 * m + (l16 & 3), seg_hi - 1) * a.r;
-
+  for (int m = 0; m < 4; ++m) {
+    const int c = F32 ? 16 * m + l16 : 32 * (m / 2) + 8 * (l16 >> 2) + 4 * (m % 2) + (l16 & 3);
+    wrow[m] = (size_t)min(n0 + c, seg_hi - 1) * a.r + 8 * g;
+  }
   f32x4 acc[XG][4];
 #pragma unroll
   for (int i = 0; i < XG; ++i)
 #pragma unroll
     for (int m = 0; m < 4; ++m) acc[i][m] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const size_t plane = (size_t)a.l.T * a.R;
-  for (int k0 = 0; k0 < a.r; k0 += 32) {
-    const int k = k0 + 8 * g;
-    const bool ok = k < a.r;
-    uint4 wv[4];
+
+  // thread: eight columns of v of row tid / 8 (+ 32)
+  constexpr int VI = (TM + 31) / 32;
+  const int vk = 8 * (tid & 7), vr = tid >> 3;
+  for (int k0 = 0; k0 < a.r; k0 += UK) {
+    Oct<true> v[VI];
 #pragma unroll
-    for (int m = 0; m < 4; ++m) wv[m] = ok ? *reinterpret_cast<const uint4*>(w + wrow[m] + k) : zero4();
+    for (int i = 0; i < VI; ++i) {
+      const int r = vr + 32 * i;
+      if (r < e.z && k0 + vk < a.r)
+        v[i].load(a.v, (size_t)row_at(a.l, a.rows.order, e.y + r) * a.R + seg * a.r + k0 + vk);
+      else
+        v[i].zero();
+    }
+    uint4 wv[4][2];
 #pragma unroll
-    for (int i = 0; i < XG; ++i) {
-      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (ok) {
-        const float* p = a.part + (size_t)row[i] * a.R + seg * a.r + k;
-        for (int s = 0; s < a.nsplit; ++s, p += plane) {
-          const float4 c = reinterpret_cast<const float4*>(p)[0], d = reinterpret_cast<const float4*>(p)[1];
-          v[0] += c.x;
-          v[1] += c.y;
-          v[2] += c.z;
-          v[3] += c.w;
-          v[4] += d.x;
-          v[5] += d.y;
-          v[6] += d.z;
-          v[7] += d.w;
-        }
-        if (a.v != nullptr && n0 == seg_lo && 16 * i + l16 < e.z) {
-          float4* o = reinterpret_cast<float4*>(a.v + (size_t)row[i] * a.R + seg * a.r + k);
-          o[0] = make_float4(v[0], v[1], v[2], v[3]);
-          o[1] = make_float4(v[4], v[5], v[6], v[7]);
-        }
-      }
-      uint4 vp[P];
-      split_bf16x8<P>(v, vp);
+    for (int t = 0; t < 2; ++t)
 #pragma unroll
       for (int m = 0; m < 4; ++m)
+        wv[m][t] = k0 + 32 * t + 8 * g < a.r ? *reinterpret_cast<const uint4*>(w + wrow[m] + k0 + 32 * t) : zero4();
+    if (k0 > 0) __syncthreads();  // the last columns' reads are done
 #pragma unroll
-        for (int p = P - 1; p >= 0; --p) acc[i][m] = mfma16(as_bf16x8(wv[m]), as_bf16x8(vp[p]), acc[i][m]);
+    for (int i = 0; i < VI; ++i)
+      if (vr + 32 * i < TM) {
+        const float f[8] = {v[i].a.x, v[i].a.y, v[i].a.z, v[i].a.w, v[i].b.x, v[i].b.y, v[i].b.z, v[i].b.w};
+        uint4 o[P];
+        split_bf16x8<P>(f, o);
+#pragma unroll
+        for (int p = 0; p < P; ++p) *reinterpret_cast<uint4*>(&vs[p][vr + 32 * i][vk]) = o[p];
+      }
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      if (k0 + 32 * t >= a.r) break;
+#pragma unroll
+      for (int i = 0; i < XG; ++i)
+#pragma unroll
+        for (int p = P - 1; p >= 0; --p) {
+          const uint4 o = *reinterpret_cast<const uint4*>(&vs[p][16 * i + l16][32 * t + 8 * g]);
+#pragma unroll
+          for (int m = 0; m < 4; ++m) acc[i][m] = mfma16(as_bf16x8(wv[m][t]), as_bf16x8(o), acc[i][m]);
+        }
     }
   }
   const float sc = a.scale[e.x];
 #pragma unroll
-  for (int i = 0; i < XG; ++i) {
-    if (!col_ok || 16 * i + l16 >= e.z) continue;
+  for (int i = 0; i < XG; ++i)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float o[8];
+    for (int h = 0; h < H; ++h) {
+      const uint32_t b[4] = {y[i][h].x, y[i][h].y, y[i][h].z, y[i][h].w};
+      uint32_t q[4];
 #pragma unroll
-      for (int c = 0; c < 8; ++c) o[c] = sc * acc[i][2 * h + c / 4][c % 4];
-      if constexpr (F32) {
-        float4* q = reinterpret_cast<float4*>(static_cast<float*>(a.out) + at[i] + 8 * h);
-        q[0] = make_float4(y[i][h].a.x + o[0], y[i][h].a.y + o[1], y[i][h].a.z + o[2], y[i][h].a.w + o[3]);
-        q[1] = make_float4(y[i][h].b.x + o[4], y[i][h].b.y + o[5], y[i][h].b.z + o[6], y[i][h].b.w + o[7]);
-      } else {
-        const uint32_t b[4] = {y[i][h].u.x, y[i][h].u.y, y[i][h].u.z, y[i][h].u.w};
-        uint32_t q[4];
+      for (int c = 0; c < 4; ++c) {
+        if constexpr (F32) {
+          q[c] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, b[c]) + sc * acc[i][h][c]);
+        } else {
+          const f32x4& s = acc[i][2 * h + c / 2];
+          q[c] = pack_bf16x2(bf16_to_f32(b[c] & 0xFFFF) + sc * s[2 * (c % 2)],
+                             bf16_to_f32(b[c] >> 16) + sc * s[2 * (c % 2) + 1]);
+        }
+      }
+      store(i, h, make_uint4(q[0], q[1], q[2], q[3]));
+    }
+}
+
+// bf16 rows in tiles of 64: base and result go through the wave's own LDS
+// tile, so that they are read and written by whole stretches of rows.
+template <bool STREAM>
+__global__ __launch_bounds__(256) void up_tile_kernel(UpArgs a) {
+  constexpr int P = 2;
+  __shared__ __attribute__((aligned(16))) uint16_t vs[P][64][UROW];
+  __shared__ __attribute__((aligned(16))) char lds[4][WaveTile::BYTES];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int l16 = lane & 15, g = lane >> 4;
+  const int tile = blockIdx.x / a.blocks, cb = blockIdx.x % a.blocks;
+  int4 e;
+  if (!list_entry(a.l, a.rows.tiles, LIST_64, tile, e)) return;
+  int seg = 0, seg_lo = 0, seg_hi = a.seg_at[1], blk_lo = 0;
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          q[c] = pack_bf16x2(bf16_to_f32(b[c] & 0xFFFF) + o[2 * c], bf16_to_f32(b[c] >> 16) + o[2 * c + 1]);
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at[i] + 8 * h) = make_uint4(q[0], q[1], q[2], q[3]);
+  for (int i = 1; i < MAX_SEG; ++i)
+    if (i < a.n_seg && cb >= a.block_at[i]) {
+      seg = i;
+      seg_lo = a.seg_at[i];
+      seg_hi = a.seg_at[i + 1];
+      blk_lo = a.block_at[i];
+    }
+  const int n0 = seg_lo + UC * (cb - blk_lo) + 64 * wave;
+  const int c = n0 + 8 * (lane & 7);  // (segments are multiples of 16: a piece is inside or not)
+  int row[8];
+  tile_rows8(a.l, a.rows.order, e, lane, row);
+  Oct<false> y[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (c < seg_hi && a.base != nullptr) y[i].load<STREAM>(a.base, (size_t)row[i] * a.C + c);
+    else y[i].zero();
+  if (e.x >= 0) {
+    const uint16_t* w = a.w + (size_t)e.x * a.w_a;
+    size_t wrow[4];
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+      wrow[m] = (size_t)min(n0 + 32 * (m / 2) + 8 * (l16 >> 2) + 4 * (m % 2) + (l16 & 3), seg_hi - 1) * a.r + 8 * g;
+    f32x4 acc[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int m = 0; m < 4; ++m) acc[i][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+    // thread: eight columns of v of rows tid / 8 and tid / 8 + 32
+    const int vk = 8 * (tid & 7), vr = tid >> 3;
+    int vrow[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) vrow[i] = row_at(a.l, a.rows.order, e.y + min(vr + 32 * i, e.z - 1));
+    for (int k0 = 0; k0 < a.r; k0 += UK) {
+      Oct<true> v[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (k0 + vk < a.r) v[i].load(a.v, (size_t)vrow[i] * a.R + seg * a.r + k0 + vk);
+        else v[i].zero();
+      uint4 wv[4][2];
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+          wv[m][t] = k0 + 32 * t + 8 * g < a.r ? *reinterpret_cast<const uint4*>(w + wrow[m] + k0 + 32 * t) : zero4();
+      if (k0 > 0) __syncthreads();  // the last columns' reads are done
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float f[8] = {v[i].a.x, v[i].a.y, v[i].a.z, v[i].a.w, v[i].b.x, v[i].b.y, v[i].b.z, v[i].b.w};
+        uint4 o[P];
+        split_bf16x8<P>(f, o);
+#pragma unroll
+        for (int p = 0; p < P; ++p) *reinterpret_cast<uint4*>(&vs[p][vr + 32 * i][vk]) = o[p];
+      }
+      __syncthreads();
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if (k0 + 32 * t >= a.r) break;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int p = P - 1; p >= 0; --p) {
+            const uint4 o = *reinterpret_cast<const uint4*>(&vs[p][16 * i + l16][32 * t + 8 * g]);
+#pragma unroll
+            for (int m = 0; m < 4; ++m) acc[i][m] = mfma16(as_bf16x8(wv[m][t]), as_bf16x8(o), acc[i][m]);
+          }
       }
     }
+    const float sc = a.scale[e.x];
+    const WaveTile t{lds[wave]};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t.by_row(i, lane) = y[i].u;
+    wave_order();
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint4& at = t.by_operand(i, 4 * h + g, lane);
+        const uint4 o = at;
+        const uint32_t b[4] = {o.x, o.y, o.z, o.w};
+        uint32_t q[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const f32x4& s = acc[i][2 * h + k / 2];
+          q[k] = pack_bf16x2(bf16_to_f32(b[k] & 0xFFFF) + sc * s[2 * (k % 2)],
+                             bf16_to_f32(b[k] >> 16) + sc * s[2 * (k % 2) + 1]);
+        }
+        at = make_uint4(q[0], q[1], q[2], q[3]);
+      }
+    wave_order();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i].u = t.by_row(i, lane);
+  } else if (a.base == a.out) {
+    return;
   }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (8 * i + (lane >> 3) < e.z && c < seg_hi) y[i].store<STREAM>(a.out, (size_t)row[i] * a.C + c);
 }
 
 // -------------------------------------------------------------- transposes
@@ -388,24 +487,24 @@ __global__ __launch_bounds__(256) void transpose_kernel(TransposeArgs a, int til
 // ------------------------------------------------------------------ pieces
 // Sums over an adapter's rows: out[j][c] = scale sum_rows U[row][j] X[row][c]
 // for 256 columns of X and up to 64 of U, over one piece of the adapter's
-// rows.  Both operands run along the rows here: tiles of 32 rows go to LDS in
+// rows.  Both operands run along the rows here: tiles of PR rows go to LDS in
 // row order and are read with the transposing LDS load.  U is fp32 in three
 // parts; so is X where it is fp32 (products of parts whose scales differ by
-// 2^-24 or more are left out).
-constexpr int PC = 256, PR = 32;  // columns, rows of a step
-constexpr int LDX = PC + 16;      // LDS row: 16 elements more, so that four rows of a transposing read fall in four banks' groups
+// 2^-24 or more are left out).  A step's rows are fetched while the last
+// step's are multiplied, and their numbers one step before that.
+constexpr int PC = 256;
+constexpr int LDX = PC + 16;  // LDS row: 16 elements more, so that the four rows of a transposing read lie in different banks
 
 struct PieceJob {
   const void* x;
   long ldx;
-  const float* u;  // summed over nsplit planes
-  int nsplit;
+  const float* u;
   float* out;      // [n][...], element (j, c) at j so_j + c so_c
   long out_a;
   long part_off;   // this sum's place in a partial slot
   int so_j, so_c;
-  int blocks;      // column blocks of one segment's columns, over all segments
-  int nj, njc;     // columns of U a segment, and chunks of 64 of them
+  int blocks;      // column blocks, over all segments
+  int nj, njc;     // columns of U a segment, and the jobs they are cut into
   int n_seg;
   bool whole;      // one segment of all columns
   int seg_at[MAX_SEG + 1], block_at[MAX_SEG + 1];
@@ -419,7 +518,7 @@ struct PieceArgs {
   long slot;  // floats of a partial slot
 };
 
-template <int NJ, bool F32>
+template <int NJ, int PR, bool F32>
 __device__ __forceinline__ void piece(const PieceArgs& a, const PieceJob& q, int4 e, int job, uint16_t* xs, uint16_t* us) {
   constexpr int PX = Oct<F32>::P, LDU = NJ * 16 + 16;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -444,43 +543,41 @@ __device__ __forceinline__ void piece(const PieceArgs& a, const PieceJob& q, int
 #pragma unroll
     for (int c = 0; c < 4; ++c) acc[j][c] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  // thread: 8 columns of rows tid / 32 + 8 i of a step; U: 4 columns of row
-  // tid / (4 NJ) (+ 64 / NJ ...)
+  // thread: 8 columns of rows tid / 32 + 8 i of a step; U: 4 columns of rows
+  // tid / UT + UR i
+  constexpr int XI = PR / 8;
   const int xc = c0 + 8 * (tid & 31), xr = tid >> 5;
   const bool xok = xc < c_hi;
   constexpr int UT = 4 * NJ, UR = 256 / UT, UI = (PR + UR - 1) / UR;
   const int uc = 4 * (tid % UT), ur = tid / UT;
-  const size_t plane = (size_t)a.l.T * a.R;
-  Oct<F32> x[4];
+  const bool uok = ur < UR && uc < nj;
+  Oct<F32> x[XI];
   float4 u[UI];
+  int xi[XI], ui[UI];
+  auto number = [&](int r0) {
+#pragma unroll
+    for (int i = 0; i < XI; ++i) xi[i] = row_at(a.l, a.rows.order, e.y + min(r0 + xr + 8 * i, e.z - 1));
+#pragma unroll
+    for (int i = 0; i < UI; ++i) ui[i] = row_at(a.l, a.rows.order, e.y + min(r0 + ur + UR * i, e.z - 1));
+  };
   auto load = [&](int r0) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = r0 + xr + 8 * i;
-      if (r < e.z && xok) x[i].load(q.x, (size_t)row_at(a.l, a.rows.order, e.y + r) * q.ldx + xc);
+    for (int i = 0; i < XI; ++i) {
+      if (r0 + xr + 8 * i < e.z && xok) x[i].load(q.x, (size_t)xi[i] * q.ldx + xc);
       else x[i].zero();
     }
 #pragma unroll
-    for (int i = 0; i < UI; ++i) {
-      u[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      const int r = r0 + ur + UR * i;
-      if (ur + UR * i < PR && r < e.z && uc < nj) {
-        const float* p = q.u + (size_t)row_at(a.l, a.rows.order, e.y + r) * a.R + ju + uc;
-        for (int s = 0; s < q.nsplit; ++s, p += plane) {
-          const float4 v = *reinterpret_cast<const float4*>(p);
-          u[i].x += v.x;
-          u[i].y += v.y;
-          u[i].z += v.z;
-          u[i].w += v.w;
-        }
-      }
-    }
+    for (int i = 0; i < UI; ++i)
+      u[i] = r0 + ur + UR * i < e.z && uok ? *reinterpret_cast<const float4*>(q.u + (size_t)ui[i] * a.R + ju + uc)
+                                           : make_float4(0.f, 0.f, 0.f, 0.f);
   };
+  number(0);
   load(0);
+  number(PR);
   for (int r0 = 0; r0 < e.z; r0 += PR) {
     __syncthreads();  // the last step's reads are done
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < XI; ++i) {
       uint4 p[PX];
       x[i].parts(p);
 #pragma unroll
@@ -489,7 +586,7 @@ __device__ __forceinline__ void piece(const PieceArgs& a, const PieceJob& q, int
     }
 #pragma unroll
     for (int i = 0; i < UI; ++i)
-      if (ur + UR * i < PR) {
+      if (ur < UR && ur + UR * i < PR) {
         const float v[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
         uint32_t h[4][3];
 #pragma unroll
@@ -500,31 +597,37 @@ __device__ __forceinline__ void piece(const PieceArgs& a, const PieceJob& q, int
               make_uint2(h[0][p] | (h[1][p] << 16), h[2][p] | (h[3][p] << 16));
       }
     __syncthreads();
-    if (r0 + PR < e.z) load(r0 + PR);
-    // lane l16 of group g: rows 8 g .. 8 g + 7 of column l16 of 16
-    const int tr = 8 * g + (l16 >> 2), tc = 4 * (l16 & 3);
-    bf16x8 xv[4][PX];
+    if (r0 + PR < e.z) {
+      load(r0 + PR);
+      number(r0 + 2 * PR);
+    }
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
+    for (int k0 = 0; k0 < PR; k0 += 32) {
+      // lane l16 of group g: rows 8 g .. 8 g + 7 of column l16 of 16
+      const int tr = k0 + 8 * g + (l16 >> 2), tc = 4 * (l16 & 3);
+      bf16x8 xv[4][PX];
 #pragma unroll
-      for (int k = 0; k < PX; ++k) {
-        const uint16_t* p = xs + (k * PR + tr) * LDX + 64 * wave + 16 * c + tc;
-        const uint2 lo = nn::ds_read_tr16(p), hi = nn::ds_read_tr16(p + 4 * LDX);
-        xv[c][k] = as_bf16x8(make_uint4(lo.x, lo.y, hi.x, hi.y));
-      }
+      for (int c = 0; c < 4; ++c)
 #pragma unroll
-    for (int j = 0; j < NJ; ++j)
+        for (int k = 0; k < PX; ++k) {
+          const uint16_t* p = xs + (k * PR + tr) * LDX + 64 * wave + 16 * c + tc;
+          const uint2 lo = nn::ds_read_tr16(p), hi = nn::ds_read_tr16(p + 4 * LDX);
+          xv[c][k] = as_bf16x8(make_uint4(lo.x, lo.y, hi.x, hi.y));
+        }
 #pragma unroll
-      for (int p = 2; p >= 0; --p) {
-        const uint16_t* s = us + (p * PR + tr) * LDU + 16 * j + tc;
-        const uint2 lo = nn::ds_read_tr16(s), hi = nn::ds_read_tr16(s + 4 * LDU);
-        const bf16x8 uv = as_bf16x8(make_uint4(lo.x, lo.y, hi.x, hi.y));
+      for (int j = 0; j < NJ; ++j)
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int p = 2; p >= 0; --p) {
+          const uint16_t* s = us + (p * PR + tr) * LDU + 16 * j + tc;
+          const uint2 lo = nn::ds_read_tr16(s), hi = nn::ds_read_tr16(s + 4 * LDU);
+          const bf16x8 uv = as_bf16x8(make_uint4(lo.x, lo.y, hi.x, hi.y));
 #pragma unroll
-          for (int k = PX - 1; k >= 0; --k)
-            if (p + k <= 2) acc[j][c] = mfma16(uv, xv[c][k], acc[j][c]);
-      }
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int k = PX - 1; k >= 0; --k)
+              if (p + k <= 2) acc[j][c] = mfma16(uv, xv[c][k], acc[j][c]);
+        }
+    }
   }
   // lane: column l16 of 16, rows (of U^T) 4 g .. 4 g + 3 of 16
   const float sc = a.scale[e.x];
@@ -548,17 +651,18 @@ __device__ __forceinline__ void piece(const PieceArgs& a, const PieceJob& q, int
   }
 }
 
+// Rows of a step: 64, or 32 of fp32 (their three parts fill the LDS)
 template <int NA, int NB, bool F32>
 __global__ __launch_bounds__(256) void piece_kernel(PieceArgs a, PieceJob qa, PieceJob qb) {
-  constexpr int NJ = NA > NB ? NA : NB;
+  constexpr int NJ = NA > NB ? NA : NB, PR = F32 ? 32 : 64;
   __shared__ __attribute__((aligned(16))) uint16_t xs[Oct<F32>::P * PR * LDX];
   __shared__ __attribute__((aligned(16))) uint16_t us[3 * PR * (NJ * 16 + 16)];
   int4 e;
   if (!list_entry(a.l, a.rows.tiles, a.list, blockIdx.y, e) || e.x < 0) return;
   e.w = min(e.w, RowLists::slots(a.list) - 1);
   const int ja = qa.blocks * qa.njc;
-  if ((int)blockIdx.x < ja) piece<NA, F32>(a, qa, e, blockIdx.x, xs, us);
-  else piece<NB, false>(a, qb, e, blockIdx.x - ja, xs, us);
+  if ((int)blockIdx.x < ja) piece<NA, PR, F32>(a, qa, e, blockIdx.x, xs, us);
+  else piece<NB, PR, false>(a, qb, e, blockIdx.x - ja, xs, us);
 }
 
 // The pieces of an adapter of two or more, in order; zeros for an adapter
@@ -604,33 +708,11 @@ size_t up256(size_t b) { return (b + 255) & ~(size_t)255; }
 // has few), else 64.
 int tile_rows(int T) { return T <= 1024 ? 16 : 64; }
 
-struct DownPlan {
-  int per, jobs_per_seg, jobs, nsplit, ng;
-};
-// len: the longest contraction; r columns for each of n_seg segments
-DownPlan plan_down(const RowLists& l, int tm, int len, int r, int n_seg) {
-  DownPlan p;
-  const int groups = (r + 15) / 16;
-  p.jobs_per_seg = (groups + 3) / 4;
-  p.ng = (groups + p.jobs_per_seg - 1) / p.jobs_per_seg;
-  p.per = 16 * p.ng;
-  p.jobs = n_seg * p.jobs_per_seg;
-  // enough workgroups for two a CU where the tiles alone do not give them,
-  // each with a step of 64 columns for every wave
-  const long tiles = (l.T + tm - 1) / tm;
-  long want = (512 + tiles * p.jobs - 1) / (tiles * p.jobs);
-  const long most = len / 256 > 1 ? len / 256 : 1;
-  want = want < 1 ? 1 : want > most ? most : want;
-  p.nsplit = (int)want;
-  return p;
-}
-
 struct Plan {
   RowLists l;
   int tm, R;
-  DownPlan down;
   int list;
-  size_t part, at, bt, sums, bytes;
+  size_t v, at, bt, sums, bytes;
   long slot;
 };
 Plan plan_of(const LowrankDims& d, bool bwd) {
@@ -638,11 +720,8 @@ Plan plan_of(const LowrankDims& d, bool bwd) {
   p.l = RowLists{d.T, d.n};
   p.tm = tile_rows(d.T);
   p.R = d.n_seg * d.r;
-  int longest = 0;
-  for (int i = 0; i < d.n_seg; ++i) longest = d.seg[i] > longest ? d.seg[i] : longest;
-  p.down = bwd ? plan_down(p.l, p.tm, longest, d.r, d.n_seg) : plan_down(p.l, p.tm, d.K, p.R, 1);
-  p.part = 0;
-  p.bytes = up256(4 * (size_t)p.down.nsplit * d.T * p.R);
+  p.v = 0;
+  p.bytes = up256(4 * (size_t)d.T * p.R);
   p.at = p.bt = p.sums = 0;
   p.slot = (long)p.R * d.K + (long)d.N * d.r;
   p.list = LIST_SHORT;
@@ -669,16 +748,21 @@ void groups_of(int ng, F f) {
   }
 }
 
-void run_down(const Plan& p, const DownArgs& a, bool f32, hipStream_t st) {
-  const dim3 grid(p.l.cap(p.tm == 16 ? LIST_16 : LIST_64), p.down.nsplit, p.down.jobs);
-  groups_of(p.down.ng, [&](auto ng) {
-    constexpr int NG = decltype(ng)::value;
+// r output columns for each of n_seg segments (one when whole)
+void run_down(const Plan& p, DownArgs a, int n_seg, bool f32, hipStream_t st) {
+  const int groups = (a.r + 15) / 16;
+  a.jobs_per_seg = (groups + 3) / 4;
+  const int ng = (groups + a.jobs_per_seg - 1) / a.jobs_per_seg;
+  a.per = 16 * ng;
+  const dim3 grid(p.tm == 16 ? p.l.cap(LIST_16) : 4 * p.l.cap(LIST_64), n_seg * a.jobs_per_seg);
+  groups_of(ng, [&](auto c) {
+    constexpr int NG = decltype(c)::value;
     if (p.tm == 16) {
-      if (f32) hipLaunchKernelGGL((down_kernel<16, NG, true>), grid, dim3(256), 0, st, a);
-      else hipLaunchKernelGGL((down_kernel<16, NG, false>), grid, dim3(256), 0, st, a);
+      if (f32) hipLaunchKernelGGL((down_kernel<LIST_16, NG, true>), grid, dim3(64 * DW), 0, st, a);
+      else hipLaunchKernelGGL((down_kernel<LIST_16, NG, false>), grid, dim3(64 * DW), 0, st, a);
     } else {
-      if (f32) hipLaunchKernelGGL((down_kernel<64, NG, true>), grid, dim3(256), 0, st, a);
-      else hipLaunchKernelGGL((down_kernel<64, NG, false>), grid, dim3(256), 0, st, a);
+      if (f32) hipLaunchKernelGGL((down_kernel<LIST_64, NG, true>), grid, dim3(64 * DW), 0, st, a);
+      else hipLaunchKernelGGL((down_kernel<LIST_64, NG, false>), grid, dim3(64 * DW), 0, st, a);
     }
   });
 }
@@ -686,15 +770,17 @@ void run_down(const Plan& p, const DownArgs& a, bool f32, hipStream_t st) {
 void run_up(const Plan& p, UpArgs a, bool f32, hipStream_t st) {
   a.block_at[0] = 0;
   for (int i = 0; i < MAX_SEG; ++i)
-    a.block_at[i + 1] = i < a.n_seg ? a.block_at[i] + (a.seg_at[i + 1] - a.seg_at[i] + 63) / 64 : a.block_at[i];
-  a.cblocks = a.block_at[a.n_seg];
-  const dim3 grid((unsigned)p.l.cap(p.tm == 16 ? LIST_16 : LIST_64) * ((a.cblocks + 3) / 4));
+    a.block_at[i + 1] = i < a.n_seg ? a.block_at[i] + (a.seg_at[i + 1] - a.seg_at[i] + UC - 1) / UC : a.block_at[i];
+  a.blocks = a.block_at[a.n_seg];
+  const dim3 grid((unsigned)p.l.cap(p.tm == 16 ? LIST_16 : LIST_64) * a.blocks);
   if (p.tm == 16) {
     if (f32) hipLaunchKernelGGL((up_kernel<16, true>), grid, dim3(256), 0, st, a);
     else hipLaunchKernelGGL((up_kernel<16, false>), grid, dim3(256), 0, st, a);
   } else {
+    const bool stream = (size_t)p.l.T * a.C * 2 > STREAM_BYTES;
     if (f32) hipLaunchKernelGGL((up_kernel<64, true>), grid, dim3(256), 0, st, a);
-    else hipLaunchKernelGGL((up_kernel<64, false>), grid, dim3(256), 0, st, a);
+    else if (stream) hipLaunchKernelGGL(up_tile_kernel<true>, grid, dim3(256), 0, st, a);
+    else hipLaunchKernelGGL(up_tile_kernel<false>, grid, dim3(256), 0, st, a);
   }
 }
 
@@ -729,7 +815,7 @@ size_t lowrank_ws_bytes(const LowrankDims& d, bool bwd) { return plan_of(d, bwd)
 hipError_t launch_lowrank_fwd(const LowrankDims& d, const LowrankPtrs& q, char* ws, hipStream_t st) {
   ProfScope prof(st, "lowrank.fwd");
   const Plan p = plan_of(d, false);
-  float* part = reinterpret_cast<float*>(ws + p.part);
+  float* v = q.v != nullptr ? q.v : reinterpret_cast<float*>(ws + p.v);
   DownArgs a{};
   a.l = p.l;
   a.rows = q.rows;
@@ -737,21 +823,16 @@ hipError_t launch_lowrank_fwd(const LowrankDims& d, const LowrankPtrs& q, char* 
   a.lds = d.K;
   a.w = q.A;
   a.w_a = (long)p.R * d.K;
-  a.part = part;
+  a.v = v;
   a.R = p.R;
-  a.nsplit = p.down.nsplit;
-  a.n_seg = 1;
   a.r = p.R;
-  a.per = p.down.per;
-  a.jobs_per_seg = p.down.jobs_per_seg;
   a.whole = true;
   a.K = d.K;
-  run_down(p, a, d.f32, st);
+  run_down(p, a, 1, d.f32, st);
   UpArgs b{};
   b.l = p.l;
   b.rows = q.rows;
-  b.part = part;
-  b.nsplit = p.down.nsplit;
+  b.v = v;
   b.R = p.R;
   b.r = d.r;
   b.w = q.B;
@@ -760,7 +841,6 @@ hipError_t launch_lowrank_fwd(const LowrankDims& d, const LowrankPtrs& q, char* 
   b.base = q.y_base;
   b.out = q.y;
   b.C = d.N;
-  b.v = q.v;
   b.n_seg = d.n_seg;
   segments(d, b.seg_at);
   run_up(p, b, d.f32, st);
@@ -770,7 +850,7 @@ hipError_t launch_lowrank_fwd(const LowrankDims& d, const LowrankPtrs& q, char* 
 hipError_t launch_lowrank_bwd(const LowrankDims& d, const LowrankGradPtrs& q, char* ws, hipStream_t st) {
   ProfScope prof(st, "lowrank.bwd");
   const Plan p = plan_of(d, true);
-  float* part = reinterpret_cast<float*>(ws + p.part);
+  float* u = reinterpret_cast<float*>(ws + p.v);
   uint16_t* at = reinterpret_cast<uint16_t*>(ws + p.at);
   uint16_t* bt = reinterpret_cast<uint16_t*>(ws + p.bt);
   float* sums = reinterpret_cast<float*>(ws + p.sums);
@@ -800,23 +880,18 @@ hipError_t launch_lowrank_bwd(const LowrankDims& d, const LowrankGradPtrs& q, ch
     a.lds = d.N;
     a.w = bt;
     a.w_a = (long)d.N * d.r;
-    a.part = part;
+    a.v = u;
     a.R = p.R;
-    a.nsplit = p.down.nsplit;
-    a.n_seg = d.n_seg;
     a.r = d.r;
-    a.per = p.down.per;
-    a.jobs_per_seg = p.down.jobs_per_seg;
     a.whole = false;
     segments(d, a.seg_at);
-    run_down(p, a, false, st);
+    run_down(p, a, d.n_seg, false, st);
   }
   if (d.T > 0 && q.dx != nullptr) {
     UpArgs b{};
     b.l = p.l;
     b.rows = q.rows;
-    b.part = part;
-    b.nsplit = p.down.nsplit;
+    b.v = u;
     b.R = b.r = p.R;
     b.w = at;
     b.w_a = (long)p.R * d.K;
@@ -841,8 +916,7 @@ hipError_t launch_lowrank_bwd(const LowrankDims& d, const LowrankGradPtrs& q, ch
   PieceJob ja{}, jb{};
   ja.x = q.x;
   ja.ldx = d.K;
-  ja.u = part;
-  ja.nsplit = p.down.nsplit;
+  ja.u = u;
   ja.out = q.dA;
   ja.out_a = (long)p.R * d.K;
   ja.part_off = 0;
@@ -856,7 +930,6 @@ hipError_t launch_lowrank_bwd(const LowrankDims& d, const LowrankGradPtrs& q, ch
   jb.x = q.dy;
   jb.ldx = d.N;
   jb.u = q.v;
-  jb.nsplit = 1;
   jb.out = q.dB;
   jb.out_a = (long)d.N * d.r;
   jb.part_off = (long)p.R * d.K;

@@ -21,104 +21,135 @@
 namespace oft {
 namespace {
 
-// Rotation operand of channels n0 .. n0 + 31 (pack `which`: 0 R, 1 R^T):
-// operand row l32 is channel 16 (l32 / 4 % 2) + 4 (l32 / 8) + l32 % 4, whose
-// results are then registers 0 .. 15 of lane group l32 / 4 % 2; contraction
-// item p of step t in lane group g is channel 16 g + 8 t + p.
+// Rotation operands of channels n0 .. n0 + 31 (pack `which`: 0 R, 1 R^T), for
+// 16 rows at a time: operand row i of matrix step m is channel
+// 8 (i / 4) + 4 m + i % 4, contraction item p of lane group g channel 8 g + p, so
+// that a lane's results of the two steps are the eight channels that it
+// brought itself.
 template <int B>
-__device__ __forceinline__ void load_rotation(const uint16_t* __restrict__ rops, int n0, int which, int l32, int g,
+__device__ __forceinline__ void load_rotation(const uint16_t* __restrict__ rops, int n0, int which, int l16, int g,
                                               uint4 (&o)[2]) {
-  const int gr = (l32 >> 2) & 1, c = 4 * (l32 >> 3) + (l32 & 3);  // channel 16 gr + c
 #pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    if constexpr (B == 32) {
-      o[t] = *reinterpret_cast<const uint4*>(rops + (size_t)(n0 / 32) * 2048 + which * 1024 + (16 * gr + c) * 32 +
-                                             16 * g + 8 * t);
-    } else {
-      o[t] = gr == g ? *reinterpret_cast<const uint4*>(rops + (size_t)(n0 / 16 + g) * 512 + which * 256 + c * 16 + 8 * t)
-                     : zero4();
-    }
+  for (int m = 0; m < 2; ++m) {
+    const int c = 8 * (l16 >> 2) + 4 * m + (l16 & 3);
+    if constexpr (B == 32)
+      o[m] = *reinterpret_cast<const uint4*>(rops + (size_t)(n0 / 32) * 2048 + which * 1024 + c * 32 + 8 * g);
+    else
+      o[m] = (c >> 4) == (g >> 1) ? *reinterpret_cast<const uint4*>(rops + (size_t)(n0 / 16 + (g >> 1)) * 512 +
+                                                                    which * 256 + (c & 15) * 16 + 8 * (g & 1))
+                                  : zero4();
   }
 }
 
 template <bool F32>
-__device__ __forceinline__ f32x16 rotate(const uint4 (&rot)[2], const Oct<F32> (&z)[2]) {
+__device__ __forceinline__ void rotate(const uint4 (&rot)[2], const Oct<F32>& z, f32x4 (&o)[2]) {
   constexpr int P = Oct<F32>::P;
-  f32x16 o;
+  uint4 p[P];
+  z.parts(p);
 #pragma unroll
-  for (int r = 0; r < 16; ++r) o[r] = 0.0f;
+  for (int m = 0; m < 2; ++m) {
+    o[m] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    uint4 p[P];
-    z[t].parts(p);
-#pragma unroll
-    for (int k = P - 1; k >= 0; --k) o = mfma32(as_bf16x8(rot[t]), as_bf16x8(p[k]), o);
-  }
-  return o;
-}
-
-template <bool F32>
-__device__ __forceinline__ void store16(void* out, size_t at, const f32x16& o) {
-  if constexpr (F32) {
-    float4* q = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) q[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-  } else {
-    uint4* q = reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at);
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      q[i] = make_uint4(pack_bf16x2(o[8 * i], o[8 * i + 1]), pack_bf16x2(o[8 * i + 2], o[8 * i + 3]),
-                        pack_bf16x2(o[8 * i + 4], o[8 * i + 5]), pack_bf16x2(o[8 * i + 6], o[8 * i + 7]));
+    for (int k = P - 1; k >= 0; --k) o[m] = mfma16(as_bf16x8(rot[m]), as_bf16x8(p[k]), o[m]);
   }
 }
 
-template <bool F32>
-__device__ __forceinline__ void copy16(void* out, size_t at, const Oct<F32> (&z)[2]) {
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    if constexpr (F32) {
-      float4* q = reinterpret_cast<float4*>(static_cast<float*>(out) + at + 8 * t);
-      q[0] = z[t].a;
-      q[1] = z[t].b;
-    } else {
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at + 8 * t) = z[t].u;
-    }
-  }
+__device__ __forceinline__ uint4 pack8(const f32x4 (&o)[2]) {
+  return make_uint4(pack_bf16x2(o[0][0], o[0][1]), pack_bf16x2(o[0][2], o[0][3]), pack_bf16x2(o[1][0], o[1][1]),
+                    pack_bf16x2(o[1][2], o[1][3]));
 }
 
 // ------------------------------------------------------------------ rows
+// A wave per TM rows and 32 channels: decoded rows, and rows of fp32.
 template <int TM, int B, bool F32>
 __global__ __launch_bounds__(256) void rotate_kernel(RowLists l, RowOrder rows, const void* z,
                                                      const uint16_t* __restrict__ rops, int N, int which, void* y) {
-  constexpr int XG = (TM + 31) / 32;
+  constexpr int XG = TM / 16;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int l32 = lane & 31, g = lane >> 5;
+  const int l16 = lane & 15, g = lane >> 4;
   const int wgs = (N + 127) / 128;
-  const int tile = blockIdx.x / wgs, n0 = (blockIdx.x % wgs) * 128 + 32 * wave;
+  const int n0 = (blockIdx.x % wgs) * 128 + 32 * wave;
   int4 e;
-  if (n0 >= N || !list_entry(l, rows.tiles, TM == 16 ? LIST_16 : LIST_64, tile, e)) return;
-  Oct<F32> x[XG][2];
+  if (n0 >= N || !list_entry(l, rows.tiles, TM == 16 ? LIST_16 : LIST_64, blockIdx.x / wgs, e)) return;
+  Oct<F32> x[XG];
   size_t at[XG];
 #pragma unroll
   for (int i = 0; i < XG; ++i) {
-    at[i] = (size_t)row_at(l, rows.order, e.y + min(32 * i + l32, e.z - 1)) * N + n0 + 16 * g;
-#pragma unroll
-    for (int t = 0; t < 2; ++t) x[i][t].load(z, at[i] + 8 * t);
+    at[i] = (size_t)row_at(l, rows.order, e.y + min(16 * i + l16, e.z - 1)) * N + n0 + 8 * g;
+    x[i].load(z, at[i]);
   }
-  if (e.x < 0) {
-    if (y == z) return;
+  if (e.x >= 0) {
+    uint4 rot[2];
+    load_rotation<B>(rops + (size_t)e.x * N * B * 2, n0, which, l16, g, rot);
 #pragma unroll
-    for (int i = 0; i < XG; ++i)
-      if (32 * i + l32 < e.z) copy16<F32>(y, at[i], x[i]);
+    for (int i = 0; i < XG; ++i) {
+      f32x4 o[2];
+      rotate<F32>(rot, x[i], o);
+      if constexpr (F32) {
+        x[i].a = make_float4(o[0][0], o[0][1], o[0][2], o[0][3]);
+        x[i].b = make_float4(o[1][0], o[1][1], o[1][2], o[1][3]);
+      } else {
+        x[i].u = pack8(o);
+      }
+    }
+  } else if (y == z) {
     return;
   }
-  uint4 rot[2];
-  load_rotation<B>(rops + (size_t)e.x * N * B * 2, n0, which, l32, g, rot);
 #pragma unroll
-  for (int i = 0; i < XG; ++i) {
-    const f32x16 o = rotate<F32>(rot, x[i]);
-    if (32 * i + l32 < e.z) store16<F32>(y, at[i], o);
+  for (int i = 0; i < XG; ++i)
+    if (16 * i + l16 < e.z) x[i].store(y, at[i]);
+}
+
+// bf16 rows in tiles of 64: a wave per tile and 64 channels, through its own
+// LDS tile.
+template <int B, bool STREAM>
+__global__ __launch_bounds__(256) void rotate_tile_kernel(RowLists l, RowOrder rows, const uint16_t* z,
+                                                          const uint16_t* __restrict__ rops, int N, int which,
+                                                          uint16_t* y) {
+  __shared__ __attribute__((aligned(16))) char lds[4][WaveTile::BYTES];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int l16 = lane & 15, g = lane >> 4;
+  const int wgs = (N + 255) / 256;
+  const int n0 = (blockIdx.x % wgs) * 256 + 64 * wave;
+  int4 e;
+  if (n0 >= N || !list_entry(l, rows.tiles, LIST_64, blockIdx.x / wgs, e)) return;
+  const int c = n0 + 8 * (lane & 7);  // (N is a multiple of 32: a piece is inside or not)
+  int row[8];
+  tile_rows8(l, rows.order, e, lane, row);
+  Oct<false> x[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (c < N) x[i].load<STREAM>(z, (size_t)row[i] * N + c);
+    else x[i].zero();
+  if (e.x >= 0) {
+    uint4 rot[2][2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      if (n0 + 32 * k < N) load_rotation<B>(rops + (size_t)e.x * N * B * 2, n0 + 32 * k, which, l16, g, rot[k]);
+      else rot[k][0] = rot[k][1] = zero4();
+    const WaveTile t{lds[wave]};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t.by_row(i, lane) = x[i].u;
+    wave_order();
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        Oct<false> v;
+        v.u = t.by_operand(i, 4 * k + g, lane);
+        f32x4 o[2];
+        rotate<false>(rot[k], v, o);
+        t.by_operand(i, 4 * k + g, lane) = pack8(o);  // (the lane's own 16 bytes)
+      }
+    wave_order();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i].u = t.by_row(i, lane);
+  } else if (y == z) {
+    return;
   }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (8 * i + (lane >> 3) < e.z && c < N) x[i].store<STREAM>(y, (size_t)row[i] * N + c);
 }
 
 // ------------------------------------------------------- sums over the rows
@@ -127,7 +158,7 @@ __global__ __launch_bounds__(256) void rotate_kernel(RowLists l, RowOrder rows, 
 // S's operands, which run along the rows, are read with the transposing load.
 constexpr int SC = 128, SR = 32, LDS_ROW = SC + 16;
 
-template <int B, bool F32>
+template <int B, bool F32, bool STREAM>
 __global__ __launch_bounds__(256) void rotate_sums_kernel(RowLists l, RowOrder rows, int list,
                                                           const uint16_t* __restrict__ dy, const void* __restrict__ y,
                                                           const float* __restrict__ Rf,
@@ -136,10 +167,12 @@ __global__ __launch_bounds__(256) void rotate_sums_kernel(RowLists l, RowOrder r
   constexpr int P = Oct<F32>::P, G = 1024 / (B * B), NP = B * (B - 1) / 2;
   constexpr int TILE = SR * LDS_ROW;
   constexpr int GRAD = 3 * G * B * (B + 4);                          // floats of the Cayley gradient
-  constexpr int FLOATS = (1 + P) * TILE / 2 > 4 * 32 * 36 + GRAD ? (1 + P) * TILE / 2 : 4 * 32 * 36 + GRAD;
+  constexpr int STEP = (2 + P) * TILE / 2;  // dy, y and dz of a step
+  constexpr int FLOATS = STEP > 4 * 32 * 36 + GRAD ? STEP : 4 * 32 * 36 + GRAD;
   __shared__ __attribute__((aligned(16))) float lds[FLOATS];
   uint16_t* ds = reinterpret_cast<uint16_t*>(lds);
-  uint16_t* ys = ds + TILE;
+  uint16_t* zs = ds + TILE;
+  uint16_t* ys = zs + TILE;
 
   int4 e;
   if (!list_entry(l, rows.tiles, list, blockIdx.y, e)) return;
@@ -160,32 +193,50 @@ __global__ __launch_bounds__(256) void rotate_sums_kernel(RowLists l, RowOrder r
     return;
   }
   uint4 rot[2] = {zero4(), zero4()};
-  if (dz != nullptr && w_ok) load_rotation<B>(rops + (size_t)e.x * N * B * 2, nw, 1, l32, g, rot);
+  if (dz != nullptr && w_ok) load_rotation<B>(rops + (size_t)e.x * N * B * 2, nw, 1, l16, lane >> 4, rot);
 
   f32x16 acc;
 #pragma unroll
   for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
   Oct<false> d[2];
   Oct<F32> v[2];
+  int idx[2], next[2];  // rows of the tiles in registers, and of the step after
+  auto number = [&](int r0) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) next[i] = row_at(l, rows.order, e.y + min(r0 + r + 16 * i, e.z - 1));
+  };
   auto load = [&](int r0) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int k = r0 + r + 16 * i;
-      if (k < e.z && c_ok) {
-        const size_t at = (size_t)row_at(l, rows.order, e.y + k) * N + c;
-        d[i].load(dy, at);
-        v[i].load(y, at);
+      idx[i] = next[i];
+      if (r0 + r + 16 * i < e.z && c_ok) {
+        const size_t at = (size_t)idx[i] * N + c;
+        d[i].template load<STREAM>(dy, at);
+        v[i].template load<STREAM>(y, at);
       } else {
         d[i].zero();
         v[i].zero();
       }
     }
   };
+  int zidx[2] = {0, 0};  // rows of the step whose dz is in LDS
+  auto put = [&](int r0) {
+    if (dz != nullptr && c_ok)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (r0 + r + 16 * i < e.z)
+          store16<STREAM>(dz + (size_t)zidx[i] * N + c,
+                          *reinterpret_cast<const uint4*>(zs + (r + 16 * i) * LDS_ROW + 8 * (tid & 15)));
+  };
+  number(0);
   load(0);
+  number(SR);
   for (int r0 = 0; r0 < e.z; r0 += SR) {
-    __syncthreads();  // the last step's reads are done
+    __syncthreads();  // the last step's reads are done, its dz complete
+    if (r0 > 0) put(r0 - SR);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
+      zidx[i] = idx[i];
       const int at = (r + 16 * i) * LDS_ROW + 8 * (tid & 15);
       *reinterpret_cast<uint4*>(ds + at) = d[i].u;
       uint4 p[P];
@@ -193,16 +244,21 @@ __global__ __launch_bounds__(256) void rotate_sums_kernel(RowLists l, RowOrder r
 #pragma unroll
       for (int k = 0; k < P; ++k) *reinterpret_cast<uint4*>(ys + k * TILE + at) = p[k];
     }
+    if (r0 + SR < e.z) {
+      load(r0 + SR);
+      number(r0 + 2 * SR);
+    }
     __syncthreads();
-    if (r0 + SR < e.z) load(r0 + SR);
     if (dz != nullptr) {
-      Oct<false> x[2];
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
-        x[t].u = *reinterpret_cast<const uint4*>(ds + l32 * LDS_ROW + 32 * wave + 16 * g + 8 * t);
-      const f32x16 o = rotate<false>(rot, x);
-      if (w_ok && r0 + l32 < e.z)
-        store16<false>(dz, (size_t)row_at(l, rows.order, e.y + r0 + l32) * N + nw + 16 * g, o);
+      for (int i = 0; i < 2; ++i) {
+        const int at = (16 * i + l16) * LDS_ROW + 32 * wave + 8 * (lane >> 4);
+        Oct<false> x;
+        x.u = *reinterpret_cast<const uint4*>(ds + at);
+        f32x4 o[2];
+        rotate<false>(rot, x, o);
+        *reinterpret_cast<uint4*>(zs + at) = pack8(o);
+      }
     }
     // lane l16 of a 16-lane group: 8 rows of one of its 16 channels
 #pragma unroll
@@ -218,6 +274,8 @@ __global__ __launch_bounds__(256) void rotate_sums_kernel(RowLists l, RowOrder r
       }
     }
   }
+  __syncthreads();
+  put((e.z - 1) / SR * SR);
   // lane: column l32 of S, rows 8 (i / 4) + 4 g + i % 4
   if (e.w >= 0) {
     if (!w_ok) return;
@@ -285,14 +343,21 @@ void run_rotate(const RotateDims& d, const RowOrder& rows, bool f32, const void*
   const RowLists l{d.T, d.n};
   // decoded rows: few to an adapter
   const bool few = d.T <= 1024;
-  const dim3 grid((unsigned)l.cap(few ? LIST_16 : LIST_64) * ((d.N + 127) / 128));
-  if (few) {
-    if (f32) hipLaunchKernelGGL((rotate_kernel<16, B, true>), grid, dim3(256), 0, st, l, rows, z, rops, d.N, which, y);
-    else hipLaunchKernelGGL((rotate_kernel<16, B, false>), grid, dim3(256), 0, st, l, rows, z, rops, d.N, which, y);
-  } else {
-    if (f32) hipLaunchKernelGGL((rotate_kernel<64, B, true>), grid, dim3(256), 0, st, l, rows, z, rops, d.N, which, y);
-    else hipLaunchKernelGGL((rotate_kernel<64, B, false>), grid, dim3(256), 0, st, l, rows, z, rops, d.N, which, y);
+  const unsigned tiles = l.cap(few ? LIST_16 : LIST_64);
+  if (!few && !f32) {
+    const dim3 grid(tiles * ((d.N + 255) / 256));
+    const uint16_t* in = static_cast<const uint16_t*>(z);
+    uint16_t* out = static_cast<uint16_t*>(y);
+    if ((size_t)d.T * d.N * 2 > STREAM_BYTES)
+      hipLaunchKernelGGL((rotate_tile_kernel<B, true>), grid, dim3(256), 0, st, l, rows, in, rops, d.N, which, out);
+    else
+      hipLaunchKernelGGL((rotate_tile_kernel<B, false>), grid, dim3(256), 0, st, l, rows, in, rops, d.N, which, out);
+    return;
   }
+  const dim3 grid(tiles * ((d.N + 127) / 128));
+  if (few && f32) hipLaunchKernelGGL((rotate_kernel<16, B, true>), grid, dim3(256), 0, st, l, rows, z, rops, d.N, which, y);
+  else if (few) hipLaunchKernelGGL((rotate_kernel<16, B, false>), grid, dim3(256), 0, st, l, rows, z, rops, d.N, which, y);
+  else hipLaunchKernelGGL((rotate_kernel<64, B, true>), grid, dim3(256), 0, st, l, rows, z, rops, d.N, which, y);
 }
 
 int sums_list(const RotateDims& d) { return (d.N + SC - 1) / SC >= 128 ? LIST_LONG : LIST_SHORT; }
@@ -304,13 +369,15 @@ hipError_t run_sums(const RotateDims& d, const RowOrder& rows, const uint16_t* d
   const RowLists l{d.T, d.n};
   const int list = sums_list(d);
   const dim3 grid((d.N + SC - 1) / SC, l.cap(list));
-  if (d.T == 0) {
-  } else if (d.f32)
-    hipLaunchKernelGGL((rotate_sums_kernel<B, true>), grid, dim3(256), 0, st, l, rows, list, dy, y, Rf, rops, d.N, dz, dq,
-                       part);
-  else
-    hipLaunchKernelGGL((rotate_sums_kernel<B, false>), grid, dim3(256), 0, st, l, rows, list, dy, y, Rf, rops, d.N, dz,
-                       dq, part);
+  auto sums = [&](auto f32, auto stream) {
+    hipLaunchKernelGGL((rotate_sums_kernel<B, decltype(f32)::value, decltype(stream)::value>), grid, dim3(256), 0, st, l,
+                       rows, list, dy, y, Rf, rops, d.N, dz, dq, part);
+  };
+  const bool stream = (size_t)d.T * d.N * 2 > STREAM_BYTES;
+  if (d.T > 0) {
+    if (d.f32) stream ? sums(std::true_type{}, std::true_type{}) : sums(std::true_type{}, std::false_type{});
+    else stream ? sums(std::false_type{}, std::true_type{}) : sums(std::false_type{}, std::false_type{});
+  }
   hipLaunchKernelGGL(rotate_join_kernel<B>, dim3((d.N / B + G - 1) / G, d.n), dim3(256), 0, st, l, rows, list, part, Rf,
                      d.N, dq);
   return hipGetLastError();
