@@ -564,7 +564,7 @@ typedef struct {
   int32_t* tiles;
 } oft_adapter_rows;
 
-/* Sizes of `tiles` and of oft_adapter_route's workspace (0 up to 16384 rows).
+/* Sizes of `tiles` and of oft_adapter_route's workspace (0 up to 4096 rows).
  * Errors here and below: OFT_EINVAL (T < 0, n < 1, null or misaligned
  * pointers), OFT_EUNSUPPORTED (T > 2^22, n > OFT_MAX_ADAPTERS). */
 int32_t oft_adapter_rows_bytes(int32_t T, int32_t n, size_t* tiles_bytes, size_t* ws_bytes);

@@ -1,14 +1,16 @@
 // Rows sorted by the adapter that they use, and the work lists of the
 // kernels that run over them (oft_adapter_route in oft.h).
 //
-// A stable counting sort: each wave counts the adapters of a contiguous run
-// of rows into its own table in LDS, the tables become first positions by a
-// scan over adapters and waves, and each wave walks its rows again, in order,
-// to hand out positions.  Rows of a wave with the same adapter find each
-// other by one ballot per bit of the adapter number, so that nothing depends
-// on the order of atomics.  Up to ONE_WG rows one workgroup does it all (the
-// call is a chain of latencies, not of bytes); above, workgroups of SLAB rows
-// count and scatter, with a scan by one workgroup between.
+// A stable counting sort: each wave takes a contiguous run of rows, keeps
+// their adapters in registers and counts them into its own table in LDS, the
+// count so far being each row's place among the wave's; a scan over adapters
+// and waves turns the tables into first positions.  Rows of a wave with the
+// same adapter find each other by one ballot per bit of the adapter number, so
+// that nothing depends on the order of atomics.  Up to ONE_WG rows one
+// workgroup does it all: the call is a chain of latencies, not of bytes (64
+// rows: 5.3 us, an empty launch 2).  More rows are too many instructions for
+// one (20011 rows: 24 us): up to SLABS workgroups count a slab each, and in a
+// second launch each adds up the slabs before it, all of them from the caches.
 #include "adapter_device.h"
 #include "oft_prof.h"
 
@@ -16,8 +18,9 @@ namespace oft {
 namespace {
 
 constexpr int THREADS = 1024, WAVES = THREADS / 64;
-constexpr int ONE_WG = 16384, SLAB = 8192;
+constexpr int ONE_WG = 4096, SLABS = 64;
 constexpr int KEYS = MAX_ADAPTERS + 1;  // adapters, and rows without one
+static_assert(THREADS >= MAX_ADAPTERS, "the scan takes an adapter a thread");
 
 __device__ __forceinline__ int key_of(int a, int n) { return (unsigned)a < (unsigned)n ? a : n; }
 
@@ -43,39 +46,51 @@ __device__ __forceinline__ uint64_t same_key(int key, bool on, int bits) {
   return m;
 }
 
-// rows of one wave: [lo, hi)
-struct Run {
-  int lo, hi;
+// The rows of one wave, RUN steps of 64, in registers: adapter (n: none, PAST
+// behind the last row) and, above KEY_BITS, the place among the wave's rows of
+// that adapter (at most 64 RUN).
+constexpr int KEY_BITS = 11, PAST = (1 << KEY_BITS) - 1;
+template <int RUN>
+struct Rows {
+  int v[RUN];
+  __device__ __forceinline__ int key(int i) const { return v[i] & PAST; }
+  __device__ __forceinline__ int place(int i) const { return v[i] >> KEY_BITS; }
 };
-__device__ __forceinline__ Run wave_run(int lo, int hi, int wave) {
-  const int per = ((hi - lo + WAVES * 64 - 1) / (WAVES * 64)) * 64;
-  const int a = min(hi, lo + wave * per);
-  return Run{a, min(hi, a + per)};
-}
 
-__device__ __forceinline__ void count_rows(const int* __restrict__ adapter, int n, int bits, Run run, int* table) {
+template <int RUN>
+__device__ __forceinline__ void load_rows(const int* __restrict__ adapter, int n, int lo, int hi, Rows<RUN>& r) {
   const int lane = threadIdx.x & 63;
-  for (int i = run.lo; i < run.hi; i += 64) {
-    const bool on = i + lane < run.hi;
-    const int key = on ? key_of(adapter[i + lane], n) : 0;
-    const uint64_t m = same_key(key, on, bits);
-    if (on && (m & ((1ull << lane) - 1)) == 0) atomicAdd(&table[key], __popcll(m));
+#pragma unroll
+  for (int i = 0; i < RUN; ++i) {
+    const int t = lo + 64 * i + lane;
+    r.v[i] = t < hi ? key_of(adapter[t], n) : PAST;
   }
 }
 
-__device__ __forceinline__ void place_rows(const int* __restrict__ adapter, int n, int bits, Run run, int* table,
-                                           int* __restrict__ order) {
+template <int RUN>
+__device__ __forceinline__ void count_rows(int bits, Rows<RUN>& r, int* table) {
   const int lane = threadIdx.x & 63;
-  for (int i = run.lo; i < run.hi; i += 64) {
-    const bool on = i + lane < run.hi;
-    const int key = on ? key_of(adapter[i + lane], n) : 0;
+#pragma unroll
+  for (int i = 0; i < RUN; ++i) {
+    const int key = r.key(i);
+    const bool on = key != PAST;
+    if (__ballot(on) == 0) break;
     const uint64_t m = same_key(key, on, bits);
     const uint64_t below = m & ((1ull << lane) - 1);
     int first = 0;
     if (on && below == 0) first = atomicAdd(&table[key], __popcll(m));
     first = __shfl(first, on ? __ffsll((unsigned long long)m) - 1 : lane);
-    if (on) order[first + __popcll(below)] = i + lane;
+    r.v[i] = key | ((first + __popcll(below)) << KEY_BITS);
   }
+}
+
+// table: the wave's first position of each adapter
+template <int RUN>
+__device__ __forceinline__ void place_rows(int lo, const Rows<RUN>& r, const int* table, int* __restrict__ order) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int i = 0; i < RUN; ++i)
+    if (r.key(i) != PAST) order[table[r.key(i)] + r.place(i)] = lo + 64 * i + lane;
 }
 
 // The sums over the adapters below each one: its rows, its tiles and pieces,
@@ -87,25 +102,27 @@ struct Scan {
   int wave[SUMS][WAVES];
 };
 
-// total[a]: rows of adapter a.  Writes offsets, the lists and their counts.
-__device__ __forceinline__ void scan_and_list(const RowLists& l, Scan& s, int total, int* __restrict__ offsets,
-                                              int* __restrict__ tiles) {
+// total: rows of this thread's adapter -> s.first[0 .. N - 1]
+template <int N>
+__device__ __forceinline__ void scan_sums(const RowLists& l, Scan& s, int total) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int n = l.n;
   int own[SUMS], sum[SUMS];
   own[0] = tid < n ? total : 0;
+  if constexpr (N > 1) {
 #pragma unroll
-  for (int i = 0; i < LISTS; ++i) own[1 + i] = l.count(i, own[0]);
-  own[5] = own[3] >= 2 ? own[3] : 0;
-  own[6] = own[4] >= 2 ? own[4] : 0;
+    for (int i = 0; i < LISTS; ++i) own[1 + i] = l.count(i, own[0]);
+    own[5] = own[3] >= 2 ? own[3] : 0;
+    own[6] = own[4] >= 2 ? own[4] : 0;
+  }
 #pragma unroll
-  for (int i = 0; i < SUMS; ++i) {
+  for (int i = 0; i < N; ++i) {
     sum[i] = wave_scan(own[i]);
     if (lane == 63) s.wave[i][wave] = sum[i];
   }
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < SUMS; ++i) {
+  for (int i = 0; i < N; ++i) {
     int before = 0;
 #pragma unroll
     for (int w = 0; w < WAVES; ++w) before += w < wave ? s.wave[i][w] : 0;
@@ -114,8 +131,13 @@ __device__ __forceinline__ void scan_and_list(const RowLists& l, Scan& s, int to
     if (tid == 0) s.first[i][0] = 0;
   }
   __syncthreads();
-  if (tid < n) offsets[tid + 1] = sum[0];
-  if (tid == 0) offsets[0] = 0;
+}
+
+// offsets, the lists and their counts from the sums
+__device__ __forceinline__ void write_lists(const RowLists& l, const Scan& s, int* __restrict__ offsets,
+                                            int* __restrict__ tiles) {
+  const int tid = threadIdx.x, n = l.n;
+  for (int a = tid; a <= n; a += THREADS) offsets[a] = s.first[0][a];
   const int rest = l.T - s.first[0][n];  // rows without an adapter
   if (tid < 8) tiles[tid] = tid < LISTS ? s.first[1 + tid][n] + l.count(tid, rest) : 0;
   for (int a = tid; a <= n; a += THREADS) {
@@ -150,106 +172,119 @@ __device__ __forceinline__ void scan_and_list(const RowLists& l, Scan& s, int to
   }
 }
 
+// RUN steps of 64 rows a wave at most; as many waves as have rows count.
+template <int RUN>
 __global__ __launch_bounds__(THREADS) void route_one_kernel(RowLists l, int bits, const int* __restrict__ adapter,
                                                             int* __restrict__ order, int* __restrict__ offsets,
                                                             int* __restrict__ tiles) {
   __shared__ int table[WAVES][KEYS];
   __shared__ Scan s;
-  const int tid = threadIdx.x, wave = tid >> 6;
-  for (int i = tid; i < WAVES * KEYS; i += THREADS) (&table[0][0])[i] = 0;
+  const int tid = threadIdx.x, wave = tid >> 6, n = l.n;
+  const int per = RUN == 1 ? 64 : ((l.T + WAVES * 64 - 1) / (WAVES * 64)) * 64;  // rows of a wave
+  const int waves = (l.T + per - 1) / per;
+  const int lo = wave * per, hi = min(l.T, lo + per);
+  Rows<RUN> r;
+  load_rows<RUN>(adapter, n, lo, hi, r);
+  for (int w = 0; w < waves; ++w)
+    for (int a = tid; a <= n; a += THREADS) table[w][a] = 0;
   __syncthreads();
-  const Run run = wave_run(0, l.T, wave);
-  count_rows(adapter, l.n, bits, run, table[wave]);
+  count_rows<RUN>(bits, r, table[wave]);
   __syncthreads();
   // rows of this thread's adapter, and of the waves before each one
   int total = 0;
-  if (tid < l.n) {
-#pragma unroll
-    for (int w = 0; w < WAVES; ++w) {
+  if (tid < n)
+    for (int w = 0; w < waves; ++w) {
       const int c = table[w][tid];
       table[w][tid] = total;
       total += c;
     }
-  }
-  scan_and_list(l, s, total, offsets, tiles);
-  // (the scan's barriers stand between its writes of s.first and these reads)
-  for (int a = tid; a < l.n; a += THREADS) {
-#pragma unroll
-    for (int w = 0; w < WAVES; ++w) table[w][a] += s.first[0][a];
-  }
+  scan_sums<SUMS>(l, s, total);
+  if (tid < n)
+    for (int w = 0; w < waves; ++w) table[w][tid] += s.first[0][tid];
   if (tid < 64) {  // rows without an adapter, behind all others
-    int v = tid < WAVES ? table[tid][l.n] : 0;
+    int v = tid < waves ? table[tid][n] : 0;
     v = wave_scan(v) - v;
-    if (tid < WAVES) table[tid][l.n] = s.first[0][l.n] + v;
+    if (tid < waves) table[tid][n] = s.first[0][n] + v;
   }
   __syncthreads();
-  place_rows(adapter, l.n, bits, run, table[wave], order);
+  place_rows<RUN>(lo, r, table[wave], order);
+  write_lists(l, s, offsets, tiles);
 }
 
 // ---- more rows than one workgroup takes
+// RUN steps of 64 rows a wave
+template <int RUN>
 __global__ __launch_bounds__(THREADS) void route_count_kernel(RowLists l, int bits, const int* __restrict__ adapter,
                                                               int* __restrict__ counts) {
   __shared__ int table[KEYS];
   const int tid = threadIdx.x;
-  for (int i = tid; i < KEYS; i += THREADS) table[i] = 0;
+  Rows<RUN> r;
+  load_rows<RUN>(adapter, l.n, (blockIdx.x * WAVES + (tid >> 6)) * 64 * RUN, l.T, r);
+  for (int a = tid; a <= l.n; a += THREADS) table[a] = 0;
   __syncthreads();
-  const int lo = blockIdx.x * SLAB;
-  count_rows(adapter, l.n, bits, wave_run(lo, min(l.T, lo + SLAB), tid >> 6), table);
+  count_rows<RUN>(bits, r, table);
   __syncthreads();
   for (int a = tid; a <= l.n; a += THREADS) counts[(size_t)blockIdx.x * (l.n + 1) + a] = table[a];
 }
 
-// counts[slab][adapter] -> the slab's first position of the adapter
-__global__ __launch_bounds__(THREADS) void route_scan_kernel(RowLists l, int slabs, int* __restrict__ counts,
-                                                             int* __restrict__ offsets, int* __restrict__ tiles) {
+template <int RUN>
+__global__ __launch_bounds__(THREADS) void route_place_kernel(RowLists l, int bits, const int* __restrict__ adapter,
+                                                              const int* __restrict__ counts, int* __restrict__ order,
+                                                              int* __restrict__ offsets, int* __restrict__ tiles) {
+  __shared__ int table[WAVES][KEYS];
   __shared__ Scan s;
-  const int tid = threadIdx.x, n = l.n;
-  int total = 0;
-  if (tid < n)
-    for (int g = 0; g < slabs; ++g) total += counts[(size_t)g * (n + 1) + tid];
-  scan_and_list(l, s, total, offsets, tiles);
-  for (int a = tid; a <= n; a += THREADS) {
-    int at = s.first[0][a];
-    for (int g = 0; g < slabs; ++g) {
-      const size_t i = (size_t)g * (n + 1) + a;
-      const int c = counts[i];
-      counts[i] = at;
-      at += c;
+  const int tid = threadIdx.x, wave = tid >> 6, n = l.n;
+  const int lo = (blockIdx.x * WAVES + wave) * 64 * RUN;
+  Rows<RUN> r;
+  load_rows<RUN>(adapter, n, lo, l.T, r);
+  // this thread's adapter: rows in all, and in the slabs before this one
+  int total = 0, before = 0;
+  if (tid < n) {
+    const int* c = counts + tid;
+#pragma unroll 8
+    for (int g = 0; g < (int)gridDim.x; ++g, c += n + 1) {
+      total += *c;
+      before += g < (int)blockIdx.x ? *c : 0;
     }
   }
-}
-
-__global__ __launch_bounds__(THREADS) void route_place_kernel(RowLists l, int bits, const int* __restrict__ adapter,
-                                                              const int* __restrict__ first,
-                                                              int* __restrict__ order) {
-  __shared__ int table[WAVES][KEYS];
-  const int tid = threadIdx.x, wave = tid >> 6;
-  for (int i = tid; i < WAVES * KEYS; i += THREADS) (&table[0][0])[i] = 0;
+  for (int w = 0; w < WAVES; ++w)
+    for (int a = tid; a <= n; a += THREADS) table[w][a] = 0;
   __syncthreads();
-  const int lo = blockIdx.x * SLAB;
-  const Run run = wave_run(lo, min(l.T, lo + SLAB), wave);
-  count_rows(adapter, l.n, bits, run, table[wave]);
-  __syncthreads();
-  for (int a = tid; a <= l.n; a += THREADS) {
-    int at = first[(size_t)blockIdx.x * (l.n + 1) + a];
+  count_rows<RUN>(bits, r, table[wave]);
+  if (blockIdx.x == 0) scan_sums<SUMS>(l, s, total);
+  else scan_sums<1>(l, s, total);
+  if (tid < n) {
+    int at = s.first[0][tid] + before;
 #pragma unroll
     for (int w = 0; w < WAVES; ++w) {
-      const int c = table[w][a];
-      table[w][a] = at;
+      const int c = table[w][tid];
+      table[w][tid] = at;
       at += c;
     }
   }
+  if (wave == 0) {  // rows without an adapter, behind all others
+    int at = tid < (int)blockIdx.x ? counts[(size_t)tid * (n + 1) + n] : 0;  // (at most 64 slabs)
+    at = __shfl(wave_scan(at), 63);
+    int v = tid < WAVES ? table[tid][n] : 0;
+    v = wave_scan(v) - v;
+    if (tid < WAVES) table[tid][n] = s.first[0][n] + at + v;
+  }
   __syncthreads();
-  place_rows(adapter, l.n, bits, run, table[wave], order);
+  place_rows<RUN>(lo, r, table[wave], order);
+  if (blockIdx.x == 0) write_lists(l, s, offsets, tiles);
 }
 
-int slabs_of(const RowLists& l) { return (l.T + SLAB - 1) / SLAB; }
+// f(steps of 64 rows a wave takes): the fewest that SLABS workgroups make do with
+template <class F>
+void slab_run(int T, F f) {
+  if (T <= SLABS * THREADS) f(std::integral_constant<int, 1>{});
+  else if (T <= 8 * SLABS * THREADS) f(std::integral_constant<int, 8>{});
+  else f(std::integral_constant<int, 64>{});
+}
 
 }  // namespace
 
-size_t adapter_route_ws_bytes(const RowLists& l) {
-  return l.T <= ONE_WG ? 0 : 4 * (size_t)slabs_of(l) * (l.n + 1);
-}
+size_t adapter_route_ws_bytes(const RowLists& l) { return l.T <= ONE_WG ? 0 : 4 * (size_t)SLABS * (l.n + 1); }
 
 hipError_t launch_adapter_route(const RowLists& l, const int* adapter, int* order, int* offsets, int* tiles, char* ws,
                                 hipStream_t st) {
@@ -257,14 +292,22 @@ hipError_t launch_adapter_route(const RowLists& l, const int* adapter, int* orde
   int bits = 0;
   while ((1 << bits) <= l.n) ++bits;
   if (l.T <= ONE_WG) {
-    hipLaunchKernelGGL(route_one_kernel, dim3(1), dim3(THREADS), 0, st, l, bits, adapter, order, offsets, tiles);
+    auto run = [&](auto steps) {
+      hipLaunchKernelGGL(route_one_kernel<decltype(steps)::value>, dim3(1), dim3(THREADS), 0, st, l, bits, adapter, order,
+                         offsets, tiles);
+    };
+    if (l.T <= THREADS) run(std::integral_constant<int, 1>{});
+    else run(std::integral_constant<int, ONE_WG / THREADS>{});
     return hipGetLastError();
   }
-  const int slabs = slabs_of(l);
   int* counts = reinterpret_cast<int*>(ws);
-  hipLaunchKernelGGL(route_count_kernel, dim3(slabs), dim3(THREADS), 0, st, l, bits, adapter, counts);
-  hipLaunchKernelGGL(route_scan_kernel, dim3(1), dim3(THREADS), 0, st, l, slabs, counts, offsets, tiles);
-  hipLaunchKernelGGL(route_place_kernel, dim3(slabs), dim3(THREADS), 0, st, l, bits, adapter, counts, order);
+  slab_run(l.T, [&](auto steps) {
+    constexpr int RUN = decltype(steps)::value;
+    const int slabs = (l.T + RUN * THREADS - 1) / (RUN * THREADS);
+    hipLaunchKernelGGL(route_count_kernel<RUN>, dim3(slabs), dim3(THREADS), 0, st, l, bits, adapter, counts);
+    hipLaunchKernelGGL(route_place_kernel<RUN>, dim3(slabs), dim3(THREADS), 0, st, l, bits, adapter, counts, order,
+                       offsets, tiles);
+  });
   return hipGetLastError();
 }
 

@@ -54,7 +54,8 @@ def _ws(nbytes):
 # --------------------------------------------------------------------- route
 @pytest.mark.parametrize("kind", ["mixed", "runs", "one", "none", "some"])
 @pytest.mark.parametrize("T,n", [(1, 1), (3, 2), (64, 64), (65, 1), (1000, 7), (1024, 1024), (1025, 1000), (4097, 33),
-                                 (16384, 300), (16385, 300), (30001, 1024)])
+                                 (30001, 1024),
+                                 (65536, 7), (65537, 300), (524288, 5), (600001, 900)])
 def test_route(T, n, kind):
     a = cases.adapters(T, n, kind)
     rows = _rows(a, n)
@@ -63,7 +64,7 @@ def test_route(T, n, kind):
     assert np.array_equal(rows.order.cpu().numpy(), order)
 
 
-@pytest.mark.parametrize("T,n", [(1, 1), (65, 3), (1000, 7), (5000, 1024), (20000, 5)])
+@pytest.mark.parametrize("T,n", [(1, 1), (65, 3), (1000, 7), (5000, 1024), (20000, 5), (40000, 1000)])
 @pytest.mark.parametrize("kind", ["mixed", "some", "none", "skewed"])
 def test_route_lists(T, n, kind):
     """Every list covers each row once, in pieces of one adapter and the list's size."""
