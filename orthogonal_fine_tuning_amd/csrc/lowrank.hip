@@ -8,8 +8,8 @@
 // their own r rows of A and their own columns of v.  All four products with
 // rows of activations are two kernels: `down` (activations -> rank, the
 // contraction long) and `up` (rank -> activations, the contraction short); the
-// backward runs them on transposed copies of the factors.  `pieces` forms the
-// sums over rows.  Everything is bound by the bytes of x, y, dy and dx, so the
+// backward runs them with the factors' other side along the contraction, read
+// with the transposing LDS load.  `pieces` forms the sums over rows.  Everything is bound by the bytes of x, y, dy and dx, so the
 // products take whatever keeps those moving: 16 x 16 x 32 matrix steps (ranks
 // and tiles of single decoded rows are small), operands straight from global
 // memory where both run along the contraction.
@@ -33,14 +33,21 @@ namespace {
 // partial sums; the waves' sums are added through LDS in their order.  A
 // wave's step goes through its own part of LDS, from loads whose lanes run
 // along the rows to operands whose lanes run across them.
+//
+// What `up` takes is written as the operands of its matrix steps, in parts of
+// bf16, so that it is split once and not by every block of columns: for each
+// 16 rows (in list order), each VR columns of v and each 32 of those, a 1 KB
+// block a part, lane l's eight items of row l % 16 and columns 8 (l / 16) ...
 struct DownArgs {
   RowLists l;
   RowOrder rows;
   const void* src;
   long lds;
-  const uint16_t* w;
-  long w_a;  // elements of an adapter's matrices
-  float* v;
+  const uint16_t* w;  // a segment's W [r][len], or its transpose [len][r]
+  long w_a;           // elements of an adapter's matrices
+  float* v;          // [T][R] (NULL: not wanted)
+  uint16_t* parts;   // the operands of `up` (NULL: not wanted)
+  int vr, nparts;    // columns of v that one product of `up` takes; parts
   int R;             // columns of v
   int r, per;        // r output columns a segment (R when whole), `per` a job
   int jobs_per_seg;
@@ -50,12 +57,13 @@ struct DownArgs {
 };
 constexpr int DW = 8;  // waves
 
-// LIST: LIST_16, or LIST_64 in four parts
-template <int LIST, int NG, bool F32>
+// LIST: LIST_16, or LIST_64 in four parts; WT: W is stored transposed
+template <int LIST, int NG, bool F32, bool WT>
 __global__ __launch_bounds__(64 * DW) void down_kernel(DownArgs a) {
   constexpr int P = Oct<F32>::P, SUB = LIST == LIST_16 ? 1 : 4;
   constexpr int XB = F32 ? 256 : 128, XI = 16 * XB / 1024;  // bytes of a row of x and step, loads of a lane
-  constexpr int WAVE = 16 * XB + 16 * NG * 128;             // bytes of a wave's step
+  constexpr int WROW = 32 * NG + 16;                        // LDS row of a transposed step: 16 bytes apart in banks
+  constexpr int WAVE = 16 * XB + (WT ? 64 * WROW : 16 * NG * 128);  // bytes of a wave's step
   __shared__ __attribute__((aligned(16))) char lds[DW * WAVE];
   int4 e;
   if (!list_entry(a.l, a.rows.tiles, LIST, blockIdx.x / SUB, e)) return;
@@ -75,7 +83,7 @@ __global__ __launch_bounds__(64 * DW) void down_kernel(DownArgs a) {
   const int l16 = lane & 15, g = lane >> 4;
 
   if (e.x >= 0) {
-    const uint16_t* w = a.w + (size_t)e.x * a.w_a + (size_t)a.r * col0 + (size_t)jw * len;
+    const uint16_t* w = a.w + (size_t)e.x * a.w_a + (size_t)a.r * col0 + (WT ? (size_t)jw : (size_t)jw * len);
     constexpr int XL = XB / 16;  // lanes along a row of x
     size_t xat[XI];
 #pragma unroll
@@ -84,7 +92,11 @@ __global__ __launch_bounds__(64 * DW) void down_kernel(DownArgs a) {
                (F32 ? 4 : 8) * (lane % XL);
     size_t wat[2 * NG];
 #pragma unroll
-    for (int i = 0; i < 2 * NG; ++i) wat[i] = (size_t)min(8 * i + (lane >> 3), nj - 1) * len + 8 * (lane & 7);
+    for (int i = 0; i < 2 * NG; ++i) {
+      const int t = 64 * i + lane;  // WT: 16 bytes t % 2NG of row t / 2NG of the step
+      wat[i] = WT ? (size_t)(t / (2 * NG)) * a.r + 8 * (t % (2 * NG))
+                  : (size_t)min(8 * i + (lane >> 3), nj - 1) * len + 8 * (lane & 7);
+    }
     const int xk = (F32 ? 4 : 8) * (lane % XL), wk = 8 * (lane & 7);
     char* xs = lds + wave * WAVE;
     char* ws = xs + 16 * XB;
@@ -108,7 +120,14 @@ __global__ __launch_bounds__(64 * DW) void down_kernel(DownArgs a) {
         x[i] = k + xk < len ? *reinterpret_cast<const uint4*>(static_cast<const char*>(a.src) + (xat[i] + k) * (F32 ? 4 : 2))
                             : zero4();
 #pragma unroll
-      for (int i = 0; i < 2 * NG; ++i) wv[i] = k + wk < len ? *reinterpret_cast<const uint4*>(w + wat[i] + k) : zero4();
+      for (int i = 0; i < 2 * NG; ++i) {
+        const int t = 64 * i + lane;
+        if constexpr (WT)
+          wv[i] = k + t / (2 * NG) < len && 8 * (t % (2 * NG)) < nj
+                      ? *reinterpret_cast<const uint4*>(w + wat[i] + (size_t)k * a.r)
+                      : zero4();
+        else wv[i] = k + wk < len ? *reinterpret_cast<const uint4*>(w + wat[i] + k) : zero4();
+      }
     };
     const int steps = (len + 63) / 64;
     int s = wave;
@@ -118,7 +137,11 @@ __global__ __launch_bounds__(64 * DW) void down_kernel(DownArgs a) {
 #pragma unroll
       for (int i = 0; i < XI; ++i) *xput(i) = x[i];
 #pragma unroll
-      for (int i = 0; i < 2 * NG; ++i) *wput(8 * i + (lane >> 3), lane & 7) = wv[i];
+      for (int i = 0; i < 2 * NG; ++i) {
+        const int t = 64 * i + lane;
+        if constexpr (WT) *reinterpret_cast<uint4*>(ws + (t / (2 * NG)) * WROW + 16 * (t % (2 * NG))) = wv[i];
+        else *wput(8 * i + (lane >> 3), lane & 7) = wv[i];
+      }
       if (s + DW < steps) load(s + DW);
       wave_order();
 #pragma unroll
@@ -134,7 +157,15 @@ __global__ __launch_bounds__(64 * DW) void down_kernel(DownArgs a) {
         o.parts(xp);
 #pragma unroll
         for (int j = 0; j < NG; ++j) {
-          const bf16x8 wj = as_bf16x8(*wput(16 * j + l16, 4 * t + g));
+          bf16x8 wj;
+          if constexpr (WT) {  // eight rows of column l16 of 16
+            const uint16_t* q = reinterpret_cast<const uint16_t*>(ws + (32 * t + 8 * g + (l16 >> 2)) * WROW + 32 * j +
+                                                                  8 * (l16 & 3));
+            const uint2 lo = nn::ds_read_tr16(q), hi = nn::ds_read_tr16(q + 4 * WROW / 2);
+            wj = as_bf16x8(make_uint4(lo.x, lo.y, hi.x, hi.y));
+          } else {
+            wj = as_bf16x8(*wput(16 * j + l16, 4 * t + g));
+          }
 #pragma unroll
           for (int p = P - 1; p >= 0; --p) acc[j] = mfma16(wj, as_bf16x8(xp[p]), acc[j]);
         }
@@ -163,71 +194,143 @@ __global__ __launch_bounds__(64 * DW) void down_kernel(DownArgs a) {
       o.w += t.w;
     }
   }
-  if (l16 < e.z && c0 < nj)  // (ranks are multiples of 8)
-    *reinterpret_cast<float4*>(a.v + (size_t)row_at(a.l, a.rows.order, e.y + l16) * a.R + seg * a.r + jw + c0) = o;
+  if (c0 >= nj) return;  // (ranks are multiples of 8)
+  const int col = seg * a.r + jw + c0;
+  if (a.v != nullptr && l16 < e.z)
+    *reinterpret_cast<float4*>(a.v + (size_t)row_at(a.l, a.rows.order, e.y + l16) * a.R + col) = o;
+  if (a.parts != nullptr && e.x >= 0) {
+    const int s = col / a.vr, k = col % a.vr, steps = (a.vr + 31) / 32;
+    uint16_t* out = a.parts + (((size_t)blockIdx.x * (a.R / a.vr) + s) * steps + k / 32) * a.nparts * 512 +
+                    ((k % 32) / 8 * 16 + l16) * 8 + k % 8;
+    uint32_t h[4][3];
+    split_bf16<3>(o.x, h[0]);
+    split_bf16<3>(o.y, h[1]);
+    split_bf16<3>(o.z, h[2]);
+    split_bf16<3>(o.w, h[3]);
+#pragma unroll
+    for (int p = 0; p < 3; ++p)
+      if (p < a.nparts)
+        *reinterpret_cast<uint2*>(out + p * 512) = make_uint2(h[0][p] | (h[1][p] << 16), h[2][p] | (h[3][p] << 16));
+  }
 }
 
 // --------------------------------------------------------------------- up
-// out[row][c] = base[row][c] + scale sum_k v[row][k] W[c][k]: a workgroup per
-// tile of rows and 256 columns of one segment, a wave per 64 of them.  The
-// tile's v is split into operands once, in LDS, 64 columns at a time.  The
-// columns that a matrix step's operand rows stand for are chosen so that a
+// out[row][c] = base[row][c] + scale sum_k v[row][k] W[c][k]: a wave per tile
+// of rows and 64 columns of one segment, v from the operands that `down` left.
+// The columns that a matrix step's operand rows stand for are chosen so that a
 // lane's results are the 16 bytes of a row next to its neighbours': bf16
 // column 32 (m / 2) + 8 (i / 4) + 4 (m % 2) + i % 4 of the 64 for operand row i
 // of step m, fp32 16 m + i.
 struct UpArgs {
   RowLists l;
   RowOrder rows;
-  const float* v;  // [T][R]
-  int R, r;        // r: the contraction, from column seg * r of v
-  const uint16_t* w;  // [n][C][r]
+  const uint16_t* parts;
+  int r, segs;        // the contraction, and how many there are in a row of v
+  const uint16_t* w;  // [n][C][r], or its transpose [n][r][C]
   long w_a;
   const float* scale;
   const void* base;
   void* out;
   int C;  // columns
   int n_seg, blocks;
-  int seg_at[MAX_SEG + 1], block_at[MAX_SEG + 1];  // columns and 256-column blocks before each segment
+  int seg_at[MAX_SEG + 1], block_at[MAX_SEG + 1];  // columns and 64-column blocks before each segment
 };
-constexpr int UC = 256, UK = 64, UROW = UK + 8;
+constexpr int UC = 64;
 
-template <int TM, bool F32>
-__global__ __launch_bounds__(256) void up_kernel(UpArgs a) {
-  constexpr int P = F32 ? 3 : 2, XG = TM / 16, H = F32 ? 4 : 2;  // H: 16-byte pieces of a lane and row
-  __shared__ __attribute__((aligned(16))) uint16_t vs[P][TM][UROW];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int l16 = lane & 15, g = lane >> 4;
-  const int tile = blockIdx.x / a.blocks, cb = blockIdx.x % a.blocks;
-  int4 e;
-  if (!list_entry(a.l, a.rows.tiles, TM == 16 ? LIST_16 : LIST_64, tile, e)) return;
-  int seg = 0, seg_lo = 0, seg_hi = a.seg_at[1], blk_lo = 0;
+// The wave's 64 columns.
+struct UpBlock {
+  int seg, n0, hi;
+};
+__device__ __forceinline__ UpBlock up_block(const UpArgs& a, int cb) {
+  UpBlock b{0, UC * cb, a.seg_at[1]};
 #pragma unroll
   for (int i = 1; i < MAX_SEG; ++i)
-    if (i < a.n_seg && cb >= a.block_at[i]) {
-      seg = i;
-      seg_lo = a.seg_at[i];
-      seg_hi = a.seg_at[i + 1];
-      blk_lo = a.block_at[i];
+    if (i < a.n_seg && cb >= a.block_at[i]) b = UpBlock{i, a.seg_at[i] + UC * (cb - a.block_at[i]), a.seg_at[i + 1]};
+  return b;
+}
+
+// W of the wave's columns as operands, contraction items k0 + 32 s .. (zero
+// past r): step m's rows are columns as above.  A transposed W comes through
+// the wave's tile, 64 items at a time, and the transposing load.
+template <bool F32, bool WT>
+struct UpOperand {
+  const UpArgs& a;
+  const uint16_t* w;
+  const UpBlock& b;
+  WaveTile t;
+  int lane;
+  __device__ __forceinline__ void stage(int k0) const {
+    if constexpr (WT) {
+      uint4 u[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int k = k0 + 8 * i + (lane >> 3), c = b.n0 + 8 * (lane & 7);
+        u[i] = k < a.r && c < b.hi ? *reinterpret_cast<const uint4*>(w + (size_t)k * a.C + c) : zero4();
+      }
+      wave_order();
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t.by_row(i, lane) = u[i];
+      wave_order();
     }
-  const int n0 = seg_lo + UC * (cb - blk_lo) + 64 * wave;
+  }
+  __device__ __forceinline__ void get(int k0, int s, bf16x8 (&o)[4]) const {
+    const int l16 = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const int first = F32 ? 16 * m : 32 * (m / 2) + 4 * (m % 2);
+      constexpr int APART = F32 ? 4 : 8;  // columns between the quarters of an operand's rows
+      if constexpr (WT) {
+        // the 16-lane group's eight-byte pieces: four columns of row l16 / 4 each
+        const int c = first + APART * (l16 & 3), k = 32 * s + 8 * g + (l16 >> 2);
+        const uint2 lo = nn::ds_read_tr16(reinterpret_cast<const uint16_t*>(t.at(k, c >> 3)) + (c & 7));
+        const uint2 hi = nn::ds_read_tr16(reinterpret_cast<const uint16_t*>(t.at(k + 4, c >> 3)) + (c & 7));
+        o[m] = as_bf16x8(make_uint4(lo.x, lo.y, hi.x, hi.y));
+      } else {
+        const int c = min(b.n0 + first + APART * (l16 >> 2) + (l16 & 3), b.hi - 1), k = k0 + 32 * s + 8 * g;
+        o[m] = as_bf16x8(k < a.r ? *reinterpret_cast<const uint4*>(w + (size_t)c * a.r + k) : zero4());
+      }
+    }
+  }
+};
+
+// v of 16 rows (block `i16` of the list's) and contraction items 32 s ..
+template <int P>
+__device__ __forceinline__ void up_rows(const UpArgs& a, int seg, int i16, int s, int lane, bf16x8 (&o)[P]) {
+  const uint16_t* p =
+      a.parts + (((size_t)i16 * a.segs + seg) * ((a.r + 31) / 32) + s) * P * 512 + 8 * lane;
+  const bool ok = 32 * s + 8 * (lane >> 4) < a.r;  // (nothing is written past r)
+#pragma unroll
+  for (int k = 0; k < P; ++k) o[k] = as_bf16x8(ok ? *reinterpret_cast<const uint4*>(p + k * 512) : zero4());
+}
+
+// Decoded rows, and rows of fp32: four waves, base and result by operands.
+template <int TM, bool F32, bool WT>
+__global__ __launch_bounds__(256) void up_kernel(UpArgs a) {
+  constexpr int P = F32 ? 3 : 2, XG = TM / 16, H = F32 ? 4 : 2;  // H: 16-byte pieces of a lane and row
+  __shared__ __attribute__((aligned(16))) char lds[WT ? 4 : 1][WT ? WaveTile::BYTES : 16];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int l16 = lane & 15, g = lane >> 4;
+  const int wgs = (a.blocks + 3) / 4, tile = blockIdx.x / wgs, cb = (blockIdx.x % wgs) * 4 + wave;
+  int4 e;
+  if (cb >= a.blocks || !list_entry(a.l, a.rows.tiles, TM == 16 ? LIST_16 : LIST_64, tile, e)) return;
+  const UpBlock b = up_block(a, cb);
   // column of piece h within the 64
   auto col = [&](int h) { return F32 ? 16 * h + 4 * g : 32 * h + 8 * g; };
-
   uint4 y[XG][H];
   size_t at[XG];
 #pragma unroll
   for (int i = 0; i < XG; ++i) {
-    at[i] = (size_t)row_at(a.l, a.rows.order, e.y + min(16 * i + l16, e.z - 1)) * a.C + n0;
+    at[i] = (size_t)row_at(a.l, a.rows.order, e.y + min(16 * i + l16, e.z - 1)) * a.C + b.n0;
 #pragma unroll
     for (int h = 0; h < H; ++h) {
       // (segments are multiples of 16: a piece is inside or not)
-      const bool ok = n0 + col(h) < seg_hi && a.base != nullptr;
+      const bool ok = b.n0 + col(h) < b.hi && a.base != nullptr;
       y[i][h] = ok ? *reinterpret_cast<const uint4*>(static_cast<const char*>(a.base) + (at[i] + col(h)) * (F32 ? 4 : 2))
                    : zero4();
     }
   }
   auto store = [&](int i, int h, const uint4& u) {
-    if (16 * i + l16 < e.z && n0 + col(h) < seg_hi)
+    if (16 * i + l16 < e.z && b.n0 + col(h) < b.hi)
       *reinterpret_cast<uint4*>(static_cast<char*>(a.out) + (at[i] + col(h)) * (F32 ? 4 : 2)) = u;
   };
   if (e.x < 0) {  // rows of the base model
@@ -238,185 +341,152 @@ __global__ __launch_bounds__(256) void up_kernel(UpArgs a) {
       for (int h = 0; h < H; ++h) store(i, h, y[i][h]);
     return;
   }
-  const uint16_t* w = a.w + (size_t)e.x * a.w_a;
-  size_t wrow[4];
-#pragma unroll
-  for (int m = 0; m < 4; ++m) {
-    const int c = F32 ? 16 * m + l16 : 32 * (m / 2) + 8 * (l16 >> 2) + 4 * (m % 2) + (l16 & 3);
-    wrow[m] = (size_t)min(n0 + c, seg_hi - 1) * a.r + 8 * g;
-  }
+  const UpOperand<F32, WT> w{a, a.w + (size_t)e.x * a.w_a, b, WaveTile{lds[WT ? wave : 0]}, lane};
+  const float sc = a.scale[e.x];
   f32x4 acc[XG][4];
 #pragma unroll
   for (int i = 0; i < XG; ++i)
 #pragma unroll
     for (int m = 0; m < 4; ++m) acc[i][m] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-  // thread: eight columns of v of row tid / 8 (+ 32)
-  constexpr int VI = (TM + 31) / 32;
-  const int vk = 8 * (tid & 7), vr = tid >> 3;
-  for (int k0 = 0; k0 < a.r; k0 += UK) {
-    Oct<true> v[VI];
+  for (int k0 = 0; k0 < a.r; k0 += 64) {
+    w.stage(k0);
 #pragma unroll
-    for (int i = 0; i < VI; ++i) {
-      const int r = vr + 32 * i;
-      if (r < e.z && k0 + vk < a.r)
-        v[i].load(a.v, (size_t)row_at(a.l, a.rows.order, e.y + r) * a.R + seg * a.r + k0 + vk);
-      else
-        v[i].zero();
-    }
-    uint4 wv[4][2];
+    for (int s = 0; s < 2; ++s) {
+      if (k0 + 32 * s >= a.r) break;
+      bf16x8 wo[4];
+      w.get(k0, s, wo);
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+      for (int i = 0; i < XG; ++i) {
+        bf16x8 v[P];
+        up_rows<P>(a, b.seg, tile * XG + i, k0 / 32 + s, lane, v);
 #pragma unroll
-      for (int m = 0; m < 4; ++m)
-        wv[m][t] = k0 + 32 * t + 8 * g < a.r ? *reinterpret_cast<const uint4*>(w + wrow[m] + k0 + 32 * t) : zero4();
-    if (k0 > 0) __syncthreads();  // the last columns' reads are done
+        for (int p = P - 1; p >= 0; --p)
 #pragma unroll
-    for (int i = 0; i < VI; ++i)
-      if (vr + 32 * i < TM) {
-        const float f[8] = {v[i].a.x, v[i].a.y, v[i].a.z, v[i].a.w, v[i].b.x, v[i].b.y, v[i].b.z, v[i].b.w};
-        uint4 o[P];
-        split_bf16x8<P>(f, o);
-#pragma unroll
-        for (int p = 0; p < P; ++p) *reinterpret_cast<uint4*>(&vs[p][vr + 32 * i][vk]) = o[p];
+          for (int m = 0; m < 4; ++m) acc[i][m] = mfma16(wo[m], v[p], acc[i][m]);
       }
-    __syncthreads();
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      if (k0 + 32 * t >= a.r) break;
-#pragma unroll
-      for (int i = 0; i < XG; ++i)
-#pragma unroll
-        for (int p = P - 1; p >= 0; --p) {
-          const uint4 o = *reinterpret_cast<const uint4*>(&vs[p][16 * i + l16][32 * t + 8 * g]);
-#pragma unroll
-          for (int m = 0; m < 4; ++m) acc[i][m] = mfma16(as_bf16x8(wv[m][t]), as_bf16x8(o), acc[i][m]);
-        }
     }
   }
-  const float sc = a.scale[e.x];
 #pragma unroll
   for (int i = 0; i < XG; ++i)
 #pragma unroll
     for (int h = 0; h < H; ++h) {
-      const uint32_t b[4] = {y[i][h].x, y[i][h].y, y[i][h].z, y[i][h].w};
+      const uint32_t u[4] = {y[i][h].x, y[i][h].y, y[i][h].z, y[i][h].w};
       uint32_t q[4];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         if constexpr (F32) {
-          q[c] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, b[c]) + sc * acc[i][h][c]);
+          q[c] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, u[c]) + sc * acc[i][h][c]);
         } else {
           const f32x4& s = acc[i][2 * h + c / 2];
-          q[c] = pack_bf16x2(bf16_to_f32(b[c] & 0xFFFF) + sc * s[2 * (c % 2)],
-                             bf16_to_f32(b[c] >> 16) + sc * s[2 * (c % 2) + 1]);
+          q[c] = pack_bf16x2(bf16_to_f32(u[c] & 0xFFFF) + sc * s[2 * (c % 2)],
+                             bf16_to_f32(u[c] >> 16) + sc * s[2 * (c % 2) + 1]);
         }
       }
       store(i, h, make_uint4(q[0], q[1], q[2], q[3]));
     }
 }
 
-// bf16 rows in tiles of 64: base and result go through the wave's own LDS
-// tile, so that they are read and written by whole stretches of rows.
-template <bool STREAM>
-__global__ __launch_bounds__(256) void up_tile_kernel(UpArgs a) {
+// bf16 rows in tiles of 64: base and result go through the wave's tile, so
+// that they are read and written by whole stretches of rows.  KS: 32-item
+// steps of the contraction whose W the wave keeps in registers while it takes
+// its rows 16 at a time; 0: any number, all rows at once.
+constexpr int UW = 2;  // waves of a workgroup; they share nothing
+
+template <bool STREAM, bool WT, int KS>
+__global__ __launch_bounds__(64 * UW) void up_tile_kernel(UpArgs a) {
   constexpr int P = 2;
-  __shared__ __attribute__((aligned(16))) uint16_t vs[P][64][UROW];
-  __shared__ __attribute__((aligned(16))) char lds[4][WaveTile::BYTES];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int l16 = lane & 15, g = lane >> 4;
-  const int tile = blockIdx.x / a.blocks, cb = blockIdx.x % a.blocks;
+  __shared__ __attribute__((aligned(16))) char lds[UW][WaveTile::BYTES];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int g = lane >> 4;
+  const int wgs = (a.blocks + UW - 1) / UW, tile = blockIdx.x / wgs, cb = (blockIdx.x % wgs) * UW + wave;
   int4 e;
-  if (!list_entry(a.l, a.rows.tiles, LIST_64, tile, e)) return;
-  int seg = 0, seg_lo = 0, seg_hi = a.seg_at[1], blk_lo = 0;
-#pragma unroll
-  for (int i = 1; i < MAX_SEG; ++i)
-    if (i < a.n_seg && cb >= a.block_at[i]) {
-      seg = i;
-      seg_lo = a.seg_at[i];
-      seg_hi = a.seg_at[i + 1];
-      blk_lo = a.block_at[i];
-    }
-  const int n0 = seg_lo + UC * (cb - blk_lo) + 64 * wave;
-  const int c = n0 + 8 * (lane & 7);  // (segments are multiples of 16: a piece is inside or not)
+  if (cb >= a.blocks || !list_entry(a.l, a.rows.tiles, LIST_64, tile, e)) return;
+  const UpBlock b = up_block(a, cb);
+  const int c = b.n0 + 8 * (lane & 7);  // (segments are multiples of 16: a piece is inside or not)
+  const WaveTile t{lds[wave]};
   int row[8];
   tile_rows8(a.l, a.rows.order, e, lane, row);
   Oct<false> y[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i)
-    if (c < seg_hi && a.base != nullptr) y[i].load<STREAM>(a.base, (size_t)row[i] * a.C + c);
+    if (c < b.hi && a.base != nullptr) y[i].load<STREAM>(a.base, (size_t)row[i] * a.C + c);
     else y[i].zero();
   if (e.x >= 0) {
-    const uint16_t* w = a.w + (size_t)e.x * a.w_a;
-    size_t wrow[4];
-#pragma unroll
-    for (int m = 0; m < 4; ++m)
-      wrow[m] = (size_t)min(n0 + 32 * (m / 2) + 8 * (l16 >> 2) + 4 * (m % 2) + (l16 & 3), seg_hi - 1) * a.r + 8 * g;
-    f32x4 acc[4][4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int m = 0; m < 4; ++m) acc[i][m] = f32x4{0.f, 0.f, 0.f, 0.f};
-    // thread: eight columns of v of rows tid / 8 and tid / 8 + 32
-    const int vk = 8 * (tid & 7), vr = tid >> 3;
-    int vrow[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) vrow[i] = row_at(a.l, a.rows.order, e.y + min(vr + 32 * i, e.z - 1));
-    for (int k0 = 0; k0 < a.r; k0 += UK) {
-      Oct<true> v[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (k0 + vk < a.r) v[i].load(a.v, (size_t)vrow[i] * a.R + seg * a.r + k0 + vk);
-        else v[i].zero();
-      uint4 wv[4][2];
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int m = 0; m < 4; ++m)
-          wv[m][t] = k0 + 32 * t + 8 * g < a.r ? *reinterpret_cast<const uint4*>(w + wrow[m] + k0 + 32 * t) : zero4();
-      if (k0 > 0) __syncthreads();  // the last columns' reads are done
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float f[8] = {v[i].a.x, v[i].a.y, v[i].a.z, v[i].a.w, v[i].b.x, v[i].b.y, v[i].b.z, v[i].b.w};
-        uint4 o[P];
-        split_bf16x8<P>(f, o);
-#pragma unroll
-        for (int p = 0; p < P; ++p) *reinterpret_cast<uint4*>(&vs[p][vr + 32 * i][vk]) = o[p];
-      }
-      __syncthreads();
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        if (k0 + 32 * t >= a.r) break;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int p = P - 1; p >= 0; --p) {
-            const uint4 o = *reinterpret_cast<const uint4*>(&vs[p][16 * i + l16][32 * t + 8 * g]);
-#pragma unroll
-            for (int m = 0; m < 4; ++m) acc[i][m] = mfma16(as_bf16x8(wv[m][t]), as_bf16x8(o), acc[i][m]);
-          }
-      }
-    }
+    const UpOperand<false, WT> w{a, a.w + (size_t)e.x * a.w_a, b, t, lane};
     const float sc = a.scale[e.x];
-    const WaveTile t{lds[wave]};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) t.by_row(i, lane) = y[i].u;
-    wave_order();
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
+    // 16 rows' results onto their base in the tile
+    auto add = [&](int i, const f32x4 (&acc)[4]) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint4& at = t.by_operand(i, 4 * h + g, lane);
         const uint4 o = at;
-        const uint32_t b[4] = {o.x, o.y, o.z, o.w};
+        const uint32_t u[4] = {o.x, o.y, o.z, o.w};
         uint32_t q[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const f32x4& s = acc[i][2 * h + k / 2];
-          q[k] = pack_bf16x2(bf16_to_f32(b[k] & 0xFFFF) + sc * s[2 * (k % 2)],
-                             bf16_to_f32(b[k] >> 16) + sc * s[2 * (k % 2) + 1]);
+          const f32x4& s = acc[2 * h + k / 2];
+          q[k] = pack_bf16x2(bf16_to_f32(u[k] & 0xFFFF) + sc * s[2 * (k % 2)],
+                             bf16_to_f32(u[k] >> 16) + sc * s[2 * (k % 2) + 1]);
         }
         at = make_uint4(q[0], q[1], q[2], q[3]);
       }
+    };
+    auto fill = [&]() {
+      wave_order();
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t.by_row(i, lane) = y[i].u;
+      wave_order();
+    };
+    if constexpr (KS > 0) {
+      bf16x8 wo[KS][4];
+      w.stage(0);
+#pragma unroll
+      for (int s = 0; s < KS; ++s) w.get(0, s, wo[s]);
+      fill();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f32x4 acc[4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) acc[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          bf16x8 v[P];
+          up_rows<P>(a, b.seg, 4 * tile + i, s, lane, v);
+#pragma unroll
+          for (int p = P - 1; p >= 0; --p)
+#pragma unroll
+            for (int m = 0; m < 4; ++m) acc[m] = mfma16(wo[s][m], v[p], acc[m]);
+        }
+        add(i, acc);
+      }
+    } else {
+      f32x4 acc[4][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int m = 0; m < 4; ++m) acc[i][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int k0 = 0; k0 < a.r; k0 += 64) {
+        w.stage(k0);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          if (k0 + 32 * s >= a.r) break;
+          bf16x8 wo[4];
+          w.get(k0, s, wo);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            bf16x8 v[P];
+            up_rows<P>(a, b.seg, 4 * tile + i, k0 / 32 + s, lane, v);
+#pragma unroll
+            for (int p = P - 1; p >= 0; --p)
+#pragma unroll
+              for (int m = 0; m < 4; ++m) acc[i][m] = mfma16(wo[m], v[p], acc[i][m]);
+          }
+        }
+      }
+      fill();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) add(i, acc[i]);
+    }
     wave_order();
 #pragma unroll
     for (int i = 0; i < 8; ++i) y[i].u = t.by_row(i, lane);
@@ -425,63 +495,7 @@ __global__ __launch_bounds__(256) void up_tile_kernel(UpArgs a) {
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i)
-    if (8 * i + (lane >> 3) < e.z && c < seg_hi) y[i].store<STREAM>(a.out, (size_t)row[i] * a.C + c);
-}
-
-// -------------------------------------------------------------- transposes
-// The factors of the adapters in use, transposed: matrix s of an adapter is
-// [rows_s, cols] at element off_s and becomes [cols, rows_s] at the same
-// place.  64 x 64 tiles through LDS.
-struct TransposeArgs {
-  const int* offsets;
-  const uint16_t* in;
-  uint16_t* out;
-  long per;  // elements of an adapter
-  int n_seg, cols;
-  int at[MAX_SEG + 1], tile_at[MAX_SEG + 1];  // rows, 64-row tiles before each matrix
-};
-
-__device__ __forceinline__ void transpose_tile(const TransposeArgs& a, int tile, int ad, uint16_t (&t)[64][66]) {
-  const int ct = (a.cols + 63) / 64;
-  const int rt = tile / ct, c0 = (tile % ct) * 64;
-  int lo = 0, hi = 0, r0 = 0;
-#pragma unroll
-  for (int i = 0; i < MAX_SEG; ++i)
-    if (i < a.n_seg && rt >= a.tile_at[i]) {
-      lo = a.at[i];
-      hi = a.at[i + 1];
-      r0 = 64 * (rt - a.tile_at[i]);
-    }
-  const uint16_t* in = a.in + (size_t)ad * a.per + (size_t)lo * a.cols;
-  uint16_t* out = a.out + (size_t)ad * a.per + (size_t)lo * a.cols;
-  const int rows = hi - lo;
-  for (int i = threadIdx.x; i < 64 * 8; i += 256) {
-    const int r = r0 + i / 8, c = c0 + 8 * (i % 8);
-    if (r < rows && c < a.cols) {
-      const uint4 u = *reinterpret_cast<const uint4*>(in + (size_t)r * a.cols + c);
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-      for (int j = 0; j < 8; ++j) t[8 * (i % 8) + j][i / 8] = (uint16_t)(w[j / 2] >> (16 * (j % 2)));
-    }
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < 64 * 8; i += 256) {
-    const int c = c0 + i / 8, r = r0 + 8 * (i % 8);
-    if (c < a.cols && r < rows) {
-      uint32_t w[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) w[j] = t[i / 8][8 * (i % 8) + 2 * j] | ((uint32_t)t[i / 8][8 * (i % 8) + 2 * j + 1] << 16);
-      *reinterpret_cast<uint4*>(out + (size_t)c * rows + r) = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-  }
-}
-
-__global__ __launch_bounds__(256) void transpose_kernel(TransposeArgs a, int tiles_a, TransposeArgs b, int tiles_b) {
-  __shared__ uint16_t t[64][66];
-  const int ad = blockIdx.y;
-  if (a.offsets[ad] >= a.offsets[ad + 1]) return;
-  if ((int)blockIdx.x < tiles_a) transpose_tile(a, blockIdx.x, ad, t);
-  else if ((int)blockIdx.x < tiles_a + tiles_b) transpose_tile(b, blockIdx.x - tiles_a, ad, t);
+    if (8 * i + (lane >> 3) < e.z && c < b.hi) y[i].store<STREAM>(a.out, (size_t)row[i] * a.C + c);
 }
 
 // ------------------------------------------------------------------ pieces
@@ -491,7 +505,8 @@ __global__ __launch_bounds__(256) void transpose_kernel(TransposeArgs a, int til
 // row order and are read with the transposing LDS load.  U is fp32 in three
 // parts; so is X where it is fp32 (products of parts whose scales differ by
 // 2^-24 or more are left out).  A step's rows are fetched while the last
-// step's are multiplied, and their numbers one step before that.
+// step's are multiplied, and their numbers one step before that (two steps
+// ahead took registers, and with them every third workgroup: no gain).
 constexpr int PC = 256;
 constexpr int LDX = PC + 16;  // LDS row: 16 elements more, so that the four rows of a transposing read lie in different banks
 
@@ -651,10 +666,9 @@ __device__ __forceinline__ void piece(const PieceArgs& a, const PieceJob& q, int
   }
 }
 
-// Rows of a step: 64, or 32 of fp32 (their three parts fill the LDS)
 template <int NA, int NB, bool F32>
-__global__ __launch_bounds__(256) void piece_kernel(PieceArgs a, PieceJob qa, PieceJob qb) {
-  constexpr int NJ = NA > NB ? NA : NB, PR = F32 ? 32 : 64;
+__global__ __launch_bounds__(256, F32 ? 2 : 4) void piece_kernel(PieceArgs a, PieceJob qa, PieceJob qb) {
+  constexpr int NJ = NA > NB ? NA : NB, PR = 32;
   __shared__ __attribute__((aligned(16))) uint16_t xs[Oct<F32>::P * PR * LDX];
   __shared__ __attribute__((aligned(16))) uint16_t us[3 * PR * (NJ * 16 + 16)];
   int4 e;
@@ -712,7 +726,7 @@ struct Plan {
   RowLists l;
   int tm, R;
   int list;
-  size_t v, at, bt, sums, bytes;
+  size_t v, parts, sums, bytes;  // workspace: v, its operands for `up`, partial sums of the gradients
   long slot;
 };
 Plan plan_of(const LowrankDims& d, bool bwd) {
@@ -721,14 +735,15 @@ Plan plan_of(const LowrankDims& d, bool bwd) {
   p.tm = tile_rows(d.T);
   p.R = d.n_seg * d.r;
   p.v = 0;
-  p.bytes = up256(4 * (size_t)d.T * p.R);
-  p.at = p.bt = p.sums = 0;
+  p.parts = bwd ? up256(4 * (size_t)d.T * p.R) : 0;
+  const size_t tiles16 = p.tm == 16 ? p.l.cap(LIST_16) : 4 * (size_t)p.l.cap(LIST_64);
+  const size_t steps = bwd ? (p.R + 31) / 32 : (size_t)d.n_seg * ((d.r + 31) / 32);
+  p.bytes = p.parts + tiles16 * steps * (d.f32 ? 3 : 2) * 1024;
+  p.sums = 0;
   p.slot = (long)p.R * d.K + (long)d.N * d.r;
   p.list = LIST_SHORT;
   if (bwd) {
-    p.at = p.bytes;
-    p.bt = p.at + up256(2 * (size_t)d.n * p.R * d.K);
-    p.sums = p.bt + up256(2 * (size_t)d.n * d.N * d.r);
+    p.sums = p.bytes;
     // column blocks: pieces of a quarter of the rows where they alone nearly
     // fill the chip
     const long blocks = (d.K + PC - 1) / PC + (d.N + PC - 1) / PC;
@@ -757,30 +772,45 @@ void run_down(const Plan& p, DownArgs a, int n_seg, bool f32, hipStream_t st) {
   const dim3 grid(p.tm == 16 ? p.l.cap(LIST_16) : 4 * p.l.cap(LIST_64), n_seg * a.jobs_per_seg);
   groups_of(ng, [&](auto c) {
     constexpr int NG = decltype(c)::value;
-    if (p.tm == 16) {
-      if (f32) hipLaunchKernelGGL((down_kernel<LIST_16, NG, true>), grid, dim3(64 * DW), 0, st, a);
-      else hipLaunchKernelGGL((down_kernel<LIST_16, NG, false>), grid, dim3(64 * DW), 0, st, a);
-    } else {
-      if (f32) hipLaunchKernelGGL((down_kernel<LIST_64, NG, true>), grid, dim3(64 * DW), 0, st, a);
-      else hipLaunchKernelGGL((down_kernel<LIST_64, NG, false>), grid, dim3(64 * DW), 0, st, a);
-    }
+    auto run = [&](auto list, auto f, auto wt) {
+      hipLaunchKernelGGL((down_kernel<decltype(list)::value, NG, decltype(f)::value, decltype(wt)::value>), grid,
+                         dim3(64 * DW), 0, st, a);
+    };
+    auto rows = [&](auto list) {
+      if (!a.whole) run(list, std::false_type{}, std::true_type{});  // (dy is bf16)
+      else if (f32) run(list, std::true_type{}, std::false_type{});
+      else run(list, std::false_type{}, std::false_type{});
+    };
+    if (p.tm == 16) rows(std::integral_constant<int, LIST_16>{});
+    else rows(std::integral_constant<int, LIST_64>{});
   });
 }
 
+template <bool WT>
 void run_up(const Plan& p, UpArgs a, bool f32, hipStream_t st) {
   a.block_at[0] = 0;
   for (int i = 0; i < MAX_SEG; ++i)
     a.block_at[i + 1] = i < a.n_seg ? a.block_at[i] + (a.seg_at[i + 1] - a.seg_at[i] + UC - 1) / UC : a.block_at[i];
   a.blocks = a.block_at[a.n_seg];
-  const dim3 grid((unsigned)p.l.cap(p.tm == 16 ? LIST_16 : LIST_64) * a.blocks);
+  const unsigned tiles = p.l.cap(p.tm == 16 ? LIST_16 : LIST_64);
+  const dim3 grid(tiles * ((a.blocks + 3) / 4));
   if (p.tm == 16) {
-    if (f32) hipLaunchKernelGGL((up_kernel<16, true>), grid, dim3(256), 0, st, a);
-    else hipLaunchKernelGGL((up_kernel<16, false>), grid, dim3(256), 0, st, a);
+    if (f32) hipLaunchKernelGGL((up_kernel<16, true, WT>), grid, dim3(256), 0, st, a);
+    else hipLaunchKernelGGL((up_kernel<16, false, WT>), grid, dim3(256), 0, st, a);
+  } else if (f32) {
+    hipLaunchKernelGGL((up_kernel<64, true, WT>), grid, dim3(256), 0, st, a);
   } else {
-    const bool stream = (size_t)p.l.T * a.C * 2 > STREAM_BYTES;
-    if (f32) hipLaunchKernelGGL((up_kernel<64, true>), grid, dim3(256), 0, st, a);
-    else if (stream) hipLaunchKernelGGL(up_tile_kernel<true>, grid, dim3(256), 0, st, a);
-    else hipLaunchKernelGGL(up_tile_kernel<false>, grid, dim3(256), 0, st, a);
+    auto run = [&](auto stream, auto ks) {
+      hipLaunchKernelGGL((up_tile_kernel<decltype(stream)::value, WT, decltype(ks)::value>),
+                         dim3(tiles * ((a.blocks + UW - 1) / UW)), dim3(64 * UW), 0, st, a);
+    };
+    auto steps = [&](auto stream) {
+      if (a.r <= 32) run(stream, std::integral_constant<int, 1>{});
+      else if (a.r <= 64) run(stream, std::integral_constant<int, 2>{});
+      else run(stream, std::integral_constant<int, 0>{});
+    };
+    if ((size_t)p.l.T * a.C * 2 > STREAM_BYTES) steps(std::true_type{});
+    else steps(std::false_type{});
   }
 }
 
@@ -801,13 +831,6 @@ void blocks_of(PieceJob& q, int per) {
   q.blocks = q.block_at[q.n_seg];
 }
 
-int tiles_of(TransposeArgs& t) {
-  t.tile_at[0] = 0;
-  for (int i = 0; i < MAX_SEG; ++i)
-    t.tile_at[i + 1] = i < t.n_seg ? t.tile_at[i] + (t.at[i + 1] - t.at[i] + 63) / 64 : t.tile_at[i];
-  return t.tile_at[t.n_seg] * ((t.cols + 63) / 64);
-}
-
 }  // namespace
 
 size_t lowrank_ws_bytes(const LowrankDims& d, bool bwd) { return plan_of(d, bwd).bytes; }
@@ -815,7 +838,7 @@ size_t lowrank_ws_bytes(const LowrankDims& d, bool bwd) { return plan_of(d, bwd)
 hipError_t launch_lowrank_fwd(const LowrankDims& d, const LowrankPtrs& q, char* ws, hipStream_t st) {
   ProfScope prof(st, "lowrank.fwd");
   const Plan p = plan_of(d, false);
-  float* v = q.v != nullptr ? q.v : reinterpret_cast<float*>(ws + p.v);
+  uint16_t* parts = reinterpret_cast<uint16_t*>(ws + p.parts);
   DownArgs a{};
   a.l = p.l;
   a.rows = q.rows;
@@ -823,7 +846,10 @@ hipError_t launch_lowrank_fwd(const LowrankDims& d, const LowrankPtrs& q, char* 
   a.lds = d.K;
   a.w = q.A;
   a.w_a = (long)p.R * d.K;
-  a.v = v;
+  a.v = q.v;
+  a.parts = parts;
+  a.vr = d.r;
+  a.nparts = d.f32 ? 3 : 2;
   a.R = p.R;
   a.r = p.R;
   a.whole = true;
@@ -832,9 +858,9 @@ hipError_t launch_lowrank_fwd(const LowrankDims& d, const LowrankPtrs& q, char* 
   UpArgs b{};
   b.l = p.l;
   b.rows = q.rows;
-  b.v = v;
-  b.R = p.R;
+  b.parts = parts;
   b.r = d.r;
+  b.segs = d.n_seg;
   b.w = q.B;
   b.w_a = (long)d.N * d.r;
   b.scale = q.scale;
@@ -843,7 +869,7 @@ hipError_t launch_lowrank_fwd(const LowrankDims& d, const LowrankPtrs& q, char* 
   b.C = d.N;
   b.n_seg = d.n_seg;
   segments(d, b.seg_at);
-  run_up(p, b, d.f32, st);
+  run_up<false>(p, b, d.f32, st);
   return hipGetLastError();
 }
 
@@ -851,36 +877,22 @@ hipError_t launch_lowrank_bwd(const LowrankDims& d, const LowrankGradPtrs& q, ch
   ProfScope prof(st, "lowrank.bwd");
   const Plan p = plan_of(d, true);
   float* u = reinterpret_cast<float*>(ws + p.v);
-  uint16_t* at = reinterpret_cast<uint16_t*>(ws + p.at);
-  uint16_t* bt = reinterpret_cast<uint16_t*>(ws + p.bt);
+  uint16_t* parts = reinterpret_cast<uint16_t*>(ws + p.parts);
   float* sums = reinterpret_cast<float*>(ws + p.sums);
 
   // (without rows only the gradients' zeros are left to write)
   if (d.T > 0 && (q.dx != nullptr || q.dA != nullptr)) {
-    TransposeArgs ta{}, tb{};
-    ta.offsets = tb.offsets = q.rows.offsets;
-    ta.in = q.A;
-    ta.out = at;
-    ta.per = (long)p.R * d.K;
-    ta.n_seg = 1;
-    ta.cols = d.K;
-    one_segment(p.R, ta.at);
-    tb.in = q.B;
-    tb.out = bt;
-    tb.per = (long)d.N * d.r;
-    tb.n_seg = d.n_seg;
-    tb.cols = d.r;
-    segments(d, tb.at);
-    const int na = q.dx != nullptr ? tiles_of(ta) : 0, nb = tiles_of(tb);
-    hipLaunchKernelGGL(transpose_kernel, dim3(na + nb, d.n), dim3(256), 0, st, ta, na, tb, nb);
     DownArgs a{};
     a.l = p.l;
     a.rows = q.rows;
     a.src = q.dy;
     a.lds = d.N;
-    a.w = bt;
+    a.w = q.B;
     a.w_a = (long)d.N * d.r;
-    a.v = u;
+    a.v = q.dA != nullptr ? u : nullptr;
+    a.parts = q.dx != nullptr ? parts : nullptr;
+    a.vr = p.R;
+    a.nparts = d.f32 ? 3 : 2;
     a.R = p.R;
     a.r = d.r;
     a.whole = false;
@@ -891,9 +903,10 @@ hipError_t launch_lowrank_bwd(const LowrankDims& d, const LowrankGradPtrs& q, ch
     UpArgs b{};
     b.l = p.l;
     b.rows = q.rows;
-    b.v = u;
-    b.R = b.r = p.R;
-    b.w = at;
+    b.parts = parts;
+    b.r = p.R;
+    b.segs = 1;
+    b.w = q.A;
     b.w_a = (long)p.R * d.K;
     b.scale = q.scale;
     b.base = q.dx_base;
@@ -901,7 +914,7 @@ hipError_t launch_lowrank_bwd(const LowrankDims& d, const LowrankGradPtrs& q, ch
     b.C = d.K;
     b.n_seg = 1;
     one_segment(d.K, b.seg_at);
-    run_up(p, b, d.f32, st);
+    run_up<true>(p, b, d.f32, st);
   }
   if (q.dA == nullptr && q.dB == nullptr) return hipGetLastError();
 

@@ -102,15 +102,17 @@ __global__ __launch_bounds__(256) void rotate_kernel(RowLists l, RowOrder rows, 
 
 // bf16 rows in tiles of 64: a wave per tile and 64 channels, through its own
 // LDS tile.
+constexpr int RW = 2;  // waves of a workgroup; they share nothing
+
 template <int B, bool STREAM>
-__global__ __launch_bounds__(256) void rotate_tile_kernel(RowLists l, RowOrder rows, const uint16_t* z,
+__global__ __launch_bounds__(64 * RW) void rotate_tile_kernel(RowLists l, RowOrder rows, const uint16_t* z,
                                                           const uint16_t* __restrict__ rops, int N, int which,
                                                           uint16_t* y) {
-  __shared__ __attribute__((aligned(16))) char lds[4][WaveTile::BYTES];
+  __shared__ __attribute__((aligned(16))) char lds[RW][WaveTile::BYTES];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int l16 = lane & 15, g = lane >> 4;
-  const int wgs = (N + 255) / 256;
-  const int n0 = (blockIdx.x % wgs) * 256 + 64 * wave;
+  const int wgs = (N + 64 * RW - 1) / (64 * RW);
+  const int n0 = ((blockIdx.x % wgs) * RW + wave) * 64;
   int4 e;
   if (n0 >= N || !list_entry(l, rows.tiles, LIST_64, blockIdx.x / wgs, e)) return;
   const int c = n0 + 8 * (lane & 7);  // (N is a multiple of 32: a piece is inside or not)
@@ -153,10 +155,13 @@ __global__ __launch_bounds__(256) void rotate_tile_kernel(RowLists l, RowOrder r
 }
 
 // ------------------------------------------------------- sums over the rows
-// One piece of an adapter's rows and 128 channels: dz of every row (dz may be
+// One piece of an adapter's rows and 64 channels: dz of every row (dz may be
 // NULL), S of the channels' blocks.  Tiles of 32 rows go to LDS in row order;
-// S's operands, which run along the rows, are read with the transposing load.
-constexpr int SC = 128, SR = 32, LDS_ROW = SC + 16;
+// S's operands, which run along the rows, are read with the transposing load;
+// a wave takes 16 rows of 32 channels.  Rows are fetched two steps ahead.  (128
+// channels a workgroup: half the workgroups, whose last round left more of the
+// chip idle.)
+constexpr int SC = 64, SR = 32, LDS_ROW = SC + 16;
 
 template <int B, bool F32, bool STREAM>
 __global__ __launch_bounds__(256) void rotate_sums_kernel(RowLists l, RowOrder rows, int list,
@@ -165,10 +170,10 @@ __global__ __launch_bounds__(256) void rotate_sums_kernel(RowLists l, RowOrder r
                                                           const uint16_t* __restrict__ rops, int N, uint16_t* dz,
                                                           float* __restrict__ dq, float* __restrict__ part) {
   constexpr int P = Oct<F32>::P, G = 1024 / (B * B), NP = B * (B - 1) / 2;
-  constexpr int TILE = SR * LDS_ROW;
-  constexpr int GRAD = 3 * G * B * (B + 4);                          // floats of the Cayley gradient
-  constexpr int STEP = (2 + P) * TILE / 2;  // dy, y and dz of a step
-  constexpr int FLOATS = STEP > 4 * 32 * 36 + GRAD ? STEP : 4 * 32 * 36 + GRAD;
+  constexpr int TILE = SR * LDS_ROW, SROW = 36, SF = 2 * 32 * SROW;
+  constexpr int GRAD = 3 * G * B * (B + 4);  // floats of the Cayley gradient
+  constexpr int STEP = (2 + P) * TILE / 2;   // dy, y and dz of a step
+  constexpr int FLOATS = STEP > SF + GRAD ? STEP : SF + GRAD;
   __shared__ __attribute__((aligned(16))) float lds[FLOATS];
   uint16_t* ds = reinterpret_cast<uint16_t*>(lds);
   uint16_t* zs = ds + TILE;
@@ -178,15 +183,16 @@ __global__ __launch_bounds__(256) void rotate_sums_kernel(RowLists l, RowOrder r
   if (!list_entry(l, rows.tiles, list, blockIdx.y, e)) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int l32 = lane & 31, l16 = lane & 15, g = lane >> 5;
-  const int n0 = blockIdx.x * SC, nw = n0 + 32 * wave;
+  const int cg = wave & 1, half = wave >> 1;  // this wave's 32 channels and 16 rows of a step
+  const int n0 = blockIdx.x * SC, nw = n0 + 32 * cg;
   const bool w_ok = nw < N;
-  // thread: 8 channels of rows tid / 16 and tid / 16 + 16
-  const int c = n0 + 8 * (tid & 15), r = tid >> 4;
+  // thread: 8 channels of row tid / 8
+  const int c = n0 + 8 * (tid & 7), r = tid >> 3;
   const bool c_ok = c < N;
 
   if (e.x < 0) {  // rows of the base model: dz = dy, no sums
     if (dz == nullptr || !c_ok || dz == dy) return;
-    for (int i = r; i < e.z; i += 16) {
+    for (int i = r; i < e.z; i += SR) {
       const size_t at = (size_t)row_at(l, rows.order, e.y + i) * N + c;
       *reinterpret_cast<uint4*>(dz + at) = *reinterpret_cast<const uint4*>(dy + at);
     }
@@ -198,107 +204,107 @@ __global__ __launch_bounds__(256) void rotate_sums_kernel(RowLists l, RowOrder r
   f32x16 acc;
 #pragma unroll
   for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
-  Oct<false> d[2];
-  Oct<F32> v[2];
-  int idx[2], next[2];  // rows of the tiles in registers, and of the step after
-  auto number = [&](int r0) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) next[i] = row_at(l, rows.order, e.y + min(r0 + r + 16 * i, e.z - 1));
-  };
-  auto load = [&](int r0) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      idx[i] = next[i];
-      if (r0 + r + 16 * i < e.z && c_ok) {
-        const size_t at = (size_t)idx[i] * N + c;
-        d[i].template load<STREAM>(dy, at);
-        v[i].template load<STREAM>(y, at);
-      } else {
-        d[i].zero();
-        v[i].zero();
-      }
+  // a step's tiles on their way, with their row; the row of the step after;
+  // the row whose dz is in LDS
+  struct Tile {
+    Oct<false> d;
+    Oct<F32> v;
+    int row;
+  } even, odd;
+  int next, zrow = 0;
+  const int at = r * LDS_ROW + 8 * (tid & 7);
+  auto number = [&](int r0) { next = row_at(l, rows.order, e.y + min(r0 + r, e.z - 1)); };
+  auto load = [&](int r0, Tile& t) {
+    t.row = next;
+    if (r0 + r < e.z && c_ok) {
+      const size_t from = (size_t)next * N + c;
+      t.d.template load<STREAM>(dy, from);
+      t.v.template load<STREAM>(y, from);
+    } else {
+      t.d.zero();
+      t.v.zero();
     }
   };
-  int zidx[2] = {0, 0};  // rows of the step whose dz is in LDS
   auto put = [&](int r0) {
-    if (dz != nullptr && c_ok)
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (r0 + r + 16 * i < e.z)
-          store16<STREAM>(dz + (size_t)zidx[i] * N + c,
-                          *reinterpret_cast<const uint4*>(zs + (r + 16 * i) * LDS_ROW + 8 * (tid & 15)));
+    if (dz != nullptr && c_ok && r0 + r < e.z)
+      store16<STREAM>(dz + (size_t)zrow * N + c, *reinterpret_cast<const uint4*>(zs + at));
   };
-  number(0);
-  load(0);
-  number(SR);
-  for (int r0 = 0; r0 < e.z; r0 += SR) {
+  auto step = [&](int r0, Tile& t) {
     __syncthreads();  // the last step's reads are done, its dz complete
     if (r0 > 0) put(r0 - SR);
+    zrow = t.row;
+    *reinterpret_cast<uint4*>(ds + at) = t.d.u;
+    uint4 p[P];
+    t.v.parts(p);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      zidx[i] = idx[i];
-      const int at = (r + 16 * i) * LDS_ROW + 8 * (tid & 15);
-      *reinterpret_cast<uint4*>(ds + at) = d[i].u;
-      uint4 p[P];
-      v[i].parts(p);
-#pragma unroll
-      for (int k = 0; k < P; ++k) *reinterpret_cast<uint4*>(ys + k * TILE + at) = p[k];
-    }
-    if (r0 + SR < e.z) {
-      load(r0 + SR);
-      number(r0 + 2 * SR);
+    for (int k = 0; k < P; ++k) *reinterpret_cast<uint4*>(ys + k * TILE + at) = p[k];
+    if (r0 + 2 * SR < e.z) {
+      load(r0 + 2 * SR, t);
+      number(r0 + 3 * SR);
     }
     __syncthreads();
     if (dz != nullptr) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int at = (16 * i + l16) * LDS_ROW + 32 * wave + 8 * (lane >> 4);
-        Oct<false> x;
-        x.u = *reinterpret_cast<const uint4*>(ds + at);
-        f32x4 o[2];
-        rotate<false>(rot, x, o);
-        *reinterpret_cast<uint4*>(zs + at) = pack8(o);
-      }
+      const int z = (16 * half + l16) * LDS_ROW + 32 * cg + 8 * (lane >> 4);
+      Oct<false> x;
+      x.u = *reinterpret_cast<const uint4*>(ds + z);
+      f32x4 o[2];
+      rotate<false>(rot, x, o);
+      *reinterpret_cast<uint4*>(zs + z) = pack8(o);
     }
     // lane l16 of a 16-lane group: 8 rows of one of its 16 channels
+    const int s = (16 * half + 8 * g + (l16 >> 2)) * LDS_ROW + 32 * cg + 16 * ((lane >> 4) & 1) + 4 * (l16 & 3);
+    const uint2 dl = nn::ds_read_tr16(ds + s), dh = nn::ds_read_tr16(ds + s + 4 * LDS_ROW);
+    const bf16x8 a = as_bf16x8(make_uint4(dl.x, dl.y, dh.x, dh.y));
 #pragma unroll
-    for (int k0 = 0; k0 < SR; k0 += 16) {
-      const int at = (k0 + 8 * g + (l16 >> 2)) * LDS_ROW + 32 * wave + 16 * ((lane >> 4) & 1) + 4 * (l16 & 3);
-      const uint2 dl = nn::ds_read_tr16(ds + at), dh = nn::ds_read_tr16(ds + at + 4 * LDS_ROW);
-      const bf16x8 a = as_bf16x8(make_uint4(dl.x, dl.y, dh.x, dh.y));
-#pragma unroll
-      for (int k = P - 1; k >= 0; --k) {
-        const uint16_t* q = ys + k * TILE + at;
-        const uint2 lo = nn::ds_read_tr16(q), hi = nn::ds_read_tr16(q + 4 * LDS_ROW);
-        acc = mfma32(a, as_bf16x8(make_uint4(lo.x, lo.y, hi.x, hi.y)), acc);
-      }
+    for (int k = P - 1; k >= 0; --k) {
+      const uint16_t* q = ys + k * TILE + s;
+      const uint2 lo = nn::ds_read_tr16(q), hi = nn::ds_read_tr16(q + 4 * LDS_ROW);
+      acc = mfma32(a, as_bf16x8(make_uint4(lo.x, lo.y, hi.x, hi.y)), acc);
     }
+  };
+  number(0);
+  load(0, even);
+  number(SR);
+  load(SR, odd);
+  number(2 * SR);
+  for (int r0 = 0; r0 < e.z; r0 += 2 * SR) {
+    step(r0, even);
+    if (r0 + SR < e.z) step(r0 + SR, odd);
   }
   __syncthreads();
   put((e.z - 1) / SR * SR);
-  // lane: column l32 of S, rows 8 (i / 4) + 4 g + i % 4
+  __syncthreads();
+  // S of the two halves of the rows together.  Lane: column l32 of S, rows
+  // 8 (i / 4) + 4 g + i % 4.
+  float* S = lds;  // [2][32][SROW]
+  auto at_s = [&](int i) { return S + (cg * 32 + 8 * (i / 4) + 4 * g + i % 4) * SROW + l32; };
+  if (half == 1)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) *at_s(i) = acc[i];
+  __syncthreads();
+  if (half == 0)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[i] += *at_s(i);
   if (e.w >= 0) {
-    if (!w_ok) return;
+    if (half == 1 || !w_ok) return;
     float* out = part + ((size_t)min(e.w, RowLists::slots(list) - 1) * (N / 32) + nw / 32) * 1024;
 #pragma unroll
     for (int i = 0; i < 16; ++i) out[(8 * (i / 4) + 4 * g + i % 4) * 32 + l32] = acc[i];
     return;
   }
-  __syncthreads();
-  float* S = lds;  // [4][32][36]
+  if (half == 0)
 #pragma unroll
-  for (int i = 0; i < 16; ++i) S[(wave * 32 + 8 * (i / 4) + 4 * g + i % 4) * 36 + l32] = acc[i];
+    for (int i = 0; i < 16; ++i) *at_s(i) = acc[i];
   const float* R = Rf + (size_t)e.x * N * B;
   float* out = dq + (size_t)e.x * (N / B) * NP;
-  for (int h = 0; h < 4 * 32 / (G * B); ++h) {  // G blocks at a time
+  for (int h = 0; h < SC / (G * B); ++h) {  // G blocks at a time
     const int b0 = n0 / B + h * G, nb = min(G, N / B - b0);
     if (nb <= 0) break;
     __syncthreads();
-    cayley_grad_group<B>(lds + 4 * 32 * 36, R + (size_t)b0 * B * B, out + (size_t)b0 * NP, nb, tid,
-                         [&](int gb, int rr, int cc) {
-                           const int ch = (h * G + gb) * B;  // channel within the 128
-                           return *reinterpret_cast<const float4*>(S + (ch + rr) * 36 + (ch & 31) + cc);
-                         });
+    cayley_grad_group<B>(lds + SF, R + (size_t)b0 * B * B, out + (size_t)b0 * NP, nb, tid, [&](int gb, int rr, int cc) {
+      const int ch = (h * G + gb) * B;  // channel within the 64
+      return *reinterpret_cast<const float4*>(S + (ch + rr) * SROW + (ch & 31) + cc);
+    });
   }
 }
 
@@ -345,13 +351,13 @@ void run_rotate(const RotateDims& d, const RowOrder& rows, bool f32, const void*
   const bool few = d.T <= 1024;
   const unsigned tiles = l.cap(few ? LIST_16 : LIST_64);
   if (!few && !f32) {
-    const dim3 grid(tiles * ((d.N + 255) / 256));
+    const dim3 grid(tiles * ((d.N + 64 * RW - 1) / (64 * RW)));
     const uint16_t* in = static_cast<const uint16_t*>(z);
     uint16_t* out = static_cast<uint16_t*>(y);
     if ((size_t)d.T * d.N * 2 > STREAM_BYTES)
-      hipLaunchKernelGGL((rotate_tile_kernel<B, true>), grid, dim3(256), 0, st, l, rows, in, rops, d.N, which, out);
+      hipLaunchKernelGGL((rotate_tile_kernel<B, true>), grid, dim3(64 * RW), 0, st, l, rows, in, rops, d.N, which, out);
     else
-      hipLaunchKernelGGL((rotate_tile_kernel<B, false>), grid, dim3(256), 0, st, l, rows, in, rops, d.N, which, out);
+      hipLaunchKernelGGL((rotate_tile_kernel<B, false>), grid, dim3(64 * RW), 0, st, l, rows, in, rops, d.N, which, out);
     return;
   }
   const dim3 grid(tiles * ((d.N + 127) / 128));
@@ -360,7 +366,8 @@ void run_rotate(const RotateDims& d, const RowOrder& rows, bool f32, const void*
   else hipLaunchKernelGGL((rotate_kernel<64, B, true>), grid, dim3(256), 0, st, l, rows, z, rops, d.N, which, y);
 }
 
-int sums_list(const RotateDims& d) { return (d.N + SC - 1) / SC >= 128 ? LIST_LONG : LIST_SHORT; }
+// pieces of a quarter of the rows where the channels alone nearly fill the chip
+int sums_list(const RotateDims& d) { return (d.N + SC - 1) / SC >= 256 ? LIST_LONG : LIST_SHORT; }
 
 template <int B>
 hipError_t run_sums(const RotateDims& d, const RowOrder& rows, const uint16_t* dy, const void* y, const float* Rf,
