@@ -146,6 +146,14 @@ __device__ __forceinline__ void tile_rows8(const RowLists& l, const int* order, 
   for (int i = 0; i < 8; ++i) row[i] = __shfl(mine, 8 * i + (lane >> 3));
 }
 
+// The rows of a piece, IDX at a time, in LDS: numbers fetched along with the
+// rows themselves would wait for them (loads come back in order), and a fetch
+// two steps ahead would be none.
+constexpr int IDX = 2048;
+__device__ __forceinline__ void fetch_rows(const RowLists& l, const int* order, int pos, int rows, int* idx) {
+  for (int i = threadIdx.x; i < rows; i += blockDim.x) idx[i] = row_at(l, order, pos + i);
+}
+
 // Rows of more bytes than this are streamed past the caches
 constexpr size_t STREAM_BYTES = (size_t)128 << 20;
 

@@ -438,25 +438,29 @@ __global__ __launch_bounds__(64 * UW) void up_tile_kernel(UpArgs a) {
       wave_order();
     };
     if constexpr (KS > 0) {
-      bf16x8 wo[KS][4];
+      // v of 16 rows is fetched while the 16 before are multiplied
+      bf16x8 wo[KS][4], v[2][KS][P];
+      auto fetch = [&](int i) {
+#pragma unroll
+        for (int s = 0; s < KS; ++s) up_rows<P>(a, b.seg, 4 * tile + i, s, lane, v[i % 2][s]);
+      };
+      fetch(0);
       w.stage(0);
 #pragma unroll
       for (int s = 0; s < KS; ++s) w.get(0, s, wo[s]);
       fill();
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
+        if (i < 3) fetch(i + 1);
         f32x4 acc[4];
 #pragma unroll
         for (int m = 0; m < 4; ++m) acc[m] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int s = 0; s < KS; ++s) {
-          bf16x8 v[P];
-          up_rows<P>(a, b.seg, 4 * tile + i, s, lane, v);
+        for (int s = 0; s < KS; ++s)
 #pragma unroll
           for (int p = P - 1; p >= 0; --p)
 #pragma unroll
-            for (int m = 0; m < 4; ++m) acc[m] = mfma16(wo[s][m], v[p], acc[m]);
-        }
+            for (int m = 0; m < 4; ++m) acc[m] = mfma16(wo[s][m], v[i % 2][s][p], acc[m]);
         add(i, acc);
       }
     } else {
@@ -500,14 +504,13 @@ __global__ __launch_bounds__(64 * UW) void up_tile_kernel(UpArgs a) {
 
 // ------------------------------------------------------------------ pieces
 // Sums over an adapter's rows: out[j][c] = scale sum_rows U[row][j] X[row][c]
-// for 256 columns of X and up to 64 of U, over one piece of the adapter's
+// for 256 columns of X and up to 32 of U, over one piece of the adapter's
 // rows.  Both operands run along the rows here: tiles of PR rows go to LDS in
 // row order and are read with the transposing LDS load.  U is fp32 in three
 // parts; so is X where it is fp32 (products of parts whose scales differ by
-// 2^-24 or more are left out).  A step's rows are fetched while the last
-// step's are multiplied, and their numbers one step before that (two steps
-// ahead took registers, and with them every third workgroup: no gain).
+// 2^-24 or more are left out).  A step's rows are fetched two steps ahead.
 constexpr int PC = 256;
+constexpr int MAXG = 2;               // 16-column groups of U a workgroup: more keep a CU to three workgroups
 constexpr int LDX = PC + 16;  // LDS row: 16 elements more, so that the four rows of a transposing read lie in different banks
 
 struct PieceJob {
@@ -534,7 +537,8 @@ struct PieceArgs {
 };
 
 template <int NJ, int PR, bool F32>
-__device__ __forceinline__ void piece(const PieceArgs& a, const PieceJob& q, int4 e, int job, uint16_t* xs, uint16_t* us) {
+__device__ __forceinline__ void piece(const PieceArgs& a, const PieceJob& q, int4 e, int job, uint16_t* xs, uint16_t* us,
+                                      int* idx) {
   constexpr int PX = Oct<F32>::P, LDU = NJ * 16 + 16;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int l16 = lane & 15, g = lane >> 4;
@@ -566,35 +570,31 @@ __device__ __forceinline__ void piece(const PieceArgs& a, const PieceJob& q, int
   constexpr int UT = 4 * NJ, UR = 256 / UT, UI = (PR + UR - 1) / UR;
   const int uc = 4 * (tid % UT), ur = tid / UT;
   const bool uok = ur < UR && uc < nj;
-  Oct<F32> x[XI];
-  float4 u[UI];
-  int xi[XI], ui[UI];
-  auto number = [&](int r0) {
-#pragma unroll
-    for (int i = 0; i < XI; ++i) xi[i] = row_at(a.l, a.rows.order, e.y + min(r0 + xr + 8 * i, e.z - 1));
-#pragma unroll
-    for (int i = 0; i < UI; ++i) ui[i] = row_at(a.l, a.rows.order, e.y + min(r0 + ur + UR * i, e.z - 1));
-  };
-  auto load = [&](int r0) {
+  struct Tile {
+    Oct<F32> x[XI];
+    float4 u[UI];
+  } even, odd;
+  // rows r0 .. of the `rows` whose numbers are in LDS
+  auto load = [&](int r0, int rows, Tile& t) {
 #pragma unroll
     for (int i = 0; i < XI; ++i) {
-      if (r0 + xr + 8 * i < e.z && xok) x[i].load(q.x, (size_t)xi[i] * q.ldx + xc);
-      else x[i].zero();
+      const int r = r0 + xr + 8 * i;
+      if (r < rows && xok) t.x[i].load(q.x, (size_t)idx[r] * q.ldx + xc);
+      else t.x[i].zero();
     }
 #pragma unroll
-    for (int i = 0; i < UI; ++i)
-      u[i] = r0 + ur + UR * i < e.z && uok ? *reinterpret_cast<const float4*>(q.u + (size_t)ui[i] * a.R + ju + uc)
-                                           : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < UI; ++i) {
+      const int r = r0 + ur + UR * i;
+      t.u[i] = r < rows && uok ? *reinterpret_cast<const float4*>(q.u + (size_t)idx[r] * a.R + ju + uc)
+                               : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
   };
-  number(0);
-  load(0);
-  number(PR);
-  for (int r0 = 0; r0 < e.z; r0 += PR) {
+  auto step = [&](int r0, int rows, Tile& t) {
     __syncthreads();  // the last step's reads are done
 #pragma unroll
     for (int i = 0; i < XI; ++i) {
       uint4 p[PX];
-      x[i].parts(p);
+      t.x[i].parts(p);
 #pragma unroll
       for (int k = 0; k < PX; ++k)
         *reinterpret_cast<uint4*>(xs + (k * PR + xr + 8 * i) * LDX + 8 * (tid & 31)) = p[k];
@@ -602,7 +602,7 @@ __device__ __forceinline__ void piece(const PieceArgs& a, const PieceJob& q, int
 #pragma unroll
     for (int i = 0; i < UI; ++i)
       if (ur < UR && ur + UR * i < PR) {
-        const float v[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+        const float v[4] = {t.u[i].x, t.u[i].y, t.u[i].z, t.u[i].w};
         uint32_t h[4][3];
 #pragma unroll
         for (int k = 0; k < 4; ++k) split_bf16<3>(v[k], h[k]);
@@ -611,11 +611,8 @@ __device__ __forceinline__ void piece(const PieceArgs& a, const PieceJob& q, int
           *reinterpret_cast<uint2*>(us + (p * PR + ur + UR * i) * LDU + uc) =
               make_uint2(h[0][p] | (h[1][p] << 16), h[2][p] | (h[3][p] << 16));
       }
+    if (r0 + 2 * PR < rows) load(r0 + 2 * PR, rows, t);
     __syncthreads();
-    if (r0 + PR < e.z) {
-      load(r0 + PR);
-      number(r0 + 2 * PR);
-    }
 #pragma unroll
     for (int k0 = 0; k0 < PR; k0 += 32) {
       // lane l16 of group g: rows 8 g .. 8 g + 7 of column l16 of 16
@@ -642,6 +639,18 @@ __device__ __forceinline__ void piece(const PieceArgs& a, const PieceJob& q, int
             for (int k = PX - 1; k >= 0; --k)
               if (p + k <= 2) acc[j][c] = mfma16(uv, xv[c][k], acc[j][c]);
         }
+    }
+  };
+  for (int from = 0; from < e.z; from += IDX) {
+    const int rows = min(IDX, e.z - from);
+    __syncthreads();
+    fetch_rows(a.l, a.rows.order, e.y + from, rows, idx);
+    __syncthreads();
+    load(0, rows, even);
+    load(PR, rows, odd);
+    for (int r0 = 0; r0 < rows; r0 += 2 * PR) {
+      step(r0, rows, even);
+      if (r0 + PR < rows) step(r0 + PR, rows, odd);
     }
   }
   // lane: column l16 of 16, rows (of U^T) 4 g .. 4 g + 3 of 16
@@ -671,12 +680,13 @@ __global__ __launch_bounds__(256, F32 ? 2 : 4) void piece_kernel(PieceArgs a, Pi
   constexpr int NJ = NA > NB ? NA : NB, PR = 32;
   __shared__ __attribute__((aligned(16))) uint16_t xs[Oct<F32>::P * PR * LDX];
   __shared__ __attribute__((aligned(16))) uint16_t us[3 * PR * (NJ * 16 + 16)];
+  __shared__ int idx[IDX];
   int4 e;
   if (!list_entry(a.l, a.rows.tiles, a.list, blockIdx.y, e) || e.x < 0) return;
   e.w = min(e.w, RowLists::slots(a.list) - 1);
   const int ja = qa.blocks * qa.njc;
-  if ((int)blockIdx.x < ja) piece<NA, PR, F32>(a, qa, e, blockIdx.x, xs, us);
-  else piece<NB, PR, false>(a, qb, e, blockIdx.x - ja, xs, us);
+  if ((int)blockIdx.x < ja) piece<NA, PR, F32>(a, qa, e, blockIdx.x, xs, us, idx);
+  else piece<NB, PR, false>(a, qb, e, blockIdx.x - ja, xs, us, idx);
 }
 
 // The pieces of an adapter of two or more, in order; zeros for an adapter
@@ -952,16 +962,17 @@ hipError_t launch_lowrank_bwd(const LowrankDims& d, const LowrankGradPtrs& q, ch
   jb.nj = d.r;
   segments(d, jb.seg_at);
   blocks_of(jb, PC);
-  // columns of U a workgroup takes: up to 64, evenly
+  // columns of U a workgroup takes: up to 16 MAXG, evenly
   const int ga = (p.R + 15) / 16, gb = (d.r + 15) / 16;
-  ja.njc = (ga + 3) / 4;
-  jb.njc = (gb + 3) / 4;
+  ja.njc = (ga + MAXG - 1) / MAXG;
+  jb.njc = (gb + MAXG - 1) / MAXG;
   const int na = (ga + ja.njc - 1) / ja.njc, nb = (gb + jb.njc - 1) / jb.njc;
   if (q.dA == nullptr) ja.blocks = 0;
   if (q.dB == nullptr) jb.blocks = 0;
   const dim3 grid(ja.blocks * ja.njc + jb.blocks * jb.njc, p.l.cap(p.list));
-  if (d.T > 0) groups_of(na, [&](auto va) {
-    groups_of(nb, [&](auto vb) {
+  auto pairs_of = [](int g, auto f) { g == 1 ? f(std::integral_constant<int, 1>{}) : f(std::integral_constant<int, MAXG>{}); };
+  if (d.T > 0) pairs_of(na, [&](auto va) {
+    pairs_of(nb, [&](auto vb) {
       constexpr int NA = decltype(va)::value, NB = decltype(vb)::value;
       if (d.f32) hipLaunchKernelGGL((piece_kernel<NA, NB, true>), grid, dim3(256), 0, st, a, ja, jb);
       else hipLaunchKernelGGL((piece_kernel<NA, NB, false>), grid, dim3(256), 0, st, a, ja, jb);

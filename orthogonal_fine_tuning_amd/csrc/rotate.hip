@@ -175,6 +175,8 @@ __global__ __launch_bounds__(256) void rotate_sums_kernel(RowLists l, RowOrder r
   constexpr int STEP = (2 + P) * TILE / 2;   // dy, y and dz of a step
   constexpr int FLOATS = STEP > SF + GRAD ? STEP : SF + GRAD;
   __shared__ __attribute__((aligned(16))) float lds[FLOATS];
+  __shared__ int idx[IDX];
+  const int* rows_order = rows.order;
   uint16_t* ds = reinterpret_cast<uint16_t*>(lds);
   uint16_t* zs = ds + TILE;
   uint16_t* ys = zs + TILE;
@@ -204,20 +206,20 @@ __global__ __launch_bounds__(256) void rotate_sums_kernel(RowLists l, RowOrder r
   f32x16 acc;
 #pragma unroll
   for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
-  // a step's tiles on their way, with their row; the row of the step after;
-  // the row whose dz is in LDS
+  // a step's tiles on their way, with their row; the row whose dz is in LDS
   struct Tile {
     Oct<false> d;
     Oct<F32> v;
     int row;
   } even, odd;
-  int next, zrow = 0;
+  int zrow = -1;
   const int at = r * LDS_ROW + 8 * (tid & 7);
-  auto number = [&](int r0) { next = row_at(l, rows.order, e.y + min(r0 + r, e.z - 1)); };
-  auto load = [&](int r0, Tile& t) {
-    t.row = next;
-    if (r0 + r < e.z && c_ok) {
-      const size_t from = (size_t)next * N + c;
+  // rows r0 .. of the `rows` whose numbers are in LDS
+  auto load = [&](int r0, int rows, Tile& t) {
+    t.row = -1;
+    if (r0 + r < rows && c_ok) {
+      t.row = idx[r0 + r];
+      const size_t from = (size_t)t.row * N + c;
       t.d.template load<STREAM>(dy, from);
       t.v.template load<STREAM>(y, from);
     } else {
@@ -225,23 +227,20 @@ __global__ __launch_bounds__(256) void rotate_sums_kernel(RowLists l, RowOrder r
       t.v.zero();
     }
   };
-  auto put = [&](int r0) {
-    if (dz != nullptr && c_ok && r0 + r < e.z)
+  auto put = [&]() {
+    if (dz != nullptr && zrow >= 0)
       store16<STREAM>(dz + (size_t)zrow * N + c, *reinterpret_cast<const uint4*>(zs + at));
   };
-  auto step = [&](int r0, Tile& t) {
+  auto step = [&](int r0, int rows, Tile& t) {
     __syncthreads();  // the last step's reads are done, its dz complete
-    if (r0 > 0) put(r0 - SR);
+    put();
     zrow = t.row;
     *reinterpret_cast<uint4*>(ds + at) = t.d.u;
     uint4 p[P];
     t.v.parts(p);
 #pragma unroll
     for (int k = 0; k < P; ++k) *reinterpret_cast<uint4*>(ys + k * TILE + at) = p[k];
-    if (r0 + 2 * SR < e.z) {
-      load(r0 + 2 * SR, t);
-      number(r0 + 3 * SR);
-    }
+    if (r0 + 2 * SR < rows) load(r0 + 2 * SR, rows, t);
     __syncthreads();
     if (dz != nullptr) {
       const int z = (16 * half + l16) * LDS_ROW + 32 * cg + 8 * (lane >> 4);
@@ -262,17 +261,20 @@ __global__ __launch_bounds__(256) void rotate_sums_kernel(RowLists l, RowOrder r
       acc = mfma32(a, as_bf16x8(make_uint4(lo.x, lo.y, hi.x, hi.y)), acc);
     }
   };
-  number(0);
-  load(0, even);
-  number(SR);
-  load(SR, odd);
-  number(2 * SR);
-  for (int r0 = 0; r0 < e.z; r0 += 2 * SR) {
-    step(r0, even);
-    if (r0 + SR < e.z) step(r0 + SR, odd);
+  for (int from = 0; from < e.z; from += IDX) {
+    const int rows = min(IDX, e.z - from);
+    __syncthreads();
+    fetch_rows(l, rows_order, e.y + from, rows, idx);
+    __syncthreads();
+    load(0, rows, even);
+    load(SR, rows, odd);
+    for (int r0 = 0; r0 < rows; r0 += 2 * SR) {
+      step(r0, rows, even);
+      if (r0 + SR < rows) step(r0 + SR, rows, odd);
+    }
   }
   __syncthreads();
-  put((e.z - 1) / SR * SR);
+  put();
   __syncthreads();
   // S of the two halves of the rows together.  Lane: column l32 of S, rows
   // 8 (i / 4) + 4 g + i % 4.
