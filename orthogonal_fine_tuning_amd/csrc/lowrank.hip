@@ -754,10 +754,12 @@ Plan plan_of(const LowrankDims& d, bool bwd) {
   p.list = LIST_SHORT;
   if (bwd) {
     p.sums = p.bytes;
-    // column blocks: pieces of a quarter of the rows where they alone nearly
-    // fill the chip
-    const long blocks = (d.K + PC - 1) / PC + (d.N + PC - 1) / PC;
-    p.list = blocks >= 128 ? LIST_LONG : LIST_SHORT;
+    // pieces of a quarter of the rows where the columns alone nearly fill the
+    // chip: fewer partial sums (4096 rows of gate/up, us of the sums and their
+    // join: rank 64, 192 workgroups a piece, quarters 80 + 8, sixteenths 97 +
+    // 24; 8192 rows, rank 16, 86 of them, quarters 98 + 5, sixteenths 87 + 7)
+    const auto jobs = [](int cols, int r) { return (cols + PC - 1) / PC * ((r + 16 * MAXG - 1) / (16 * MAXG)); };
+    p.list = jobs(d.K, p.R) + jobs(d.N, d.r) >= 128 ? LIST_LONG : LIST_SHORT;
     p.bytes = p.sums + up256(4 * (size_t)RowLists::slots(p.list) * p.slot);
   }
   return p;

@@ -155,13 +155,11 @@ __global__ __launch_bounds__(64 * RW) void rotate_tile_kernel(RowLists l, RowOrd
 }
 
 // ------------------------------------------------------- sums over the rows
-// One piece of an adapter's rows and 64 channels: dz of every row (dz may be
+// One piece of an adapter's rows and SC channels: dz of every row (dz may be
 // NULL), S of the channels' blocks.  Tiles of 32 rows go to LDS in row order;
-// S's operands, which run along the rows, are read with the transposing load;
-// a wave takes 16 rows of 32 channels.  Rows are fetched two steps ahead.  (128
-// channels a workgroup: half the workgroups, whose last round left more of the
-// chip idle.)
-constexpr int SC = 64, SR = 32, LDS_ROW = SC + 16;
+// S's operands, which run along the rows, are read with the transposing load.
+// Rows are fetched two steps ahead.
+constexpr int SC = 128, SR = 32, LDS_ROW = SC + 16;
 
 template <int B, bool F32, bool STREAM>
 __global__ __launch_bounds__(256) void rotate_sums_kernel(RowLists l, RowOrder rows, int list,
@@ -170,13 +168,14 @@ __global__ __launch_bounds__(256) void rotate_sums_kernel(RowLists l, RowOrder r
                                                           const uint16_t* __restrict__ rops, int N, uint16_t* dz,
                                                           float* __restrict__ dq, float* __restrict__ part) {
   constexpr int P = Oct<F32>::P, G = 1024 / (B * B), NP = B * (B - 1) / 2;
-  constexpr int TILE = SR * LDS_ROW, SROW = 36, SF = 2 * 32 * SROW;
+  constexpr int TILE = SR * LDS_ROW, SROW = 36, SF = SC * SROW;
   constexpr int GRAD = 3 * G * B * (B + 4);  // floats of the Cayley gradient
   constexpr int STEP = (2 + P) * TILE / 2;   // dy, y and dz of a step
   constexpr int FLOATS = STEP > SF + GRAD ? STEP : SF + GRAD;
+  constexpr int CL = SC / 8, RL = 256 / CL, NL = SR / RL;  // threads along a row, rows at a time, loads of a thread
+  constexpr int CW = SC / 128;                             // groups of 32 channels a wave
   __shared__ __attribute__((aligned(16))) float lds[FLOATS];
   __shared__ int idx[IDX];
-  const int* rows_order = rows.order;
   uint16_t* ds = reinterpret_cast<uint16_t*>(lds);
   uint16_t* zs = ds + TILE;
   uint16_t* ys = zs + TILE;
@@ -185,118 +184,136 @@ __global__ __launch_bounds__(256) void rotate_sums_kernel(RowLists l, RowOrder r
   if (!list_entry(l, rows.tiles, list, blockIdx.y, e)) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int l32 = lane & 31, l16 = lane & 15, g = lane >> 5;
-  const int cg = wave & 1, half = wave >> 1;  // this wave's 32 channels and 16 rows of a step
-  const int n0 = blockIdx.x * SC, nw = n0 + 32 * cg;
-  const bool w_ok = nw < N;
-  // thread: 8 channels of row tid / 8
-  const int c = n0 + 8 * (tid & 7), r = tid >> 3;
+  const int n0 = blockIdx.x * SC;
+  const int c = n0 + 8 * (tid % CL), r = tid / CL;
   const bool c_ok = c < N;
 
   if (e.x < 0) {  // rows of the base model: dz = dy, no sums
     if (dz == nullptr || !c_ok || dz == dy) return;
-    for (int i = r; i < e.z; i += SR) {
+    for (int i = r; i < e.z; i += RL) {
       const size_t at = (size_t)row_at(l, rows.order, e.y + i) * N + c;
       *reinterpret_cast<uint4*>(dz + at) = *reinterpret_cast<const uint4*>(dy + at);
     }
     return;
   }
-  uint4 rot[2] = {zero4(), zero4()};
-  if (dz != nullptr && w_ok) load_rotation<B>(rops + (size_t)e.x * N * B * 2, nw, 1, l16, lane >> 4, rot);
-
-  f32x16 acc;
+  uint4 rot[CW][2];
+  f32x16 acc[CW];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
-  // a step's tiles on their way, with their row; the row whose dz is in LDS
+  for (int w = 0; w < CW; ++w) {
+    rot[w][0] = rot[w][1] = zero4();
+    const int nw = n0 + 32 * (wave * CW + w);
+    if (dz != nullptr && nw < N) load_rotation<B>(rops + (size_t)e.x * N * B * 2, nw, 1, l16, lane >> 4, rot[w]);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[w][i] = 0.0f;
+  }
+  // a step's tiles on their way
   struct Tile {
-    Oct<false> d;
-    Oct<F32> v;
-    int row;
+    Oct<false> d[NL];
+    Oct<F32> v[NL];
+    int row[NL];
   } even, odd;
-  int zrow = -1;
-  const int at = r * LDS_ROW + 8 * (tid & 7);
+  int zrow[NL];  // the rows whose dz is in LDS
+#pragma unroll
+  for (int i = 0; i < NL; ++i) zrow[i] = -1;
+  const int at = r * LDS_ROW + 8 * (tid % CL);
   // rows r0 .. of the `rows` whose numbers are in LDS
   auto load = [&](int r0, int rows, Tile& t) {
-    t.row = -1;
-    if (r0 + r < rows && c_ok) {
-      t.row = idx[r0 + r];
-      const size_t from = (size_t)t.row * N + c;
-      t.d.template load<STREAM>(dy, from);
-      t.v.template load<STREAM>(y, from);
-    } else {
-      t.d.zero();
-      t.v.zero();
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      t.row[i] = -1;
+      if (r0 + r + RL * i < rows && c_ok) {
+        t.row[i] = idx[r0 + r + RL * i];
+        const size_t from = (size_t)t.row[i] * N + c;
+        t.d[i].template load<STREAM>(dy, from);
+        t.v[i].template load<STREAM>(y, from);
+      } else {
+        t.d[i].zero();
+        t.v[i].zero();
+      }
     }
   };
   auto put = [&]() {
-    if (dz != nullptr && zrow >= 0)
-      store16<STREAM>(dz + (size_t)zrow * N + c, *reinterpret_cast<const uint4*>(zs + at));
+    if (dz != nullptr)
+#pragma unroll
+      for (int i = 0; i < NL; ++i)
+        if (zrow[i] >= 0)
+          store16<STREAM>(dz + (size_t)zrow[i] * N + c, *reinterpret_cast<const uint4*>(zs + at + RL * i * LDS_ROW));
   };
   auto step = [&](int r0, int rows, Tile& t) {
     __syncthreads();  // the last step's reads are done, its dz complete
     put();
-    zrow = t.row;
-    *reinterpret_cast<uint4*>(ds + at) = t.d.u;
-    uint4 p[P];
-    t.v.parts(p);
 #pragma unroll
-    for (int k = 0; k < P; ++k) *reinterpret_cast<uint4*>(ys + k * TILE + at) = p[k];
+    for (int i = 0; i < NL; ++i) {
+      zrow[i] = t.row[i];
+      *reinterpret_cast<uint4*>(ds + at + RL * i * LDS_ROW) = t.d[i].u;
+      uint4 p[P];
+      t.v[i].parts(p);
+#pragma unroll
+      for (int k = 0; k < P; ++k) *reinterpret_cast<uint4*>(ys + k * TILE + at + RL * i * LDS_ROW) = p[k];
+    }
     if (r0 + 2 * SR < rows) load(r0 + 2 * SR, rows, t);
     __syncthreads();
-    if (dz != nullptr) {
-      const int z = (16 * half + l16) * LDS_ROW + 32 * cg + 8 * (lane >> 4);
-      Oct<false> x;
-      x.u = *reinterpret_cast<const uint4*>(ds + z);
-      f32x4 o[2];
-      rotate<false>(rot, x, o);
-      *reinterpret_cast<uint4*>(zs + z) = pack8(o);
-    }
-    // lane l16 of a 16-lane group: 8 rows of one of its 16 channels
-    const int s = (16 * half + 8 * g + (l16 >> 2)) * LDS_ROW + 32 * cg + 16 * ((lane >> 4) & 1) + 4 * (l16 & 3);
-    const uint2 dl = nn::ds_read_tr16(ds + s), dh = nn::ds_read_tr16(ds + s + 4 * LDS_ROW);
-    const bf16x8 a = as_bf16x8(make_uint4(dl.x, dl.y, dh.x, dh.y));
 #pragma unroll
-    for (int k = P - 1; k >= 0; --k) {
-      const uint16_t* q = ys + k * TILE + s;
-      const uint2 lo = nn::ds_read_tr16(q), hi = nn::ds_read_tr16(q + 4 * LDS_ROW);
-      acc = mfma32(a, as_bf16x8(make_uint4(lo.x, lo.y, hi.x, hi.y)), acc);
+    for (int w = 0; w < CW; ++w) {
+      const int ch = 32 * (wave * CW + w);
+      if (dz != nullptr) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int z = (16 * i + l16) * LDS_ROW + ch + 8 * (lane >> 4);
+          Oct<false> x;
+          x.u = *reinterpret_cast<const uint4*>(ds + z);
+          f32x4 o[2];
+          rotate<false>(rot[w], x, o);
+          *reinterpret_cast<uint4*>(zs + z) = pack8(o);
+        }
+      }
+      // lane l16 of a 16-lane group: 8 rows of one of its 16 channels
+#pragma unroll
+      for (int k0 = 0; k0 < SR; k0 += 16) {
+        const int q0 = (k0 + 8 * g + (l16 >> 2)) * LDS_ROW + ch + 16 * ((lane >> 4) & 1) + 4 * (l16 & 3);
+        const uint2 dl = nn::ds_read_tr16(ds + q0), dh = nn::ds_read_tr16(ds + q0 + 4 * LDS_ROW);
+        const bf16x8 a = as_bf16x8(make_uint4(dl.x, dl.y, dh.x, dh.y));
+#pragma unroll
+        for (int k = P - 1; k >= 0; --k) {
+          const uint16_t* q = ys + k * TILE + q0;
+          const uint2 lo = nn::ds_read_tr16(q), hi = nn::ds_read_tr16(q + 4 * LDS_ROW);
+          acc[w] = mfma32(a, as_bf16x8(make_uint4(lo.x, lo.y, hi.x, hi.y)), acc[w]);
+        }
+      }
     }
   };
   for (int from = 0; from < e.z; from += IDX) {
-    const int rows = min(IDX, e.z - from);
+    const int count = min(IDX, e.z - from);
     __syncthreads();
-    fetch_rows(l, rows_order, e.y + from, rows, idx);
+    fetch_rows(l, rows.order, e.y + from, count, idx);
     __syncthreads();
-    load(0, rows, even);
-    load(SR, rows, odd);
-    for (int r0 = 0; r0 < rows; r0 += 2 * SR) {
-      step(r0, rows, even);
-      if (r0 + SR < rows) step(r0 + SR, rows, odd);
+    load(0, count, even);
+    load(SR, count, odd);
+    for (int r0 = 0; r0 < count; r0 += 2 * SR) {
+      step(r0, count, even);
+      if (r0 + SR < count) step(r0 + SR, count, odd);
     }
   }
   __syncthreads();
   put();
-  __syncthreads();
-  // S of the two halves of the rows together.  Lane: column l32 of S, rows
-  // 8 (i / 4) + 4 g + i % 4.
-  float* S = lds;  // [2][32][SROW]
-  auto at_s = [&](int i) { return S + (cg * 32 + 8 * (i / 4) + 4 * g + i % 4) * SROW + l32; };
-  if (half == 1)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) *at_s(i) = acc[i];
-  __syncthreads();
-  if (half == 0)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) acc[i] += *at_s(i);
+  // lane: column l32 of S, rows 8 (i / 4) + 4 g + i % 4
   if (e.w >= 0) {
-    if (half == 1 || !w_ok) return;
-    float* out = part + ((size_t)min(e.w, RowLists::slots(list) - 1) * (N / 32) + nw / 32) * 1024;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) out[(8 * (i / 4) + 4 * g + i % 4) * 32 + l32] = acc[i];
+    for (int w = 0; w < CW; ++w) {
+      const int nw = n0 + 32 * (wave * CW + w);
+      if (nw >= N) break;
+      float* out = part + ((size_t)min(e.w, RowLists::slots(list) - 1) * (N / 32) + nw / 32) * 1024;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) out[(8 * (i / 4) + 4 * g + i % 4) * 32 + l32] = acc[w][i];
+    }
     return;
   }
-  if (half == 0)
+  __syncthreads();
+  float* S = lds;  // [SC][SROW]
 #pragma unroll
-    for (int i = 0; i < 16; ++i) *at_s(i) = acc[i];
+  for (int w = 0; w < CW; ++w)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) S[(32 * (wave * CW + w) + 8 * (i / 4) + 4 * g + i % 4) * SROW + l32] = acc[w][i];
   const float* R = Rf + (size_t)e.x * N * B;
   float* out = dq + (size_t)e.x * (N / B) * NP;
   for (int h = 0; h < SC / (G * B); ++h) {  // G blocks at a time
@@ -304,7 +321,7 @@ __global__ __launch_bounds__(256) void rotate_sums_kernel(RowLists l, RowOrder r
     if (nb <= 0) break;
     __syncthreads();
     cayley_grad_group<B>(lds + SF, R + (size_t)b0 * B * B, out + (size_t)b0 * NP, nb, tid, [&](int gb, int rr, int cc) {
-      const int ch = (h * G + gb) * B;  // channel within the 64
+      const int ch = (h * G + gb) * B;  // channel within the SC
       return *reinterpret_cast<const float4*>(S + (ch + rr) * SROW + (ch & 31) + cc);
     });
   }
@@ -369,7 +386,7 @@ void run_rotate(const RotateDims& d, const RowOrder& rows, bool f32, const void*
 }
 
 // pieces of a quarter of the rows where the channels alone nearly fill the chip
-int sums_list(const RotateDims& d) { return (d.N + SC - 1) / SC >= 256 ? LIST_LONG : LIST_SHORT; }
+int sums_list(const RotateDims& d) { return (d.N + SC - 1) / SC >= 16384 / SC ? LIST_LONG : LIST_SHORT; }
 
 template <int B>
 hipError_t run_sums(const RotateDims& d, const RowOrder& rows, const uint16_t* dy, const void* y, const float* Rf,
