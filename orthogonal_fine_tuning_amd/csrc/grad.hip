@@ -4,8 +4,8 @@
 //   sumsq = sum over all tensors of g^2,  norm = sqrt(sumsq),
 //   coef = min(1, max_norm / (norm + 1e-6)),  out = coef g
 // One read for the sum, one read and one write for the clipping: bound by
-// those bytes.  The tensors' addresses travel in the kernel's arguments, 100
-// to a launch, so that nothing has to be copied to the GPU and a captured
+// those bytes.  The tensors' addresses travel in the kernel's arguments, up to
+// 100 to a launch (or, for the host's sake, 12), so that nothing has to be copied to the GPU and a captured
 // call replays.  Squares are added in fp64 (two instructions an element, far
 // below what the reads take): no finite gradient overflows, and the order of
 // the chunks does not show in fp32.
@@ -18,7 +18,6 @@
 namespace oft {
 namespace {
 
-constexpr int ITEMS = 100;
 constexpr float EPS = 1e-6f;
 // Gradients of more bytes than this in all are streamed past the caches;
 // fewer are still there, in part, when the clipping reads them again.
@@ -29,10 +28,12 @@ struct Item {
   void* out;
   int64_t n;
 };
+template <int N>
 struct Items {
-  int first[128];  // chunk of the launch at which each tensor starts; INT_MAX past the last
+  static constexpr int MOST = N, WAVES = (N + 63) / 64;
+  int first[64 * WAVES];  // chunk of the launch at which each tensor starts; INT_MAX past the last
   int count, chunks, chunk, pad;  // chunk: elements of one
-  Item at[ITEMS];
+  Item at[N];
 };
 
 // 16 bytes from an address that only its 4-byte alignment is known of
@@ -51,10 +52,13 @@ __device__ __forceinline__ void store16(u32x4* p, const u32x4& v) {
 // The tensor of a chunk: the arguments lie in host memory, far away, so all
 // the tensors' starts are looked at at once instead of by halves (585 MB in 48
 // tensors: 141 us for the sum by halves).
-__device__ __forceinline__ int item_of(const Items& s, int chunk) {
+template <int N>
+__device__ __forceinline__ int item_of(const Items<N>& s, int chunk) {
   const int lane = threadIdx.x & 63;
-  const int at = __popcll(__ballot(s.first[lane] <= chunk)) + __popcll(__ballot(s.first[64 + lane] <= chunk)) - 1;
-  return __builtin_amdgcn_readfirstlane(at);
+  int before = 0;
+#pragma unroll
+  for (int i = 0; i < Items<N>::WAVES; ++i) before += __popcll(__ballot(s.first[64 * i + lane] <= chunk));
+  return __builtin_amdgcn_readfirstlane(before - 1);
 }
 
 template <bool F32>
@@ -136,8 +140,8 @@ __device__ __forceinline__ double block_sum(double v) {
   return s;
 }
 
-template <bool F32, bool STREAM>
-__global__ __launch_bounds__(256) void sumsq_kernel(Items s, double* __restrict__ part) {
+template <bool F32, bool STREAM, int N>
+__global__ __launch_bounds__(256) void sumsq_kernel(Items<N> s, double* __restrict__ part) {
   const int i = item_of(s, blockIdx.x);
   const Item& t = s.at[i];
   const int64_t lo = (int64_t)((int)blockIdx.x - s.first[i]) * s.chunk;
@@ -155,7 +159,7 @@ __global__ __launch_bounds__(1024) void sumsq_join_kernel(const double* __restri
 
 // few elements in all: one workgroup, one launch
 template <bool F32>
-__global__ __launch_bounds__(256) void sumsq_few_kernel(Items s, double* __restrict__ sumsq) {
+__global__ __launch_bounds__(256) void sumsq_few_kernel(Items<12> s, double* __restrict__ sumsq) {
   double v = 0.0;
   for (int i = 0; i < s.count; ++i) v += sum_range<F32, false>(s.at[i].g, 0, s.at[i].n);
   v = block_sum<256>(v);
@@ -212,8 +216,8 @@ __device__ __forceinline__ void scale_range(const void* g, void* out, int64_t lo
   if (tid < E && t < hi) one(t);
 }
 
-template <bool F32, bool STREAM>
-__global__ __launch_bounds__(256) void clip_kernel(Items s, const double* __restrict__ sumsq, float max_norm,
+template <bool F32, bool STREAM, int N>
+__global__ __launch_bounds__(256) void clip_kernel(Items<N> s, const double* __restrict__ sumsq, float max_norm,
                                                    float* __restrict__ stats) {
   float norm;
   const float c = coefficient(sumsq, max_norm, norm);
@@ -241,23 +245,29 @@ constexpr int64_t FEW = 16384;
 
 // f(items) for each launch's worth of tensors that are not empty, and the
 // chunks before it
-template <class F>
-void launches(const GradList& l, void* const* out, F f) {
-  Items s;
+template <int N, class F>
+void launches_of(const GradList& l, void* const* out, F f) {
+  Items<N> s;
   s.chunk = chunk_of(l.m, l.numel);
   int before = 0;
   for (int i = 0; i < l.m;) {
     s.count = s.chunks = 0;
-    for (; i < l.m && s.count < ITEMS; ++i) {
+    for (; i < l.m && s.count < N; ++i) {
       if (l.numel[i] == 0) continue;
       s.first[s.count] = s.chunks;
       s.at[s.count++] = Item{l.grads[i], out != nullptr ? out[i] : nullptr, l.numel[i]};
       s.chunks += (int)((l.numel[i] + s.chunk - 1) / s.chunk);
     }
-    for (int k = s.count; k < 128; ++k) s.first[k] = 0x7FFFFFFF;
+    for (int k = s.count; k < 64 * Items<N>::WAVES; ++k) s.first[k] = 0x7FFFFFFF;
     if (s.count > 0) f(s, before);
     before += s.chunks;
   }
+}
+
+template <class F>
+void launches(const GradList& l, void* const* out, F f) {
+  if (l.m <= 12) launches_of<12>(l, out, f);
+  else launches_of<100>(l, out, f);
 }
 
 int64_t chunks_of(int m, const int64_t* numel) {
@@ -272,7 +282,7 @@ int64_t total_of(const GradList& l) {
   for (int i = 0; i < l.m; ++i) total += l.numel[i];
   return total;
 }
-bool few(const GradList& l) { return l.m <= 16 && total_of(l) <= FEW; }
+bool few(const GradList& l) { return l.m <= 12 && total_of(l) <= FEW; }
 bool streamed(const GradList& l) { return total_of(l) * (l.f32 ? 4 : 2) > STREAM_BYTES; }
 
 template <class F>
@@ -289,7 +299,7 @@ hipError_t launch_grad_sumsq(const GradList& l, double* sumsq, char* ws, hipStre
   ProfScope prof(st, "grad.sumsq");
   if (few(l)) {
     bool any = false;
-    launches(l, nullptr, [&](const Items& s, int) {
+    launches_of<12>(l, nullptr, [&](const Items<12>& s, int) {
       any = true;
       if (l.f32) hipLaunchKernelGGL(sumsq_few_kernel<true>, dim3(1), dim3(256), 0, st, s, sumsq);
       else hipLaunchKernelGGL(sumsq_few_kernel<false>, dim3(1), dim3(256), 0, st, s, sumsq);
@@ -297,9 +307,10 @@ hipError_t launch_grad_sumsq(const GradList& l, double* sumsq, char* ws, hipStre
     if (any) return hipGetLastError();
   }
   double* part = reinterpret_cast<double*>(ws);
-  launches(l, nullptr, [&](const Items& s, int before) {
+  launches(l, nullptr, [&](const auto& s, int before) {
+    constexpr int N = std::remove_reference_t<decltype(s)>::MOST;
     choose(l.f32, streamed(l), [&](auto f32, auto stream) {
-      hipLaunchKernelGGL((sumsq_kernel<decltype(f32)::value, decltype(stream)::value>), dim3(s.chunks), dim3(256), 0, st,
+      hipLaunchKernelGGL((sumsq_kernel<decltype(f32)::value, decltype(stream)::value, N>), dim3(s.chunks), dim3(256), 0, st,
                          s, part + before);
     });
   });
@@ -311,18 +322,19 @@ hipError_t launch_grad_clip(const GradList& l, const double* sumsq, float max_no
                             hipStream_t st) {
   ProfScope prof(st, "grad.clip");
   bool first = true;
-  auto run = [&](const Items& s, int) {
+  auto run = [&](const auto& s, int) {
+    constexpr int N = std::remove_reference_t<decltype(s)>::MOST;
     float* to = first ? stats : nullptr;
     first = false;
     const dim3 grid(s.chunks > 0 ? s.chunks : 1);
     choose(l.f32, streamed(l), [&](auto f32, auto stream) {
-      hipLaunchKernelGGL((clip_kernel<decltype(f32)::value, decltype(stream)::value>), grid, dim3(256), 0, st, s, sumsq,
+      hipLaunchKernelGGL((clip_kernel<decltype(f32)::value, decltype(stream)::value, N>), grid, dim3(256), 0, st, s, sumsq,
                          max_norm, to);
     });
   };
   launches(l, out, run);
   if (first) {  // nothing to scale: the norm and coefficient alone
-    Items s;
+    Items<12> s;
     s.count = s.chunks = 0;
     s.chunk = 1;
     run(s, 0);

@@ -26,10 +26,10 @@ namespace oft {
 namespace {
 
 // ------------------------------------------------------------------- down
-// v[row][j] = sum_k src[row][k] W[j][k]: a workgroup per 16 rows and up to 64
+// v[row][j] = sum_k src[row][k] W[j][k]: a workgroup per 16 XT rows and up to 64
 // output columns of one segment (of all, where the rows of src are whole).
-// Its eight waves deal the columns of src among them, 64 at a time, so that a
-// long contraction is as many loads in flight and no second launch has to add
+// Its DW waves deal the columns of src among them, 64 at a time, so that a long
+// contraction is as many loads in flight and no second launch has to add
 // partial sums; the waves' sums are added through LDS in their order.  A
 // wave's step goes through its own part of LDS, from loads whose lanes run
 // along the rows to operands whose lanes run across them.
@@ -50,28 +50,36 @@ struct DownArgs {
   int vr, nparts;    // columns of v that one product of `up` takes; parts
   int R;             // columns of v
   int r, per;        // r output columns a segment (R when whole), `per` a job
-  int jobs_per_seg;
+  int jobs_per_seg, jobs;
   bool whole;
   int K;
   int seg_at[MAX_SEG + 1];
 };
-constexpr int DW = 8;  // waves
 
-// LIST: LIST_16, or LIST_64 in four parts; WT: W is stored transposed
-template <int LIST, int NG, bool F32, bool WT>
+// LIST: LIST_16, or LIST_64 in 4 / XT parts; WT: W is stored transposed
+template <int LIST, int XT, int DW, int NG, bool F32, bool WT>
 __global__ __launch_bounds__(64 * DW) void down_kernel(DownArgs a) {
-  constexpr int P = Oct<F32>::P, SUB = LIST == LIST_16 ? 1 : 4;
-  constexpr int XB = F32 ? 256 : 128, XI = 16 * XB / 1024;  // bytes of a row of x and step, loads of a lane
+  constexpr int P = Oct<F32>::P, SUB = LIST == LIST_16 ? 1 : 4 / XT, ROWS = 16 * XT;
+  constexpr int XB = F32 ? 256 : 128, XI = ROWS * XB / 1024;  // bytes of a row of x and step, loads of a lane
   constexpr int WROW = 32 * NG + 16;                        // LDS row of a transposed step: 16 bytes apart in banks
-  constexpr int WAVE = 16 * XB + (WT ? 64 * WROW : 16 * NG * 128);  // bytes of a wave's step
+  constexpr int WAVE = ROWS * XB + (WT ? 64 * WROW : 16 * NG * 128);  // bytes of a wave's step
+  static_assert(XT == 1 || (!F32 && LIST == LIST_64), "rows of a tile");
+  static_assert(DW * WAVE >= DW * XT * NG * 1024, "the sums take the steps' place");
   __shared__ __attribute__((aligned(16))) char lds[DW * WAVE];
+  // Tiles in runs to the eight XCDs (workgroup b runs on XCD b % 8): the
+  // workgroups that share an L2 read few adapters' W.  (8192 rows of 16
+  // adapters, K 2560, 64 columns of v: 18 us, 20 with tile b on workgroup b.)
   int4 e;
-  if (!list_entry(a.l, a.rows.tiles, LIST, blockIdx.x / SUB, e)) return;
-  e.y += 16 * (blockIdx.x % SUB);
-  e.z -= 16 * (blockIdx.x % SUB);
+  const int tiles = min(a.rows.tiles[LIST], a.l.cap(LIST)) * SUB, total = tiles * a.jobs;
+  if ((int)blockIdx.x >= total) return;
+  const int xcd = blockIdx.x & 7;
+  const int at = xcd * (total >> 3) + min(xcd, total & 7) + (int)(blockIdx.x >> 3);
+  const int job = at % a.jobs, tile = at / a.jobs;
+  if (!list_entry(a.l, a.rows.tiles, LIST, tile / SUB, e)) return;
+  e.y += ROWS * (tile % SUB);
+  e.z -= ROWS * (tile % SUB);
   if (e.z <= 0) return;
-  e.z = min(e.z, 16);
-  const int job = blockIdx.y;
+  e.z = min(e.z, ROWS);
   int seg = 0, col0 = 0, len = a.K;
   if (!a.whole) {
     seg = job / a.jobs_per_seg;
@@ -99,7 +107,7 @@ __global__ __launch_bounds__(64 * DW) void down_kernel(DownArgs a) {
     }
     const int xk = (F32 ? 4 : 8) * (lane % XL), wk = 8 * (lane & 7);
     char* xs = lds + wave * WAVE;
-    char* ws = xs + 16 * XB;
+    char* ws = xs + ROWS * XB;
     // chunks of a row exchanged as in WaveTile, over the 256 bytes of two rows
     // of bf16 or one of fp32
     auto xput = [&](int i) {
@@ -108,9 +116,11 @@ __global__ __launch_bounds__(64 * DW) void down_kernel(DownArgs a) {
     };
     auto wput = [&](int r, int c) { return reinterpret_cast<uint4*>(ws + r * 128 + 16 * (c ^ ((r >> 1) & 7))); };
 
-    f32x4 acc[NG];
+    f32x4 acc[XT][NG];
 #pragma unroll
-    for (int j = 0; j < NG; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < XT; ++i)
+#pragma unroll
+      for (int j = 0; j < NG; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     uint4 x[XI], wv[2 * NG];
     // (segments are multiples of 16: a lane's columns are inside or not)
     auto load = [&](int s) {
@@ -132,7 +142,7 @@ __global__ __launch_bounds__(64 * DW) void down_kernel(DownArgs a) {
     const int steps = (len + 63) / 64;
     int s = wave;
     if (s < steps) load(s);
-    for (; s < steps; s += DW) {
+    for (; s < steps; s += DW) {  // (a fetch of two steps ahead was no faster)
       wave_order();  // the last step's reads are before these writes
 #pragma unroll
       for (int i = 0; i < XI; ++i) *xput(i) = x[i];
@@ -146,15 +156,19 @@ __global__ __launch_bounds__(64 * DW) void down_kernel(DownArgs a) {
       wave_order();
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        uint4 xp[P];
-        Oct<F32> o;
-        if constexpr (F32) {
-          o.a = *reinterpret_cast<const float4*>(xs + l16 * XB + 16 * ((8 * t + 2 * g) ^ l16));
-          o.b = *reinterpret_cast<const float4*>(xs + l16 * XB + 16 * ((8 * t + 2 * g + 1) ^ l16));
-        } else {
-          o.u = *reinterpret_cast<const uint4*>(xs + l16 * XB + 16 * ((4 * t + g) ^ ((l16 >> 1) & 7)));
+        uint4 xp[XT][P];
+#pragma unroll
+        for (int i = 0; i < XT; ++i) {
+          const char* row = xs + (16 * i + l16) * XB;
+          Oct<F32> o;
+          if constexpr (F32) {
+            o.a = *reinterpret_cast<const float4*>(row + 16 * ((8 * t + 2 * g) ^ l16));
+            o.b = *reinterpret_cast<const float4*>(row + 16 * ((8 * t + 2 * g + 1) ^ l16));
+          } else {
+            o.u = *reinterpret_cast<const uint4*>(row + 16 * ((4 * t + g) ^ ((l16 >> 1) & 7)));
+          }
+          o.parts(xp[i]);
         }
-        o.parts(xp);
 #pragma unroll
         for (int j = 0; j < NG; ++j) {
           bf16x8 wj;
@@ -167,50 +181,55 @@ __global__ __launch_bounds__(64 * DW) void down_kernel(DownArgs a) {
             wj = as_bf16x8(*wput(16 * j + l16, 4 * t + g));
           }
 #pragma unroll
-          for (int p = P - 1; p >= 0; --p) acc[j] = mfma16(wj, as_bf16x8(xp[p]), acc[j]);
+          for (int i = 0; i < XT; ++i)
+#pragma unroll
+            for (int p = P - 1; p >= 0; --p) acc[i][j] = mfma16(wj, as_bf16x8(xp[i][p]), acc[i][j]);
         }
       }
     }
     __syncthreads();  // the sums take the steps' place
-    float4* red = reinterpret_cast<float4*>(lds);  // [wave][NG][64]
+    float4* red = reinterpret_cast<float4*>(lds);  // [wave][XT NG][64]
 #pragma unroll
-    for (int j = 0; j < NG; ++j)
-      red[(wave * NG + j) * 64 + lane] = make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
+    for (int i = 0; i < XT; ++i)
+#pragma unroll
+      for (int j = 0; j < NG; ++j)
+        red[((wave * XT + i) * NG + j) * 64 + lane] = make_float4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]);
     __syncthreads();
   }
-  // lane: row l16, four consecutive output columns of 16; rows without an
-  // adapter have v = 0
-  if (wave >= NG) return;
-  const int c0 = 16 * wave + 4 * g;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (e.x >= 0) {
-    const float4* red = reinterpret_cast<const float4*>(lds);
+  // lane: row l16 of 16, four consecutive output columns of 16; rows without
+  // an adapter have v = 0
+  for (int it = wave; it < XT * NG; it += DW) {
+    const int i = it / NG, c0 = 16 * (it % NG) + 4 * g, r = 16 * i + l16;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (e.x >= 0) {
+      const float4* red = reinterpret_cast<const float4*>(lds);
 #pragma unroll
-    for (int k = 0; k < DW; ++k) {
-      const float4 t = red[(k * NG + wave) * 64 + lane];
-      o.x += t.x;
-      o.y += t.y;
-      o.z += t.z;
-      o.w += t.w;
+      for (int k = 0; k < DW; ++k) {
+        const float4 t = red[(k * XT * NG + it) * 64 + lane];
+        o.x += t.x;
+        o.y += t.y;
+        o.z += t.z;
+        o.w += t.w;
+      }
     }
-  }
-  if (c0 >= nj) return;  // (ranks are multiples of 8)
-  const int col = seg * a.r + jw + c0;
-  if (a.v != nullptr && l16 < e.z)
-    *reinterpret_cast<float4*>(a.v + (size_t)row_at(a.l, a.rows.order, e.y + l16) * a.R + col) = o;
-  if (a.parts != nullptr && e.x >= 0) {
-    const int s = col / a.vr, k = col % a.vr, steps = (a.vr + 31) / 32;
-    uint16_t* out = a.parts + (((size_t)blockIdx.x * (a.R / a.vr) + s) * steps + k / 32) * a.nparts * 512 +
-                    ((k % 32) / 8 * 16 + l16) * 8 + k % 8;
-    uint32_t h[4][3];
-    split_bf16<3>(o.x, h[0]);
-    split_bf16<3>(o.y, h[1]);
-    split_bf16<3>(o.z, h[2]);
-    split_bf16<3>(o.w, h[3]);
+    if (c0 >= nj) continue;  // (ranks are multiples of 8)
+    const int col = seg * a.r + jw + c0;
+    if (a.v != nullptr && r < e.z)
+      *reinterpret_cast<float4*>(a.v + (size_t)row_at(a.l, a.rows.order, e.y + r) * a.R + col) = o;
+    if (a.parts != nullptr && e.x >= 0) {
+      const int s = col / a.vr, k = col % a.vr, steps = (a.vr + 31) / 32;
+      uint16_t* out = a.parts + ((((size_t)tile * XT + i) * (a.R / a.vr) + s) * steps + k / 32) * a.nparts * 512 +
+                      ((k % 32) / 8 * 16 + l16) * 8 + k % 8;
+      uint32_t h[4][3];
+      split_bf16<3>(o.x, h[0]);
+      split_bf16<3>(o.y, h[1]);
+      split_bf16<3>(o.z, h[2]);
+      split_bf16<3>(o.w, h[3]);
 #pragma unroll
-    for (int p = 0; p < 3; ++p)
-      if (p < a.nparts)
-        *reinterpret_cast<uint2*>(out + p * 512) = make_uint2(h[0][p] | (h[1][p] << 16), h[2][p] | (h[3][p] << 16));
+      for (int p = 0; p < 3; ++p)
+        if (p < a.nparts)
+          *reinterpret_cast<uint2*>(out + p * 512) = make_uint2(h[0][p] | (h[1][p] << 16), h[2][p] | (h[3][p] << 16));
+    }
   }
 }
 
@@ -314,6 +333,18 @@ __global__ __launch_bounds__(256) void up_kernel(UpArgs a) {
   int4 e;
   if (cb >= a.blocks || !list_entry(a.l, a.rows.tiles, TM == 16 ? LIST_16 : LIST_64, tile, e)) return;
   const UpBlock b = up_block(a, cb);
+  const UpOperand<F32, WT> w{a, a.w + (size_t)max(e.x, 0) * a.w_a, b, WaveTile{lds[WT ? wave : 0]}, lane};
+  // what does not wait for the rows' numbers first
+  bf16x8 wo[4], v[XG][P];
+  auto operands = [&](int k0, int s) {
+    w.get(k0, s, wo);
+#pragma unroll
+    for (int i = 0; i < XG; ++i) up_rows<P>(a, b.seg, tile * XG + i, k0 / 32 + s, lane, v[i]);
+  };
+  if (e.x >= 0) {
+    w.stage(0);
+    operands(0, 0);
+  }
   // column of piece h within the 64
   auto col = [&](int h) { return F32 ? 16 * h + 4 * g : 32 * h + 8 * g; };
   uint4 y[XG][H];
@@ -341,30 +372,23 @@ __global__ __launch_bounds__(256) void up_kernel(UpArgs a) {
       for (int h = 0; h < H; ++h) store(i, h, y[i][h]);
     return;
   }
-  const UpOperand<F32, WT> w{a, a.w + (size_t)e.x * a.w_a, b, WaveTile{lds[WT ? wave : 0]}, lane};
   const float sc = a.scale[e.x];
   f32x4 acc[XG][4];
 #pragma unroll
   for (int i = 0; i < XG; ++i)
 #pragma unroll
     for (int m = 0; m < 4; ++m) acc[i][m] = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (int k0 = 0; k0 < a.r; k0 += 64) {
-    w.stage(k0);
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      if (k0 + 32 * s >= a.r) break;
-      bf16x8 wo[4];
-      w.get(k0, s, wo);
-#pragma unroll
-      for (int i = 0; i < XG; ++i) {
-        bf16x8 v[P];
-        up_rows<P>(a, b.seg, tile * XG + i, k0 / 32 + s, lane, v);
-#pragma unroll
-        for (int p = P - 1; p >= 0; --p)
-#pragma unroll
-          for (int m = 0; m < 4; ++m) acc[i][m] = mfma16(wo[m], v[p], acc[i][m]);
-      }
+  for (int k = 0; k < a.r; k += 32) {
+    if (k > 0) {
+      if (k % 64 == 0) w.stage(k);
+      operands(k & ~63, k / 32 % 2);
     }
+#pragma unroll
+    for (int i = 0; i < XG; ++i)
+#pragma unroll
+      for (int p = P - 1; p >= 0; --p)
+#pragma unroll
+        for (int m = 0; m < 4; ++m) acc[i][m] = mfma16(wo[m], v[i][p], acc[i][m]);
   }
 #pragma unroll
   for (int i = 0; i < XG; ++i)
@@ -775,27 +799,47 @@ void groups_of(int ng, F f) {
   }
 }
 
-// r output columns for each of n_seg segments (one when whole)
+// r output columns for each of n_seg segments (one when whole).  Decoded rows
+// (LIST_16) are few and long: 16 columns of v a workgroup, so that more of them
+// share A (64 rows, K 2560, 48 columns: 7.0 us, 8.8 with all in one).  Many
+// rows: 32 at a time, each of which reads all of W, and four waves; that takes
+// 256 workgroups to fill the chip (8192 rows 20 us, 22 by 16 rows and eight
+// waves; 2048 rows 13 and 9).
 void run_down(const Plan& p, DownArgs a, int n_seg, bool f32, hipStream_t st) {
-  const int groups = (a.r + 15) / 16;
-  a.jobs_per_seg = (groups + 3) / 4;
+  const int groups = (a.r + 15) / 16, most = p.tm == 16 ? 1 : 4;
+  a.jobs_per_seg = (groups + most - 1) / most;
   const int ng = (groups + a.jobs_per_seg - 1) / a.jobs_per_seg;
   a.per = 16 * ng;
-  const dim3 grid(p.tm == 16 ? p.l.cap(LIST_16) : 4 * p.l.cap(LIST_64), n_seg * a.jobs_per_seg);
-  groups_of(ng, [&](auto c) {
-    constexpr int NG = decltype(c)::value;
-    auto run = [&](auto list, auto f, auto wt) {
-      hipLaunchKernelGGL((down_kernel<decltype(list)::value, NG, decltype(f)::value, decltype(wt)::value>), grid,
-                         dim3(64 * DW), 0, st, a);
-    };
-    auto rows = [&](auto list) {
-      if (!a.whole) run(list, std::false_type{}, std::true_type{});  // (dy is bf16)
-      else if (f32) run(list, std::true_type{}, std::false_type{});
-      else run(list, std::false_type{}, std::false_type{});
-    };
-    if (p.tm == 16) rows(std::integral_constant<int, LIST_16>{});
-    else rows(std::integral_constant<int, LIST_64>{});
-  });
+  const int jobs = a.jobs = n_seg * a.jobs_per_seg;
+  const bool wide = p.tm != 16 && !(a.whole && f32) && ng >= 2 && (long)(p.l.T / 32) * jobs >= 256;
+  auto run = [&](auto list, auto xt, auto dw, auto ng, auto f, auto wt) {
+    constexpr int LIST = decltype(list)::value, XT = decltype(xt)::value, DW = decltype(dw)::value;
+    const dim3 grid((unsigned)p.l.cap(LIST) * (LIST == LIST_16 ? 1 : 4 / XT) * jobs);
+    hipLaunchKernelGGL((down_kernel<LIST, XT, DW, decltype(ng)::value, decltype(f)::value, decltype(wt)::value>), grid,
+                       dim3(64 * DW), 0, st, a);
+  };
+  using std::integral_constant;
+  using I1 = integral_constant<int, 1>;
+  auto rows = [&](auto f, auto wt) {
+    if (p.tm == 16) {
+      run(integral_constant<int, LIST_16>{}, I1{}, integral_constant<int, 8>{}, I1{}, f, wt);
+      return;
+    }
+    groups_of(ng, [&](auto c) {
+      constexpr int NG = decltype(c)::value;
+      const integral_constant<int, LIST_64> list;
+      if constexpr (NG >= 2 && !decltype(f)::value) {
+        if (wide) {
+          run(list, integral_constant<int, 2>{}, integral_constant<int, 4>{}, c, f, wt);
+          return;
+        }
+      }
+      run(list, I1{}, integral_constant<int, 8>{}, c, f, wt);
+    });
+  };
+  if (!a.whole) rows(std::false_type{}, std::true_type{});  // (dy is bf16)
+  else if (f32) rows(std::true_type{}, std::false_type{});
+  else rows(std::false_type{}, std::false_type{});
 }
 
 template <bool WT>

@@ -71,6 +71,8 @@ __global__ __launch_bounds__(256) void rotate_kernel(RowLists l, RowOrder rows, 
   const int n0 = (blockIdx.x % wgs) * 128 + 32 * wave;
   int4 e;
   if (n0 >= N || !list_entry(l, rows.tiles, TM == 16 ? LIST_16 : LIST_64, blockIdx.x / wgs, e)) return;
+  uint4 rot[2];  // (does not wait for the rows' numbers)
+  if (e.x >= 0) load_rotation<B>(rops + (size_t)e.x * N * B * 2, n0, which, l16, g, rot);
   Oct<F32> x[XG];
   size_t at[XG];
 #pragma unroll
@@ -79,8 +81,6 @@ __global__ __launch_bounds__(256) void rotate_kernel(RowLists l, RowOrder rows, 
     x[i].load(z, at[i]);
   }
   if (e.x >= 0) {
-    uint4 rot[2];
-    load_rotation<B>(rops + (size_t)e.x * N * B * 2, n0, which, l16, g, rot);
 #pragma unroll
     for (int i = 0; i < XG; ++i) {
       f32x4 o[2];
