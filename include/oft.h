@@ -577,9 +577,10 @@ int32_t oft_adapter_route(const int32_t* adapter, const oft_adapter_rows* rows, 
  *   y[t, c]       = y_base[t, c] + scale[a] sum_j v[t, s r + j] B[a, c, j]
  * with a the row's adapter; y = y_base and v = 0 in rows without one.
  * A bf16 [n, n_seg r, K], B bf16 [n, N, r], scale fp32 [n].
- * Constraints: r and n_seg at least 1 and K % 64 == 0, r % 8 == 0, every
- * seg[s] % 16 == 0 (else OFT_ESHAPE); r <= OFT_MAX_RANK, n_seg <= 8, K and N <=
- * 2^20 (else OFT_EUNSUPPORTED); dtype OFT_DT_BF16 or OFT_DT_F32.
+ * Constraints: K, N and r at least 1 (else OFT_EINVAL); K % 64 == 0,
+ * r % 8 == 0, every seg[s] > 0 and seg[s] % 16 == 0 (else OFT_ESHAPE);
+ * r <= OFT_MAX_RANK, 1 <= n_seg <= 8, K and N <= 2^20, T K and T N <= 2^34
+ * (else OFT_EUNSUPPORTED); dtype OFT_DT_BF16 or OFT_DT_F32 (else OFT_EDTYPE).
  * All sums are fp32, and a result is rounded once, to its own type: v and fp32
  * rows enter the matrix products as bf16 parts that hold all their bits (16
  * of them where the result is bf16).  A row's infinite or NaN values reach its
@@ -623,8 +624,9 @@ int32_t oft_lowrank_bwd(const oft_lowrank_desc* d, const oft_adapter_rows* rows,
  * R_ops bf16 [n, N/b, 2, b, b] and R_f32 [n, N/b, b, b] as cayley_build writes
  * them for the n N/b blocks of all adapters together.  Segments of a fused
  * projection need no mention: their blocks follow each other.
- * Constraints: b in {16, 32} and N <= 2^20 (else OFT_EUNSUPPORTED),
- * N % 32 == 0 (else OFT_ESHAPE); dtype OFT_DT_BF16 or OFT_DT_F32.
+ * Constraints: N at least 1 (else OFT_EINVAL); b in {16, 32}, N <= 2^20 and
+ * T N <= 2^34 (else OFT_EUNSUPPORTED); N % 32 == 0 (else OFT_ESHAPE); dtype
+ * OFT_DT_BF16 or OFT_DT_F32 (else OFT_EDTYPE).
  * Sums are fp32 and a result is rounded once; fp32 rows enter the matrix
  * products with all their bits (oft_linear_fwd rounds its z to bf16 there). */
 typedef struct {
@@ -668,7 +670,7 @@ int32_t oft_rotate_bwd(const oft_rotate_desc* d, const oft_adapter_rows* rows, c
  * norm has coefficient 0, a NaN among the gradients makes all of it NaN.
  * Deterministic.  Errors: OFT_EINVAL (m < 0, a negative count, max_norm
  * negative or NaN, null or misaligned pointers), OFT_EDTYPE, OFT_EUNSUPPORTED
- * (m > OFT_MAX_GRADS, 2^40 elements or more), OFT_EWORKSPACE. */
+ * (m > OFT_MAX_GRADS, 2^36 elements or more), OFT_EWORKSPACE. */
 #define OFT_MAX_GRADS 65536
 int32_t oft_grad_workspace_bytes(int32_t m, const int64_t* numel, int32_t dtype, size_t* bytes);
 int32_t oft_grad_sumsq(int32_t m, const void* const* grads, const int64_t* numel, int32_t dtype, double* sumsq,

@@ -26,13 +26,18 @@ int32_t validate_counts(int32_t T, int32_t n) {
   return T > (1 << 22) || n > OFT_MAX_ADAPTERS ? OFT_EUNSUPPORTED : OFT_OK;
 }
 
+// A launch has fewer than 2^32 threads along its grid's x dimension, where
+// tiles of 64 rows and 64 columns (and one unfull row tile per adapter) lie: a
+// wave each, 2^28 threads at this limit.
+bool elements_ok(int32_t T, int32_t cols) { return (int64_t)T * cols <= (1LL << 34); }
+
 int32_t validate_lowrank(const oft_lowrank_desc* d) {
   if (d == nullptr) return OFT_EINVAL;
   if (d->K <= 0 || d->N <= 0 || d->r <= 0) return OFT_EINVAL;
   const int32_t v = validate_counts(d->T, d->n);
   if (v != OFT_OK) return v;
-  // column tiles times row tiles fill the launch grid's x dimension
   if (d->K > (1 << 20) || d->N > (1 << 20) || d->r > OFT_MAX_RANK) return OFT_EUNSUPPORTED;
+  if (!elements_ok(d->T, d->K) || !elements_ok(d->T, d->N)) return OFT_EUNSUPPORTED;
   if (d->dtype != OFT_DT_BF16 && d->dtype != OFT_DT_F32) return OFT_EDTYPE;
   if (d->n_seg < 1 || d->n_seg > OFT_MAX_SEGMENTS) return OFT_EUNSUPPORTED;
   long long sum = 0;
@@ -54,7 +59,7 @@ int32_t validate_rotate(const oft_rotate_desc* d) {
   if (d == nullptr || d->N <= 0) return OFT_EINVAL;
   const int32_t v = validate_counts(d->T, d->n);
   if (v != OFT_OK) return v;
-  if (d->N > (1 << 20)) return OFT_EUNSUPPORTED;
+  if (d->N > (1 << 20) || !elements_ok(d->T, d->N)) return OFT_EUNSUPPORTED;
   if (d->dtype != OFT_DT_BF16 && d->dtype != OFT_DT_F32) return OFT_EDTYPE;
   if (d->b != 16 && d->b != 32) return OFT_EUNSUPPORTED;
   return d->N % 32 != 0 ? OFT_ESHAPE : OFT_OK;

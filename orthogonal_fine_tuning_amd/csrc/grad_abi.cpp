@@ -20,12 +20,13 @@ int32_t validate_sizes(int32_t m, const int64_t* numel, int32_t dtype) {
   int64_t total = 0;
   for (int32_t i = 0; i < m; ++i) {
     if (numel[i] < 0) return OFT_EINVAL;
-    // (each below 2^40 and at most 2^16 of them: the sum stays inside 64 bits)
-    if (numel[i] >= (1LL << 40)) return OFT_EUNSUPPORTED;
+    // (each below 2^36 and at most 2^16 of them: the sum stays inside 64 bits)
+    if (numel[i] >= (1LL << 36)) return OFT_EUNSUPPORTED;
     total += numel[i];
   }
-  // chunks of 16384 elements are counted in 32 bits
-  return total >= (1LL << 40) ? OFT_EUNSUPPORTED : OFT_OK;
+  // a workgroup of 256 threads takes 16384 elements, and a launch has fewer
+  // than 2^32 threads
+  return total >= (1LL << 36) ? OFT_EUNSUPPORTED : OFT_OK;
 }
 
 int32_t validate_list(int32_t m, const void* const* grads, const int64_t* numel, int32_t dtype) {

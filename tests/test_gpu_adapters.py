@@ -107,6 +107,11 @@ SHAPES = [  # T, n, K, segments, r, kind
     (2050, 40, 64, (16,) * 8, 16, "runs"),
     (2051, 2, 512, (64,) * 8, 128, "skewed"),
     (40, 5, 128, (64,), 16, "none"),
+    (2100, 5, 128, (32,) * 8, 32, "some"),     # 32 rows at a time
+    (1300, 3, 128, (80,), 48, "mixed"),
+    (1200, 2, 64, (48,), 24, "runs"),
+    (300, 2, 64, (16384,), 64, "skewed"),      # pieces of a quarter of the rows
+    (40001, 2, 64, (16,), 8, "skewed"),        # pieces of more rows than have their numbers in LDS
 ]
 
 
@@ -178,6 +183,8 @@ ROT = [  # T, n, N, kind
     (2500, 3, 64, "some"),
     (3001, 70, 32, "mixed"),
     (50, 2, 96, "none"),
+    (300, 2, 16416, "skewed"),  # pieces of a quarter of the rows
+    (40001, 2, 32, "skewed"),   # pieces of more rows than have their numbers in LDS
 ]
 
 
