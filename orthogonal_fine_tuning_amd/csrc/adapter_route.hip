@@ -8,8 +8,8 @@
 // same adapter find each other by one ballot per bit of the adapter number, so
 // that nothing depends on the order of atomics.  Up to ONE_WG rows one
 // workgroup does it all: the call is a chain of latencies, not of bytes (64
-// rows: 5.3 us, an empty launch 2).  More rows are too many instructions for
-// one (20011 rows: 24 us): up to SLABS workgroups count a slab each, and in a
+// rows: 4.7 us, an empty launch 2).  More rows are too many instructions for
+// one (20011 rows: 24 us): workgroups count a slab of them each, and in a
 // second launch each adds up the slabs before it, all of them from the caches.
 #include "adapter_device.h"
 #include "oft_prof.h"
@@ -18,7 +18,8 @@ namespace oft {
 namespace {
 
 constexpr int THREADS = 1024, WAVES = THREADS / 64;
-constexpr int ONE_WG = 4096, SLABS = 64;
+constexpr int ONE_WG = 4096, SLABS = 192;
+constexpr int FEW = 256;  // rows that four waves take
 constexpr int KEYS = MAX_ADAPTERS + 1;  // adapters, and rows without one
 static_assert(THREADS >= MAX_ADAPTERS, "the scan takes an adapter a thread");
 
@@ -97,14 +98,15 @@ __device__ __forceinline__ void place_rows(int lo, const Rows<RUN>& r, const int
 // its partial slots.
 constexpr int SUMS = 7;  // rows, the four lists, partial slots of the two lists of pieces
 
+template <int TH>  // threads, and adapters at most
 struct Scan {
-  int first[SUMS][KEYS + 1];
-  int wave[SUMS][WAVES];
+  int first[SUMS][TH + 2];
+  int wave[SUMS][TH / 64];
 };
 
 // total: rows of this thread's adapter -> s.first[0 .. N - 1]
-template <int N>
-__device__ __forceinline__ void scan_sums(const RowLists& l, Scan& s, int total) {
+template <int N, int TH>
+__device__ __forceinline__ void scan_sums(const RowLists& l, Scan<TH>& s, int total) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int n = l.n;
   int own[SUMS], sum[SUMS];
@@ -125,7 +127,7 @@ __device__ __forceinline__ void scan_sums(const RowLists& l, Scan& s, int total)
   for (int i = 0; i < N; ++i) {
     int before = 0;
 #pragma unroll
-    for (int w = 0; w < WAVES; ++w) before += w < wave ? s.wave[i][w] : 0;
+    for (int w = 0; w < TH / 64; ++w) before += w < wave ? s.wave[i][w] : 0;
     sum[i] += before;
     if (tid < n) s.first[i][tid + 1] = sum[i];
     if (tid == 0) s.first[i][0] = 0;
@@ -134,13 +136,14 @@ __device__ __forceinline__ void scan_sums(const RowLists& l, Scan& s, int total)
 }
 
 // offsets, the lists and their counts from the sums
-__device__ __forceinline__ void write_lists(const RowLists& l, const Scan& s, int* __restrict__ offsets,
+template <int TH>
+__device__ __forceinline__ void write_lists(const RowLists& l, const Scan<TH>& s, int* __restrict__ offsets,
                                             int* __restrict__ tiles) {
   const int tid = threadIdx.x, n = l.n;
-  for (int a = tid; a <= n; a += THREADS) offsets[a] = s.first[0][a];
+  for (int a = tid; a <= n; a += TH) offsets[a] = s.first[0][a];
   const int rest = l.T - s.first[0][n];  // rows without an adapter
   if (tid < 8) tiles[tid] = tid < LISTS ? s.first[1 + tid][n] + l.count(tid, rest) : 0;
-  for (int a = tid; a <= n; a += THREADS) {
+  for (int a = tid; a <= n; a += TH) {
     tiles[l.part_at(LIST_LONG) + a] = s.first[5][a];
     tiles[l.part_at(LIST_SHORT) + a] = s.first[6][a];
   }
@@ -151,7 +154,7 @@ __device__ __forceinline__ void write_lists(const RowLists& l, const Scan& s, in
     all += s.first[1 + i][n] + l.count(i, rest);
     end[i] = all;
   }
-  for (int e = tid; e < all; e += THREADS) {
+  for (int e = tid; e < all; e += TH) {
     int list = 0;
 #pragma unroll
     for (int i = 0; i + 1 < LISTS; ++i) list += e >= end[i];
@@ -173,12 +176,13 @@ __device__ __forceinline__ void write_lists(const RowLists& l, const Scan& s, in
 }
 
 // RUN steps of 64 rows a wave at most; as many waves as have rows count.
-template <int RUN>
-__global__ __launch_bounds__(THREADS) void route_one_kernel(RowLists l, int bits, const int* __restrict__ adapter,
+template <int RUN, int TH>
+__global__ __launch_bounds__(TH) void route_one_kernel(RowLists l, int bits, const int* __restrict__ adapter,
                                                             int* __restrict__ order, int* __restrict__ offsets,
                                                             int* __restrict__ tiles) {
-  __shared__ int table[WAVES][KEYS];
-  __shared__ Scan s;
+  constexpr int WAVES = TH / 64;
+  __shared__ int table[WAVES][TH + 1];
+  __shared__ Scan<TH> s;
   const int tid = threadIdx.x, wave = tid >> 6, n = l.n;
   const int per = RUN == 1 ? 64 : ((l.T + WAVES * 64 - 1) / (WAVES * 64)) * 64;  // rows of a wave
   const int waves = (l.T + per - 1) / per;
@@ -186,7 +190,7 @@ __global__ __launch_bounds__(THREADS) void route_one_kernel(RowLists l, int bits
   Rows<RUN> r;
   load_rows<RUN>(adapter, n, lo, hi, r);
   for (int w = 0; w < waves; ++w)
-    for (int a = tid; a <= n; a += THREADS) table[w][a] = 0;
+    for (int a = tid; a <= n; a += TH) table[w][a] = 0;
   __syncthreads();
   count_rows<RUN>(bits, r, table[wave]);
   __syncthreads();
@@ -198,7 +202,7 @@ __global__ __launch_bounds__(THREADS) void route_one_kernel(RowLists l, int bits
       table[w][tid] = total;
       total += c;
     }
-  scan_sums<SUMS>(l, s, total);
+  scan_sums<SUMS, TH>(l, s, total);
   if (tid < n)
     for (int w = 0; w < waves; ++w) table[w][tid] += s.first[0][tid];
   if (tid < 64) {  // rows without an adapter, behind all others
@@ -232,7 +236,7 @@ __global__ __launch_bounds__(THREADS) void route_place_kernel(RowLists l, int bi
                                                               const int* __restrict__ counts, int* __restrict__ order,
                                                               int* __restrict__ offsets, int* __restrict__ tiles) {
   __shared__ int table[WAVES][KEYS];
-  __shared__ Scan s;
+  __shared__ Scan<THREADS> s;
   const int tid = threadIdx.x, wave = tid >> 6, n = l.n;
   const int lo = (blockIdx.x * WAVES + wave) * 64 * RUN;
   Rows<RUN> r;
@@ -251,8 +255,8 @@ __global__ __launch_bounds__(THREADS) void route_place_kernel(RowLists l, int bi
     for (int a = tid; a <= n; a += THREADS) table[w][a] = 0;
   __syncthreads();
   count_rows<RUN>(bits, r, table[wave]);
-  if (blockIdx.x == 0) scan_sums<SUMS>(l, s, total);
-  else scan_sums<1>(l, s, total);
+  if (blockIdx.x == 0) scan_sums<SUMS, THREADS>(l, s, total);
+  else scan_sums<1, THREADS>(l, s, total);
   if (tid < n) {
     int at = s.first[0][tid] + before;
 #pragma unroll
@@ -263,7 +267,8 @@ __global__ __launch_bounds__(THREADS) void route_place_kernel(RowLists l, int bi
     }
   }
   if (wave == 0) {  // rows without an adapter, behind all others
-    int at = tid < (int)blockIdx.x ? counts[(size_t)tid * (n + 1) + n] : 0;  // (at most 64 slabs)
+    int at = 0;
+    for (int g = tid; g < (int)blockIdx.x; g += 64) at += counts[(size_t)g * (n + 1) + n];
     at = __shfl(wave_scan(at), 63);
     int v = tid < WAVES ? table[tid][n] : 0;
     v = wave_scan(v) - v;
@@ -274,17 +279,15 @@ __global__ __launch_bounds__(THREADS) void route_place_kernel(RowLists l, int bi
   if (blockIdx.x == 0) write_lists(l, s, offsets, tiles);
 }
 
-// f(steps of 64 rows a wave takes): the fewest that SLABS workgroups make do with
-template <class F>
-void slab_run(int T, F f) {
-  if (T <= SLABS * THREADS) f(std::integral_constant<int, 1>{});
-  else if (T <= 8 * SLABS * THREADS) f(std::integral_constant<int, 8>{});
-  else f(std::integral_constant<int, 64>{});
-}
+// Steps of 64 rows a wave takes: one while that gives SLABS workgroups at
+// most, else eight, so that each has fewer slabs to add up (300 adapters, us:
+// 131072 rows 18.5 and 25.2, 196608 21.4 and 26.7, 262144 28 with either).
+int slab_rows(int T) { return T <= SLABS * THREADS ? THREADS : 8 * THREADS; }
+int slabs_of(int T) { return (T + slab_rows(T) - 1) / slab_rows(T); }
 
 }  // namespace
 
-size_t adapter_route_ws_bytes(const RowLists& l) { return l.T <= ONE_WG ? 0 : 4 * (size_t)SLABS * (l.n + 1); }
+size_t adapter_route_ws_bytes(const RowLists& l) { return l.T <= ONE_WG ? 0 : 4 * (size_t)slabs_of(l.T) * (l.n + 1); }
 
 hipError_t launch_adapter_route(const RowLists& l, const int* adapter, int* order, int* offsets, int* tiles, char* ws,
                                 hipStream_t st) {
@@ -292,22 +295,29 @@ hipError_t launch_adapter_route(const RowLists& l, const int* adapter, int* orde
   int bits = 0;
   while ((1 << bits) <= l.n) ++bits;
   if (l.T <= ONE_WG) {
-    auto run = [&](auto steps) {
-      hipLaunchKernelGGL(route_one_kernel<decltype(steps)::value>, dim3(1), dim3(THREADS), 0, st, l, bits, adapter, order,
+    auto run = [&](auto steps, auto threads) {
+      constexpr int TH = decltype(threads)::value;
+      hipLaunchKernelGGL((route_one_kernel<decltype(steps)::value, TH>), dim3(1), dim3(TH), 0, st, l, bits, adapter, order,
                          offsets, tiles);
     };
-    if (l.T <= THREADS) run(std::integral_constant<int, 1>{});
-    else run(std::integral_constant<int, ONE_WG / THREADS>{});
+    using std::integral_constant;
+    // decoded rows of few adapters: four waves' barriers (64 rows, 64 adapters
+    // 4.7 us, 5.7 with sixteen; 256 rows, 128 adapters 5.9 and 6.1, 256 of both 7.0 and 6.4)
+    if (l.T <= FEW && l.n <= FEW / 2) run(integral_constant<int, 1>{}, integral_constant<int, FEW>{});
+    else if (l.T <= THREADS) run(integral_constant<int, 1>{}, integral_constant<int, THREADS>{});
+    else run(integral_constant<int, ONE_WG / THREADS>{}, integral_constant<int, THREADS>{});
     return hipGetLastError();
   }
   int* counts = reinterpret_cast<int*>(ws);
-  slab_run(l.T, [&](auto steps) {
+  auto run = [&](auto steps) {
     constexpr int RUN = decltype(steps)::value;
-    const int slabs = (l.T + RUN * THREADS - 1) / (RUN * THREADS);
+    const int slabs = slabs_of(l.T);
     hipLaunchKernelGGL(route_count_kernel<RUN>, dim3(slabs), dim3(THREADS), 0, st, l, bits, adapter, counts);
     hipLaunchKernelGGL(route_place_kernel<RUN>, dim3(slabs), dim3(THREADS), 0, st, l, bits, adapter, counts, order,
                        offsets, tiles);
-  });
+  };
+  if (slab_rows(l.T) == THREADS) run(std::integral_constant<int, 1>{});
+  else run(std::integral_constant<int, 8>{});
   return hipGetLastError();
 }
 

@@ -53,7 +53,7 @@ def _ws(nbytes):
 
 # --------------------------------------------------------------------- route
 @pytest.mark.parametrize("kind", ["mixed", "runs", "one", "none", "some"])
-@pytest.mark.parametrize("T,n", [(1, 1), (3, 2), (64, 64), (65, 1), (1000, 7), (1024, 1024), (1025, 1000), (4097, 33),
+@pytest.mark.parametrize("T,n", [(1, 1), (3, 2), (64, 64), (256, 128), (256, 129), (257, 128), (65, 1), (1000, 7), (1024, 1024), (1025, 1000), (4097, 33),
                                  (30001, 1024),
                                  (65536, 7), (65537, 300), (524288, 5), (600001, 900)])
 def test_route(T, n, kind):
