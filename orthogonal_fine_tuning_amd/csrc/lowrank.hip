@@ -753,8 +753,12 @@ __global__ __launch_bounds__(256) void join_kernel(JoinArgs a) {
 size_t up256(size_t b) { return (b + 255) & ~(size_t)255; }
 
 // Rows of a tile: 16 while the batch is one of decoded rows (an adapter then
-// has few), else 64.
-int tile_rows(int T) { return T <= 1024 ? 16 : 64; }
+// has few), else 64; small ranks gain longer, since the factors that each tile
+// reads again are small.  Forward calls in us by 16 and by 64 rows, 8 adapters
+// and 64: rank 16 beside QKV, 2048 rows 20.6, 20.7 and 22, 28; 4096 rows 31,
+// 33 and 33, 36, but the gradients 59, 57 and 75, 73; rank 64 on gate/up, 256
+// rows 20, 21 and 51, 56; 512 rows 27, 26 and 59, 57; 1024 rows 40, 34 and 81, 76.
+int tile_rows(int T, int r) { return T <= (r <= 32 ? T16_MAX : 512) ? 16 : 64; }
 
 struct Plan {
   RowLists l;
@@ -766,7 +770,7 @@ struct Plan {
 Plan plan_of(const LowrankDims& d, bool bwd) {
   Plan p;
   p.l = RowLists{d.T, d.n};
-  p.tm = tile_rows(d.T);
+  p.tm = tile_rows(d.T, d.r);
   p.R = d.n_seg * d.r;
   p.v = 0;
   p.parts = bwd ? up256(4 * (size_t)d.T * p.R) : 0;

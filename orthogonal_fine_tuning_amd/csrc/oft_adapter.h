@@ -22,7 +22,7 @@ constexpr int MAX_SEG = 8;
 //               more pieces gets a partial slot for each (`part` counts them
 //               up to the adapter); one of a single piece has slot -1.
 enum : int { LIST_16 = 0, LIST_64 = 1, LIST_LONG = 2, LIST_SHORT = 3, LISTS = 4 };
-constexpr int T16_MAX = 4096;
+constexpr int T16_MAX = 2048;
 
 struct RowLists {
   int T, n;

@@ -64,7 +64,7 @@ def test_route(T, n, kind):
     assert np.array_equal(rows.order.cpu().numpy(), order)
 
 
-@pytest.mark.parametrize("T,n", [(1, 1), (65, 3), (1000, 7), (5000, 1024), (20000, 5), (40000, 1000)])
+@pytest.mark.parametrize("T,n", [(1, 1), (65, 3), (1000, 7), (2048, 40), (2049, 3), (5000, 1024), (20000, 5), (40000, 1000)])
 @pytest.mark.parametrize("kind", ["mixed", "some", "none", "skewed"])
 def test_route_lists(T, n, kind):
     """Every list covers each row once, in pieces of one adapter and the list's size."""
@@ -76,10 +76,10 @@ def test_route_lists(T, n, kind):
     at = 8 + 2 * up4(n + 1)
     piece = lambda d: max(64, ((T + d - 1) // d + 63) & ~63)  # noqa: E731
     for i, size in enumerate((16, 64, piece(4), piece(16))):
-        cap = 0 if i == 0 and T > 4096 else min(T, T // size + n + 1)
+        cap = 0 if i == 0 and T > 2048 else min(T, T // size + n + 1)
         got = tiles[at:at + 4 * cap].reshape(-1, 4)[:tiles[i]]
         at += 4 * cap
-        if i == 0 and T > 4096:
+        if i == 0 and T > 2048:
             assert tiles[i] == 0
             continue
         want, slot = [], 0
@@ -110,6 +110,10 @@ SHAPES = [  # T, n, K, segments, r, kind
     (2100, 5, 128, (32,) * 8, 32, "some"),     # 32 rows at a time
     (1300, 3, 128, (80,), 48, "mixed"),
     (1200, 2, 64, (48,), 24, "runs"),
+    (2060, 2, 64, (48,), 24, "runs"),
+    (2070, 3, 128, (80, 16), 48, "mixed"),
+    (513, 2, 64, (48,), 40, "some"),
+    (512, 2, 64, (48,), 40, "some"),
     (300, 2, 64, (16384,), 64, "skewed"),      # pieces of a quarter of the rows
     (40001, 2, 64, (16,), 8, "skewed"),        # pieces of more rows than have their numbers in LDS
 ]
