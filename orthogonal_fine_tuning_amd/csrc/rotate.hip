@@ -387,8 +387,11 @@ void run_rotate(const RotateDims& d, const RowOrder& rows, bool f32, const void*
   else hipLaunchKernelGGL((rotate_kernel<64, B, true>), grid, dim3(256), 0, st, l, rows, z, rops, d.N, which, y);
 }
 
-// pieces of a quarter of the rows where the channels alone nearly fill the chip
-int sums_list(const RotateDims& d) { return (d.N + SC - 1) / SC >= 16384 / SC ? LIST_LONG : LIST_SHORT; }
+// Pieces of a quarter of few rows, a sixteenth of many: fewer partial sums
+// against more workgroups (us, one adapter and 16; 6144 channels: 1024 rows 16,
+// 25 by quarters and 19, 32 by sixteenths, 8192 rows 74, 85 and 68, 84; 19456
+// channels: 1024 rows 29, 59 and 37, 61, 4096 rows 111, 121 and 108, 122).
+int sums_list(const RotateDims& d) { return d.T <= 2048 ? LIST_LONG : LIST_SHORT; }
 
 template <int B>
 hipError_t run_sums(const RotateDims& d, const RowOrder& rows, const uint16_t* dy, const void* y, const float* Rf,
