@@ -5,10 +5,10 @@
 //   coef = min(1, max_norm / (norm + 1e-6)),  out = coef g
 // One read for the sum, one read and one write for the clipping: bound by
 // those bytes.  The tensors' addresses travel in the kernel's arguments, up to
-// 100 to a launch (or, for the host's sake, 12), so that nothing has to be copied to the GPU and a captured
-// call replays.  Squares are added in fp64 (two instructions an element, far
-// below what the reads take): no finite gradient overflows, and the order of
-// the chunks does not show in fp32.
+// 100 to a launch (or, for the host's sake, 12), so that nothing has to be
+// copied to the GPU and a captured call replays.  Squares are added in fp64
+// (two instructions an element, far below what the reads take): no finite
+// gradient overflows, and the order of the chunks does not show in fp32.
 #include "oft_device.h"
 #include "oft_grad.h"
 #include "oft_prof.h"
@@ -19,9 +19,11 @@ namespace oft {
 namespace {
 
 constexpr float EPS = 1e-6f;
-// Gradients of more bytes than this in all are streamed past the caches;
-// fewer are still there, in part, when the clipping reads them again.
-constexpr int64_t STREAM_BYTES = 128LL << 20;
+// Gradients of more bytes than this in all are streamed past the caches (norm
+// and clipping into other tensors in us, streamed and not: 64 MB 38 and 42
+// from memory, 35 and 35 from the caches, 120 MB 67, 78 and 64, 62, 512 MB 269
+// and 308; 16 MB 13.5 and 12.6 from memory).
+constexpr int64_t STREAM_BYTES = 64LL << 20;
 
 struct Item {
   const void* g;

@@ -9,15 +9,16 @@
 // rows of activations are two kernels: `down` (activations -> rank, the
 // contraction long) and `up` (rank -> activations, the contraction short); the
 // backward runs them with the factors' other side along the contraction, read
-// with the transposing LDS load.  `pieces` forms the sums over rows.  Everything is bound by the bytes of x, y, dy and dx, so the
-// products take whatever keeps those moving: 16 x 16 x 32 matrix steps (ranks
-// and tiles of single decoded rows are small), operands straight from global
-// memory where both run along the contraction.
+// with the transposing LDS load.  `pieces` forms the sums over rows.
+// Everything is bound by the bytes of x, y, dy and dx, so the products take
+// whatever keeps those moving: 16 x 16 x 32 matrix steps (ranks and tiles of
+// single decoded rows are small), operands straight from global memory where
+// both run along the contraction.
 //
 // Precision: bf16 factors and activations are matrix operands as they are.
 // fp32 values (v, u, fp32 activations) are split into bf16 parts whose sum is
 // the value (split_bf16): all three where the result is fp32, two where it is
-// rounded to bf16, whose half step of 2^-9 hides the 2^-16 left out.
+// rounded to bf16, whose half step of 2^-8 hides the 2^-16 left out.
 #include "adapter_device.h"
 #include "gemm_nn.h"
 #include "oft_prof.h"
