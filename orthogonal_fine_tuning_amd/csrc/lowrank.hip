@@ -783,15 +783,15 @@ Plan plan_of(const LowrankDims& d, bool bwd) {
   p.list = LIST_SHORT;
   if (bwd) {
     p.sums = p.bytes;
-    // pieces of a quarter of the rows where they are few or the columns alone
-    // give workgroups enough: fewer partial sums (us of a backward pass of one
-    // adapter by quarters and by sixteenths, K 2560: rank 16 on gate/up, 86
-    // workgroups a piece, 2048 rows 56 and 56, 8192 rows 181 and 173; rank 64
-    // beside QKV, 108 of them, 81 and 93, 192 and 200; on gate/up, 212 of
-    // them, 94 and 118, 267 and 297; rank 16 beside QKV, 44 of them, 1024 rows
-    // 32 and 33, 2048 rows 46 and 42, 8192 rows 125 and 88)
+    // pieces of a quarter of the rows where the columns alone give workgroups
+    // enough, or bf16 rows are few: fewer partial sums (us of a backward pass of
+    // one adapter by quarters and by sixteenths, K 2560: rank 64 beside QKV,
+    // 108 workgroups a piece, 2048 rows 81 and 93, of fp32 97 and 102; on
+    // gate/up, 212 of them, 94 and 118, 118 and 134; rank 16 on gate/up, 86 of
+    // them, 56 and 56, 84 and 71; beside QKV, 44 of them, 46 and 42, 69 and 57,
+    // but 512 rows of bf16 25 and 27, 1024 rows 32 and 33)
     const auto jobs = [](int cols, int r) { return (cols + PC - 1) / PC * ((r + 16 * MAXG - 1) / (16 * MAXG)); };
-    p.list = d.T <= 1024 || jobs(d.K, p.R) + jobs(d.N, d.r) >= 64 ? LIST_LONG : LIST_SHORT;
+    p.list = jobs(d.K, p.R) + jobs(d.N, d.r) >= 100 || (!d.f32 && d.T <= 1024) ? LIST_LONG : LIST_SHORT;
     p.bytes = p.sums + up256(4 * (size_t)RowLists::slots(p.list) * p.slot);
   }
   return p;

@@ -390,8 +390,10 @@ void run_rotate(const RotateDims& d, const RowOrder& rows, bool f32, const void*
 // Pieces of a quarter of few rows, a sixteenth of many: fewer partial sums
 // against more workgroups (us, one adapter and 16; 6144 channels: 1024 rows 16,
 // 25 by quarters and 19, 32 by sixteenths, 8192 rows 74, 85 and 68, 84; 19456
-// channels: 1024 rows 29, 59 and 37, 61, 4096 rows 111, 121 and 108, 122).
-int sums_list(const RotateDims& d) { return d.T <= 2048 ? LIST_LONG : LIST_SHORT; }
+// channels: 1024 rows 29, 59 and 37, 61, 4096 rows 111, 121 and 108, 122).  A
+// step of fp32 rows is longer (1024 rows of 6144 channels, blocks of 16: 22, 25
+// and 25, 27; of 2560 channels 20, 17 and 17, 16, 1501 rows 25, 22 and 18, 20).
+int sums_list(const RotateDims& d) { return d.T <= (d.f32 ? 1024 : 2048) ? LIST_LONG : LIST_SHORT; }
 
 template <int B>
 hipError_t run_sums(const RotateDims& d, const RowOrder& rows, const uint16_t* dy, const void* y, const float* Rf,

@@ -115,7 +115,7 @@ SHAPES = [  # T, n, K, segments, r, kind
     (513, 2, 64, (48,), 40, "some"),
     (512, 2, 64, (48,), 40, "some"),
     (300, 2, 64, (16384,), 64, "skewed"),      # pieces of a quarter of the rows, by their number
-    (2100, 3, 64, (9728,), 32, "skewed"),      # or by the columns
+    (2100, 3, 64, (9728,), 128, "skewed"),     # or by the columns
     (40001, 2, 64, (16,), 8, "skewed"),        # pieces of more rows than have their numbers in LDS
 ]
 
