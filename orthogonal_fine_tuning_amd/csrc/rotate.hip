@@ -156,14 +156,14 @@ __global__ __launch_bounds__(64 * RW) void rotate_tile_kernel(RowLists l, RowOrd
 
 // ------------------------------------------------------- sums over the rows
 // One piece of an adapter's rows and SC channels: dz of every row (dz may be
-// NULL), S of the channels' blocks.  Tiles of 32 rows go to LDS in row order;
+// NULL, or dy itself), S of the channels' blocks.  Tiles of 32 rows go to LDS in row order;
 // S's operands, which run along the rows, are read with the transposing load.
 // Rows are fetched two steps ahead.
 constexpr int SC = 128, SR = 32, LDS_ROW = SC + 16;
 
 template <int B, bool F32, bool STREAM>
 __global__ __launch_bounds__(256) void rotate_sums_kernel(RowLists l, RowOrder rows, int list,
-                                                          const uint16_t* __restrict__ dy, const void* __restrict__ y,
+                                                          const uint16_t* dy, const void* __restrict__ y,
                                                           const float* __restrict__ Rf,
                                                           const uint16_t* __restrict__ rops, int N, uint16_t* dz,
                                                           float* __restrict__ dq, float* __restrict__ part) {
