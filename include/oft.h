@@ -581,9 +581,9 @@ int32_t oft_adapter_route(const int32_t* adapter, const oft_adapter_rows* rows, 
  * r % 8 == 0, every seg[s] > 0 and seg[s] % 16 == 0 (else OFT_ESHAPE);
  * r <= OFT_MAX_RANK, 1 <= n_seg <= 8, K and N <= 2^20, T K and T N <= 2^34
  * (else OFT_EUNSUPPORTED); dtype OFT_DT_BF16 or OFT_DT_F32 (else OFT_EDTYPE).
- * All sums are fp32, and a result is rounded once, to its own type: v and fp32
- * rows enter the matrix products as bf16 parts that hold all their bits (16
- * of them where the result is bf16).  A row's infinite or NaN values reach its
+ * All sums are fp32, and a result is rounded once, to its own type: u, v and
+ * fp32 rows enter the matrix products as bf16 parts that hold all their bits
+ * (of magnitudes above 2^-100).  A row's infinite or NaN values reach its
  * own results and its adapter's gradients alone; there they may become NaN
  * where the formula has an infinity. */
 #define OFT_MAX_RANK 128

@@ -16,9 +16,9 @@
 // both run along the contraction.
 //
 // Precision: bf16 factors and activations are matrix operands as they are.
-// fp32 values (v, u, fp32 activations) are split into bf16 parts whose sum is
-// the value (split_bf16): all three where the result is fp32, two where it is
-// rounded to bf16, whose half step of 2^-8 hides the 2^-16 left out.
+// fp32 values (v, u, fp32 activations) are split into three bf16 parts whose
+// sum is the value (split_bf16), whatever the type of the result: where an
+// update cancels its base, a bf16 result has as many bits as v does.
 #include "adapter_device.h"
 #include "gemm_nn.h"
 #include "oft_prof.h"
@@ -35,10 +35,11 @@ namespace {
 // wave's step goes through its own part of LDS, from loads whose lanes run
 // along the rows to operands whose lanes run across them.
 //
-// What `up` takes is written as the operands of its matrix steps, in parts of
-// bf16, so that it is split once and not by every block of columns: for each
+// What `up` takes is written as the operands of its matrix steps, in VP parts
+// of bf16, so that it is split once and not by every block of columns: for each
 // 16 rows (in list order), each VR columns of v and each 32 of those, a 1 KB
 // block a part, lane l's eight items of row l % 16 and columns 8 (l / 16) ...
+constexpr int VP = 3;
 struct DownArgs {
   RowLists l;
   RowOrder rows;
@@ -48,7 +49,7 @@ struct DownArgs {
   long w_a;           // elements of an adapter's matrices
   float* v;          // [T][R] (NULL: not wanted)
   uint16_t* parts;   // the operands of `up` (NULL: not wanted)
-  int vr, nparts;    // columns of v that one product of `up` takes; parts
+  int vr;            // columns of v that one product of `up` takes
   int R;             // columns of v
   int r, per;        // r output columns a segment (R when whole), `per` a job
   int jobs_per_seg, jobs;
@@ -219,17 +220,16 @@ __global__ __launch_bounds__(64 * DW) void down_kernel(DownArgs a) {
       *reinterpret_cast<float4*>(a.v + (size_t)row_at(a.l, a.rows.order, e.y + r) * a.R + col) = o;
     if (a.parts != nullptr && e.x >= 0) {
       const int s = col / a.vr, k = col % a.vr, steps = (a.vr + 31) / 32;
-      uint16_t* out = a.parts + ((((size_t)tile * XT + i) * (a.R / a.vr) + s) * steps + k / 32) * a.nparts * 512 +
+      uint16_t* out = a.parts + ((((size_t)tile * XT + i) * (a.R / a.vr) + s) * steps + k / 32) * VP * 512 +
                       ((k % 32) / 8 * 16 + l16) * 8 + k % 8;
-      uint32_t h[4][3];
-      split_bf16<3>(o.x, h[0]);
-      split_bf16<3>(o.y, h[1]);
-      split_bf16<3>(o.z, h[2]);
-      split_bf16<3>(o.w, h[3]);
+      uint32_t h[4][VP];
+      split_bf16<VP>(o.x, h[0]);
+      split_bf16<VP>(o.y, h[1]);
+      split_bf16<VP>(o.z, h[2]);
+      split_bf16<VP>(o.w, h[3]);
 #pragma unroll
-      for (int p = 0; p < 3; ++p)
-        if (p < a.nparts)
-          *reinterpret_cast<uint2*>(out + p * 512) = make_uint2(h[0][p] | (h[1][p] << 16), h[2][p] | (h[3][p] << 16));
+      for (int p = 0; p < VP; ++p)
+        *reinterpret_cast<uint2*>(out + p * 512) = make_uint2(h[0][p] | (h[1][p] << 16), h[2][p] | (h[3][p] << 16));
     }
   }
 }
@@ -314,19 +314,18 @@ struct UpOperand {
 };
 
 // v of 16 rows (block `i16` of the list's) and contraction items 32 s ..
-template <int P>
-__device__ __forceinline__ void up_rows(const UpArgs& a, int seg, int i16, int s, int lane, bf16x8 (&o)[P]) {
+__device__ __forceinline__ void up_rows(const UpArgs& a, int seg, int i16, int s, int lane, bf16x8 (&o)[VP]) {
   const uint16_t* p =
-      a.parts + (((size_t)i16 * a.segs + seg) * ((a.r + 31) / 32) + s) * P * 512 + 8 * lane;
+      a.parts + (((size_t)i16 * a.segs + seg) * ((a.r + 31) / 32) + s) * VP * 512 + 8 * lane;
   const bool ok = 32 * s + 8 * (lane >> 4) < a.r;  // (nothing is written past r)
 #pragma unroll
-  for (int k = 0; k < P; ++k) o[k] = as_bf16x8(ok ? *reinterpret_cast<const uint4*>(p + k * 512) : zero4());
+  for (int k = 0; k < VP; ++k) o[k] = as_bf16x8(ok ? *reinterpret_cast<const uint4*>(p + k * 512) : zero4());
 }
 
 // Decoded rows, and rows of fp32: four waves, base and result by operands.
 template <int TM, bool F32, bool WT>
 __global__ __launch_bounds__(256) void up_kernel(UpArgs a) {
-  constexpr int P = F32 ? 3 : 2, XG = TM / 16, H = F32 ? 4 : 2;  // H: 16-byte pieces of a lane and row
+  constexpr int XG = TM / 16, H = F32 ? 4 : 2;  // H: 16-byte pieces of a lane and row
   __shared__ __attribute__((aligned(16))) char lds[WT ? 4 : 1][WT ? WaveTile::BYTES : 16];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int l16 = lane & 15, g = lane >> 4;
@@ -336,11 +335,11 @@ __global__ __launch_bounds__(256) void up_kernel(UpArgs a) {
   const UpBlock b = up_block(a, cb);
   const UpOperand<F32, WT> w{a, a.w + (size_t)max(e.x, 0) * a.w_a, b, WaveTile{lds[WT ? wave : 0]}, lane};
   // what does not wait for the rows' numbers first
-  bf16x8 wo[4], v[XG][P];
+  bf16x8 wo[4], v[XG][VP];
   auto operands = [&](int k0, int s) {
     w.get(k0, s, wo);
 #pragma unroll
-    for (int i = 0; i < XG; ++i) up_rows<P>(a, b.seg, tile * XG + i, k0 / 32 + s, lane, v[i]);
+    for (int i = 0; i < XG; ++i) up_rows(a, b.seg, tile * XG + i, k0 / 32 + s, lane, v[i]);
   };
   if (e.x >= 0) {
     w.stage(0);
@@ -387,7 +386,7 @@ __global__ __launch_bounds__(256) void up_kernel(UpArgs a) {
 #pragma unroll
     for (int i = 0; i < XG; ++i)
 #pragma unroll
-      for (int p = P - 1; p >= 0; --p)
+      for (int p = VP - 1; p >= 0; --p)
 #pragma unroll
         for (int m = 0; m < 4; ++m) acc[i][m] = mfma16(wo[m], v[i][p], acc[i][m]);
   }
@@ -419,7 +418,6 @@ constexpr int UW = 2;  // waves of a workgroup; they share nothing
 
 template <bool STREAM, bool WT, int KS>
 __global__ __launch_bounds__(64 * UW) void up_tile_kernel(UpArgs a) {
-  constexpr int P = 2;
   __shared__ __attribute__((aligned(16))) char lds[UW][WaveTile::BYTES];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int g = lane >> 4;
@@ -464,10 +462,10 @@ __global__ __launch_bounds__(64 * UW) void up_tile_kernel(UpArgs a) {
     };
     if constexpr (KS > 0) {
       // v of 16 rows is fetched while the 16 before are multiplied
-      bf16x8 wo[KS][4], v[2][KS][P];
+      bf16x8 wo[KS][4], v[2][KS][VP];
       auto fetch = [&](int i) {
 #pragma unroll
-        for (int s = 0; s < KS; ++s) up_rows<P>(a, b.seg, 4 * tile + i, s, lane, v[i % 2][s]);
+        for (int s = 0; s < KS; ++s) up_rows(a, b.seg, 4 * tile + i, s, lane, v[i % 2][s]);
       };
       fetch(0);
       w.stage(0);
@@ -483,7 +481,7 @@ __global__ __launch_bounds__(64 * UW) void up_tile_kernel(UpArgs a) {
 #pragma unroll
         for (int s = 0; s < KS; ++s)
 #pragma unroll
-          for (int p = P - 1; p >= 0; --p)
+          for (int p = VP - 1; p >= 0; --p)
 #pragma unroll
             for (int m = 0; m < 4; ++m) acc[m] = mfma16(wo[s][m], v[i % 2][s][p], acc[m]);
         add(i, acc);
@@ -503,10 +501,10 @@ __global__ __launch_bounds__(64 * UW) void up_tile_kernel(UpArgs a) {
           w.get(k0, s, wo);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            bf16x8 v[P];
-            up_rows<P>(a, b.seg, 4 * tile + i, k0 / 32 + s, lane, v);
+            bf16x8 v[VP];
+            up_rows(a, b.seg, 4 * tile + i, k0 / 32 + s, lane, v);
 #pragma unroll
-            for (int p = P - 1; p >= 0; --p)
+            for (int p = VP - 1; p >= 0; --p)
 #pragma unroll
               for (int m = 0; m < 4; ++m) acc[i][m] = mfma16(wo[m], v[p], acc[i][m]);
           }
@@ -777,7 +775,7 @@ Plan plan_of(const LowrankDims& d, bool bwd) {
   p.parts = bwd ? up256(4 * (size_t)d.T * p.R) : 0;
   const size_t tiles16 = p.tm == 16 ? p.l.cap(LIST_16) : 4 * (size_t)p.l.cap(LIST_64);
   const size_t steps = bwd ? (p.R + 31) / 32 : (size_t)d.n_seg * ((d.r + 31) / 32);
-  p.bytes = p.parts + tiles16 * steps * (d.f32 ? 3 : 2) * 1024;
+  p.bytes = p.parts + tiles16 * steps * VP * 1024;
   p.sums = 0;
   p.slot = (long)p.R * d.K + (long)d.N * d.r;
   p.list = LIST_SHORT;
@@ -913,7 +911,6 @@ hipError_t launch_lowrank_fwd(const LowrankDims& d, const LowrankPtrs& q, char* 
   a.v = q.v;
   a.parts = parts;
   a.vr = d.r;
-  a.nparts = d.f32 ? 3 : 2;
   a.R = p.R;
   a.r = p.R;
   a.whole = true;
@@ -956,7 +953,6 @@ hipError_t launch_lowrank_bwd(const LowrankDims& d, const LowrankGradPtrs& q, ch
     a.v = q.dA != nullptr ? u : nullptr;
     a.parts = q.dx != nullptr ? parts : nullptr;
     a.vr = p.R;
-    a.nparts = d.f32 ? 3 : 2;
     a.R = p.R;
     a.r = d.r;
     a.whole = false;
