@@ -628,7 +628,10 @@ int32_t oft_lowrank_bwd(const oft_lowrank_desc* d, const oft_adapter_rows* rows,
  * T N <= 2^34 (else OFT_EUNSUPPORTED); N % 32 == 0 (else OFT_ESHAPE); dtype
  * OFT_DT_BF16 or OFT_DT_F32 (else OFT_EDTYPE).
  * Sums are fp32 and a result is rounded once; fp32 rows enter the matrix
- * products with all their bits (oft_linear_fwd rounds its z to bf16 there). */
+ * products with all their bits, of magnitudes above 2^-100 (oft_linear_fwd
+ * rounds its z to bf16 there).  A block's infinite or NaN values reach that
+ * block of the row's results and of its adapter's dq alone, where they may
+ * become NaN. */
 typedef struct {
   int32_t T, n, N, b;
   int32_t dtype;  /* of z, y and y_saved (dy and dz are bf16) */

@@ -10,7 +10,7 @@
 // rotations.  A wave takes 32 channels of a tile of rows and keeps their
 // rotation in registers as a matrix operand (two 16-channel blocks as one
 // block-diagonal operand); the channels of a lane's operand are also those of
-// its result, 16 consecutive ones of a row.
+// its result, eight consecutive ones of a row.
 //
 // fp32 rows are split into three bf16 parts whose sum is the value; bf16 rows
 // and rotations are operands as they are.
@@ -41,16 +41,35 @@ __device__ __forceinline__ void load_rotation(const uint16_t* __restrict__ rops,
   }
 }
 
-template <bool F32>
-__device__ __forceinline__ void rotate(const uint4 (&rot)[2], const Oct<F32>& z, f32x4 (&o)[2]) {
+// Of two 16-channel blocks, lane groups 0 and 1 bring the first and take its
+// results, 2 and 3 the second.  Each block is a product of its own, with zeros
+// in place of the other's rows: a NaN or an infinity times the zeros beside a
+// block's rotation would be NaN.  (us with both blocks in one product and with
+// two: 64 rows of 6144 channels 4.6 and 4.7, 8192 rows of 19456 channels 120
+// and 119, sums of 4096 such rows 96 and 97, of 1501 fp32 rows of 6144 22.6 and
+// 24.1)
+template <int B, bool F32>
+__device__ __forceinline__ void rotate(const uint4 (&rot)[2], const Oct<F32>& z, int g, f32x4 (&o)[2]) {
   constexpr int P = Oct<F32>::P;
   uint4 p[P];
   z.parts(p);
+  const bool second = g >= 2;
 #pragma unroll
   for (int m = 0; m < 2; ++m) {
     o[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if constexpr (B == 32) {
 #pragma unroll
-    for (int k = P - 1; k >= 0; --k) o[m] = mfma16(as_bf16x8(rot[m]), as_bf16x8(p[k]), o[m]);
+      for (int k = P - 1; k >= 0; --k) o[m] = mfma16(as_bf16x8(rot[m]), as_bf16x8(p[k]), o[m]);
+    } else {
+      f32x4 q = o[m];
+#pragma unroll
+      for (int k = P - 1; k >= 0; --k) {
+        o[m] = mfma16(as_bf16x8(rot[m]), as_bf16x8(second ? zero4() : p[k]), o[m]);
+        q = mfma16(as_bf16x8(rot[m]), as_bf16x8(second ? p[k] : zero4()), q);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[m][i] = second ? q[i] : o[m][i];
+    }
   }
 }
 
@@ -84,7 +103,7 @@ __global__ __launch_bounds__(256) void rotate_kernel(RowLists l, RowOrder rows, 
 #pragma unroll
     for (int i = 0; i < XG; ++i) {
       f32x4 o[2];
-      rotate<F32>(rot, x[i], o);
+      rotate<B, F32>(rot, x[i], g, o);
       if constexpr (F32) {
         x[i].a = make_float4(o[0][0], o[0][1], o[0][2], o[0][3]);
         x[i].b = make_float4(o[1][0], o[1][1], o[1][2], o[1][3]);
@@ -140,7 +159,7 @@ __global__ __launch_bounds__(64 * RW) void rotate_tile_kernel(RowLists l, RowOrd
         Oct<false> v;
         v.u = t.by_operand(i, 4 * k + g, lane);
         f32x4 o[2];
-        rotate<false>(rot[k], v, o);
+        rotate<B, false>(rot[k], v, g, o);
         t.by_operand(i, 4 * k + g, lane) = pack8(o);  // (the lane's own 16 bytes)
       }
     wave_order();
@@ -263,7 +282,7 @@ __global__ __launch_bounds__(256) void rotate_sums_kernel(RowLists l, RowOrder r
           Oct<false> x;
           x.u = *reinterpret_cast<const uint4*>(ds + z);
           f32x4 o[2];
-          rotate<false>(rot[w], x, o);
+          rotate<B, false>(rot[w], x, lane >> 4, o);
           *reinterpret_cast<uint4*>(zs + z) = pack8(o);
         }
       }

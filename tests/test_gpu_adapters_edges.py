@@ -88,3 +88,51 @@ def test_gradient_that_cancels_its_base(T, r, dtype):
     oft.oft_lowrank_bwd(d, rows, _up(f32(dy), "bf16"), None, None, _up(f32(A), "bf16"), _up(f32(B), "bf16"),
                         _up(f32(scale)), dx=gx, dx_base=_up(f32(base), dtype), ws=ws, ws_bytes=nb)
     assert np.array_equal(_down(gx), want.astype(np.float64))
+
+
+# ------------------------------------------------ what a NaN or infinity reaches
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("b", [16, 32])
+@pytest.mark.parametrize("T", [40, 1500])
+def test_blocks_of_a_rotated_row_are_apart(T, b, dtype, bad):
+    """A block's y, dz and dq depend on the block alone: one bad channel leaves
+    all others as they are, bit for bit."""
+    import torch
+
+    oft = _oft()
+    n, N = 3, 160
+    rng = np.random.default_rng([T, b])
+    p, _ = cases.rotations(n, N // b, b)
+    Rf = torch.empty((n, N // b, b, b), device="cuda")
+    Rops = torch.empty((n, N // b, 2, b, b), dtype=torch.bfloat16, device="cuda")
+    oft.cayley_build(_up(p, "bf16"), n * (N // b), b, Rf, Rops)
+    a = cases.adapters(T, n, "mixed")
+    rows = _rows(a, n)
+    d = oft.rotate_desc(T, n, N, b, oft.OFT_DT_F32 if dtype == "f32" else oft.OFT_DT_BF16)
+    z, dy = _up(cases.as_type(rng.normal(0, 1, (T, N)), dtype), dtype), _up(cases.bf16(rng.normal(0, 1, (T, N))), "bf16")
+    ws, nb = _ws(oft.oft_rotate_workspace_bytes(d, oft.OFT_PASS_BWD))
+    saved = z.clone()  # (any rows do for the saved output)
+
+    def run(z, dy, saved):
+        y, dz, alone = _empty((T, N), dtype), _empty((T, N), "bf16"), _empty((T, N), "bf16")
+        dq = _empty((n, N // b, b * (b - 1) // 2))
+        oft.oft_rotate_fwd(d, rows, z, Rops, y)
+        oft.oft_rotate_bwd(d, rows, dy, None, None, Rops, dz=alone)
+        oft.oft_rotate_bwd(d, rows, dy, saved, Rf, Rops, dz=dz, dq=dq, ws=ws, ws_bytes=nb)
+        return y, alone, dz, dq
+
+    clean = run(z, dy, saved)
+    for t, ch in ((0, 5), (T // 2, N - 20), (T - 1, 37)):
+        blk, ad = ch // b, int(a[t])
+        bz, bd, bs = z.clone(), dy.clone(), saved.clone()
+        bz[t, ch] = bd[t, ch] = bad
+        got = run(bz, bd, bs)
+        for g, c in zip(got[:3], clean[:3]):
+            hit = torch.zeros((T, N), dtype=torch.bool, device="cuda")
+            hit[t, blk * b:(blk + 1) * b] = True
+            assert torch.equal(g[~hit], c[~hit]), (t, ch)
+            assert not torch.isfinite(g[hit]).all()
+        hit = torch.zeros((n, N // b), dtype=torch.bool, device="cuda")
+        hit[ad, blk] = True
+        assert torch.equal(got[3][~hit], clean[3][~hit]) and not torch.isfinite(got[3][hit]).all(), (t, ch)
