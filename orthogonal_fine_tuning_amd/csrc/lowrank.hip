@@ -579,12 +579,7 @@ __device__ __forceinline__ void piece(const PieceArgs& a, const PieceJob& q, int
   const int j0 = NJ * 16 * jc, nj = min(NJ * 16, q.nj - j0);
   const int ju = (q.whole ? 0 : seg * q.nj) + j0;  // column of U
 
-  f32x4 acc[NJ][4];
-#pragma unroll
-  for (int j = 0; j < NJ; ++j)
-#pragma unroll
-    for (int c = 0; c < 4; ++c) acc[j][c] = f32x4{0.f, 0.f, 0.f, 0.f};
-
+  f32x4 acc[NJ][4];  // of the rows whose numbers are in LDS
   // thread: 8 columns of rows tid / 32 + 8 i of a step; U: 4 columns of rows
   // tid / UT + UR i
   constexpr int XI = PR / 8;
@@ -664,8 +659,39 @@ __device__ __forceinline__ void piece(const PieceArgs& a, const PieceJob& q, int
         }
     }
   };
+  // lane: column l16 of 16, rows (of U^T) 4 g .. 4 g + 3 of 16.  The sums of
+  // further rows are added to those that the lane wrote itself.
+  const float sc = a.scale[e.x];
+  float* out = e.w < 0 ? q.out + (size_t)e.x * q.out_a : a.part + (size_t)e.w * a.slot + q.part_off;
+  auto write = [&](bool first) {
+    int col0 = c0 + 64 * wave + l16;  // (opaque: the addresses are not kept in registers over the rows)
+    asm volatile("" : "+v"(col0));
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const int jj = 16 * j + 4 * g;
+      if (jj >= nj) continue;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int col = col0 + 16 * c;
+        if (col >= c_hi) continue;
+        float* o = out + (size_t)(j0 + jj) * q.so_j + (size_t)col * q.so_c;
+        f32x4 v = sc * acc[j][c];
+        if (q.so_j == 1) {
+          if (!first) v += *reinterpret_cast<const f32x4*>(o);
+          *reinterpret_cast<f32x4*>(o) = v;
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) o[(size_t)k * q.so_j] = first ? v[k] : o[(size_t)k * q.so_j] + v[k];
+        }
+      }
+    }
+  };
   for (int from = 0; from < e.z; from += IDX) {
     const int rows = min(IDX, e.z - from);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) acc[j][c] = f32x4{0.f, 0.f, 0.f, 0.f};
     __syncthreads();
     fetch_rows(a.l, a.rows.order, e.y + from, rows, idx);
     __syncthreads();
@@ -675,26 +701,7 @@ __device__ __forceinline__ void piece(const PieceArgs& a, const PieceJob& q, int
       step(r0, rows, even);
       if (r0 + PR < rows) step(r0 + PR, rows, odd);
     }
-  }
-  // lane: column l16 of 16, rows (of U^T) 4 g .. 4 g + 3 of 16
-  const float sc = a.scale[e.x];
-  float* out = e.w < 0 ? q.out + (size_t)e.x * q.out_a : a.part + (size_t)e.w * a.slot + q.part_off;
-#pragma unroll
-  for (int j = 0; j < NJ; ++j) {
-    const int jj = 16 * j + 4 * g;
-    if (jj >= nj) continue;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const int col = c0 + 64 * wave + 16 * c + l16;
-      if (col >= c_hi) continue;
-      float* o = out + (size_t)(j0 + jj) * q.so_j + (size_t)col * q.so_c;
-      if (q.so_j == 1) {
-        *reinterpret_cast<float4*>(o) = make_float4(sc * acc[j][c][0], sc * acc[j][c][1], sc * acc[j][c][2], sc * acc[j][c][3]);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) o[(size_t)k * q.so_j] = sc * acc[j][c][k];
-      }
-    }
+    write(from == 0);
   }
 }
 

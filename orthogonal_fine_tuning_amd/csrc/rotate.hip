@@ -181,7 +181,7 @@ __global__ __launch_bounds__(64 * RW) void rotate_tile_kernel(RowLists l, RowOrd
 constexpr int SC = 128, SR = 32, LDS_ROW = SC + 16;
 
 template <int B, bool F32, bool STREAM>
-__global__ __launch_bounds__(256) void rotate_sums_kernel(RowLists l, RowOrder rows, int list,
+__global__ __launch_bounds__(256, B == 32 && !F32 ? 4 : 1) void rotate_sums_kernel(RowLists l, RowOrder rows, int list,
                                                           const uint16_t* dy, const void* __restrict__ y,
                                                           const float* __restrict__ Rf,
                                                           const uint16_t* __restrict__ rops, int N, uint16_t* dz,
@@ -216,14 +216,14 @@ __global__ __launch_bounds__(256) void rotate_sums_kernel(RowLists l, RowOrder r
     return;
   }
   uint4 rot[CW][2];
-  f32x16 acc[CW];
+  f32x16 acc[CW], sum[CW];  // of the rows whose numbers are in LDS, and of all
 #pragma unroll
   for (int w = 0; w < CW; ++w) {
     rot[w][0] = rot[w][1] = zero4();
     const int nw = n0 + 32 * (wave * CW + w);
     if (dz != nullptr && nw < N) load_rotation<B>(rops + (size_t)e.x * N * B * 2, nw, 1, l16, lane >> 4, rot[w]);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) acc[w][i] = 0.0f;
+    for (int i = 0; i < 16; ++i) acc[w][i] = sum[w][i] = 0.0f;
   }
   // a step's tiles on their way
   struct Tile {
@@ -312,6 +312,13 @@ __global__ __launch_bounds__(256) void rotate_sums_kernel(RowLists l, RowOrder r
       step(r0, count, even);
       if (r0 + SR < count) step(r0 + SR, count, odd);
     }
+#pragma unroll
+    for (int w = 0; w < CW; ++w)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        sum[w][i] += acc[w][i];
+        acc[w][i] = 0.0f;
+      }
   }
   __syncthreads();
   put();
@@ -323,7 +330,7 @@ __global__ __launch_bounds__(256) void rotate_sums_kernel(RowLists l, RowOrder r
       if (nw >= N) break;
       float* out = part + ((size_t)min(e.w, RowLists::slots(list) - 1) * (N / 32) + nw / 32) * 1024;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) out[(8 * (i / 4) + 4 * g + i % 4) * 32 + l32] = acc[w][i];
+      for (int i = 0; i < 16; ++i) out[(8 * (i / 4) + 4 * g + i % 4) * 32 + l32] = sum[w][i];
     }
     return;
   }
@@ -332,7 +339,7 @@ __global__ __launch_bounds__(256) void rotate_sums_kernel(RowLists l, RowOrder r
 #pragma unroll
   for (int w = 0; w < CW; ++w)
 #pragma unroll
-    for (int i = 0; i < 16; ++i) S[(32 * (wave * CW + w) + 8 * (i / 4) + 4 * g + i % 4) * SROW + l32] = acc[w][i];
+    for (int i = 0; i < 16; ++i) S[(32 * (wave * CW + w) + 8 * (i / 4) + 4 * g + i % 4) * SROW + l32] = sum[w][i];
   const float* R = Rf + (size_t)e.x * N * B;
   float* out = dq + (size_t)e.x * (N / B) * NP;
   for (int h = 0; h < SC / (G * B); ++h) {  // G blocks at a time

@@ -136,3 +136,86 @@ def test_blocks_of_a_rotated_row_are_apart(T, b, dtype, bad):
         hit = torch.zeros((n, N // b), dtype=torch.bool, device="cuda")
         hit[ad, blk] = True
         assert torch.equal(got[3][~hit], clean[3][~hit]) and not torch.isfinite(got[3][hit]).all(), (t, ch)
+
+
+# ------------------------------------------------------ sums over very many rows
+# A few large products and then small ones, LARGE / 2^30 each: the 32 of a
+# matrix step are a quarter of a step of fp32 beside the large ones' sum, and a
+# sum of them all in one accumulator loses every one.  Sums of at most 2048
+# rows that are then added to each other lose those beside the large ones
+# alone: the small sums are whole multiples of the large one's step.
+LONG_T, LARGE, SMALL, FIRST, CHAIN = 1 << 20, 2.0 ** 20, 2.0 ** -5, 32, 2048
+
+
+def _long(n):
+    """(adapters of LONG_T rows in n runs, the row's values, sums by adapter, how far they may be off)."""
+    a = (np.arange(LONG_T, dtype=np.int64) * n // LONG_T).astype(np.int32)
+    counts = np.bincount(a, minlength=n)
+    first = np.concatenate([[0], np.cumsum(counts)[:-1]])
+    val = np.full(LONG_T, SMALL, dtype=np.float32)
+    for f in first:
+        val[f:f + FIRST] = LARGE
+    want = FIRST * LARGE + (counts - FIRST) * SMALL
+    # what a chain beside the large products may lose, and two steps of the
+    # whole (4 each) for the last chain, whose sum is no multiple of them
+    return a, val, want, CHAIN * SMALL + 8.0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [1, 20])
+def test_lowrank_sums_over_many_rows(n, dtype):
+    import torch
+
+    oft = _oft()
+    K, N, r = 64, 16, 8
+    a, val, want, tol = _long(n)
+    rows = _rows(a, n)
+    col = _up(val)[:, None]
+    one = lambda *s: torch.zeros(s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    x = torch.zeros((LONG_T, K), dtype=torch.float32 if dtype == "f32" else torch.bfloat16, device="cuda")
+    x[:, 3:5] = col
+    v = torch.zeros((LONG_T, r), device="cuda")
+    v[:, 2:4] = col
+    dy, A, B = one(LONG_T, N), one(n, r, K), one(n, N, r)
+    dy[:, 1] = 1.0
+    B[:, 1, 6] = 1.0  # u = 1 in column 6
+    d = oft.lowrank_desc(LONG_T, n, K, (N,), r, oft.OFT_DT_F32 if dtype == "f32" else oft.OFT_DT_BF16)
+    dA, dB = _empty((n, r, K)), _empty((n, N, r))
+    ws, nb = _ws(oft.oft_lowrank_workspace_bytes(d, oft.OFT_PASS_BWD))
+    oft.oft_lowrank_bwd(d, rows, dy, x, v, A, B, torch.ones(n, device="cuda"), dA=dA, dB=dB, ws=ws, ws_bytes=nb)
+    gA, gB = _down(dA), _down(dB)
+    for got in (gA[:, 6, 3], gA[:, 6, 4], gB[:, 1, 2], gB[:, 1, 3]):
+        assert (np.abs(got - want) <= tol).all(), (got - want, tol)
+    gA[:, 6, 3:5] = 0
+    gB[:, 1, 2:4] = 0
+    assert not gA.any() and not gB.any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [1, 20])
+@pytest.mark.parametrize("b", [16, 32])
+def test_rotation_sums_over_many_rows(b, n, dtype):
+    """Identity rotations: dq = 2 (S - S^T)."""
+    import torch
+
+    oft = _oft()
+    N = 32
+    a, val, want, tol = _long(n)
+    rows = _rows(a, n)
+    y = torch.zeros((LONG_T, N), dtype=torch.float32 if dtype == "f32" else torch.bfloat16, device="cuda")
+    y[:, 7] = _up(val)
+    dy = torch.zeros((LONG_T, N), dtype=torch.bfloat16, device="cuda")
+    dy[:, 2] = 1.0
+    eye = torch.eye(b, device="cuda").expand(n, N // b, b, b).contiguous()
+    ops = torch.stack([eye, eye], 2).bfloat16().contiguous()
+    d = oft.rotate_desc(LONG_T, n, N, b, oft.OFT_DT_F32 if dtype == "f32" else oft.OFT_DT_BF16)
+    dq, dz = _empty((n, N // b, b * (b - 1) // 2)), _empty((LONG_T, N), "bf16")
+    ws, nb = _ws(oft.oft_rotate_workspace_bytes(d, oft.OFT_PASS_BWD))
+    oft.oft_rotate_bwd(d, rows, dy, y, eye, ops, dz=dz, dq=dq, ws=ws, ws_bytes=nb)
+    assert torch.equal(dz, dy)
+    got = _down(dq)
+    i, l = np.triu_indices(b, 1)
+    at = int(np.flatnonzero((i == 2) & (l == 7))[0])
+    assert (np.abs(got[:, 0, at] - 2 * want) <= 2 * tol).all(), (got[:, 0, at] - 2 * want, tol)
+    got[:, 0, at] = 0
+    assert not got.any()
