@@ -554,6 +554,8 @@ int32_t oft_moe_balance_bwd(const oft_moe_desc* d, int32_t seq_len, const float*
  *   tiles    work lists for the other calls, of the size that
  *            oft_adapter_rows_bytes gives
  * Rows keep their places in x, y and the rest; nothing is gathered or moved.
+ * Arrays that oft_adapter_route has not written yet give results without
+ * meaning, but no access outside of what the call is given.
  * T and n of a call's descriptor have to be those of its rows (else
  * OFT_ESHAPE).  T == 0 leaves nothing to write but zero gradients. */
 #define OFT_MAX_ADAPTERS 1024

@@ -22,6 +22,14 @@ __device__ __forceinline__ bool list_entry(const RowLists& l, const int* tiles, 
   return e.z > 0;
 }
 
+// The partial slots of an adapter of `pieces` pieces, from `first` on, clipped
+// to those there are.
+__device__ __forceinline__ int slots_of(const RowLists& l, const int* tiles, int list, int ad, int pieces, int& first) {
+  const int all = RowLists::slots(list);
+  first = min(max(tiles[l.part_at(list) + ad], 0), all);
+  return min(pieces, all - first);
+}
+
 // the row at position `pos` of the order
 __device__ __forceinline__ int row_at(const RowLists& l, const int* order, int pos) {
   return min(max(order[pos], 0), l.T - 1);

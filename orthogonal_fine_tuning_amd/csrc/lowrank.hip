@@ -734,8 +734,8 @@ __global__ __launch_bounds__(256) void join_kernel(JoinArgs a) {
   const int ad = blockIdx.y;
   const int pieces = a.l.count(a.list, a.offsets[ad + 1] - a.offsets[ad]);
   if (pieces == 1) return;
-  const int first = a.tiles[a.l.part_at(a.list) + ad];
-  const int slots = min(pieces, RowLists::slots(a.list) - first);
+  int first;
+  const int slots = slots_of(a.l, a.tiles, a.list, ad, pieces, first);
   long i = 4 * ((long)blockIdx.x * 256 + threadIdx.x);
   int which = 0;
   if (i >= a.per[0]) {

@@ -370,8 +370,8 @@ __global__ __launch_bounds__(256) void rotate_join_kernel(RowLists l, RowOrder r
     for (int i = tid; i < nb * NP; i += 256) out[i] = 0.0f;
     return;
   }
-  const int first = rows.tiles[l.part_at(list) + ad];
-  const int slots = min(pieces, RowLists::slots(list) - first);
+  int first;
+  const int slots = slots_of(l, rows.tiles, list, ad, pieces, first);
   const size_t plane = (size_t)N * 32;
   cayley_grad_group<B>(lds, Rf + ((size_t)ad * (N / B) + b0) * B * B, out, nb, tid, [&](int gb, int rr, int cc) {
     const int ch = (b0 + gb) * B, in = ch & 31;

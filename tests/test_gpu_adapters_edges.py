@@ -219,3 +219,49 @@ def test_rotation_sums_over_many_rows(b, n, dtype):
     assert (np.abs(got[:, 0, at] - 2 * want) <= 2 * tol).all(), (got[:, 0, at] - 2 * want, tol)
     got[:, 0, at] = 0
     assert not got.any()
+
+
+# ------------------------------------------------------------- rows never sorted
+@pytest.mark.parametrize("fill", [-2 ** 31, -1, 0, 5, 2 ** 31 - 1, None])
+@pytest.mark.parametrize("T", [70, 3000])
+def test_arrays_that_were_never_written_stay_inside(T, fill):
+    """Whatever an order, its offsets and lists hold, a call writes to its own
+    results and nothing else: guards around every one of them are left alone."""
+    import torch
+
+    oft = _oft()
+    n, K, segs, r, b = 4, 128, (64, 96), 16, 32
+    N, R = sum(segs), 2 * r
+    rng = np.random.default_rng([T, 0 if fill is None else fill % 1000])
+    rows = oft.adapter_rows(T, n)
+    for t in (rows.order, rows.offsets, rows.tiles):
+        if fill is None:
+            t.copy_(torch.from_numpy(rng.integers(-2 ** 31, 2 ** 31, t.numel()).astype(np.int32)))
+        else:
+            t.fill_(fill)
+    guarded = []
+
+    def out(*shape, dtype=torch.float32):
+        count = int(np.prod(shape))
+        buf = torch.full((count + 512,), 7.0, dtype=dtype, device="cuda")
+        guarded.append((buf, count))
+        return buf[256:256 + count].view(*shape)
+
+    bf = dict(dtype=torch.bfloat16)
+    ones = lambda *s: torch.ones(s, device="cuda", **bf)  # noqa: E731
+    ld, rd = oft.lowrank_desc(T, n, K, segs, r), oft.rotate_desc(T, n, N, b)
+    need = [oft.oft_lowrank_workspace_bytes(ld, 0), oft.oft_lowrank_workspace_bytes(ld, 1), oft.oft_rotate_workspace_bytes(rd, 1)]
+    ws = [out(nb // 4) for nb in need]
+    scale = torch.ones(n, device="cuda")
+    Rf = torch.eye(b, device="cuda").expand(n, N // b, b, b).contiguous()
+    Rops = torch.stack([Rf, Rf], 2).bfloat16().contiguous()
+    oft.oft_lowrank_fwd(ld, rows, ones(T, K), ones(n, R, K), ones(n, N, r), scale, ones(T, N), out(T, N, **bf), v=out(T, R),
+                        ws=ws[0], ws_bytes=need[0])
+    oft.oft_lowrank_bwd(ld, rows, ones(T, N), ones(T, K), torch.ones((T, R), device="cuda"), ones(n, R, K), ones(n, N, r),
+                        scale, dx=out(T, K, **bf), dA=out(n, R, K), dB=out(n, N, r), ws=ws[1], ws_bytes=need[1])
+    oft.oft_rotate_fwd(rd, rows, ones(T, N), Rops, out(T, N, **bf))
+    oft.oft_rotate_bwd(rd, rows, ones(T, N), ones(T, N), Rf, Rops, dz=out(T, N, **bf), dq=out(n, N // b, b * (b - 1) // 2),
+                       ws=ws[2], ws_bytes=need[2])
+    torch.cuda.synchronize()
+    for buf, count in guarded:
+        assert bool((buf[:256] == 7).all()) and bool((buf[256 + count:] == 7).all())
