@@ -671,8 +671,9 @@ int32_t oft_rotate_bwd(const oft_rotate_desc* d, const oft_adapter_rows* rows, c
  * empty (their address is then not looked at).  out[i] is grads[i] itself or
  * lies apart from it (else OFT_EINVAL); no out may overlap another's tensors.
  * Gradients in place with coefficient 1 are not written.  sumsq: device fp64;
- * stats: device fp32 [2] = (norm, coefficient), 8-byte aligned.  An infinite
- * norm has coefficient 0, a NaN among the gradients makes all of it NaN.
+ * stats: device fp32 [2] = (norm, coefficient), 8-byte aligned.  A norm that is
+ * infinite as fp32 has coefficient 0 whatever max_norm is, a NaN among the
+ * gradients makes all of it NaN; max_norm may be infinite.
  * Deterministic.  Errors: OFT_EINVAL (m < 0, a negative count, max_norm
  * negative or NaN, null or misaligned pointers), OFT_EDTYPE, OFT_EUNSUPPORTED
  * (m > OFT_MAX_GRADS, 2^36 elements or more), OFT_EWORKSPACE. */

@@ -171,7 +171,8 @@ __global__ __launch_bounds__(256) void sumsq_few_kernel(Items<12> s, double* __r
 __device__ __forceinline__ float coefficient(const double* sumsq, float max_norm, float& norm) {
   norm = (float)sqrt(*sumsq);
   const float c = max_norm / (norm + EPS);
-  return c > 1.0f ? 1.0f : c;  // (NaN stays)
+  if (norm == __builtin_inff()) return 0.0f;  // (also beside an infinite limit)
+  return c > 1.0f ? 1.0f : c;                 // (NaN stays)
 }
 
 // out = c g over [lo, hi)
