@@ -488,12 +488,17 @@ def oft_rotate_bwd(desc, rows, dy, y_saved, R_f32, R_ops, dz=None, dq=None, ws=N
 # ---- global gradient norm and clipping --------------------------------------
 class GradList:
     """Gradients and where their clipped values go, checked once: a program
-    whose gradients keep their addresses makes one and uses it every step."""
+    whose gradients keep their addresses makes one and uses it every step.  The
+    list means the memory that they have when it is made, and keeps it: after
+    t.data = other or t.set_(other) make another list; no tensor of a list may
+    be resized."""
 
     def __init__(self, grads, out=None):
         import torch
 
-        self.grads, self.out = list(grads), list(grads if out is None else out)
+        grads = list(grads)
+        # (aliases: a tensor that is given other memory does not free what the list names)
+        self.grads, self.out = ([t.detach() for t in ts] for ts in (grads, grads if out is None else list(out)))
         self.m = len(self.grads)
         if len(self.out) != self.m or self.m == 0:
             raise ValueError(f"grad_list: {self.m} gradients, {len(self.out)} outputs: want as many, and one at least")

@@ -27,3 +27,31 @@ def test_infinite_limit(out):
     g = torch.full((30,), float("nan"), device="cuda")
     _, stats = _clip([g], None, float("inf"))
     assert np.isnan(stats).all()
+
+
+@pytest.mark.parametrize("swap", ["data", "set_"])
+def test_list_keeps_its_memory(swap):
+    """A list means the memory that its tensors had: a tensor that is given
+    other memory does not free it for others."""
+    import torch
+
+    import orthogonal_fine_tuning_amd as oft
+
+    n = 5 << 20  # (large tensors have blocks of their own, which the next of that size would get)
+    grads, out = [torch.ones(n, device="cuda")], [torch.zeros(n, device="cuda")]
+    lst = oft.grad_list(grads, out)
+    nb = oft.oft_grad_workspace_bytes(lst)
+    ws, sumsq = torch.empty(nb, dtype=torch.uint8, device="cuda"), torch.zeros(1, dtype=torch.float64, device="cuda")
+    stats = torch.zeros(2, device="cuda")
+    was = [grads[0].data_ptr(), out[0].data_ptr()]
+    for t in (grads[0], out[0]):
+        other = torch.full((8,), 3.0, device="cuda")
+        if swap == "data":
+            t.data = other
+        else:
+            t.set_(other)
+    others = [torch.full((n,), 5.0, device="cuda") for _ in range(4)]
+    assert not {t.data_ptr() for t in others} & set(was)
+    oft.oft_grad_sumsq(lst, sumsq, ws=ws, ws_bytes=nb)
+    oft.oft_grad_clip(lst, sumsq, 1.0, stats)
+    assert float(sumsq) == n and all(bool((t == 5).all()) for t in others)
