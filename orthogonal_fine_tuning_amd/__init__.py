@@ -225,19 +225,32 @@ def _workspace(ws, ws_bytes, dev):
     return ws.data_ptr()
 
 
+_ASK = []
+
+
+def _asked():
+    """(the current stream of a GPU, the current GPU): below torch.cuda's objects
+    where torch has that (0.2 us; 1.3 through them, of the 7.3 us that a call of
+    one short kernel takes), else through them."""
+    if not _ASK:
+        import torch
+
+        _ASK[:] = (getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream),
+                   getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device))
+    return _ASK
+
+
 def _launch(name, dev, stream, *args):
-    """Call `name` with the logits' GPU current, on its current stream unless one is given.
-
-    The stream and the device are asked for below torch.cuda's objects (0.2 us;
-    1.3 through them, of the 7.3 us that a call of one short kernel takes)."""
-    import torch
-
+    """Call `name` with the logits' GPU current, on its current stream unless one is given."""
     f = getattr(_lib.load(), name)
+    current_stream, current_device = _asked()
     if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(dev)
-    if torch._C._cuda_getDevice() == dev:
+        stream = current_stream(dev)
+    if current_device() == dev:
         status = f(*args, int(stream))
     else:
+        import torch
+
         with torch.cuda.device(dev):
             status = f(*args, int(stream))
     _lib.check(status, name)
