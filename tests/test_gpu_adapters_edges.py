@@ -265,3 +265,31 @@ def test_arrays_that_were_never_written_stay_inside(T, fill):
     torch.cuda.synchronize()
     for buf, count in guarded:
         assert bool((buf[:256] == 7).all()) and bool((buf[256 + count:] == 7).all())
+
+
+# --------------------------------------------------- fp32 rows times an fp32 u
+@pytest.mark.parametrize("T", [3, 70])
+def test_products_of_fp32_values_keep_their_bits(T):
+    """A row an adapter: dA is one product u x.  Both factors are 1 and then all
+    ones from the eighth bit on, so that their parts below the first are as
+    large as parts can be.  The product is exact but for the parts' own sums
+    (the last is off by a step at most, 2^-23 of it, those before it by 2^-7 of
+    that each) and the scale's rounding (half a step)."""
+    import torch
+
+    oft = _oft()
+    K, N, r = 64, 32, 8
+    val = 1.0 + 2.0 ** -7 - 2.0 ** -23
+    rows = _rows(np.arange(T, dtype=np.int32), T)
+    x = torch.full((T, K), val, device="cuda")
+    x[:, 1::2] *= -4.0
+    dy, B = torch.zeros((T, N), device="cuda"), torch.zeros((T, N, r), device="cuda")
+    dy[:, 2:5] = 1.0
+    B[:, 2], B[:, 3], B[:, 4] = 1.0, 2.0 ** -7, -(2.0 ** -23)  # u = val, exactly
+    d = oft.lowrank_desc(T, T, K, (N,), r, oft.OFT_DT_F32)
+    dA = _empty((T, r, K))
+    ws, nb = _ws(oft.oft_lowrank_workspace_bytes(d, oft.OFT_PASS_BWD))
+    oft.oft_lowrank_bwd(d, rows, dy.bfloat16(), x, None, None, B.bfloat16(), torch.ones(T, device="cuda"), dA=dA, ws=ws,
+                        ws_bytes=nb)
+    want = val * _down(x)[:, None, :]
+    assert (np.abs(_down(dA) - want) <= 4 * cases.U * np.abs(want)).all()
