@@ -478,19 +478,23 @@ def oft_rotate_workspace_bytes(desc, pass_) -> int:
     return n.value
 
 
+def _blocks(desc):
+    return desc.N // desc.b if desc.b > 0 else 0  # (the library refuses other blocks)
+
+
 def oft_rotate_fwd(desc, rows, z, R_ops, y, stream=None):
     """y = R z in every block of channels, with each row's own R; y may be z."""
     d, dev, t = desc, rows.dev, _row_type(desc)
     _same_batch(d, rows)
     _launch("oft_rotate_fwd", dev, stream, C.byref(d), C.byref(rows.c), _tensor("z", z, t, (d.T, d.N), dev),
-            _tensor("R_ops", R_ops, _BF16, (d.n, d.N // d.b, 2, d.b, d.b), dev), _tensor("y", y, t, (d.T, d.N), dev))
+            _tensor("R_ops", R_ops, _BF16, (d.n, _blocks(d), 2, d.b, d.b), dev), _tensor("y", y, t, (d.T, d.N), dev))
 
 
 def oft_rotate_bwd(desc, rows, dy, y_saved, R_f32, R_ops, dz=None, dq=None, ws=None, ws_bytes=0, stream=None):
     """dz (may be dy) and dq of <dy, y>."""
     d, dev = desc, rows.dev
     _same_batch(d, rows)
-    nblk = d.N // d.b
+    nblk = _blocks(d)
     _launch("oft_rotate_bwd", dev, stream, C.byref(d), C.byref(rows.c), _tensor("dy", dy, _BF16, (d.T, d.N), dev),
             _maybe("y_saved", y_saved, _row_type(d), (d.T, d.N), dev),
             _maybe("R_f32", R_f32, "float32", (d.n, nblk, d.b, d.b), dev),

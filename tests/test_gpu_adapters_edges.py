@@ -293,3 +293,18 @@ def test_products_of_fp32_values_keep_their_bits(T):
                         ws_bytes=nb)
     want = val * _down(x)[:, None, :]
     assert (np.abs(_down(dA) - want) <= 4 * cases.U * np.abs(want)).all()
+
+
+def test_descriptor_without_blocks_is_refused():
+    import torch
+
+    oft = _oft()
+    rows = _rows(np.zeros(4, dtype=np.int32), 2)
+    bf = lambda *s: torch.ones(s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    d = oft.rotate_desc(4, 2, 64, 0)
+    with pytest.raises(ValueError):  # (no R_ops has blocks of 0 channels)
+        oft.oft_rotate_fwd(d, rows, bf(4, 64), bf(2, 2, 2, 32, 32), bf(4, 64))
+    with pytest.raises(oft.OftError):
+        oft.oft_rotate_fwd(d, rows, bf(4, 64), bf(2, 0, 2, 0, 0), bf(4, 64))
+    with pytest.raises(oft.OftError):
+        oft.oft_rotate_bwd(d, rows, bf(4, 64), None, None, bf(2, 0, 2, 0, 0), dz=bf(4, 64))
