@@ -6,7 +6,8 @@ import pytest
 
 from oracle import adapters as oracle
 from tests import adapter_cases as cases
-from tests.test_gpu_adapters import _down, _empty, _rows, _up, _ws
+from tests import test_gpu_adapters as plain
+from tests.test_gpu_adapters import _down, _empty, _rows, _up, _within, _ws
 
 pytestmark = pytest.mark.gpu
 
@@ -308,3 +309,87 @@ def test_descriptor_without_blocks_is_refused():
         oft.oft_rotate_fwd(d, rows, bf(4, 64), bf(2, 0, 2, 0, 0), bf(4, 64))
     with pytest.raises(oft.OftError):
         oft.oft_rotate_bwd(d, rows, bf(4, 64), None, None, bf(2, 0, 2, 0, 0), dz=bf(4, 64))
+
+
+# ------------------------------------------- rows and ranks of the streamed kernels
+def _picked(T):
+    return np.concatenate([[0, 1, T - 2, T - 1], np.random.default_rng(1).integers(0, T, 60)])
+
+
+@pytest.mark.parametrize("r", [16, 48, 72])
+def test_streamed_low_rank(r):
+    """Rows of more bytes than the caches hold, both directions, every length
+    of v that the kernel keeps in another way: rows picked from them, in 64 bits."""
+    import torch
+
+    oft = _oft()
+    T, n, wide, thin = 36000, 3, 2048, 64
+    g = torch.Generator(device="cuda").manual_seed(r)
+    bf = lambda *s: torch.randn(s, generator=g, device="cuda").bfloat16()  # noqa: E731
+    ad = torch.randint(-1, n, (T,), generator=g, device="cuda").int()
+    rows = oft.adapter_rows(T, n)
+    oft.oft_adapter_route(rows, ad)
+    scale = torch.tensor([0.5, 1.0, 2.0], device="cuda")
+    pick = _picked(T)
+    base = bf(T, wide)
+    for K, N in ((thin, wide), (wide, thin)):
+        d = oft.lowrank_desc(T, n, K, (N,), r)
+        x, dy, A, B = bf(T, K), bf(T, N), bf(n, r, K) / 8, bf(n, N, r) / 4
+        c = {"x": _down(x[pick]), "dy": _down(dy[pick]), "A": _down(A), "B": _down(B), "scale": _down(scale),
+             "adapter": ad.cpu().numpy()[pick]}
+        got = torch.empty_like(base)
+        if N == wide:
+            ws, nb = _ws(oft.oft_lowrank_workspace_bytes(d, oft.OFT_PASS_FWD))
+            oft.oft_lowrank_fwd(d, rows, x, A, B, scale, base, got, ws=ws, ws_bytes=nb)
+            (want, tol), _ = cases.lowrank_fwd({**c, "y_base": _down(base[pick])}, (N,), "bf16")
+        else:
+            ws, nb = _ws(oft.oft_lowrank_workspace_bytes(d, oft.OFT_PASS_BWD))
+            oft.oft_lowrank_bwd(d, rows, dy, None, None, A, B, scale, dx=got, dx_base=base, ws=ws, ws_bytes=nb)
+            (want, tol), _, _ = cases.lowrank_bwd({**c, "dx_base": _down(base[pick])}, np.zeros((len(pick), r)), (N,), "bf16")
+        _within(got[pick], want, tol, (r, K, N))
+        none = ad < 0
+        assert torch.equal(got[none], base[none])
+
+
+@pytest.mark.parametrize("b", [16, 32])
+def test_streamed_rotation_gradients_of_fp32_rows(b):
+    """dz against calls of 1000 rows, bit for bit; dq of some blocks in 64 bits."""
+    import torch
+
+    oft = _oft()
+    T, n, N, few = 36000, 3, 2048, 4
+    g = torch.Generator(device="cuda").manual_seed(b)
+    ad = torch.randint(-1, n, (T,), generator=g, device="cuda").int()
+    y, dy = torch.randn((T, N), generator=g, device="cuda"), torch.randn((T, N), generator=g, device="cuda").bfloat16()
+    p, _ = cases.rotations(n, N // b, b)
+    Rf = torch.empty((n, N // b, b, b), device="cuda")
+    Rops = torch.empty((n, N // b, 2, b, b), dtype=torch.bfloat16, device="cuda")
+    oft.cayley_build(_up(p, "bf16"), n * (N // b), b, Rf, Rops)
+    rows = oft.adapter_rows(T, n)
+    oft.oft_adapter_route(rows, ad)
+    d = oft.rotate_desc(T, n, N, b, oft.OFT_DT_F32)
+    dz, dq = torch.empty_like(dy), _empty((n, N // b, b * (b - 1) // 2))
+    ws, nb = _ws(oft.oft_rotate_workspace_bytes(d, oft.OFT_PASS_BWD))
+    oft.oft_rotate_bwd(d, rows, dy, y, Rf, Rops, dz=dz, dq=dq, ws=ws, ws_bytes=nb)
+    for at in range(0, T, 1000):
+        part = oft.adapter_rows(1000, n)
+        oft.oft_adapter_route(part, ad[at:at + 1000].clone())
+        one = torch.empty((1000, N), dtype=torch.bfloat16, device="cuda")
+        oft.oft_rotate_bwd(oft.rotate_desc(1000, n, N, b), part, dy[at:at + 1000].clone(), None, None, Rops, dz=one)
+        assert torch.equal(one, dz[at:at + 1000])
+    i, l = np.triu_indices(b, 1)
+    eye = np.eye(b)
+    for k in range(n):
+        sel = (ad == k).nonzero()[:, 0]
+        o, s = _down(dy[sel, :few * b]).reshape(-1, few, b), _down(y[sel, :few * b]).reshape(-1, few, b)
+        for j in range(few):
+            R = _down(Rf[k, j])
+            gq = 0.5 * (R.T + eye) @ (o[:, j].T @ s[:, j]) @ (eye + R)
+            m = abs(o[:, j]).T @ abs(s[:, j])
+            e = 0.5 * (abs(R).T + eye) @ (cases.sum_err(len(sel), m) + 4 * cases.U * (b + 64) * m) @ (eye + abs(R))
+            assert (np.abs(_down(dq[k, j]) - (gq - gq.T)[i, l]) <= (e + e.T)[i, l]).all(), (k, j)
+
+
+@pytest.mark.parametrize("kind", ["mixed", "some", "none", "skewed"])
+def test_lists_of_rows_sorted_eight_steps_a_wave(kind):
+    plain.test_route_lists(600001, 900, kind)
