@@ -513,9 +513,10 @@ class GradList:
     def __init__(self, grads, out=None):
         import torch
 
-        grads = list(grads)
-        # (aliases: a tensor that is given other memory does not free what the list names)
-        self.grads, self.out = ([t.detach() for t in ts] for ts in (grads, grads if out is None else list(out)))
+        self.grads = list(grads)
+        self.out = self.grads if out is None else list(out)
+        # (a tensor that is given other memory does not free what the list names)
+        self._memory = [t.untyped_storage() for t in self.grads + self.out]
         self.m = len(self.grads)
         if len(self.out) != self.m or self.m == 0:
             raise ValueError(f"grad_list: {self.m} gradients, {len(self.out)} outputs: want as many, and one at least")
