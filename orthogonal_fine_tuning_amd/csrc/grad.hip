@@ -22,7 +22,8 @@ constexpr float EPS = 1e-6f;
 // Gradients of more bytes than this in all are streamed past the caches (norm
 // and clipping into other tensors in us, streamed and not: 64 MB 38 and 42
 // from memory, 35 and 35 from the caches, 120 MB 67, 78 and 64, 62, 512 MB 269
-// and 308; 16 MB 13.5 and 12.6 from memory).
+// and 308; 16 MB 13.5 and 12.6 from memory).  Where the two differ, gradients are
+// taken to come from memory: most were written layers ago.
 constexpr int64_t STREAM_BYTES = 64LL << 20;
 
 struct Item {

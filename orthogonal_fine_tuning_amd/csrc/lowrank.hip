@@ -764,9 +764,10 @@ size_t up256(size_t b) { return (b + 255) & ~(size_t)255; }
 // Rows of a tile: 16 while the batch is one of decoded rows (an adapter then
 // has few), else 64; small ranks gain longer, since the factors that each tile
 // reads again are small.  Forward calls in us by 16 and by 64 rows, 8 adapters
-// and 64: rank 16 beside QKV, 2048 rows 20.6, 20.7 and 22, 28; 4096 rows 31,
-// 33 and 33, 36, but the gradients 59, 57 and 75, 73; rank 64 on gate/up, 256
-// rows 20, 21 and 51, 56; 512 rows 27, 26 and 59, 57; 1024 rows 40, 34 and 81, 76.
+// and 64: rank 16 beside QKV, 2048 rows 21.6, 22.2 and 23, 30, gradients 43, 43
+// and 55, 57; 4096 rows 33, 35 and 34, 38, but the gradients 61, 59 and 77, 78,
+// and one rule serves both; rank 64 on gate/up, 256 rows 21, 22 and 60, 66; 512
+// rows 27.7, 28.2 and 67, 67; 1024 rows 43, 38 and 86, 87.
 int tile_rows(int T, int r) { return T <= (r <= 32 ? T16_MAX : 512) ? 16 : 64; }
 
 struct Plan {
@@ -794,10 +795,10 @@ Plan plan_of(const LowrankDims& d, bool bwd) {
     // pieces of a quarter of the rows where the columns alone give workgroups
     // enough, or bf16 rows are few: fewer partial sums (us of a backward pass of
     // one adapter by quarters and by sixteenths, K 2560: rank 64 beside QKV,
-    // 108 workgroups a piece, 2048 rows 81 and 93, of fp32 97 and 102; on
-    // gate/up, 212 of them, 94 and 118, 118 and 134; rank 16 on gate/up, 86 of
-    // them, 56 and 56, 84 and 71; beside QKV, 44 of them, 46 and 42, 69 and 57,
-    // but 512 rows of bf16 25 and 27, 1024 rows 32 and 33)
+    // 108 workgroups a piece, 2048 rows 84 and 94, of fp32 100 and 101; on
+    // gate/up, 212 of them, 94 and 117, 120 and 131; rank 16 on gate/up, 86 of
+    // them, 56 and 56, 87 and 70; beside QKV, 44 of them, 46 and 43, 71 and 57,
+    // but 512 rows of bf16 26 and 27, 1024 rows 32 and 33)
     const auto jobs = [](int cols, int r) { return (cols + PC - 1) / PC * ((r + 16 * MAXG - 1) / (16 * MAXG)); };
     p.list = jobs(d.K, p.R) + jobs(d.N, d.r) >= 100 || (!d.f32 && d.T <= 1024) ? LIST_LONG : LIST_SHORT;
     p.bytes = p.sums + up256(4 * (size_t)RowLists::slots(p.list) * p.slot);
