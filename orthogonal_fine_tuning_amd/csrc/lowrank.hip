@@ -218,7 +218,7 @@ __global__ __launch_bounds__(64 * DW) void down_kernel(DownArgs a) {
     const int col = seg * a.r + jw + c0;
     if (a.v != nullptr && r < e.z)
       *reinterpret_cast<float4*>(a.v + (size_t)row_at(a.l, a.rows.order, e.y + r) * a.R + col) = o;
-    if (a.parts != nullptr && e.x >= 0) {
+    if (a.parts != nullptr && e.x >= 0 && r < e.z) {
       const int s = col / a.vr, k = col % a.vr, steps = (a.vr + 31) / 32;
       uint16_t* out = a.parts + ((((size_t)tile * XT + i) * (a.R / a.vr) + s) * steps + k / 32) * VP * 512 +
                       ((k % 32) / 8 * 16 + l16) * 8 + k % 8;
@@ -313,13 +313,19 @@ struct UpOperand {
   }
 };
 
-// v of 16 rows (block `i16` of the list's) and contraction items 32 s ..
-__device__ __forceinline__ void up_rows(const UpArgs& a, int seg, int i16, int s, int lane, bf16x8 (&o)[VP]) {
+// v of 16 rows (block `i16` of the list's, `rows` of them there) and contraction
+// items 32 s ..
+__device__ __forceinline__ void up_rows(const UpArgs& a, int seg, int i16, int rows, int s, int lane,
+                                        bf16x8 (&o)[VP]) {
   const uint16_t* p =
       a.parts + (((size_t)i16 * a.segs + seg) * ((a.r + 31) / 32) + s) * VP * 512 + 8 * lane;
-  const bool ok = 32 * s + 8 * (lane >> 4) < a.r;  // (nothing is written past r)
+  const bool ok = 32 * s + 8 * (lane >> 4) < a.r && (lane & 15) < rows;  // (nothing else is written)
 #pragma unroll
-  for (int k = 0; k < VP; ++k) o[k] = as_bf16x8(ok ? *reinterpret_cast<const uint4*>(p + k * 512) : zero4());
+  for (int k = 0; k < VP; ++k) o[k] = as_bf16x8(zero4());
+  if (ok) {  // (one branch: a choice per load made the compiler wait between them)
+#pragma unroll
+    for (int k = 0; k < VP; ++k) o[k] = as_bf16x8(*reinterpret_cast<const uint4*>(p + k * 512));
+  }
 }
 
 // Decoded rows, and rows of fp32: four waves, base and result by operands.
@@ -339,7 +345,7 @@ __global__ __launch_bounds__(256) void up_kernel(UpArgs a) {
   auto operands = [&](int k0, int s) {
     w.get(k0, s, wo);
 #pragma unroll
-    for (int i = 0; i < XG; ++i) up_rows(a, b.seg, tile * XG + i, k0 / 32 + s, lane, v[i]);
+    for (int i = 0; i < XG; ++i) up_rows(a, b.seg, tile * XG + i, e.z - 16 * i, k0 / 32 + s, lane, v[i]);
   };
   if (e.x >= 0) {
     w.stage(0);
@@ -465,7 +471,7 @@ __global__ __launch_bounds__(64 * UW) void up_tile_kernel(UpArgs a) {
       bf16x8 wo[KS][4], v[2][KS][VP];
       auto fetch = [&](int i) {
 #pragma unroll
-        for (int s = 0; s < KS; ++s) up_rows(a, b.seg, 4 * tile + i, s, lane, v[i % 2][s]);
+        for (int s = 0; s < KS; ++s) up_rows(a, b.seg, 4 * tile + i, e.z - 16 * i, s, lane, v[i % 2][s]);
       };
       fetch(0);
       w.stage(0);
@@ -502,7 +508,7 @@ __global__ __launch_bounds__(64 * UW) void up_tile_kernel(UpArgs a) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             bf16x8 v[VP];
-            up_rows(a, b.seg, 4 * tile + i, k0 / 32 + s, lane, v);
+            up_rows(a, b.seg, 4 * tile + i, e.z - 16 * i, k0 / 32 + s, lane, v);
 #pragma unroll
             for (int p = VP - 1; p >= 0; --p)
 #pragma unroll
