@@ -170,7 +170,7 @@ __device__ __forceinline__ void fetch_rows(const RowLists& l, const int* order, 
 // Rows of more bytes than this are streamed past the caches: two batches in
 // turn and one again and again, rotated in us, streamed and not: 76 MB 36, 38
 // and 36, 30; 129 MB 55, 60 and 56, 52; 222 MB 92, 98 and 92, 99; low-rank
-// updates of 129 MB 66, 76 and 67, 73, of 76 MB 44, 50 and 45, 41.  Where the
+// updates of 129 MB 66, 74 and 67, 73, of 76 MB 44, 49 and 44, 40.  Where the
 // two differ, rows are taken to be in the caches: the projection has just
 // written them.
 constexpr size_t STREAM_BYTES = (size_t)128 << 20;

@@ -770,10 +770,11 @@ size_t up256(size_t b) { return (b + 255) & ~(size_t)255; }
 // Rows of a tile: 16 while the batch is one of decoded rows (an adapter then
 // has few), else 64; small ranks gain longer, since the factors that each tile
 // reads again are small.  Forward calls in us by 16 and by 64 rows, 8 adapters
-// and 64: rank 16 beside QKV, 2048 rows 21.6, 22.2 and 23, 30, gradients 43, 43
-// and 55, 57; 4096 rows 33, 35 and 34, 38, but the gradients 61, 59 and 77, 78,
-// and one rule serves both; rank 64 on gate/up, 256 rows 21, 22 and 60, 66; 512
-// rows 27.7, 28.2 and 67, 67; 1024 rows 43, 38 and 86, 87.
+// and 64: rank 16 beside QKV, 2048 rows 21.5, 21.9 and 22.5, 29, gradients 43, 42
+// and 54, 56; 4096 rows 32, 34 and 34, 36, but the gradients 61, 59 and 76, 76,
+// and one rule serves both; rank 64 beside QKV, 512 rows of 4 and 64 adapters
+// 17, 17 and 32, 35, gradients of 4 and 16 40, 48 and 52, 59; on gate/up, 256
+// rows 20, 21 and 56, 52; 512 rows 27, 27 and 61, 54; 1024 rows 42, 35 and 80, 73.
 int tile_rows(int T, int r) { return T <= (r <= 32 ? T16_MAX : 512) ? 16 : 64; }
 
 struct Plan {

@@ -7,6 +7,7 @@ import pytest
 from oracle import adapters as oracle
 from tests import adapter_cases as cases
 from tests import test_gpu_adapters as plain
+from tests import test_gpu_adapters_use as use
 from tests.test_gpu_adapters import _down, _empty, _rows, _up, _within, _ws
 
 pytestmark = pytest.mark.gpu
@@ -393,3 +394,9 @@ def test_streamed_rotation_gradients_of_fp32_rows(b):
 @pytest.mark.parametrize("kind", ["mixed", "some", "none", "skewed"])
 def test_lists_of_rows_sorted_eight_steps_a_wave(kind):
     plain.test_route_lists(600001, 900, kind)
+
+
+def test_graphs_of_sums_in_several_chains():
+    """Pieces of more rows than one accumulator takes, replayed by two graphs
+    that share their workspaces: what a replay before left is not added to."""
+    use.test_graphs_that_share_workspaces_follow_their_inputs(41000)
