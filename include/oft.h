@@ -37,6 +37,8 @@
  *   - Results are deterministic: no floating-point atomics; every reduction
  *     runs in a fixed order.  Calls are re-entrant; calls on different
  *     streams may overlap only if they share no output or workspace.
+ *   - An output or a workspace overlaps no other argument of its call, unless
+ *     the call says that it may.
  *   - Encodings: bf16 / fp16 tensors are uint16_t bit patterns; fp8 is OCP
  *     e4m3fn (bias 7, max 448, no infinities).  INT4 weights are uint8
  *     [rows, cols/2]: element c of a row sits in byte c/2, low nibble for
